@@ -289,6 +289,216 @@ int gdn_decode_step_native(const gdn_shape_t* shape, int32_t n_seqs, const void*
                            const float* g, float* S, float* o, void* stream);
 
 /*
+ * ---- Gated linear recurrence ------------------------------------------------
+ *
+ * The layer with a vector for a state: per sequence and channel,
+ *
+ *     alpha_t = exp(g_t)
+ *     h_t     = alpha_t h_{t-1} + b_t x_t
+ *     o_t     = h_t
+ *
+ * with b_t = 1 (GDN_LRU_GATE_NONE), 1 - alpha_t (GDN_LRU_GATE_COMPLEMENT) or
+ * sqrt(max(0, 1 - alpha_t^2)) (GDN_LRU_GATE_NORM).  g_t = -inf resets the
+ * state; g_t <= 0 is meant, larger values follow the same formulas.
+ *
+ * As above, chunks are counted from each sequence's first token, here of
+ * GDN_LRU_CHUNK tokens, whatever the batch.  Within a chunk
+ *     A_p = alpha_p A_{p-1},  B_p = fma(alpha_p, B_{p-1}, b_p x_p),
+ *     h_p = fma(A_p, S, B_p)
+ * from A = 1, B = 0 and the state S at the chunk's start; the next chunk
+ * starts from its last h.  Prefill, continuation, decode and the trainer's
+ * forward run these operations in this order, so they give bit-identical o and
+ * states, for any batch composition.
+ *
+ * Rows: x, o, dO and dx hold D channels in in_dtype, g and dg in g_dtype; ldx,
+ * ldg, ... is the distance between tokens' rows in elements (0 = D, and at
+ * least D otherwise), so that they may be slices of wider rows.  h0, hT, dhT,
+ * dh0 are fp32 [N, D] and dense.  o may be x itself (same ld); no other buffers
+ * may overlap.  Rows past cu_seqlens[N] are neither read nor written.  The
+ * conventions at the top hold (16-byte aligned starts, cu_seqlens in a device
+ * and a host copy, host copy nullable); a host copy that disagrees with the
+ * device copy gives wrong values, never an access outside the rows [0, T).
+ */
+#define GDN_LRU_CHUNK 32
+
+typedef enum {
+  GDN_LRU_GATE_NONE = 0,
+  GDN_LRU_GATE_COMPLEMENT = 1,
+  GDN_LRU_GATE_NORM = 2
+} gdn_lru_gate_t;
+
+typedef struct {
+  int32_t D;        /* channels, 1 .. 2^20                */
+  int32_t in_dtype; /* gdn_dtype_t of x, o, dO, dx        */
+  int32_t g_dtype;  /* gdn_dtype_t of g, dg               */
+  int32_t gate;     /* gdn_lru_gate_t                     */
+} gdn_lru_shape_t;
+
+/* Decode cache of N sequences, plain device memory owned by the caller: the
+ * state of sequence n is h = A S + B.  pos counts the tokens that the current
+ * chunk has taken, 0..GDN_LRU_CHUNK-1, once for each 256 channels (all equal);
+ * values outside are clamped. */
+typedef struct {
+  float* S;     /* [N, D] state at the start of the current chunk      */
+  float* A;     /* [N, D] product of the current chunk's alpha         */
+  float* B;     /* [N, D] the current chunk's state from a zero start  */
+  int32_t* pos; /* [N, ceil(D / 256)]                                  */
+} gdn_lru_cache_t;
+
+/* Cache of n_seqs sequences with nothing decoded yet: S = h0 (or zero when h0
+ * is NULL), A = 1, B = 0, pos = 0. */
+int gdn_lru_cache_init(const gdn_lru_shape_t* shape, int32_t n_seqs, const float* h0,
+                       gdn_lru_cache_t* cache, void* stream);
+
+/* Packed prefill from h0 (nullable: zero).  Writes o and, where given, each
+ * sequence's final state hT and the cache from which decode or continuation
+ * goes on.  No workspace. */
+int gdn_lru_prefill(const gdn_lru_shape_t* shape, int32_t n_seqs, const int32_t* cu_seqlens_dev,
+                    const int32_t* cu_seqlens_host, const void* x, int64_t ldx, const void* g,
+                    int64_t ldg, const float* h0, void* o, int64_t ldo, float* hT,
+                    gdn_lru_cache_t* cache, void* stream);
+
+/* The next tokens of sequences whose cache stands anywhere inside a chunk: the
+ * same bits as one prefill of the whole history.  The cache is left where the
+ * sequences now stand.  Unlike gdn_prefill_continue it needs no host copy of
+ * the positions. */
+int gdn_lru_prefill_continue(const gdn_lru_shape_t* shape, int32_t n_seqs,
+                             const int32_t* cu_seqlens_dev, const int32_t* cu_seqlens_host,
+                             const void* x, int64_t ldx, const void* g, int64_t ldg,
+                             gdn_lru_cache_t* cache, void* o, int64_t ldo, float* hT,
+                             void* stream);
+
+/* One token for each of n_seqs sequences: x, o and g hold n_seqs rows. */
+int gdn_lru_decode_step(const gdn_lru_shape_t* shape, int32_t n_seqs, const void* x, int64_t ldx,
+                        const void* g, int64_t ldg, gdn_lru_cache_t* cache, void* o, int64_t ldo,
+                        void* stream);
+
+/* Bytes of workspace of gdn_lru_fwd_bwd; 0 for an invalid shape. */
+size_t gdn_lru_workspace_bytes(const gdn_lru_shape_t* shape, int32_t n_seqs, int64_t total_tokens);
+
+/*
+ * Trainer forward + backward.  o (nullable) and hT (nullable) are gdn_lru_prefill's
+ * bits; without them the call is the backward alone.  dhT nullable (zero).
+ * With delta_t the gradient of h_t,
+ *     delta_t = dO_t + alpha_{t+1} delta_{t+1}        (+ dhT at the last token)
+ *     dx_t    = b_t delta_t
+ *     dg_t    = delta_t (alpha_t h_{t-1} + b'_t x_t)
+ *     dh0     = alpha_1 delta_1                        (dhT for an empty sequence)
+ * where b' = db/dg is 0, -alpha or -alpha^2 / b (0 where b = 0, at g = 0,
+ * where the derivative has no finite value).  No atomics: bitwise reproducible.
+ */
+int gdn_lru_fwd_bwd(const gdn_lru_shape_t* shape, int32_t n_seqs, const int32_t* cu_seqlens_dev,
+                    const int32_t* cu_seqlens_host, const void* x, int64_t ldx, const void* g,
+                    int64_t ldg, const float* h0, const void* dO, int64_t lddo, const float* dhT,
+                    void* o, int64_t ldo, float* hT, void* dx, int64_t lddx, void* dg,
+                    int64_t lddg, float* dh0, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * ---- Norms of q and k per head, with rotary positions -----------------------
+ *
+ * What a layer does to q and k before it (with gdn_prefill's qk_l2norm = 0), in
+ * one pass.  Per token and head, on a vector x of d elements:
+ *
+ *     n = 1 / sqrt(sum x^2 + eps)   (GDN_NORM_L2),  1 / sqrt(mean x^2 + eps)
+ *         (GDN_NORM_RMS),  1 (GDN_NORM_NONE)
+ *     z = x n                        (L2, NONE),   x n (weight_offset + w)  (RMS)
+ *     y = z, its first r elements turned in pairs (z_a, z_b):
+ *         y_a = c (z_a cos - z_b sin),  y_b = c (z_b cos + z_a sin),
+ *         angle = pos inv_freq[i],  c = rope_scale,
+ *         pair i: (i, i + r/2) for GDN_ROPE_HALF, (2i, 2i + 1) for
+ *         GDN_ROPE_INTERLEAVED
+ *     q is multiplied by `scale` besides.
+ *
+ * Angles are formed in fp64 and reduced there, so far positions lose nothing;
+ * sums are fp32, and each output is rounded once.
+ *
+ * Rows: token t's heads are H_q (H_k) vectors of d elements one after another,
+ * at q + t ldq (ld in elements; 0 = dense; a multiple of 8), so that q and k
+ * may be slices of one projection's rows.  qo may be q and ko may be k (same
+ * type and ld); no other overlap.  Every start is 16-byte aligned.
+ *
+ * Positions: pos [T] int32 on the device if given; else token t of sequence n
+ * stands at start[n] + t - cu_seqlens[n] (start NULL = 0; all on the device),
+ * and rows past cu_seqlens[n_seqs] are neither read nor written.
+ *
+ * Supported: d a multiple of 8 up to 512, r a multiple of 8 up to d (0: no
+ * rotation, inv_freq may be NULL), H_q >= 1, H_k >= 0 (0: k is not touched),
+ * fp32 or bf16 on either side.
+ */
+typedef enum { GDN_NORM_NONE = 0, GDN_NORM_L2 = 1, GDN_NORM_RMS = 2 } gdn_norm_t;
+typedef enum { GDN_ROPE_HALF = 0, GDN_ROPE_INTERLEAVED = 1 } gdn_rope_layout_t;
+
+typedef struct {
+  int32_t H_q, H_k;
+  int32_t d, r;
+  int32_t in_dtype;    /* gdn_dtype_t of q, k (and dq, dk)             */
+  int32_t out_dtype;   /* gdn_dtype_t of qo, ko (and dqo, dko)         */
+  int32_t norm;        /* gdn_norm_t                                   */
+  int32_t layout;      /* gdn_rope_layout_t                            */
+  float eps;
+  float scale;         /* multiplies q                                 */
+  float rope_scale;    /* multiplies cos and sin                       */
+  float weight_offset; /* RMS: the factor is weight_offset + w         */
+} gdn_qk_shape_t;
+
+/* w_q, w_k: fp32 [d], RMS only (NULL: w = 0 with weight_offset as given). */
+int gdn_qk_rotary(const gdn_qk_shape_t* shape, int64_t n_tokens, const int32_t* pos,
+                  int32_t n_seqs, const int32_t* cu_seqlens, const int32_t* start,
+                  const float* inv_freq, const float* w_q, const float* w_k, const void* q,
+                  int64_t ldq, const void* k, int64_t ldk, void* qo, int64_t ldqo, void* ko,
+                  int64_t ldko, void* stream);
+
+/* Bytes of workspace of gdn_qk_rotary_bwd; 0 for an invalid shape. */
+size_t gdn_qk_workspace_bytes(const gdn_qk_shape_t* shape, int64_t n_tokens);
+
+/* Its gradient, from the inputs q, k and the gradients dqo, dko of qo, ko:
+ * with dz the turned-back dy times scale, u = dz (weight_offset + w) and m = d
+ * (RMS) or 1 (L2),
+ *     dx = n (u - x (n^2 / m) sum(u x)),   dw = sum over tokens and heads of dz x n.
+ * dw_q, dw_k: fp32 [d], RMS only, nullable; their sums run in a fixed order
+ * for given sizes (no atomics). */
+int gdn_qk_rotary_bwd(const gdn_qk_shape_t* shape, int64_t n_tokens, const int32_t* pos,
+                      int32_t n_seqs, const int32_t* cu_seqlens, const int32_t* start,
+                      const float* inv_freq, const float* w_q, const float* w_k, const void* q,
+                      int64_t ldq, const void* k, int64_t ldk, const void* dqo, int64_t lddqo,
+                      const void* dko, int64_t lddko, void* dq, int64_t lddq, void* dk,
+                      int64_t lddk, float* dw_q, float* dw_k, void* ws, size_t ws_bytes,
+                      void* stream);
+
+/* Frequencies of the r/2 pairs, base^(-2i/r), scaled for contexts longer than
+ * trained on: `factor` times longer than orig_len tokens.
+ *   NONE    as they are
+ *   LINEAR  divided by factor
+ *   NTK     base replaced by base factor^(r / (r - 2))
+ *   YARN    a pair that turns more than `high` times in orig_len tokens stays,
+ *           one that turns fewer than `low` times is divided by factor, and
+ *           between the (whole) pair indices where that is so the two are
+ *           blended in proportion to the index; rope_scale = 0.1 ln factor + 1
+ *           unless attn > 0 gives it
+ *   BANDS   as YARN, blended in proportion to the number of turns, with
+ *           rope_scale 1 (or attn)
+ * Writes inv_freq [r/2] and *rope_scale in host memory; formed in fp64 and
+ * rounded once.  Host only. */
+typedef enum {
+  GDN_ROPE_NONE = 0,
+  GDN_ROPE_LINEAR = 1,
+  GDN_ROPE_NTK = 2,
+  GDN_ROPE_YARN = 3,
+  GDN_ROPE_BANDS = 4
+} gdn_rope_scaling_kind_t;
+
+typedef struct {
+  int32_t kind;     /* gdn_rope_scaling_kind_t                 */
+  double factor;    /* >= 1; not read for NONE                 */
+  double orig_len;  /* > 0; YARN and BANDS                     */
+  double low, high; /* 0 < low < high; YARN and BANDS          */
+  double attn;      /* YARN, BANDS: rope_scale, 0 = as above   */
+} gdn_rope_scaling_t;
+
+int gdn_rope_freqs(int32_t r, double base, const gdn_rope_scaling_t* scaling, float* inv_freq,
+                   float* rope_scale);
+
+/*
  * Kernel timing (instrumentation).  While enabled, every launch the entry
  * points make is bracketed by HIP events recorded on the call's stream.
  * gdn_profile_read waits for the recorded events, returns the summed
@@ -297,8 +507,9 @@ int gdn_decode_step_native(const gdn_shape_t* shape, int32_t n_seqs, const void*
  * k_plan, k_prep, k_wy, k_scan, k_rec, k_decode, k_wy_resync, k_scan_resync,
  * k_cache_init, k_chunk_o (gdn_prefill_chunked, gdn_fwd_bwd_chunked),
  * k_decode_native (gdn_decode_step_native), k_cont_plan, k_cont_gather,
- * k_cont_scatter (gdn_prefill_continue) and the k_bwd_* kernels of
- * gdn_fwd_bwd.  Events are created
+ * k_cont_scatter (gdn_prefill_continue), the k_bwd_* kernels of gdn_fwd_bwd,
+ * the k_lru_* kernels of gdn_lru_* and the k_qk_* kernels of gdn_qk_*.  Events
+ * are created
  * by the library on first use and reused; no device memory is allocated.
  * Thread-safe; records from concurrent calls are merged.
  */

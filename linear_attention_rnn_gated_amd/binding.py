@@ -26,7 +26,19 @@ EXPORTS = ["gdn_workspace_bytes", "gdn_cache_init", "gdn_prefill", "gdn_decode_s
            "gdn_fwd_bwd", "gdn_profile_enable", "gdn_profile_read", "gdn_contract_id",
            "gdn_contract_check", "gdn_error_string", "gdn_prefill_chunked",
            "gdn_prefill_continue", "gdn_fwd_bwd_ex", "gdn_decode_step_noalloc",
-           "gdn_fwd_bwd_chunked", "gdn_decode_step_native", "gdn_profile_filter"]
+           "gdn_fwd_bwd_chunked", "gdn_decode_step_native", "gdn_profile_filter",
+           "gdn_lru_cache_init", "gdn_lru_prefill", "gdn_lru_prefill_continue",
+           "gdn_lru_decode_step", "gdn_lru_workspace_bytes", "gdn_lru_fwd_bwd",
+           "gdn_qk_rotary", "gdn_qk_workspace_bytes", "gdn_qk_rotary_bwd", "gdn_rope_freqs"]
+
+LRU_CHUNK = 32    # tokens per chunk of the gated linear recurrence
+LRU_GROUP = 256   # channels per position counter of its cache
+LRU_GATES = {"none": 0, "complement": 1, "norm": 2}
+QK_NORMS = {"none": 0, "l2": 1, "rms": 2}
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
+_DTYPE_CODES = {torch.float32: GDN_F32, torch.bfloat16: GDN_BF16}
+_DTYPES = {GDN_F32: torch.float32, GDN_BF16: torch.bfloat16}
 
 
 class Shape(ctypes.Structure):
@@ -40,6 +52,30 @@ class CacheStruct(ctypes.Structure):
                 ("kbuf", ctypes.c_void_p), ("vbuf", ctypes.c_void_p),
                 ("bbuf", ctypes.c_void_p), ("gbuf", ctypes.c_void_p),
                 ("pos", ctypes.c_void_p)]
+
+
+class LruShape(ctypes.Structure):
+    _fields_ = [("D", ctypes.c_int32), ("in_dtype", ctypes.c_int32),
+                ("g_dtype", ctypes.c_int32), ("gate", ctypes.c_int32)]
+
+
+class LruCacheStruct(ctypes.Structure):
+    _fields_ = [("S", ctypes.c_void_p), ("A", ctypes.c_void_p), ("B", ctypes.c_void_p),
+                ("pos", ctypes.c_void_p)]
+
+
+class QkShape(ctypes.Structure):
+    _fields_ = [("H_q", ctypes.c_int32), ("H_k", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("r", ctypes.c_int32), ("in_dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("norm", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("eps", ctypes.c_float), ("scale", ctypes.c_float),
+                ("rope_scale", ctypes.c_float), ("weight_offset", ctypes.c_float)]
+
+
+class RopeScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("factor", ctypes.c_double),
+                ("orig_len", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("attn", ctypes.c_double)]
 
 
 _lib = None
@@ -96,6 +132,25 @@ def lib():
         L.gdn_contract_check.restype = ctypes.c_int
         L.gdn_error_string.argtypes = [ctypes.c_int]
         L.gdn_error_string.restype = ctypes.c_char_p
+        ls, lc, qs = (ctypes.POINTER(t) for t in (LruShape, LruCacheStruct, QkShape))
+        L.gdn_lru_cache_init.argtypes = [ls, i32, vp, lc, vp]
+        L.gdn_lru_prefill.argtypes = [ls, i32, vp, vp, vp, i64, vp, i64, vp, vp, i64, vp, lc, vp]
+        L.gdn_lru_prefill_continue.argtypes = [ls, i32, vp, vp, vp, i64, vp, i64, lc, vp, i64, vp,
+                                               vp]
+        L.gdn_lru_decode_step.argtypes = [ls, i32, vp, i64, vp, i64, lc, vp, i64, vp]
+        L.gdn_lru_workspace_bytes.argtypes = [ls, i32, i64]
+        L.gdn_lru_fwd_bwd.argtypes = [ls, i32, vp, vp, vp, i64, vp, i64, vp, vp, i64, vp, vp, i64,
+                                      vp, vp, i64, vp, i64, vp, vp, sz, vp]
+        L.gdn_qk_rotary.argtypes = [qs, i64, vp, i32, vp, vp, vp, vp, vp, vp, i64, vp, i64, vp,
+                                    i64, vp, i64, vp]
+        L.gdn_qk_workspace_bytes.argtypes = [qs, i64]
+        L.gdn_qk_rotary_bwd.argtypes = [qs, i64, vp, i32, vp, vp, vp, vp, vp, vp, i64, vp, i64, vp,
+                                        i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, sz, vp]
+        L.gdn_rope_freqs.argtypes = [i32, ctypes.c_double, ctypes.POINTER(RopeScaling), vp, vp]
+        for name in ("lru_cache_init", "lru_prefill", "lru_prefill_continue", "lru_decode_step",
+                     "lru_fwd_bwd", "qk_rotary", "qk_rotary_bwd", "rope_freqs"):
+            getattr(L, "gdn_" + name).restype = ctypes.c_int
+        L.gdn_lru_workspace_bytes.restype = L.gdn_qk_workspace_bytes.restype = sz
         _lib = L
     return _lib
 
@@ -451,4 +506,355 @@ def gdn_fwd_bwd(shape, q, k, v, beta, g, cu_seqlens, dO, h0=None, dhT=None, ws=N
                               _ptr(r["dbeta"]), _ptr(r["dg"]), _ptr(r["dh0"]), _ptr(ws),
                               ws.numel(), _stream(dev))
     _check(st, "gdn_fwd_bwd_ex")
+    return r
+
+
+# ---- gated linear recurrence, and the norms and rotation of q and k -----------
+# These calls take rows with any distance between tokens (slices of wider
+# projections), check that every tensor lies on the first one's GPU, and run
+# there on that GPU's current stream, whichever GPU is current.
+
+
+def _gpu(t, name):
+    if t.device.type != "cuda":
+        raise ValueError(f"{name}: expected a GPU tensor, got one on {t.device}")
+    return t.device
+
+
+def _rows(t, dtype, n, width, dev, name):
+    """The distance between the rows of t [n, width], after checking it."""
+    if t.dtype != dtype or t.device != dev or t.dim() != 2 or t.shape[0] != n or t.shape[1] != width:
+        raise ValueError(f"{name}: expected {dtype} ({n}, {width}) on {dev}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    ld, unit = t.stride()
+    if n <= 1:
+        ld = width
+    if (unit != 1 and width > 1) or ld < width:
+        raise ValueError(f"{name}: rows must be contiguous and must not overlap, got strides "
+                         f"{t.stride()}")
+    return ld
+
+
+def _heads(t, dtype, T, H, d, dev, name):
+    """The distance between the tokens' rows of t [T, H, d], after checking it."""
+    if t.dtype != dtype or t.device != dev or t.dim() != 3 or tuple(t.shape) != (T, H, d):
+        raise ValueError(f"{name}: expected {dtype} ({T}, {H}, {d}) on {dev}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    ld, head, unit = t.stride()
+    if T <= 1:
+        ld = H * d
+    if unit != 1 or (head != d and H > 1) or ld < H * d:
+        raise ValueError(f"{name}: a token's heads must be contiguous and tokens must not "
+                         f"overlap, got strides {t.stride()}")
+    return ld
+
+
+def _dense(t, dtype, shape, dev, name):
+    if t.dtype != dtype or t.device != dev or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on {dev}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device} "
+                         f"contiguous={t.is_contiguous()}")
+    return t.data_ptr()
+
+
+def _optional(t, dtype, shape, dev, name):
+    return None if t is None else _dense(t, dtype, shape, dev, name)
+
+
+def _launch(name, dev, *args):
+    """Calls library function `name` with the stream of `dev` as last argument."""
+    fn = getattr(lib(), name)
+    if dev.index == torch.cuda.current_device():
+        status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if status != GDN_OK:
+        raise GdnError(status, name)
+
+
+def _packed(cu_seqlens, cu_seqlens_host, dev, T):
+    """(N, device copy, host copy) of cu_seqlens over T rows."""
+    cu_dev, cu_host = _cu_pair(cu_seqlens, dev, cu_seqlens_host)
+    if cu_host is None:
+        raise ValueError("cu_seqlens_host: expected a CPU int32 tensor or None")
+    n = cu_host.numel() - 1
+    if cu_host.dim() != 1 or n < 0:
+        raise ValueError("cu_seqlens: expected one dimension of N + 1 values")
+    if int(cu_host[n]) > T:
+        raise ValueError(f"cu_seqlens: ends at {int(cu_host[n])}, past the {T} rows given")
+    return n, cu_dev, cu_host
+
+
+def make_lru_shape(D, in_dtype, g_dtype=torch.float32, gate="none"):
+    """Shape of a gated linear recurrence of D channels: x, o in in_dtype, the
+    log decay g in g_dtype; gate "none", "complement" or "norm" gives the
+    input's weight 1, 1 - alpha or sqrt(1 - alpha^2)."""
+    return LruShape(D, _DTYPE_CODES[in_dtype], _DTYPE_CODES[g_dtype], LRU_GATES[gate])
+
+
+def lru_workspace_bytes(shape, n_seqs, total_tokens):
+    return int(lib().gdn_lru_workspace_bytes(ctypes.byref(shape), n_seqs, total_tokens))
+
+
+class LruCache:
+    """Decode cache (gdn_lru_cache_t) of n sequences of D channels, owned by
+    torch tensors."""
+
+    def __init__(self, D, n, device):
+        f32 = dict(dtype=torch.float32, device=device)
+        self._hold(torch.empty(n, D, **f32), torch.empty(n, D, **f32), torch.empty(n, D, **f32),
+                   torch.zeros(n, -(-D // LRU_GROUP), dtype=torch.int32, device=device))
+
+    @classmethod
+    def of(cls, S, A, B, pos):
+        """A cache over existing tensors: S, A, B fp32 [n, D], pos int32
+        [n, ceil(D / 256)]."""
+        c = object.__new__(cls)
+        n, D = S.shape
+        dev = _gpu(S, "S")
+        for t, name in ((S, "S"), (A, "A"), (B, "B")):
+            _dense(t, torch.float32, (n, D), dev, name)
+        _dense(pos, torch.int32, (n, -(-D // LRU_GROUP)), dev, "pos")
+        c._hold(S, A, B, pos)
+        return c
+
+    def _hold(self, S, A, B, pos):
+        self.S, self.A, self.B, self.pos = S, A, B, pos
+        self.n, self.D = S.shape
+        self.device = S.device
+        self._struct = LruCacheStruct(S.data_ptr(), A.data_ptr(), B.data_ptr(), pos.data_ptr())
+
+    def struct(self):
+        return self._struct
+
+    def tensors(self):
+        return [self.S, self.A, self.B, self.pos]
+
+    def state(self):
+        """The states now, [n, D]: A S + B."""
+        return self.A * self.S + self.B
+
+    def clone(self):
+        return LruCache.of(*[t.clone() for t in self.tensors()])
+
+    def check(self, shape, n, dev):
+        if self.n != n or self.D != shape.D or self.device != dev:
+            raise ValueError(f"cache: expected {n} sequences of {shape.D} channels on {dev}, got "
+                             f"{self.n} of {self.D} on {self.device}")
+
+
+def gdn_lru_cache_init(shape, n, device, h0=None):
+    """Cache of n sequences with nothing decoded yet, from h0 (fp32 [n, D])."""
+    c = LruCache(shape.D, n, device)
+    dev = _gpu(c.S, "device")
+    _launch("gdn_lru_cache_init", dev, ctypes.byref(shape), n,
+            _optional(h0, torch.float32, (n, shape.D), dev, "h0"), ctypes.byref(c.struct()))
+    return c
+
+
+def _lru_prefill(name, shape, x, g, cu_seqlens, h0, cache, want_hT, out, hT_out, cu_seqlens_host):
+    dev = _gpu(x, "x")
+    T, D = x.shape[0], shape.D
+    xt = _DTYPES.get(shape.in_dtype)
+    ldx = _rows(x, xt, T, D, dev, "x")
+    ldg = _rows(g, _DTYPES.get(shape.g_dtype), T, D, dev, "g")
+    n, cu_dev, cu_host = _packed(cu_seqlens, cu_seqlens_host, dev, T)
+    o = torch.empty(T, D, dtype=xt, device=dev) if out is None else out
+    ldo = _rows(o, xt, T, D, dev, "out")
+    hT = hT_out
+    if hT is None and want_hT:
+        hT = torch.empty(n, D, dtype=torch.float32, device=dev)
+    p_hT = _optional(hT, torch.float32, (n, D), dev, "hT_out")
+    if cache is not None:
+        cache.check(shape, n, dev)
+    cs = None if cache is None else ctypes.byref(cache.struct())
+    head = (ctypes.byref(shape), n, cu_dev.data_ptr(), cu_host.data_ptr(), x.data_ptr(), ldx,
+            g.data_ptr(), ldg)
+    if name == "gdn_lru_prefill":
+        p_h0 = _optional(h0, torch.float32, (n, D), dev, "h0")
+        _launch(name, dev, *head, p_h0, o.data_ptr(), ldo, p_hT, cs)
+    else:
+        _launch(name, dev, *head, cs, o.data_ptr(), ldo, p_hT)
+    return o, hT
+
+
+def gdn_lru_prefill(shape, x, g, cu_seqlens, h0=None, cache=None, want_hT=True, out=None,
+                    hT_out=None, cu_seqlens_host=None):
+    """Packed prefill of the gated linear recurrence: x, g [T, D] from h0 (fp32
+    [N, D]); fills `cache` for decode if given.  Returns (o [T, D] in x's type,
+    hT fp32 [N, D]).  out may be x."""
+    return _lru_prefill("gdn_lru_prefill", shape, x, g, cu_seqlens, h0, cache, want_hT, out,
+                        hT_out, cu_seqlens_host)
+
+
+def gdn_lru_prefill_continue(shape, x, g, cu_seqlens, cache, want_hT=True, out=None, hT_out=None,
+                             cu_seqlens_host=None):
+    """The next tokens of the sequences of `cache`, which may stand anywhere in
+    their chunks; the cache moves on.  Returns (o, hT) of the new tokens."""
+    return _lru_prefill("gdn_lru_prefill_continue", shape, x, g, cu_seqlens, None, cache, want_hT,
+                        out, hT_out, cu_seqlens_host)
+
+
+def gdn_lru_decode_step(shape, x, g, cache, out=None):
+    """One token per sequence: x, g [N, D]; the cache moves on.  Returns o."""
+    dev = _gpu(x, "x")
+    n, D = x.shape[0], shape.D
+    xt = _DTYPES.get(shape.in_dtype)
+    ldx = _rows(x, xt, n, D, dev, "x")
+    ldg = _rows(g, _DTYPES.get(shape.g_dtype), n, D, dev, "g")
+    o = torch.empty(n, D, dtype=xt, device=dev) if out is None else out
+    ldo = _rows(o, xt, n, D, dev, "out")
+    cache.check(shape, n, dev)
+    _launch("gdn_lru_decode_step", dev, ctypes.byref(shape), n, x.data_ptr(), ldx, g.data_ptr(),
+            ldg, ctypes.byref(cache.struct()), o.data_ptr(), ldo)
+    return o
+
+
+def gdn_lru_fwd_bwd(shape, x, g, cu_seqlens, dO, h0=None, dhT=None, ws=None, want_o=True,
+                    out=None, cu_seqlens_host=None):
+    """Trainer forward + backward of the gated linear recurrence, or with
+    want_o=False the backward alone.  Returns dict(o, hT, dx, dg, dh0), without
+    o and hT in the latter case; o, dx in x's type, dg in g's.  out: optional
+    dict of caller-owned tensors for some of them."""
+    dev = _gpu(x, "x")
+    T, D = x.shape[0], shape.D
+    xt, gt = _DTYPES.get(shape.in_dtype), _DTYPES.get(shape.g_dtype)
+    ldx = _rows(x, xt, T, D, dev, "x")
+    ldg = _rows(g, gt, T, D, dev, "g")
+    lddo = _rows(dO, xt, T, D, dev, "dO")
+    n, cu_dev, cu_host = _packed(cu_seqlens, cu_seqlens_host, dev, T)
+    kinds = {"o": (xt, T), "hT": (torch.float32, n), "dx": (xt, T), "dg": (gt, T),
+             "dh0": (torch.float32, n)}
+    if not want_o:
+        del kinds["o"], kinds["hT"]
+    out = out or {}
+    if not set(out) <= set(kinds):
+        raise ValueError(f"out: expected some of {sorted(kinds)}, got {sorted(out)}")
+    r = {key: out[key] if key in out else torch.empty(rows, D, dtype=dt, device=dev)
+         for key, (dt, rows) in kinds.items()}
+    ld = {key: _rows(r[key], kinds[key][0], T, D, dev, f"out[{key!r}]")
+          for key in ("o", "dx", "dg") if key in r}
+    for key in ("hT", "dh0"):
+        if key in r:
+            _dense(r[key], torch.float32, (n, D), dev, f"out[{key!r}]")
+    ws = _scratch(ws, lru_workspace_bytes(shape, n, T), dev, "gdn_lru_workspace_bytes")
+    ptr = {key: t.data_ptr() for key, t in r.items()}
+    _launch("gdn_lru_fwd_bwd", dev, ctypes.byref(shape), n, cu_dev.data_ptr(), cu_host.data_ptr(),
+            x.data_ptr(), ldx, g.data_ptr(), ldg,
+            _optional(h0, torch.float32, (n, D), dev, "h0"), dO.data_ptr(), lddo,
+            _optional(dhT, torch.float32, (n, D), dev, "dhT"), ptr.get("o"), ld.get("o", 0),
+            ptr.get("hT"), ptr["dx"], ld["dx"], ptr["dg"], ld["dg"], ptr["dh0"], ws.data_ptr(),
+            ws.numel())
+    return r
+
+
+def _scratch(ws, need, dev, where):
+    if need == 0:
+        raise GdnError(GDN_ERR_UNSUPPORTED, where)
+    if ws is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    if ws.device != dev or ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise ValueError(f"ws: expected contiguous uint8 on {dev}")
+    return ws
+
+
+def rope_freqs(r, base=10000.0, kind="none", factor=1.0, orig_len=0.0, low=1.0, high=32.0,
+               attn=0.0):
+    """(inv_freq fp32 CPU [r / 2], rope_scale): the rotary frequencies of r
+    elements, scaled for contexts `factor` times longer than orig_len (kind
+    "none", "linear", "ntk", "yarn" or "bands"; see include/gdn.h)."""
+    inv_freq = torch.empty(max(r, 0) // 2, dtype=torch.float32)
+    scale = ctypes.c_float()
+    s = RopeScaling(ROPE_SCALINGS[kind], factor, orig_len, low, high, attn)
+    _check(lib().gdn_rope_freqs(r, base, ctypes.byref(s), inv_freq.data_ptr() or None,
+                                ctypes.addressof(scale)), "gdn_rope_freqs")
+    return inv_freq, scale.value
+
+
+def make_qk_shape(H_q, H_k, d, r, in_dtype, out_dtype=None, norm="l2", layout="half", eps=1e-6,
+                  scale=1.0, rope_scale=1.0, weight_offset=0.0):
+    """Shape of gdn_qk_rotary: H_q and H_k heads of d elements, the first r of
+    them rotated; norm "l2", "rms" or "none"; layout "half" or "interleaved";
+    q is multiplied by scale; RMS weights act as weight_offset + w."""
+    return QkShape(H_q, H_k, d, r, _DTYPE_CODES[in_dtype],
+                   _DTYPE_CODES[in_dtype if out_dtype is None else out_dtype], QK_NORMS[norm],
+                   ROPE_LAYOUTS[layout], eps, scale, rope_scale, weight_offset)
+
+
+def qk_workspace_bytes(shape, total_tokens):
+    return int(lib().gdn_qk_workspace_bytes(ctypes.byref(shape), total_tokens))
+
+
+def _qk_args(shape, q, k, inv_freq, pos, cu_seqlens, start, w_q, w_k):
+    """The device of q, the arguments that the two calls share, and the types."""
+    dev = _gpu(q, "q")
+    T, d = q.shape[0], shape.d
+    it = _DTYPES.get(shape.in_dtype)
+    ldq = _heads(q, it, T, shape.H_q, d, dev, "q")
+    ldk, pk = 0, None
+    if shape.H_k > 0:
+        ldk, pk = _heads(k, it, T, shape.H_k, d, dev, "k"), k.data_ptr()
+    if (pos is None) == (cu_seqlens is None):
+        raise ValueError("expected either pos or cu_seqlens")
+    n, i32 = 0, torch.int32
+    if pos is None:
+        n = cu_seqlens.numel() - 1
+        if n < 0 or (n == 0 and T > 0):
+            raise ValueError("cu_seqlens: expected N + 1 values")
+        p_cu = _dense(cu_seqlens, i32, (n + 1,), dev, "cu_seqlens")
+        where = (None, n, p_cu, _optional(start, i32, (n,), dev, "start"))
+    else:
+        if start is not None:
+            raise ValueError("start: only with cu_seqlens")
+        where = (_dense(pos, i32, (T,), dev, "pos"), 0, None, None)
+    f32 = torch.float32
+    freq = None
+    if shape.r > 0:
+        if inv_freq is None:
+            raise ValueError("inv_freq: expected the frequencies of the rotation")
+        freq = _dense(inv_freq, f32, (shape.r // 2,), dev, "inv_freq")
+    weights = (_optional(w_q, f32, (d,), dev, "w_q"), _optional(w_k, f32, (d,), dev, "w_k"))
+    return dev, (ctypes.byref(shape), T, *where, freq, *weights, q.data_ptr(), ldq, pk, ldk)
+
+
+def gdn_qk_rotary(shape, q, k, inv_freq, pos=None, cu_seqlens=None, start=None, w_q=None,
+                  w_k=None, q_out=None, k_out=None):
+    """Norms of q [T, H_q, d] and k [T, H_k, d] per head and the rotation by
+    each token's position, in one pass.  Positions: pos (int32 GPU tensor [T]),
+    or, from cu_seqlens (int32 GPU tensor), the place in the sequence plus
+    start[n].  Returns (q, k) in the shape's output type; q_out / k_out may be q
+    and k themselves.  Prepares q and k for gdn_prefill and gdn_decode_step with
+    qk_l2norm=False (and scale 1)."""
+    dev, args = _qk_args(shape, q, k, inv_freq, pos, cu_seqlens, start, w_q, w_k)
+    T, d, ot = q.shape[0], shape.d, _DTYPES.get(shape.out_dtype)
+    qo = torch.empty(T, shape.H_q, d, dtype=ot, device=dev) if q_out is None else q_out
+    ko = torch.empty(T, shape.H_k, d, dtype=ot, device=dev) if k_out is None else k_out
+    ldq = _heads(qo, ot, T, shape.H_q, d, dev, "q_out")
+    ldk = _heads(ko, ot, T, shape.H_k, d, dev, "k_out")
+    _launch("gdn_qk_rotary", dev, *args, qo.data_ptr(), ldq, ko.data_ptr(), ldk)
+    return qo, ko
+
+
+def gdn_qk_rotary_bwd(shape, q, k, dq_out, dk_out, inv_freq, pos=None, cu_seqlens=None,
+                      start=None, w_q=None, w_k=None, ws=None):
+    """Gradient of gdn_qk_rotary: from the gradients of its outputs, dict(dq,
+    dk) in q's type and, with norm "rms", dw_q and dw_k (fp32 [d])."""
+    dev, args = _qk_args(shape, q, k, inv_freq, pos, cu_seqlens, start, w_q, w_k)
+    T, d = q.shape[0], shape.d
+    ot = _DTYPES.get(shape.out_dtype)
+    lddq = _heads(dq_out, ot, T, shape.H_q, d, dev, "dq_out")
+    lddk, pdk = 0, None
+    if shape.H_k > 0:
+        lddk, pdk = _heads(dk_out, ot, T, shape.H_k, d, dev, "dk_out"), dk_out.data_ptr()
+    r = {"dq": torch.empty(T, shape.H_q, d, dtype=q.dtype, device=dev),
+         "dk": torch.empty(T, shape.H_k, d, dtype=q.dtype, device=dev)}
+    p_dw, p_ws, ws_bytes = (None, None), None, 0
+    if shape.norm == QK_NORMS["rms"]:
+        r["dw_q"] = torch.empty(d, dtype=torch.float32, device=dev)
+        r["dw_k"] = torch.empty(d, dtype=torch.float32, device=dev)
+        ws = _scratch(ws, qk_workspace_bytes(shape, T), dev, "gdn_qk_workspace_bytes")
+        p_dw, p_ws, ws_bytes = (r["dw_q"].data_ptr(), r["dw_k"].data_ptr()), ws.data_ptr(), ws.numel()
+    _launch("gdn_qk_rotary_bwd", dev, *args, dq_out.data_ptr(), lddq, pdk, lddk,
+            r["dq"].data_ptr(), 0, r["dk"].data_ptr(), 0, *p_dw, p_ws, ws_bytes)
     return r

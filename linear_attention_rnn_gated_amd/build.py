@@ -17,7 +17,8 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libgdn.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
-SOURCES = ["gdn_kernels.hip", "gdn_plan.cpp"]
+SOURCES = ["gdn_library.hip", "gdn_plan.cpp", "gdn_rope.cpp"]
+INCLUDED = ["gdn_plan.h", "gdn_kernels.hip", "gdn_lru.hip", "gdn_qk.hip"]  # by the sources
 FLAGS = [
     "--offload-arch=gfx950",
     "-O3",
@@ -39,8 +40,8 @@ def source_digest(extra_flags=()):
     compile flags: part of gdn_contract_id(), so two builds that could differ in
     arithmetic never report the same id."""
     h = hashlib.sha256()
-    for path in [os.path.join(ROOT, "include", "gdn.h"), os.path.join(CSRC, "gdn_plan.h"),
-                 *[os.path.join(CSRC, s) for s in SOURCES]]:
+    for path in [os.path.join(ROOT, "include", "gdn.h"),
+                 *[os.path.join(CSRC, s) for s in [*INCLUDED, *SOURCES]]]:
         with open(path, "rb") as f:
             h.update(f.read())
     h.update(" ".join([*FLAGS, *extra_flags]).encode())

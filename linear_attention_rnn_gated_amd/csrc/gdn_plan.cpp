@@ -122,4 +122,45 @@ bool aligned16(std::initializer_list<const void*> ptrs) {
   return true;
 }
 
+int check_lru_shape(const gdn_lru_shape_t* s) {
+  if (!s || s->D <= 0) return GDN_ERR_INVALID_ARG;
+  if (s->gate != GDN_LRU_GATE_NONE && s->gate != GDN_LRU_GATE_COMPLEMENT && s->gate != GDN_LRU_GATE_NORM)
+    return GDN_ERR_INVALID_ARG;
+  if (s->in_dtype != GDN_F32 && s->in_dtype != GDN_BF16) return GDN_ERR_UNSUPPORTED;
+  if (s->g_dtype != GDN_F32 && s->g_dtype != GDN_BF16) return GDN_ERR_UNSUPPORTED;
+  if (s->D > (1 << 20)) return GDN_ERR_UNSUPPORTED;
+  return GDN_OK;
+}
+
+int check_lru_cache(const gdn_lru_cache_t* c) {
+  if (!c || !c->S || !c->A || !c->B || !c->pos) return GDN_ERR_INVALID_ARG;
+  return aligned16({c->S, c->A, c->B, c->pos}) ? GDN_OK : GDN_ERR_INVALID_ARG;
+}
+
+int64_t row_stride(int64_t ld, int64_t row) {
+  if (ld == 0) return row;
+  // rows past 2^40 elements apart would take offsets past 63 bits
+  return ld >= row && ld <= (int64_t{1} << 40) ? ld : -1;
+}
+
+int check_qk_shape(const gdn_qk_shape_t* s) {
+  if (!s || s->H_q <= 0 || s->H_k < 0 || s->d <= 0 || s->r < 0 || s->r > s->d) return GDN_ERR_INVALID_ARG;
+  if (s->norm != GDN_NORM_NONE && s->norm != GDN_NORM_L2 && s->norm != GDN_NORM_RMS) return GDN_ERR_INVALID_ARG;
+  if (s->layout != GDN_ROPE_HALF && s->layout != GDN_ROPE_INTERLEAVED) return GDN_ERR_INVALID_ARG;
+  if (!std::isfinite(s->eps) || s->eps < 0 || !std::isfinite(s->scale) || !std::isfinite(s->rope_scale) ||
+      !std::isfinite(s->weight_offset))
+    return GDN_ERR_INVALID_ARG;
+  if (s->in_dtype != GDN_F32 && s->in_dtype != GDN_BF16) return GDN_ERR_UNSUPPORTED;
+  if (s->out_dtype != GDN_F32 && s->out_dtype != GDN_BF16) return GDN_ERR_UNSUPPORTED;
+  if (s->d % 8 != 0 || s->d > 512 || s->r % 8 != 0) return GDN_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(s->H_q) + s->H_k > 4096) return GDN_ERR_UNSUPPORTED;
+  return GDN_OK;
+}
+
+int64_t qk_bwd_blocks(const gdn_qk_shape_t* s, int64_t T) {
+  (void)s;
+  const int64_t b = (T + 3) / 4;  // a wave takes one token at a time, a block has four
+  return b < 1024 ? b : 1024;
+}
+
 }  // namespace gdn

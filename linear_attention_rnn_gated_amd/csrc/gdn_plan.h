@@ -77,4 +77,21 @@ int check_cache(const gdn_cache_t* c);
 // True if every pointer is 16-byte aligned (NULL counts as aligned).
 bool aligned16(std::initializer_list<const void*> ptrs);
 
+// Gated linear recurrence.  Channels per decode-cache position counter.
+constexpr int32_t kLruGroup = 256;
+int check_lru_shape(const gdn_lru_shape_t* s);
+// All fields of a recurrence cache non-NULL and aligned.
+int check_lru_cache(const gdn_lru_cache_t* c);
+// A row distance as given (0 = dense): the distance, or -1 if it is too small.
+int64_t row_stride(int64_t ld, int64_t row);
+// Chunk slots that the backward keeps states for: T / 32 + N bounds every
+// split of T tokens into N sequences.
+inline int64_t lru_slots(int64_t T, int64_t N) { return T / GDN_LRU_CHUNK + N; }
+
+// Norms of q and k with rotary positions.
+int check_qk_shape(const gdn_qk_shape_t* s);
+// Blocks of the gradient kernel that keep partial weight sums (a function of
+// the sizes alone).
+int64_t qk_bwd_blocks(const gdn_qk_shape_t* s, int64_t T);
+
 }  // namespace gdn

@@ -1,0 +1,456 @@
+// Norms of q and k per head with rotary positions (include/gdn.h): kernels and
+// C ABI.  Part of gdn_library.hip.
+//
+// A head's d elements are spread over a group of lanes, eight elements each in
+// two quads chosen so that both elements of a rotated pair lie in one lane:
+// with the half layout quads 4u and r/2 + 4u, with neighbouring pairs (and in
+// the part that is not rotated) the eight elements from 8u.  A wave holds 64 /
+// group heads at once and goes over all heads of a token, so a pair's angle,
+// sine and cosine are formed once per token and lane.
+//
+// Bound: HBM (4 to 12 bytes and about 12 vector instructions per element).
+
+namespace {
+
+constexpr double kInvTwoPi = 0.15915494309189533576888376337251;
+
+struct QkIO {
+  const void* q;
+  const void* k;
+  void* qo;
+  void* ko;
+  const void* dqo;
+  const void* dko;
+  const int32_t* pos;
+  const int32_t* cu;
+  const int32_t* start;
+  const float* inv_freq;
+  const float* w_q;
+  const float* w_k;
+  float* part;  // [blocks][2][d] sums for dw_q, dw_k; nullptr: not wanted
+  int64_t T, ldq, ldk, ldqo, ldko, lddqo, lddko;
+  int N, H_q, H_k, d, r, norm;
+  int lg;     // log2 of the lanes per head
+  int split;  // parts that a token's heads are cut into
+  float eps, scale, rope_scale, offset;
+};
+
+__device__ __forceinline__ void ld_quad(const float* p, float* v) {
+  const float4 x = *reinterpret_cast<const float4*>(p);
+  v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+}
+__device__ __forceinline__ void ld_quad(const bf16_t* p, float* v) {
+  const float4 x = ld4in(p);
+  v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+}
+__device__ __forceinline__ void st_quad(float* p, const float* v) {
+  *reinterpret_cast<float4*>(p) = float4{v[0], v[1], v[2], v[3]};
+}
+__device__ __forceinline__ void st_quad(bf16_t* p, const float* v) {
+  *reinterpret_cast<uint2*>(p) = uint2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+}
+
+// Where a lane's two quads start in a head, and whether they are rotated.
+struct QkLane {
+  int u, head, heads;  // lane in its group, the group's head, heads per wave
+  int oa, ob;
+  bool active, rot;
+  double rev[4];  // turns per position of the lane's four pairs
+};
+template <bool HALF>
+__device__ __forceinline__ QkLane qk_lane(const QkIO& io) {
+  QkLane l;
+  const int lane = threadIdx.x & 63;
+  l.u = lane & ((1 << io.lg) - 1);
+  l.head = lane >> io.lg;
+  l.heads = 64 >> io.lg;
+  l.active = 8 * l.u < io.d;
+  l.rot = 8 * l.u < io.r;
+  // without a rotation the whole head is read in halves: at d = 128 the sum
+  // of squares is then the prep kernel's, bit for bit
+  const int half = io.r ? io.r : io.d;
+  const bool h = HALF && 8 * l.u < half;
+  l.oa = h ? 4 * l.u : 8 * l.u;
+  l.ob = h ? half / 2 + 4 * l.u : 8 * l.u + 4;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) l.rev[e] = l.rot ? io.inv_freq[4 * l.u + e] * kInvTwoPi : 0.0;
+  return l;
+}
+
+// Token t's position; false for a row behind the last sequence.
+__device__ __forceinline__ bool qk_position(const QkIO& io, int64_t t, int64_t& p) {
+  if (io.pos) {
+    p = io.pos[t];
+    return true;
+  }
+  if (t >= io.cu[io.N]) return false;
+  const int n = find_seq(io.cu, io.N, t);
+  p = t - io.cu[n] + (io.start ? io.start[n] : 0);
+  return true;
+}
+
+// cos and sin of the lane's pairs, times rope_scale.  The angle in turns is an
+// fp64 product (2^-53 of at most 2^31 turns), its whole part dropped there.
+__device__ __forceinline__ void qk_angles(const QkIO& io, const QkLane& l, int64_t p, float* c, float* s) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const double turn = static_cast<double>(p) * l.rev[e];
+    float sn, cs;
+    sincospif(2.0f * static_cast<float>(turn - rint(turn)), &sn, &cs);
+    c[e] = cs * io.rope_scale;
+    s[e] = sn * io.rope_scale;
+  }
+}
+
+// Turns the lane's pairs by (c, s); a[] and b[] are its quads.
+template <bool HALF>
+__device__ __forceinline__ void qk_turn(float* a, float* b, const float* c, const float* s) {
+  if constexpr (HALF) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float x = a[e], y = b[e];
+      a[e] = fmaf(x, c[e], -(y * s[e]));
+      b[e] = fmaf(y, c[e], x * s[e]);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float* z = e < 2 ? a + 2 * e : b + 2 * (e - 2);
+      const float x = z[0], y = z[1];
+      z[0] = fmaf(x, c[e], -(y * s[e]));
+      z[1] = fmaf(y, c[e], x * s[e]);
+    }
+  }
+}
+
+// Sum over the head of e[0..3] of every lane of the group.
+__device__ __forceinline__ float qk_sum(const QkIO& io, float* e) {
+  for (int m = (1 << io.lg) >> 1; m >= 1; m >>= 1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e[i] += __shfl_xor(e[i], m, 64);
+  }
+  return (e[0] + e[2]) + (e[1] + e[3]);
+}
+__device__ __forceinline__ float qk_inverse_norm(const QkIO& io, const float* a, const float* b) {
+  float e[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) e[i] = fmaf(b[i], b[i], a[i] * a[i]);
+  const float ss = qk_sum(io, e);
+  return 1.0f / sqrtf((io.norm == GDN_NORM_RMS ? ss / static_cast<float>(io.d) : ss) + io.eps);
+}
+
+// The lane's eight weights of q or k, offset included.
+__device__ __forceinline__ void qk_weights(const QkIO& io, const QkLane& l, const float* w, float* v) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int at = e < 4 ? l.oa + e : l.ob + e - 4;
+    v[e] = io.norm == GDN_NORM_RMS ? io.offset + (w && l.active ? w[at] : 0.0f) : 1.0f;
+  }
+}
+
+constexpr int kQkUnroll = 4;  // head groups whose loads are in flight at once
+
+template <typename TIn, typename TOut, bool HALF>
+__global__ __launch_bounds__(256) void k_qk_fwd(QkIO io) {
+  const QkLane l = qk_lane<HALF>(io);
+  float wq[8], wk[8];
+  qk_weights(io, l, io.w_q, wq);
+  qk_weights(io, l, io.w_k, wk);
+  const int H = io.H_q + io.H_k;
+  const int steps = (H + l.heads - 1) / l.heads;
+  const int per = (steps + io.split - 1) / io.split;
+  const int64_t items = io.T * io.split;
+  for (int64_t it = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6); it < items;
+       it += static_cast<int64_t>(gridDim.x) * 4) {
+    const int64_t t = it / io.split;
+    const int part = static_cast<int>(it - t * io.split);
+    int64_t p;
+    if (!qk_position(io, t, p)) continue;
+    float c[4], s[4];
+    if (l.rot) qk_angles(io, l, p, c, s);
+    const int s1 = (part + 1) * per < steps ? (part + 1) * per : steps;
+    for (int s0 = part * per; s0 < s1; s0 += kQkUnroll) {
+      float a[kQkUnroll][4], b[kQkUnroll][4];
+#pragma unroll
+      for (int j = 0; j < kQkUnroll; ++j) {
+        const int h = (s0 + j) * l.heads + l.head;
+        const bool on = l.active && s0 + j < s1 && h < H;
+        if (on) {
+          const TIn* x = h < io.H_q ? static_cast<const TIn*>(io.q) + t * io.ldq + h * io.d
+                                    : static_cast<const TIn*>(io.k) + t * io.ldk + (h - io.H_q) * io.d;
+          ld_quad(x + l.oa, a[j]);
+          ld_quad(x + l.ob, b[j]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) a[j][e] = b[j][e] = 0.0f;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kQkUnroll; ++j) {
+        if (s0 + j >= s1) break;
+        const int h = (s0 + j) * l.heads + l.head;
+        const bool is_q = h < io.H_q;
+        if (io.norm != GDN_NORM_NONE) {
+          const float n = qk_inverse_norm(io, a[j], b[j]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            a[j][e] *= n;
+            b[j][e] *= n;
+          }
+          if (io.norm == GDN_NORM_RMS) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              a[j][e] *= is_q ? wq[e] : wk[e];
+              b[j][e] *= is_q ? wq[4 + e] : wk[4 + e];
+            }
+          }
+        }
+        if (l.rot) qk_turn<HALF>(a[j], b[j], c, s);
+        if (is_q) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            a[j][e] *= io.scale;
+            b[j][e] *= io.scale;
+          }
+        }
+        if (l.active && h < H) {
+          TOut* y = is_q ? static_cast<TOut*>(io.qo) + t * io.ldqo + h * io.d
+                         : static_cast<TOut*>(io.ko) + t * io.ldko + (h - io.H_q) * io.d;
+          st_quad(y + l.oa, a[j]);
+          st_quad(y + l.ob, b[j]);
+        }
+      }
+    }
+  }
+}
+
+// The gradient: the same walk over q, k and the gradients of the outputs; the
+// weights' gradients are summed per lane over all tokens that its wave takes,
+// then over the block, and k_qk_dw adds the blocks.
+template <typename TIn, typename TOut, bool HALF>
+__global__ __launch_bounds__(256) void k_qk_bwd(QkIO io) {
+  const QkLane l = qk_lane<HALF>(io);
+  float wq[8], wk[8], gq[8], gk[8];
+  qk_weights(io, l, io.w_q, wq);
+  qk_weights(io, l, io.w_k, wk);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) gq[e] = gk[e] = 0.0f;
+  const int H = io.H_q + io.H_k;
+  const int steps = (H + l.heads - 1) / l.heads;
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6); t < io.T;
+       t += static_cast<int64_t>(gridDim.x) * 4) {
+    int64_t p;
+    if (!qk_position(io, t, p)) continue;
+    float c[4], s[4];
+    if (l.rot) {
+      qk_angles(io, l, p, c, s);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[e] = -s[e];
+    }
+    for (int st = 0; st < steps; ++st) {
+      const int h = st * l.heads + l.head;
+      const bool on = l.active && h < H;
+      const bool is_q = h < io.H_q;
+      float x[8], y[8];
+      if (on) {
+        const TIn* px = is_q ? static_cast<const TIn*>(io.q) + t * io.ldq + h * io.d
+                             : static_cast<const TIn*>(io.k) + t * io.ldk + (h - io.H_q) * io.d;
+        const TOut* py = is_q ? static_cast<const TOut*>(io.dqo) + t * io.lddqo + h * io.d
+                              : static_cast<const TOut*>(io.dko) + t * io.lddko + (h - io.H_q) * io.d;
+        ld_quad(py + l.oa, y);
+        ld_quad(py + l.ob, y + 4);
+        if (io.norm != GDN_NORM_NONE) {
+          ld_quad(px + l.oa, x);
+          ld_quad(px + l.ob, x + 4);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = y[e] = 0.0f;
+      }
+      if (is_q) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] *= io.scale;
+      }
+      if (l.rot) qk_turn<HALF>(y, y + 4, c, s);
+      if (io.norm != GDN_NORM_NONE) {
+        const float n = qk_inverse_norm(io, x, x + 4);
+        if (io.norm == GDN_NORM_RMS) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float w = y[e] * (x[e] * n);
+            gq[e] += is_q ? w : 0.0f;
+            gk[e] += is_q ? 0.0f : w;
+            y[e] *= is_q ? wq[e] : wk[e];
+          }
+        }
+        float e4[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) e4[e] = fmaf(x[4 + e], y[4 + e], x[e] * y[e]);
+        const float dot = qk_sum(io, e4) * (n * n / (io.norm == GDN_NORM_RMS ? static_cast<float>(io.d) : 1.0f));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = n * fmaf(-x[e], dot, y[e]);
+      }
+      if (on) {
+        TIn* z = is_q ? static_cast<TIn*>(io.qo) + t * io.ldqo + h * io.d
+                      : static_cast<TIn*>(io.ko) + t * io.ldko + (h - io.H_q) * io.d;
+        st_quad(z + l.oa, y);
+        st_quad(z + l.ob, y + 4);
+      }
+    }
+  }
+  if (!io.part) return;
+  __shared__ float acc[256][17];  // a column more than 16: no bank holds a whole column
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    acc[threadIdx.x][e] = gq[e];
+    acc[threadIdx.x][8 + e] = gk[e];
+  }
+  __syncthreads();
+  const int group = 1 << io.lg;
+  for (int e = threadIdx.x; e < 2 * io.d; e += 256) {
+    const int u = e >> 4, j = e & 15;  // lane of the group, its element
+    float sum = 0.0f;
+    for (int i = u; i < 256; i += group) sum += acc[i][j];
+    const int half = io.r ? io.r : io.d;
+    const bool hf = HALF && 8 * u < half;
+    const int je = j & 7;
+    const int at = je < 4 ? (hf ? 4 * u : 8 * u) + je : (hf ? half / 2 + 4 * u : 8 * u + 4) + je - 4;
+    io.part[(static_cast<int64_t>(blockIdx.x) * 2 + (j >> 3)) * io.d + at] = sum;
+  }
+}
+
+// dw = sum of the blocks' sums: 16 columns a block, 16 threads a column, each
+// over every sixteenth row, joined in order.
+__global__ __launch_bounds__(256) void k_qk_dw(const float* __restrict__ part, int64_t rows, int d,
+                                               float* __restrict__ dw_q, float* __restrict__ dw_k) {
+  __shared__ float acc[16][17];
+  const int col = threadIdx.x & 15, row = threadIdx.x >> 4;
+  const int e = blockIdx.x * 16 + col;  // 2 d columns, d a multiple of 8
+  float sum = 0.0f;
+  for (int64_t r = row; r < rows; r += 16) sum += part[r * 2 * d + e];
+  acc[row][col] = sum;
+  __syncthreads();
+  if (row == 0) {
+    for (int i = 1; i < 16; ++i) sum += acc[i][col];
+    float* out = e < d ? dw_q : dw_k;
+    if (out) out[e < d ? e : e - d] = sum;
+  }
+}
+
+// ---- host side ----------------------------------------------------------------
+
+template <typename F>
+int qk_dispatch(const gdn_qk_shape_t* s, F&& f) {
+  const bool half = s->layout == GDN_ROPE_HALF;
+  const bool ib = s->in_dtype == GDN_BF16, ob = s->out_dtype == GDN_BF16;
+  if (ib && ob) return half ? f.template operator()<bf16_t, bf16_t, true>() : f.template operator()<bf16_t, bf16_t, false>();
+  if (ib) return half ? f.template operator()<bf16_t, float, true>() : f.template operator()<bf16_t, float, false>();
+  if (ob) return half ? f.template operator()<float, bf16_t, true>() : f.template operator()<float, bf16_t, false>();
+  return half ? f.template operator()<float, float, true>() : f.template operator()<float, float, false>();
+}
+
+// Checks what the two calls share and fills io.
+int qk_common(const gdn_qk_shape_t* s, int64_t T, const int32_t* pos, int32_t N, const int32_t* cu,
+              const int32_t* start, const float* inv_freq, const float* w_q, const float* w_k, const void* q,
+              int64_t ldq, const void* k, int64_t ldk, QkIO* io) {
+  int rc = gdn::check_qk_shape(s);
+  if (rc != GDN_OK) return rc;
+  if (T < 0 || N < 0) return GDN_ERR_INVALID_ARG;
+  if (!gdn::aligned16({pos, cu, start, inv_freq, w_q, w_k, q, k})) return GDN_ERR_INVALID_ARG;
+  if (!pos && (!cu || N == 0) && T > 0) return GDN_ERR_INVALID_ARG;
+  if (s->r > 0 && !inv_freq) return GDN_ERR_INVALID_ARG;
+  if (s->norm != GDN_NORM_RMS && (w_q || w_k)) return GDN_ERR_INVALID_ARG;
+  if (T > 0 && (!q || (s->H_k > 0 && !k))) return GDN_ERR_INVALID_ARG;
+  if (T > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+  io->ldq = gdn::row_stride(ldq, static_cast<int64_t>(s->H_q) * s->d);
+  io->ldk = gdn::row_stride(ldk, static_cast<int64_t>(s->H_k) * s->d);
+  if (io->ldq < 0 || io->ldk < 0 || io->ldq % 8 || io->ldk % 8) return GDN_ERR_INVALID_ARG;
+  io->q = q; io->k = k; io->pos = pos; io->cu = cu; io->start = start; io->inv_freq = inv_freq;
+  io->w_q = w_q; io->w_k = w_k;
+  io->T = T; io->N = N; io->H_q = s->H_q; io->H_k = s->H_k; io->d = s->d; io->r = s->r; io->norm = s->norm;
+  io->eps = s->eps; io->scale = s->scale; io->rope_scale = s->rope_scale; io->offset = s->weight_offset;
+  io->lg = 0;
+  while ((8 << io->lg) < s->d) ++io->lg;
+  io->split = 1;
+  return GDN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int gdn_qk_rotary(const gdn_qk_shape_t* shape, int64_t n_tokens, const int32_t* pos, int32_t n_seqs,
+                  const int32_t* cu_seqlens, const int32_t* start, const float* inv_freq, const float* w_q,
+                  const float* w_k, const void* q, int64_t ldq, const void* k, int64_t ldk, void* qo, int64_t ldqo,
+                  void* ko, int64_t ldko, void* stream) {
+  QkIO io{};
+  int rc = qk_common(shape, n_tokens, pos, n_seqs, cu_seqlens, start, inv_freq, w_q, w_k, q, ldq, k, ldk, &io);
+  if (rc != GDN_OK) return rc;
+  if (!gdn::aligned16({qo, ko})) return GDN_ERR_INVALID_ARG;
+  if (n_tokens > 0 && (!qo || (shape->H_k > 0 && !ko))) return GDN_ERR_INVALID_ARG;
+  io.ldqo = gdn::row_stride(ldqo, static_cast<int64_t>(shape->H_q) * shape->d);
+  io.ldko = gdn::row_stride(ldko, static_cast<int64_t>(shape->H_k) * shape->d);
+  if (io.ldqo < 0 || io.ldko < 0 || io.ldqo % 8 || io.ldko % 8) return GDN_ERR_INVALID_ARG;
+  if (n_tokens == 0) return GDN_OK;
+  io.qo = qo; io.ko = ko;
+  const int heads = 64 >> io.lg;
+  const int steps = (io.H_q + io.H_k + heads - 1) / heads;
+  // few tokens: cut each token's heads into parts until the chip has work
+  while (io.split < steps && n_tokens * io.split < 2048) io.split *= 2;
+  if (io.split > steps) io.split = steps;
+  const int64_t want = (n_tokens * io.split + 3) / 4;
+  const unsigned blocks = static_cast<unsigned>(want < 2048 ? want : 2048);
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return qk_dispatch(shape, [&]<typename TIn, typename TOut, bool HALF>() {
+    Timed t_("k_qk_fwd", st);
+    hipLaunchKernelGGL((k_qk_fwd<TIn, TOut, HALF>), dim3(blocks), dim3(256), 0, st, io);
+    return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+  });
+}
+
+size_t gdn_qk_workspace_bytes(const gdn_qk_shape_t* shape, int64_t n_tokens) {
+  if (gdn::check_qk_shape(shape) != GDN_OK || n_tokens < 0 || n_tokens > INT32_MAX) return 0;
+  const size_t bytes = static_cast<size_t>(gdn::qk_bwd_blocks(shape, n_tokens)) * 2 * shape->d * sizeof(float);
+  return (bytes + gdn::kAlign) / gdn::kAlign * gdn::kAlign;
+}
+
+int gdn_qk_rotary_bwd(const gdn_qk_shape_t* shape, int64_t n_tokens, const int32_t* pos, int32_t n_seqs,
+                      const int32_t* cu_seqlens, const int32_t* start, const float* inv_freq, const float* w_q,
+                      const float* w_k, const void* q, int64_t ldq, const void* k, int64_t ldk, const void* dqo,
+                      int64_t lddqo, const void* dko, int64_t lddko, void* dq, int64_t lddq, void* dk, int64_t lddk,
+                      float* dw_q, float* dw_k, void* ws, size_t ws_bytes, void* stream) {
+  QkIO io{};
+  int rc = qk_common(shape, n_tokens, pos, n_seqs, cu_seqlens, start, inv_freq, w_q, w_k, q, ldq, k, ldk, &io);
+  if (rc != GDN_OK) return rc;
+  if (!gdn::aligned16({dqo, dko, dq, dk, dw_q, dw_k, ws})) return GDN_ERR_INVALID_ARG;
+  if (n_tokens > 0 && (!dqo || !dq || (shape->H_k > 0 && (!dko || !dk)))) return GDN_ERR_INVALID_ARG;
+  if (shape->norm != GDN_NORM_RMS && (dw_q || dw_k)) return GDN_ERR_INVALID_ARG;
+  const int64_t rq = static_cast<int64_t>(shape->H_q) * shape->d, rk = static_cast<int64_t>(shape->H_k) * shape->d;
+  io.lddqo = gdn::row_stride(lddqo, rq);
+  io.lddko = gdn::row_stride(lddko, rk);
+  io.ldqo = gdn::row_stride(lddq, rq);
+  io.ldko = gdn::row_stride(lddk, rk);
+  if (io.lddqo < 0 || io.lddko < 0 || io.ldqo < 0 || io.ldko < 0) return GDN_ERR_INVALID_ARG;
+  if (io.lddqo % 8 || io.lddko % 8 || io.ldqo % 8 || io.ldko % 8) return GDN_ERR_INVALID_ARG;
+  const bool sums = dw_q || dw_k;
+  if (sums && (!ws || ws_bytes < gdn_qk_workspace_bytes(shape, n_tokens))) return GDN_ERR_WORKSPACE;
+  io.dqo = dqo; io.dko = dko; io.qo = dq; io.ko = dk;
+  io.part = sums ? static_cast<float*>(ws) : nullptr;
+  const int64_t blocks = gdn::qk_bwd_blocks(shape, n_tokens);
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (blocks > 0) {
+    rc = qk_dispatch(shape, [&]<typename TIn, typename TOut, bool HALF>() {
+      Timed t_("k_qk_bwd", st);
+      hipLaunchKernelGGL((k_qk_bwd<TIn, TOut, HALF>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, io);
+      return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+    });
+    if (rc != GDN_OK) return rc;
+  }
+  if (sums) {
+    Timed t_("k_qk_dw", st);
+    hipLaunchKernelGGL(k_qk_dw, dim3(shape->d / 8), dim3(256), 0, st, io.part, blocks, shape->d, dw_q, dw_k);
+  }
+  return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+}
+
+}  // extern "C"
