@@ -350,13 +350,20 @@ typedef struct {
 int gdn_lru_cache_init(const gdn_lru_shape_t* shape, int32_t n_seqs, const float* h0,
                        gdn_lru_cache_t* cache, void* stream);
 
+/* Bytes of workspace of `op` (GDN_OP_PREFILL, GDN_OP_PREFILL_CONTINUE or
+ * GDN_OP_FWD_BWD); 0 for an invalid shape or another op.  A prefill or
+ * continuation of at most GDN_LRU_SMALL tokens needs none: ws may be NULL. */
+#define GDN_LRU_SMALL 2048
+size_t gdn_lru_workspace_bytes(const gdn_lru_shape_t* shape, int32_t n_seqs, int64_t total_tokens,
+                               int32_t op);
+
 /* Packed prefill from h0 (nullable: zero).  Writes o and, where given, each
  * sequence's final state hT and the cache from which decode or continuation
- * goes on.  No workspace. */
+ * goes on. */
 int gdn_lru_prefill(const gdn_lru_shape_t* shape, int32_t n_seqs, const int32_t* cu_seqlens_dev,
                     const int32_t* cu_seqlens_host, const void* x, int64_t ldx, const void* g,
                     int64_t ldg, const float* h0, void* o, int64_t ldo, float* hT,
-                    gdn_lru_cache_t* cache, void* stream);
+                    gdn_lru_cache_t* cache, void* ws, size_t ws_bytes, void* stream);
 
 /* The next tokens of sequences whose cache stands anywhere inside a chunk: the
  * same bits as one prefill of the whole history.  The cache is left where the
@@ -365,16 +372,13 @@ int gdn_lru_prefill(const gdn_lru_shape_t* shape, int32_t n_seqs, const int32_t*
 int gdn_lru_prefill_continue(const gdn_lru_shape_t* shape, int32_t n_seqs,
                              const int32_t* cu_seqlens_dev, const int32_t* cu_seqlens_host,
                              const void* x, int64_t ldx, const void* g, int64_t ldg,
-                             gdn_lru_cache_t* cache, void* o, int64_t ldo, float* hT,
-                             void* stream);
+                             gdn_lru_cache_t* cache, void* o, int64_t ldo, float* hT, void* ws,
+                             size_t ws_bytes, void* stream);
 
 /* One token for each of n_seqs sequences: x, o and g hold n_seqs rows. */
 int gdn_lru_decode_step(const gdn_lru_shape_t* shape, int32_t n_seqs, const void* x, int64_t ldx,
                         const void* g, int64_t ldg, gdn_lru_cache_t* cache, void* o, int64_t ldo,
                         void* stream);
-
-/* Bytes of workspace of gdn_lru_fwd_bwd; 0 for an invalid shape. */
-size_t gdn_lru_workspace_bytes(const gdn_lru_shape_t* shape, int32_t n_seqs, int64_t total_tokens);
 
 /*
  * Trainer forward + backward.  o (nullable) and hT (nullable) are gdn_lru_prefill's

@@ -32,6 +32,7 @@ EXPORTS = ["gdn_workspace_bytes", "gdn_cache_init", "gdn_prefill", "gdn_decode_s
            "gdn_qk_rotary", "gdn_qk_workspace_bytes", "gdn_qk_rotary_bwd", "gdn_rope_freqs"]
 
 LRU_CHUNK = 32    # tokens per chunk of the gated linear recurrence
+LRU_SMALL = 2048  # a prefill of at most so many tokens needs no workspace
 LRU_GROUP = 256   # channels per position counter of its cache
 LRU_GATES = {"none": 0, "complement": 1, "norm": 2}
 QK_NORMS = {"none": 0, "l2": 1, "rms": 2}
@@ -134,11 +135,12 @@ def lib():
         L.gdn_error_string.restype = ctypes.c_char_p
         ls, lc, qs = (ctypes.POINTER(t) for t in (LruShape, LruCacheStruct, QkShape))
         L.gdn_lru_cache_init.argtypes = [ls, i32, vp, lc, vp]
-        L.gdn_lru_prefill.argtypes = [ls, i32, vp, vp, vp, i64, vp, i64, vp, vp, i64, vp, lc, vp]
+        L.gdn_lru_prefill.argtypes = [ls, i32, vp, vp, vp, i64, vp, i64, vp, vp, i64, vp, lc, vp,
+                                      sz, vp]
         L.gdn_lru_prefill_continue.argtypes = [ls, i32, vp, vp, vp, i64, vp, i64, lc, vp, i64, vp,
-                                               vp]
+                                               vp, sz, vp]
         L.gdn_lru_decode_step.argtypes = [ls, i32, vp, i64, vp, i64, lc, vp, i64, vp]
-        L.gdn_lru_workspace_bytes.argtypes = [ls, i32, i64]
+        L.gdn_lru_workspace_bytes.argtypes = [ls, i32, i64, i32]
         L.gdn_lru_fwd_bwd.argtypes = [ls, i32, vp, vp, vp, i64, vp, i64, vp, vp, i64, vp, vp, i64,
                                       vp, vp, i64, vp, i64, vp, vp, sz, vp]
         L.gdn_qk_rotary.argtypes = [qs, i64, vp, i32, vp, vp, vp, vp, vp, vp, i64, vp, i64, vp,
@@ -516,14 +518,15 @@ def gdn_fwd_bwd(shape, q, k, v, beta, g, cu_seqlens, dO, h0=None, dhT=None, ws=N
 
 
 def _gpu(t, name):
-    if t.device.type != "cuda":
-        raise ValueError(f"{name}: expected a GPU tensor, got one on {t.device}")
-    return t.device
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError(f"{name}: expected a GPU tensor, got one on {dev}")
+    return dev
 
 
 def _rows(t, dtype, n, width, dev, name):
     """The distance between the rows of t [n, width], after checking it."""
-    if t.dtype != dtype or t.device != dev or t.dim() != 2 or t.shape[0] != n or t.shape[1] != width:
+    if t.dtype != dtype or t.shape != (n, width) or t.device != dev:
         raise ValueError(f"{name}: expected {dtype} ({n}, {width}) on {dev}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     ld, unit = t.stride()
@@ -537,7 +540,7 @@ def _rows(t, dtype, n, width, dev, name):
 
 def _heads(t, dtype, T, H, d, dev, name):
     """The distance between the tokens' rows of t [T, H, d], after checking it."""
-    if t.dtype != dtype or t.device != dev or t.dim() != 3 or tuple(t.shape) != (T, H, d):
+    if t.dtype != dtype or t.shape != (T, H, d) or t.device != dev:
         raise ValueError(f"{name}: expected {dtype} ({T}, {H}, {d}) on {dev}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     ld, head, unit = t.stride()
@@ -550,7 +553,7 @@ def _heads(t, dtype, T, H, d, dev, name):
 
 
 def _dense(t, dtype, shape, dev, name):
-    if t.dtype != dtype or t.device != dev or t.shape != shape or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
         raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on {dev}, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device} "
                          f"contiguous={t.is_contiguous()}")
@@ -562,27 +565,37 @@ def _optional(t, dtype, shape, dev, name):
 
 
 def _launch(name, dev, *args):
-    """Calls library function `name` with the stream of `dev` as last argument."""
-    fn = getattr(lib(), name)
-    if dev.index == torch.cuda.current_device():
-        status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    """Calls library function `name` with the current stream of `dev` as last
+    argument (its raw handle: a stream object would cost 2 us a call)."""
+    fn = getattr(_lib or lib(), name)
+    index = dev.index
+    if index == torch._C._cuda_getDevice():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if status != GDN_OK:
         raise GdnError(status, name)
 
 
 def _packed(cu_seqlens, cu_seqlens_host, dev, T):
     """(N, device copy, host copy) of cu_seqlens over T rows."""
-    cu_dev, cu_host = _cu_pair(cu_seqlens, dev, cu_seqlens_host)
-    if cu_host is None:
-        raise ValueError("cu_seqlens_host: expected a CPU int32 tensor or None")
+    i32 = torch.int32
+    if (cu_seqlens_host is not None and cu_seqlens_host is not False and cu_seqlens.device == dev
+            and cu_seqlens.dtype == i32 and cu_seqlens_host.dtype == i32
+            and cu_seqlens_host.device.type == "cpu" and cu_seqlens.shape == cu_seqlens_host.shape
+            and cu_seqlens.is_contiguous() and cu_seqlens_host.is_contiguous()):
+        cu_dev, cu_host = cu_seqlens, cu_seqlens_host
+    else:
+        cu_dev, cu_host = _cu_pair(cu_seqlens, dev, cu_seqlens_host)
+        if cu_host is None:
+            raise ValueError("cu_seqlens_host: expected a CPU int32 tensor or None")
     n = cu_host.numel() - 1
     if cu_host.dim() != 1 or n < 0:
         raise ValueError("cu_seqlens: expected one dimension of N + 1 values")
-    if int(cu_host[n]) > T:
-        raise ValueError(f"cu_seqlens: ends at {int(cu_host[n])}, past the {T} rows given")
+    end = ctypes.c_int32.from_address(cu_host.data_ptr() + 4 * n).value
+    if end > T:
+        raise ValueError(f"cu_seqlens: ends at {end}, past the {T} rows given")
     return n, cu_dev, cu_host
 
 
@@ -593,8 +606,8 @@ def make_lru_shape(D, in_dtype, g_dtype=torch.float32, gate="none"):
     return LruShape(D, _DTYPE_CODES[in_dtype], _DTYPE_CODES[g_dtype], LRU_GATES[gate])
 
 
-def lru_workspace_bytes(shape, n_seqs, total_tokens):
-    return int(lib().gdn_lru_workspace_bytes(ctypes.byref(shape), n_seqs, total_tokens))
+def lru_workspace_bytes(shape, n_seqs, total_tokens, op=OP_FWD_BWD):
+    return int(lib().gdn_lru_workspace_bytes(ctypes.byref(shape), n_seqs, total_tokens, op))
 
 
 class LruCache:
@@ -653,7 +666,8 @@ def gdn_lru_cache_init(shape, n, device, h0=None):
     return c
 
 
-def _lru_prefill(name, shape, x, g, cu_seqlens, h0, cache, want_hT, out, hT_out, cu_seqlens_host):
+def _lru_prefill(name, shape, x, g, cu_seqlens, h0, cache, want_hT, ws, out, hT_out,
+                 cu_seqlens_host):
     dev = _gpu(x, "x")
     T, D = x.shape[0], shape.D
     xt = _DTYPES.get(shape.in_dtype)
@@ -669,31 +683,36 @@ def _lru_prefill(name, shape, x, g, cu_seqlens, h0, cache, want_hT, out, hT_out,
     if cache is not None:
         cache.check(shape, n, dev)
     cs = None if cache is None else ctypes.byref(cache.struct())
+    tail = (None, 0)
+    if T > LRU_SMALL:
+        ws = _scratch(ws, lru_workspace_bytes(shape, n, T, OP_PREFILL), dev,
+                      "gdn_lru_workspace_bytes")
+        tail = (ws.data_ptr(), ws.numel())
     head = (ctypes.byref(shape), n, cu_dev.data_ptr(), cu_host.data_ptr(), x.data_ptr(), ldx,
             g.data_ptr(), ldg)
     if name == "gdn_lru_prefill":
         p_h0 = _optional(h0, torch.float32, (n, D), dev, "h0")
-        _launch(name, dev, *head, p_h0, o.data_ptr(), ldo, p_hT, cs)
+        _launch(name, dev, *head, p_h0, o.data_ptr(), ldo, p_hT, cs, *tail)
     else:
-        _launch(name, dev, *head, cs, o.data_ptr(), ldo, p_hT)
+        _launch(name, dev, *head, cs, o.data_ptr(), ldo, p_hT, *tail)
     return o, hT
 
 
-def gdn_lru_prefill(shape, x, g, cu_seqlens, h0=None, cache=None, want_hT=True, out=None,
-                    hT_out=None, cu_seqlens_host=None):
+def gdn_lru_prefill(shape, x, g, cu_seqlens, h0=None, cache=None, want_hT=True, ws=None,
+                    out=None, hT_out=None, cu_seqlens_host=None):
     """Packed prefill of the gated linear recurrence: x, g [T, D] from h0 (fp32
     [N, D]); fills `cache` for decode if given.  Returns (o [T, D] in x's type,
     hT fp32 [N, D]).  out may be x."""
-    return _lru_prefill("gdn_lru_prefill", shape, x, g, cu_seqlens, h0, cache, want_hT, out,
-                        hT_out, cu_seqlens_host)
+    return _lru_prefill("gdn_lru_prefill", shape, x, g, cu_seqlens, h0, cache, want_hT, ws,
+                        out, hT_out, cu_seqlens_host)
 
 
-def gdn_lru_prefill_continue(shape, x, g, cu_seqlens, cache, want_hT=True, out=None, hT_out=None,
-                             cu_seqlens_host=None):
+def gdn_lru_prefill_continue(shape, x, g, cu_seqlens, cache, want_hT=True, ws=None, out=None,
+                             hT_out=None, cu_seqlens_host=None):
     """The next tokens of the sequences of `cache`, which may stand anywhere in
     their chunks; the cache moves on.  Returns (o, hT) of the new tokens."""
     return _lru_prefill("gdn_lru_prefill_continue", shape, x, g, cu_seqlens, None, cache, want_hT,
-                        out, hT_out, cu_seqlens_host)
+                        ws, out, hT_out, cu_seqlens_host)
 
 
 def gdn_lru_decode_step(shape, x, g, cache, out=None):

@@ -3,5 +3,8 @@
 // timing of the first.
 #include "gdn_kernels.hip"
 
+#include <cmath>
+#include <new>
+
 #include "gdn_lru.hip"
 #include "gdn_qk.hip"

@@ -7,13 +7,28 @@
 // starts follow one another with one fma per chunk, and h_p = fma(A_p, S, B_p).
 // The same operations in the same order run in decode, one token at a time.
 //
-// Bound: HBM.  An element takes 6 to 12 bytes and about 20 vector
-// instructions.
+// Going back, a chunk maps the gradient K of the state behind its last token to
+// that in front of its first one, K -> A K + Q with Q = sum_p A_p dO_p, which
+// needs no state either.
+//
+// Two schedules give these operations, and the same bits:
+//   one pass     k_lru_fwd: a block holds a channel tile of one sequence, its
+//                waves one chunk each, and goes over the sequence in rounds;
+//                inputs are read once.  Prefill with enough sequences and
+//                channels to fill the chip.
+//   three steps  k_lru_fold (every chunk's A, B and Q), k_lru_chain (the states
+//                and gradients at the chunks' edges), k_lru_apply or k_lru_grad
+//                (outputs): every step runs over all chunks at once, and the
+//                inputs are read twice.  Prefill of few sequences, and the
+//                trainer.
+//
+// Bound: HBM.  An element takes 6 to 16 bytes and 20 to 40 vector instructions.
 
 namespace {
 
 constexpr int kLruC = GDN_LRU_CHUNK;
-constexpr int kLruThreads = 512;  // most threads of a scan block
+constexpr int kLruPack = 64;     // most sequences that the host packs into units
+constexpr int kLruThreads = 1024;  // most threads of a scan block
 
 struct LruIO {
   const void* x;
@@ -26,15 +41,26 @@ struct LruIO {
   const int32_t* cu;
   int N, D, gate;
   int64_t T, ldx, ldg, ldo;
-  int lps;    // lanes per chunk: a block's channel tile is lps times a lane's channels
+  // one pass
+  int lps;    // lanes per chunk = channels of a block's tile
   int tiles;  // channel tiles
+  int units;  // sequences or, packed, groups of sequences that a block takes
+  int packed; // 1: unit u is the sequences seq[first[u]] .. seq[first[u + 1] - 1]
+  uint8_t seq[kLruPack];
+  uint8_t first[kLruPack + 1];
+  // three steps
+  int cw;        // lanes of a block over channels; 256 / cw chunks a block
+  int64_t slots; // chunk slots
+  float* wA;     // [slots][D] chunk products
+  float* wB;     // [slots][D] chunk states from zero, then the states at the starts
+  float* wQ;     // [slots][D] the gradient's, then the gradients behind the ends
+  float* keep;   // [N][2][D] the cache's A and B before the call
   // trainer
   const void* dO;
   const float* dhT;
   void* dx;
   void* dg;
   float* dh0;
-  float* states;  // [T / 32 + N][D] chunk-start states
   int64_t lddo, lddx, lddg;
 };
 
@@ -43,16 +69,53 @@ __device__ __forceinline__ void stout(bf16_t* p, float x) {
   *p = static_cast<bf16_t>(pack_bf16(x, 0.0f));  // round to nearest even
 }
 
-// alpha and u = b x of one element.
-__device__ __forceinline__ void lru_gate(int gate, float g, float x, float& a, float& u) {
-  a = expf(g);
-  if (gate == GDN_LRU_GATE_NONE) {
-    u = x;
-  } else if (gate == GDN_LRU_GATE_COMPLEMENT) {
-    u = -expm1f(g) * x;
-  } else {
-    u = sqrtf(fmaxf(-expm1f(2.0f * g), 0.0f)) * x;
-  }
+// exp(g) and 1 - exp(g) of one g, both to fp32's last place, from one
+// reduction g = n ln 2 + f: with p = e^f - 1 = f + f^2 q(f) (|f| <= ln 2 / 2, q
+// of degree 4 fitted to a relative 2^-26 of p),
+//     exp(g) = 2^n (1 + p),   1 - exp(g) = -2 (2^(n-1) p + (2^(n-1) - 1/2)),
+// the latter without cancellation near g = 0, where n = 0 leaves -p.  Limits:
+// below -104 the result is 0 (2^-150), above 89 infinite; NaN stays NaN.
+// Measured by rounding model over 2e6 values: 1.4 and 1.5 times 2^-24.
+struct LruExp {
+  float a, m;  // exp(g), 1 - exp(g)
+};
+__device__ __forceinline__ LruExp lru_exp(float g) {
+  float c = __builtin_amdgcn_fmed3f(g, -104.0f, 89.0f);
+  c = g != g ? g : c;
+  const float n = rintf(c * 1.44269504f);
+  float f = fmaf(n, -0.693145751953125f, c);  // 17 bits of ln 2: the product is exact
+  f = fmaf(n, -1.42860677e-06f, f);
+  float q = 0.0013882518978789449f;
+  q = fmaf(q, f, 0.008366530761122704f);
+  q = fmaf(q, f, 0.04166720062494278f);
+  q = fmaf(q, f, 0.1666654348373413f);
+  q = fmaf(q, f, 0.4999999701976776f);
+  const float p = fmaf(f * f, q, f);
+  const int e = static_cast<int>(n);
+  LruExp r;
+  r.a = __builtin_amdgcn_ldexpf(1.0f + p, e);
+  const float h = __builtin_amdgcn_ldexpf(0.5f, e);
+  r.m = -2.0f * fmaf(h, p, h - 0.5f);
+  return r;
+}
+
+// alpha and the input's weight b of one element.  In the norm gate 1 - alpha^2
+// = m (1 + alpha), and the root is the hardware's (1 ulp): the correctly
+// rounded one takes about ten instructions more per element for a bit that
+// the products after it lose again.
+template <int GATE>
+__device__ __forceinline__ float lru_weight(float g, float& a) {
+  const LruExp r = lru_exp(g);
+  a = r.a;
+  if constexpr (GATE == GDN_LRU_GATE_NONE) return 1.0f;
+  if constexpr (GATE == GDN_LRU_GATE_COMPLEMENT) return r.m;
+  return __builtin_amdgcn_sqrtf(fmaxf(r.m * (1.0f + r.a), 0.0f));
+}
+// u = b x; without a gate x itself.
+template <int GATE>
+__device__ __forceinline__ float lru_input(float g, float x, float& a) {
+  const float b = lru_weight<GATE>(g, a);
+  return GATE == GDN_LRU_GATE_NONE ? x : b * x;
 }
 
 // Sequence n's rows, kept inside [0, T) whatever the device copy holds.
@@ -71,148 +134,195 @@ __device__ __forceinline__ int lru_pos(const LruIO& io, int n, int c) {
   return p < 0 ? 0 : (p >= kLruC ? kLruC - 1 : p);
 }
 
-// Block -> (sequence, channel tile).  Groups of four neighbouring tiles of a
-// sequence go to one XCD (blocks are dealt to the eight XCDs in turn), where
-// tiles narrower than a cache line share it in that XCD's L2.
-__device__ __forceinline__ bool lru_item(const LruIO& io, int& n, int& tile) {
+// Block -> (unit, channel tile).  Groups of four neighbouring tiles of a unit
+// go to one XCD (blocks are dealt to the eight XCDs in turn), where tiles
+// narrower than a cache line share it in that XCD's L2.
+__device__ __forceinline__ bool lru_item(const LruIO& io, int& unit, int& tile) {
   const int64_t b = blockIdx.x;
   const int64_t xcd = b & 7, j = b >> 3;
   const int64_t group = (j >> 2) * 8 + xcd;
-  const int gps = (io.tiles + 3) >> 2;  // groups per sequence
-  const int64_t seq = group / gps;
-  tile = static_cast<int>(group - seq * gps) * 4 + static_cast<int>(j & 3);
-  n = static_cast<int>(seq);
-  return seq < io.N && tile < io.tiles;
+  const int gpu = (io.tiles + 3) >> 2;  // groups per unit
+  const int64_t u = group / gpu;
+  tile = static_cast<int>(group - u * gpu) * 4 + static_cast<int>(j & 3);
+  unit = static_cast<int>(u);
+  return u < io.units && tile < io.tiles;
 }
-int64_t lru_blocks(int64_t N, int tiles) {
-  const int64_t groups = N * ((tiles + 3) / 4);
+int64_t lru_blocks(int64_t units, int tiles) {
+  const int64_t groups = units * ((tiles + 3) / 4);
   return (groups + 7) / 8 * 8 * 4;
 }
 
-// Two channels per lane where rows are evenly aligned, else one at a time.
-template <typename TX, typename TG, int V>
-__global__ __launch_bounds__(kLruThreads) void k_lru_fwd(LruIO io) {
-  __shared__ float2 agg[kLruThreads * V];  // [slot][channel of the tile]
-  __shared__ float start[kLruThreads * V];
-  int n, tile;
-  if (!lru_item(io, n, tile)) return;
-  int64_t t0, L;
-  lru_rows(io, n, t0, L);
-  const int W = io.lps * V;
-  const int slots = blockDim.x / io.lps;
-  const int slot = threadIdx.x / io.lps;
-  const int lc = (threadIdx.x - slot * io.lps) * V;  // channel inside the tile
-  const int c = tile * W + lc;
-  const bool live = c < io.D;  // (D is even where V = 2)
-  const int cc = live ? c : io.D - V;
-  const TX* x = static_cast<const TX*>(io.x) + t0 * io.ldx + cc;
-  const TG* g = static_cast<const TG*>(io.g) + t0 * io.ldg + cc;
-  TX* o = io.o ? static_cast<TX*>(io.o) + t0 * io.ldo + cc : nullptr;
-  const int64_t sn = static_cast<int64_t>(n) * io.D;
-  const int p0 = io.resume ? lru_pos(io, n, tile * W < io.D ? tile * W : 0) : 0;
-  const int64_t nch = (p0 + L + kLruC - 1) / kLruC;
-  // the chain over chunks, one thread per channel of the tile
-  const int fc = tile * W + static_cast<int>(threadIdx.x);
-  const bool folds = static_cast<int>(threadIdx.x) < W && fc < io.D;
-  float S = 0.0f;
-  if (folds) S = io.resume ? io.cache.S[sn + fc] : (io.h0 ? io.h0[sn + fc] : 0.0f);
-  if (L == 0) {
-    if (folds) {
-      if (io.resume) {
-        if (io.hT) io.hT[sn + fc] = fmaf(io.cache.A[sn + fc], S, io.cache.B[sn + fc]);
-      } else {
-        if (io.hT) io.hT[sn + fc] = S;
-        if (io.cache.S) {
-          io.cache.S[sn + fc] = S;
-          io.cache.A[sn + fc] = 1.0f;
-          io.cache.B[sn + fc] = 0.0f;
-        }
-      }
-    }
+// What an empty sequence's channel e = n D + c ends with: where it began.
+__device__ __forceinline__ void lru_empty(const LruIO& io, int64_t e) {
+  if (io.resume) {
+    if (io.hT) io.hT[e] = fmaf(io.cache.A[e], io.cache.S[e], io.cache.B[e]);
     return;
   }
+  const float S = io.h0 ? io.h0[e] : 0.0f;
+  if (io.hT) io.hT[e] = S;
+  if (io.cache.S) {
+    io.cache.S[e] = S;
+    io.cache.A[e] = 1.0f;
+    io.cache.B[e] = 0.0f;
+  }
+}
+
+// The chain over a round's m slots for one channel: start[s] = S, S = a S + b,
+// the maps eight at a time out of LDS so that their latency is paid once.
+// Where a sequence begins (begin[s]) S is the state that its lanes left in
+// start[s].
+__device__ __forceinline__ float lru_chain(const float2* agg, float* start, const int* begin, int W, int m, float S) {
+  for (int s0 = 0; s0 < m; s0 += 8) {
+    float2 ab[8];
+    float h0[8];
+    int fresh[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int s = s0 + j < m ? s0 + j : m - 1;
+      ab[j] = agg[s * W];
+      h0[j] = start[s * W];
+      fresh[j] = begin[s];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (s0 + j >= m) break;
+      S = fresh[j] ? h0[j] : S;
+      start[(s0 + j) * W] = S;
+      S = fmaf(ab[j].x, S, ab[j].y);
+    }
+  }
+  return S;
+}
+
+template <typename TX, typename TG, int GATE>
+__global__ __launch_bounds__(kLruThreads) void k_lru_fwd(LruIO io) {
+  __shared__ float2 agg[kLruThreads];  // [slot][channel of the tile]
+  __shared__ float start[kLruThreads];
+  __shared__ int begin[kLruThreads / 8];
+  __shared__ int64_t chunk0[kLruPack + 1];  // chunks of the unit before each of its sequences
+  int unit, tile;
+  if (!lru_item(io, unit, tile)) return;
+  const int W = io.lps;
+  const int slots = blockDim.x / W;
+  const int slot = threadIdx.x / W;
+  const int c = tile * W + static_cast<int>(threadIdx.x) - slot * W;
+  const bool live = c < io.D;
+  const int cc = live ? c : io.D - 1;
+  const bool folds = slot == 0 && live;  // these threads hold the chain of one channel each
+  const int i0 = io.packed ? io.first[unit] : 0;
+  const int count = io.packed ? io.first[unit + 1] - i0 : 1;
+  if (threadIdx.x < 64) {
+    int64_t t0, L = 0, chunks = 0;
+    if (static_cast<int>(threadIdx.x) < count) {
+      const int n = io.packed ? io.seq[i0 + threadIdx.x] : unit;
+      lru_rows(io, n, t0, L);
+      if (L > 0) chunks = ((io.resume ? lru_pos(io, n, 0) : 0) + L + kLruC - 1) / kLruC;
+    }
+    int64_t before = chunks;
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+      const int64_t up = __shfl_up(before, m, 64);
+      if (static_cast<int>(threadIdx.x) >= m) before += up;
+    }
+    chunk0[threadIdx.x + 1] = before;
+    if (threadIdx.x == 0) chunk0[0] = 0;
+  }
+  __syncthreads();
+  if (folds) {
+    for (int i = 0; i < count; ++i)
+      if (chunk0[i + 1] == chunk0[i])
+        lru_empty(io, static_cast<int64_t>(io.packed ? io.seq[i0 + i] : unit) * io.D + c);
+  }
+  const int64_t nch = chunk0[count];
+  float S = 0.0f;
   for (int64_t cb = 0; cb < nch; cb += slots) {
-    const int64_t ch = cb + slot;
-    const bool has = ch < nch;
-    const int64_t tb = ch * kLruC - p0;  // row of the chunk's place 0
-    const int lo = has && tb < 0 ? static_cast<int>(-tb) : 0;
-    const int64_t left = L - tb;
-    const int hi = has ? (left < kLruC ? static_cast<int>(left) : kLruC) : 0;
-    float A[kLruC][V], B[kLruC][V];
+    const bool has = cb + slot < nch;
+    int lo = 0, hi = 0;
+    bool last = false;
+    int64_t row = 0, sn = 0;  // row of the chunk's place 0, the sequence's states
+    float A[kLruC], B[kLruC];
     if (has) {
+      int i = 0;
+      for (int d = kLruPack / 2; d >= 1; d >>= 1)  // the last sequence that begins at or before the slot's chunk
+        if (i + d < count && chunk0[i + d] <= cb + slot) i += d;
+      const int n = io.packed ? io.seq[i0 + i] : unit;
+      int64_t t0, L;
+      lru_rows(io, n, t0, L);
+      sn = static_cast<int64_t>(n) * io.D;
+      const int64_t ch = cb + slot - chunk0[i];
+      const int64_t tb = ch * kLruC - (io.resume ? lru_pos(io, n, 0) : 0);
+      row = t0 + tb;
+      lo = tb < 0 ? static_cast<int>(-tb) : 0;
+      hi = L - tb < kLruC ? static_cast<int>(L - tb) : kLruC;
+      last = cb + slot + 1 == chunk0[i + 1];
+      const TX* x = static_cast<const TX*>(io.x) + cc;
+      const TG* g = static_cast<const TG*>(io.g) + cc;
+      float a = 1.0f, b = 0.0f;
+      if (lo == 0 && hi == kLruC) {
 #pragma unroll
-      for (int i = 0; i < kLruC; ++i) {
-        const int ii = i < lo ? lo : (i >= hi ? hi - 1 : i);  // a row of this chunk
-        const int64_t t = tb + ii;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          A[i][v] = ldin(g + t * io.ldg + v);
-          B[i][v] = ldin(x + t * io.ldx + v);
+        for (int j = 0; j < kLruC; ++j) {
+          A[j] = ldin(g + (row + j) * io.ldg);
+          B[j] = ldin(x + (row + j) * io.ldx);
         }
-      }
-      float a[V], b[V];
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        a[v] = 1.0f;
-        b[v] = 0.0f;
+        for (int j = 0; j < kLruC; ++j) {
+          float al;
+          const float u = lru_input<GATE>(A[j], B[j], al);
+          A[j] = a = al * a;
+          B[j] = b = fmaf(al, b, u);
+        }
+      } else {
         if (lo > 0) {
-          a[v] = io.cache.A[sn + cc + v];
-          b[v] = io.cache.B[sn + cc + v];
+          a = io.cache.A[sn + cc];
+          b = io.cache.B[sn + cc];
         }
-      }
 #pragma unroll
-      for (int i = 0; i < kLruC; ++i) {
+        for (int j = 0; j < kLruC; ++j) {
+          const int64_t t = row + (j < lo ? lo : (j >= hi ? hi - 1 : j));  // a row of this chunk
+          A[j] = ldin(g + t * io.ldg);
+          B[j] = ldin(x + t * io.ldx);
+        }
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          float al, u;
-          lru_gate(io.gate, A[i][v], B[i][v], al, u);
-          // places outside the rows change nothing: a 1 = a, fma(1, b, -0) = b
-          const bool in = i >= lo && i < hi;
+        for (int j = 0; j < kLruC; ++j) {
+          float al;
+          float u = lru_input<GATE>(A[j], B[j], al);
+          // places outside the rows change nothing: 1 a = a, fma(1, b, -0) = b
+          const bool in = j >= lo && j < hi;
           al = in ? al : 1.0f;
           u = in ? u : -0.0f;
-          a[v] = al * a[v];
-          b[v] = fmaf(al, b[v], u);
-          A[i][v] = a[v];
-          B[i][v] = b[v];
+          A[j] = a = al * a;
+          B[j] = b = fmaf(al, b, u);
         }
       }
-#pragma unroll
-      for (int v = 0; v < V; ++v) agg[slot * W + lc + v] = float2{A[kLruC - 1][v], B[kLruC - 1][v]};
+      agg[threadIdx.x] = float2{a, b};
+      if (ch == 0) start[threadIdx.x] = io.resume ? io.cache.S[sn + cc] : (io.h0 ? io.h0[sn + cc] : 0.0f);
+      if (static_cast<int>(threadIdx.x) == slot * W) begin[slot] = ch == 0;
     }
     __syncthreads();
-    if (folds) {
-      const int m = static_cast<int>(nch - cb < slots ? nch - cb : slots);
-      for (int s = 0; s < m; ++s) {
-        const float2 ab = agg[s * W + threadIdx.x];
-        start[s * W + threadIdx.x] = S;
-        S = fmaf(ab.x, S, ab.y);
-      }
-    }
+    if (folds)
+      S = lru_chain(agg + threadIdx.x, start + threadIdx.x, begin, W,
+                    static_cast<int>(nch - cb < slots ? nch - cb : slots), S);
     __syncthreads();
     if (has && live) {
-      float st[V];
+      const float st = start[threadIdx.x];
+      TX* o = static_cast<TX*>(io.o) + c;
+      if (lo == 0 && hi == kLruC) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) st[v] = start[slot * W + lc + v];
-      if (o) {
+        for (int j = 0; j < kLruC; ++j) stout(o + (row + j) * io.ldo, fmaf(A[j], st, B[j]));
+      } else {
 #pragma unroll
-        for (int i = 0; i < kLruC; ++i) {
-          if (i >= lo && i < hi) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) stout(o + (tb + i) * io.ldo + v, fmaf(A[i][v], st[v], B[i][v]));
-          }
-        }
+        for (int j = 0; j < kLruC; ++j)
+          if (j >= lo && j < hi) stout(o + (row + j) * io.ldo, fmaf(A[j], st, B[j]));
       }
-      if (ch == nch - 1) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float h = fmaf(A[kLruC - 1][v], st[v], B[kLruC - 1][v]);
-          if (io.hT) io.hT[sn + c + v] = h;
-          if (io.cache.S) {
-            const bool full = hi == kLruC;
-            io.cache.S[sn + c + v] = full ? h : st[v];
-            io.cache.A[sn + c + v] = full ? 1.0f : A[kLruC - 1][v];
-            io.cache.B[sn + c + v] = full ? 0.0f : B[kLruC - 1][v];
-          }
+      if (last) {
+        const float al = A[kLruC - 1], bl = B[kLruC - 1];
+        const float h = fmaf(al, st, bl);
+        if (io.hT) io.hT[sn + c] = h;
+        if (io.cache.S) {
+          const bool full = hi == kLruC;
+          io.cache.S[sn + c] = full ? h : st;
+          io.cache.A[sn + c] = full ? 1.0f : al;
+          io.cache.B[sn + c] = full ? 0.0f : bl;
         }
       }
     }
@@ -233,18 +343,20 @@ __global__ void k_lru_pos(LruIO io) {
 }
 
 __global__ void k_lru_cache_init(LruIO io) {
-  const int64_t e = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   const int64_t groups = (io.D + gdn::kLruGroup - 1) / gdn::kLruGroup;
-  if (e < io.N * groups) io.cache.pos[e] = 0;
-  if (e >= static_cast<int64_t>(io.N) * io.D) return;
-  io.cache.S[e] = io.h0 ? io.h0[e] : 0.0f;
-  io.cache.A[e] = 1.0f;
-  io.cache.B[e] = 0.0f;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  for (int64_t e = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; e < static_cast<int64_t>(io.N) * io.D;
+       e += stride) {
+    if (e < io.N * groups) io.cache.pos[e] = 0;
+    io.cache.S[e] = io.h0 ? io.h0[e] : 0.0f;
+    io.cache.A[e] = 1.0f;
+    io.cache.B[e] = 0.0f;
+  }
 }
 
 // One token of one sequence, 256 channels a block of one wave, which alone
 // reads and advances their position counter.
-template <typename TX, typename TG>
+template <typename TX, typename TG, int GATE>
 __global__ __launch_bounds__(64) void k_lru_decode(LruIO io) {
   const int n = blockIdx.y;
   const int c0 = blockIdx.x * gdn::kLruGroup;
@@ -257,8 +369,8 @@ __global__ __launch_bounds__(64) void k_lru_decode(LruIO io) {
     if (c < io.D) {
       const float g = ldin(static_cast<const TG*>(io.g) + n * io.ldg + c);
       const float x = ldin(static_cast<const TX*>(io.x) + n * io.ldx + c);
-      float al, u;
-      lru_gate(io.gate, g, x, al, u);
+      float al;
+      const float u = lru_input<GATE>(g, x, al);
       const float S = io.cache.S[sn + c];
       const float A = al * io.cache.A[sn + c];
       const float B = fmaf(al, io.cache.B[sn + c], u);
@@ -272,176 +384,402 @@ __global__ __launch_bounds__(64) void k_lru_decode(LruIO io) {
   if (threadIdx.x == 0) io.cache.pos[static_cast<int64_t>(n) * gridDim.x + blockIdx.x] = full ? 0 : p + 1;
 }
 
-// Trainer: a sweep forward over the rounds of chunks (as k_lru_fwd, keeping
-// the chunk-start states), then one backward.  Going back, a chunk maps the
-// gradient K of the state behind its last token to that in front of its first
-// token, K -> P K + Q, so the same three steps run in reverse.
-template <typename TX, typename TG>
-__global__ __launch_bounds__(kLruThreads) void k_lru_bwd(LruIO io) {
-  __shared__ float2 agg[kLruThreads];
-  __shared__ float start[kLruThreads];
-  int n, tile;
-  if (!lru_item(io, n, tile)) return;
+// ---- three steps ---------------------------------------------------------------
+
+// Sequence n's chunks have the slots from cu[n] / 32 + 2 n on: floor(b / 32) -
+// floor(a / 32) + 2 >= ceil((31 + b - a) / 32), so they end before the next
+// sequence's also where the first chunk was begun by the cache.
+__device__ __forceinline__ int64_t lru_slot0(const LruIO& io, int n) {
+  int64_t a = io.cu[n];
+  a = a < 0 ? 0 : (a > io.T ? io.T : a);
+  return a / kLruC + 2 * static_cast<int64_t>(n);
+}
+
+// The chunk of a slot: its sequence, the row of its place 0 and the places
+// [lo, hi) that hold tokens.  False for a slot that no chunk uses.
+struct LruChunk {
+  int n, lo, hi;
+  int64_t row;
+};
+__device__ __forceinline__ bool lru_chunk(const LruIO& io, int64_t slot, LruChunk& k) {
+  int lo = 0, hi = io.N - 1;  // the last sequence that starts at or before the slot
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (lru_slot0(io, mid) <= slot) lo = mid; else hi = mid - 1;
+  }
+  k.n = lo;
+  int64_t t0, L;
+  lru_rows(io, lo, t0, L);
+  const int64_t tb = (slot - lru_slot0(io, lo)) * kLruC - (io.resume ? lru_pos(io, lo, 0) : 0);
+  if (L == 0 || tb >= L) return false;  // (an empty sequence may stand inside a chunk: tb < 0)
+  k.row = t0 + tb;
+  k.lo = tb < 0 ? static_cast<int>(-tb) : 0;
+  k.hi = L - tb < kLruC ? static_cast<int>(L - tb) : kLruC;
+  return true;
+}
+// Row of place i, or the nearest that holds a token.
+template <bool WHOLE>
+__device__ __forceinline__ int64_t lru_row(const LruChunk& k, int i) {
+  return k.row + (WHOLE ? i : (i < k.lo ? k.lo : (i >= k.hi ? k.hi - 1 : i)));
+}
+
+// The block's slot and the lane's first channel; false past the ends.
+__device__ __forceinline__ bool lru_unit(const LruIO& io, int64_t& slot, int& c) {
+  const int per = 256 / io.cw;
+  const int groups = (io.D + io.cw - 1) / io.cw;
+  const int64_t b = blockIdx.x;
+  const int sub = threadIdx.x / io.cw;
+  slot = b / groups * per + sub;
+  c = static_cast<int>(b % groups) * io.cw + static_cast<int>(threadIdx.x) - sub * io.cw;
+  return slot < io.slots && c < io.D;
+}
+
+template <typename TX, typename TG, int GATE, bool GRAD, bool WHOLE>
+__device__ __forceinline__ void lru_fold(const LruIO& io, const LruChunk& k, int64_t slot, int c) {
+  const TX* x = static_cast<const TX*>(io.x) + c;
+  const TG* g = static_cast<const TG*>(io.g) + c;
+  const TX* dO = static_cast<const TX*>(io.dO) + c;
+  float G[kLruC], X[kLruC], Y[GRAD ? kLruC : 1];
+#pragma unroll
+  for (int i = 0; i < kLruC; ++i) {
+    const int64_t t = lru_row<WHOLE>(k, i);
+    G[i] = ldin(g + t * io.ldg);
+    X[i] = ldin(x + t * io.ldx);
+    if constexpr (GRAD) Y[i] = ldin(dO + t * io.lddo);
+  }
+  float a = 1.0f, b = 0.0f, q = 0.0f;
+  if (!WHOLE && k.lo > 0) {
+    // the cache's composition, kept for k_lru_apply: k_lru_chain moves the cache on
+    a = io.cache.A[static_cast<int64_t>(k.n) * io.D + c];
+    b = io.cache.B[static_cast<int64_t>(k.n) * io.D + c];
+    io.keep[2 * static_cast<int64_t>(k.n) * io.D + c] = a;
+    io.keep[(2 * static_cast<int64_t>(k.n) + 1) * io.D + c] = b;
+  }
+#pragma unroll
+  for (int i = 0; i < kLruC; ++i) {
+    float al;
+    float u = lru_input<GATE>(G[i], X[i], al);
+    if constexpr (!WHOLE) {
+      // places outside the rows change nothing: 1 a = a, fma(1, b, -0) = b
+      const bool in = i >= k.lo && i < k.hi;
+      al = in ? al : 1.0f;
+      u = in ? u : -0.0f;
+      if constexpr (GRAD) Y[i] = in ? Y[i] : -0.0f;
+    }
+    a = al * a;
+    b = fmaf(al, b, u);
+    if constexpr (GRAD) q = fmaf(a, Y[i], q);
+  }
+  const int64_t at = slot * io.D + c;
+  io.wA[at] = a;
+  io.wB[at] = b;
+  if constexpr (GRAD) io.wQ[at] = q;
+}
+template <typename TX, typename TG, int GATE, bool GRAD>
+__global__ __launch_bounds__(256) void k_lru_fold(LruIO io) {
+  int64_t slot;
+  int c;
+  LruChunk k;
+  if (!lru_unit(io, slot, c) || !lru_chunk(io, slot, k)) return;
+  if (k.lo == 0 && k.hi == kLruC)
+    lru_fold<TX, TG, GATE, GRAD, true>(io, k, slot, c);
+  else
+    lru_fold<TX, TG, GATE, GRAD, false>(io, k, slot, c);
+}
+
+// The chains over a sequence's chunks, 32 channels a block, up to 256 chunks at
+// a time through LDS: forward S -> A S + B (wB then holds the states at the
+// chunks' starts), backward (grid.y = 1) K -> A K + Q (wQ then holds the
+// gradients of the states behind the chunks' ends).  Also what a sequence ends
+// with: hT, the cache, dh0.
+constexpr int kChainW = 32, kChainRows = 256;
+__global__ __launch_bounds__(256) void k_lru_chain(LruIO io) {
+  __shared__ float2 agg[kChainRows * kChainW];
+  const int tiles = (io.D + kChainW - 1) / kChainW;
+  const int n = blockIdx.x / tiles;
+  const int c0 = (blockIdx.x % tiles) * kChainW;
   int64_t t0, L;
   lru_rows(io, n, t0, L);
-  const int W = io.lps;
-  const int slots = blockDim.x / W;
-  const int slot = threadIdx.x / W;
-  const int lc = threadIdx.x - slot * W;
-  const int c = tile * W + lc;
-  const bool live = c < io.D;
-  const int cc = live ? c : io.D - 1;
-  const TX* x = static_cast<const TX*>(io.x) + t0 * io.ldx + cc;
-  const TG* g = static_cast<const TG*>(io.g) + t0 * io.ldg + cc;
-  const TX* dO = static_cast<const TX*>(io.dO) + t0 * io.lddo + cc;
-  TX* o = io.o ? static_cast<TX*>(io.o) + t0 * io.ldo + cc : nullptr;
-  TX* dx = static_cast<TX*>(io.dx) + t0 * io.lddx + cc;
-  TG* dg = static_cast<TG*>(io.dg) + t0 * io.lddg + cc;
   const int64_t sn = static_cast<int64_t>(n) * io.D;
-  const int64_t nch = (L + kLruC - 1) / kLruC;
-  const int fc = tile * W + static_cast<int>(threadIdx.x);
-  const bool folds = static_cast<int>(threadIdx.x) < W && fc < io.D;
-  float S = 0.0f, K = 0.0f;
-  if (folds) {
-    S = io.h0 ? io.h0[sn + fc] : 0.0f;
-    K = io.dhT ? io.dhT[sn + fc] : 0.0f;
-  }
-  // chunk ch of sequence n keeps its state in slot cu[n] / 32 + n + ch: at most
-  // L / 32 + 1 chunks, and floor(b / 32) - floor(a / 32) + 1 >= ceil((b - a) / 32)
-  float* states = io.states + (t0 / kLruC + n) * static_cast<int64_t>(io.D) + cc;
-  const int64_t rounds = (nch + slots - 1) / slots;
-  for (int64_t r = 0; r < rounds; ++r) {
-    const int64_t ch = r * slots + slot;
-    const bool has = ch < nch;
-    const int64_t tb = ch * kLruC;
-    const int hi = has ? static_cast<int>(L - tb < kLruC ? L - tb : kLruC) : 0;
-    float A[kLruC], B[kLruC];
-    if (has) {
-#pragma unroll
-      for (int i = 0; i < kLruC; ++i) {
-        const int64_t t = tb + (i < hi ? i : hi - 1);
-        A[i] = ldin(g + t * io.ldg);
-        B[i] = ldin(x + t * io.ldx);
+  const bool up = blockIdx.y == 0;
+  const int p0 = io.resume ? lru_pos(io, n, c0) : 0;
+  const int64_t nch = L > 0 ? (p0 + L + kLruC - 1) / kLruC : 0;
+  const int col = threadIdx.x & (kChainW - 1), row = threadIdx.x / kChainW;
+  const int c = c0 + col;
+  const bool live = c < io.D;
+  const int64_t base = lru_slot0(io, n) * io.D + c;
+  float* w = up ? io.wB : io.wQ;
+  float S = 0.0f;
+  const bool folds = row == 0 && live;
+  if (folds) S = up ? (io.resume ? io.cache.S[sn + c] : (io.h0 ? io.h0[sn + c] : 0.0f)) : (io.dhT ? io.dhT[sn + c] : 0.0f);
+  float before = S;  // the state at the start of the last chunk
+  for (int64_t r0 = 0; r0 < nch; r0 += kChainRows) {
+    const int m = static_cast<int>(nch - r0 < kChainRows ? nch - r0 : kChainRows);
+    // rows in the chain's order: from the first chunk up, or from the last down
+    if (live) {
+#pragma unroll 8
+      for (int r = row; r < m; r += 256 / kChainW) {
+        const int64_t at = base + (up ? r0 + r : nch - 1 - r0 - r) * io.D;
+        agg[r * kChainW + col] = float2{io.wA[at], w[at]};
       }
-      float a = 1.0f, b = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kLruC; ++i) {
-        float al, u;
-        lru_gate(io.gate, A[i], B[i], al, u);
-        al = i < hi ? al : 1.0f;
-        u = i < hi ? u : -0.0f;
-        a = al * a;
-        b = fmaf(al, b, u);
-        A[i] = a;
-        B[i] = b;
-      }
-      agg[threadIdx.x] = float2{a, b};
     }
     __syncthreads();
     if (folds) {
-      const int m = static_cast<int>(nch - r * slots < slots ? nch - r * slots : slots);
-      for (int s = 0; s < m; ++s) {
-        const float2 ab = agg[s * W + threadIdx.x];
-        start[s * W + threadIdx.x] = S;
-        S = fmaf(ab.x, S, ab.y);
-      }
-    }
-    __syncthreads();
-    if (has && live) {
-      const float st = start[threadIdx.x];
-      states[ch * io.D] = st;
-      if (o) {
+      for (int s0 = 0; s0 < m; s0 += 8) {
+        float2 ab[8];
 #pragma unroll
-        for (int i = 0; i < kLruC; ++i)
-          if (i < hi) stout(o + (tb + i) * io.ldo, fmaf(A[i], st, B[i]));
-      }
-    }
-  }
-  if (folds && io.hT) io.hT[sn + fc] = S;
-  for (int64_t r = rounds - 1; r >= 0; --r) {
-    const int64_t ch = r * slots + slot;
-    const bool has = ch < nch;
-    const int64_t tb = ch * kLruC;
-    const int hi = has ? static_cast<int>(L - tb < kLruC ? L - tb : kLruC) : 0;
-    float al[kLruC], hp[kLruC], dy[kLruC], xx[kLruC], b[kLruC];
-    if (has) {
+        for (int j = 0; j < 8; ++j) ab[j] = agg[(s0 + j < m ? s0 + j : m - 1) * kChainW + col];
 #pragma unroll
-      for (int i = 0; i < kLruC; ++i) {
-        const int64_t t = tb + (i < hi ? i : hi - 1);
-        b[i] = ldin(g + t * io.ldg);
-        xx[i] = ldin(x + t * io.ldx);
-        dy[i] = ldin(dO + t * io.lddo);
-      }
-      float h = live ? states[ch * io.D] : 0.0f;
-#pragma unroll
-      for (int i = 0; i < kLruC; ++i) {
-        hp[i] = h;
-        const float gi = b[i];
-        al[i] = expf(gi);
-        b[i] = io.gate == GDN_LRU_GATE_NONE         ? 1.0f
-               : io.gate == GDN_LRU_GATE_COMPLEMENT ? -expm1f(gi)
-                                                    : sqrtf(fmaxf(-expm1f(2.0f * gi), 0.0f));
-        al[i] = i < hi ? al[i] : 1.0f;
-        dy[i] = i < hi ? dy[i] : 0.0f;
-        h = fmaf(al[i], h, b[i] * xx[i]);
-      }
-      float p = 1.0f, q = 0.0f;
-#pragma unroll
-      for (int i = kLruC - 1; i >= 0; --i) {
-        q = al[i] * (q + dy[i]);
-        p = al[i] * p;
-      }
-      agg[threadIdx.x] = float2{p, q};
-    }
-    __syncthreads();
-    if (folds) {
-      const int m = static_cast<int>(nch - r * slots < slots ? nch - r * slots : slots);
-      for (int s = m - 1; s >= 0; --s) {
-        const float2 pq = agg[s * W + threadIdx.x];
-        start[s * W + threadIdx.x] = K;
-        K = fmaf(pq.x, K, pq.y);
-      }
-    }
-    __syncthreads();
-    if (has && live) {
-      float k = start[threadIdx.x];
-#pragma unroll
-      for (int i = kLruC - 1; i >= 0; --i) {
-        const float d = dy[i] + k;
-        k = al[i] * d;
-        if (i < hi) {
-          stout(dx + (tb + i) * io.lddx, b[i] * d);
-          float e = al[i] * hp[i];
-          if (io.gate == GDN_LRU_GATE_COMPLEMENT) e = fmaf(-al[i], xx[i], e);
-          if (io.gate == GDN_LRU_GATE_NORM) e = fmaf(b[i] > 0.0f ? -(al[i] * al[i]) / b[i] : 0.0f, xx[i], e);
-          stout(dg + (tb + i) * io.lddg, d * e);
+        for (int j = 0; j < 8; ++j) {
+          if (s0 + j >= m) break;
+          agg[(s0 + j) * kChainW + col].x = S;
+          before = S;
+          S = fmaf(ab[j].x, S, ab[j].y);
         }
       }
     }
+    __syncthreads();
+    if (live) {
+      if (up && r0 + m == nch && io.cache.S && row == (m - 1) % (256 / kChainW)) {
+        // the last chunk as the cache keeps it; wB's own thread, before it is overwritten
+        const int64_t at = base + (nch - 1) * io.D;
+        const bool full = (p0 + L) % kLruC == 0;
+        io.cache.A[sn + c] = full ? 1.0f : io.wA[at];
+        io.cache.B[sn + c] = full ? 0.0f : io.wB[at];
+      }
+#pragma unroll 8
+      for (int r = row; r < m; r += 256 / kChainW)
+        w[base + (up ? r0 + r : nch - 1 - r0 - r) * io.D] = agg[r * kChainW + col].x;
+    }
+    __syncthreads();
   }
-  if (folds) io.dh0[sn + fc] = K;
+  if (!folds) return;
+  if (!up) {
+    io.dh0[sn + c] = S;
+    return;
+  }
+  if (L == 0) {
+    lru_empty(io, sn + c);
+    return;
+  }
+  if (io.hT) io.hT[sn + c] = S;
+  if (io.cache.S) io.cache.S[sn + c] = (p0 + L) % kLruC == 0 ? S : before;
+}
+
+template <typename TX, typename TG, int GATE, bool WHOLE>
+__device__ __forceinline__ void lru_apply(const LruIO& io, const LruChunk& k, int64_t slot, int c) {
+  const TX* x = static_cast<const TX*>(io.x) + c;
+  const TG* g = static_cast<const TG*>(io.g) + c;
+  TX* o = static_cast<TX*>(io.o) + c;
+  float G[kLruC], X[kLruC];
+  const float S = io.wB[slot * io.D + c];
+#pragma unroll
+  for (int i = 0; i < kLruC; ++i) {
+    const int64_t t = lru_row<WHOLE>(k, i);
+    G[i] = ldin(g + t * io.ldg);
+    X[i] = ldin(x + t * io.ldx);
+  }
+  float a = 1.0f, b = 0.0f;
+  if (!WHOLE && k.lo > 0) {
+    a = io.keep[2 * static_cast<int64_t>(k.n) * io.D + c];
+    b = io.keep[(2 * static_cast<int64_t>(k.n) + 1) * io.D + c];
+  }
+#pragma unroll
+  for (int i = 0; i < kLruC; ++i) {
+    if (WHOLE || (i >= k.lo && i < k.hi)) {
+      float al;
+      const float u = lru_input<GATE>(G[i], X[i], al);
+      a = al * a;
+      b = fmaf(al, b, u);
+      stout(o + (k.row + i) * io.ldo, fmaf(a, S, b));
+    }
+  }
+}
+template <typename TX, typename TG, int GATE>
+__global__ __launch_bounds__(256) void k_lru_apply(LruIO io) {
+  int64_t slot;
+  int c;
+  LruChunk k;
+  if (!lru_unit(io, slot, c) || !lru_chunk(io, slot, k)) return;
+  if (k.lo == 0 && k.hi == kLruC)
+    lru_apply<TX, TG, GATE, true>(io, k, slot, c);
+  else
+    lru_apply<TX, TG, GATE, false>(io, k, slot, c);
+}
+
+// Outputs and gradients of one chunk of one channel: forward for h and
+//     e_i = alpha_i h_{i-1} + b'_i x_i      (dg_i = delta_i e_i)
+// then backward for delta.
+template <typename TX, typename TG, int GATE, bool WHOLE>
+__device__ __forceinline__ void lru_grad(const LruIO& io, const LruChunk& k, int64_t slot, int c) {
+  const TX* x = static_cast<const TX*>(io.x) + c;
+  const TG* g = static_cast<const TG*>(io.g) + c;
+  const TX* dO = static_cast<const TX*>(io.dO) + c;
+  TX* o = io.o ? static_cast<TX*>(io.o) + c : nullptr;
+  TX* dx = static_cast<TX*>(io.dx) + c;
+  TG* dg = static_cast<TG*>(io.dg) + c;
+  const float S = io.wB[slot * io.D + c];
+  float K = io.wQ[slot * io.D + c];
+  float al[kLruC], e[kLruC], dy[kLruC], w[GATE == GDN_LRU_GATE_NONE ? 1 : kLruC];
+#pragma unroll
+  for (int i = 0; i < kLruC; ++i) {
+    const int64_t t = lru_row<WHOLE>(k, i);
+    al[i] = ldin(g + t * io.ldg);
+    e[i] = ldin(x + t * io.ldx);
+    dy[i] = ldin(dO + t * io.lddo);
+  }
+  float a = 1.0f, b = 0.0f, hp = S;
+#pragma unroll
+  for (int i = 0; i < kLruC; ++i) {
+    const float xi = e[i];
+    const float wi = lru_weight<GATE>(al[i], al[i]);
+    const float u = GATE == GDN_LRU_GATE_NONE ? xi : wi * xi;
+    a = al[i] * a;
+    b = fmaf(al[i], b, u);
+    const float h = fmaf(a, S, b);
+    if (o && (WHOLE || i < k.hi)) stout(o + (k.row + i) * io.ldo, h);
+    e[i] = al[i] * hp;
+    if constexpr (GATE == GDN_LRU_GATE_COMPLEMENT) e[i] = fmaf(-al[i], xi, e[i]);
+    // b' = -alpha^2 / b, the reciprocal the hardware's (1 ulp)
+    if constexpr (GATE == GDN_LRU_GATE_NORM)
+      e[i] = fmaf(wi > 0.0f ? -(al[i] * al[i]) * __builtin_amdgcn_rcpf(wi) : 0.0f, xi, e[i]);
+    if constexpr (GATE != GDN_LRU_GATE_NONE) w[i] = wi;
+    hp = h;
+  }
+#pragma unroll
+  for (int i = kLruC - 1; i >= 0; --i) {
+    if (WHOLE || i < k.hi) {
+      const float d = dy[i] + K;
+      K = al[i] * d;
+      stout(dx + (k.row + i) * io.lddx, GATE == GDN_LRU_GATE_NONE ? d : w[i] * d);
+      stout(dg + (k.row + i) * io.lddg, d * e[i]);
+    }
+  }
+}
+template <typename TX, typename TG, int GATE>
+__global__ __launch_bounds__(256) void k_lru_grad(LruIO io) {
+  int64_t slot;
+  int c;
+  LruChunk k;
+  if (!lru_unit(io, slot, c) || !lru_chunk(io, slot, k)) return;
+  if (k.hi == kLruC)
+    lru_grad<TX, TG, GATE, true>(io, k, slot, c);
+  else
+    lru_grad<TX, TG, GATE, false>(io, k, slot, c);
 }
 
 // ---- host side ----------------------------------------------------------------
 
-// Calls f.template operator()<TX, TG>() for the shape's types.
+// Calls f.template operator()<TX, TG, GATE>() for the shape's types and gate.
+template <typename TX, typename TG, typename F>
+int lru_dispatch_gate(const gdn_lru_shape_t* s, F&& f) {
+  if (s->gate == GDN_LRU_GATE_NONE) return f.template operator()<TX, TG, GDN_LRU_GATE_NONE>();
+  if (s->gate == GDN_LRU_GATE_COMPLEMENT) return f.template operator()<TX, TG, GDN_LRU_GATE_COMPLEMENT>();
+  return f.template operator()<TX, TG, GDN_LRU_GATE_NORM>();
+}
 template <typename F>
 int lru_dispatch(const gdn_lru_shape_t* s, F&& f) {
   if (s->in_dtype == GDN_BF16)
-    return s->g_dtype == GDN_BF16 ? f.template operator()<bf16_t, bf16_t>() : f.template operator()<bf16_t, float>();
-  return s->g_dtype == GDN_BF16 ? f.template operator()<float, bf16_t>() : f.template operator()<float, float>();
+    return s->g_dtype == GDN_BF16 ? lru_dispatch_gate<bf16_t, bf16_t>(s, f) : lru_dispatch_gate<bf16_t, float>(s, f);
+  return s->g_dtype == GDN_BF16 ? lru_dispatch_gate<float, bf16_t>(s, f) : lru_dispatch_gate<float, float>(s, f);
 }
 
-// Lanes per chunk and threads per block.
-void lru_tiling(const LruIO& io, int V, int64_t longest, int* lps, int* threads) {
-  int l = 64;
-  while (l > 8 && io.T * io.D < static_cast<int64_t>(l) * V * 512 * longest) l >>= 1;
-  const int64_t chunks = longest / kLruC + 2;
-  int64_t t = (chunks * l + 63) / 64 * 64;
-  if (t < l) t = l;
-  if (t < l * V) t = l * V;  // one thread per channel of the tile folds
-  *lps = l;
-  *threads = static_cast<int>(t < kLruThreads ? t : kLruThreads);
+// The one pass's tile, threads and units.
+//
+// A block goes over its unit in rounds of threads / tile chunks, one block of
+// 1024 threads a CU, so a pass takes the larger of the longest unit's rounds
+// and the rounds of all units and tiles over 256 CUs, times a round's time.
+// That one is longer with narrow tiles, whose rows are 16- or 32-byte pieces of
+// a cache line, so that L2's request rate bounds them; measured with all CUs at
+// work (bf16 x, fp32 g, norm gate): 33, 20, 16 and 13.5 us a round at tiles of 8,
+// 16, 32 and 64 channels.  The tile with the least time is taken.
+//
+// Up to kLruPack sequences are packed: those shorter than a round share units
+// of up to a round (first fit, longest first), and the longest units begin
+// first.  More sequences are units of their own.
+//
+// Blocks of 512 threads, two a CU, where all tiles and units keep them busy: one
+// block's loads then overlap the other's chain (16 x 2048 tokens x 2048 channels:
+// 119 us against 125; with half as many blocks 122 against 108 us).
+struct LruTiling {
+  int lps = 64, threads = 1024;
+  double us = 0;  // expected
+};
+LruTiling lru_tiling(const LruIO& io, const int32_t* cu_host, int64_t longest) {
+  static constexpr int kTile[4] = {64, 32, 16, 8};
+  static constexpr double kRound[4] = {13.5, 16.0, 20.0, 33.0};
+  LruTiling best;
+  for (int k = 0; k < 4; ++k) {
+    const int l = kTile[k];
+    const int64_t round = static_cast<int64_t>(kLruThreads) / l * kLruC;
+    double rounds = 0;
+    if (io.N <= kLruPack) {
+      int64_t shorts = 0;
+      for (int32_t n = 0; n < io.N; ++n) {
+        const int64_t len = static_cast<int64_t>(cu_host[n + 1]) - cu_host[n];
+        if (len >= round) rounds += static_cast<double>((len + round - 1) / round);
+        else shorts += len;
+      }
+      rounds += static_cast<double>((shorts + round - 1) / round);
+    } else {
+      rounds = static_cast<double>(io.T / round + io.N);
+    }
+    const double all = std::ceil(rounds * ((io.D + l - 1) / l) / 256.0);
+    const double one = static_cast<double>((longest + round - 1) / round);
+    const double us = (all > one ? all : one) * kRound[k];
+    if (best.us == 0 || us < best.us) {
+      best.us = us;
+      best.lps = l;
+    }
+  }
+  const int64_t blocks = longest > 0 ? io.T * ((io.D + 63) / 64) / longest : 0;
+  const int64_t most = blocks >= 400 ? 512 : kLruThreads;
+  const int64_t t = ((longest / kLruC + 2) * best.lps + 63) / 64 * 64;
+  best.threads = static_cast<int>(t < most ? t : most);
+  return best;
+}
+
+// Packs the sequences into units of at most a round.
+void lru_pack(LruIO* io, const int32_t* cu_host, int threads) {
+  io->units = io->N;
+  io->packed = 0;
+  if (io->N > kLruPack) return;
+  const int64_t round = static_cast<int64_t>(threads) / io->lps * kLruC;
+  const int N = io->N;
+  int order[kLruPack], unit[kLruPack], units = 0;
+  int64_t len[kLruPack], sum[kLruPack];
+  for (int n = 0; n < N; ++n) {
+    len[n] = static_cast<int64_t>(cu_host[n + 1]) - cu_host[n];
+    int at = n;
+    for (; at > 0 && len[order[at - 1]] < len[n]; --at) order[at] = order[at - 1];
+    order[at] = n;
+  }
+  for (int i = 0; i < N; ++i) {
+    const int n = order[i];
+    // a chunk more for the places before a resumed sequence's first token
+    const int64_t need = (len[n] + (io->resume ? 2 * kLruC - 1 : kLruC - 1)) / kLruC * kLruC;
+    int u = 0;
+    while (u < units && sum[u] + need > round) ++u;
+    if (u == units) sum[units++] = 0;
+    sum[u] += need;
+    unit[i] = u;
+  }
+  int at = 0;
+  for (int u = 0; u < units; ++u) {
+    io->first[u] = static_cast<uint8_t>(at);
+    for (int i = 0; i < N; ++i)
+      if (unit[i] == u) io->seq[at++] = static_cast<uint8_t>(order[i]);
+  }
+  io->first[units] = static_cast<uint8_t>(at);
+  io->units = units;
+  io->packed = 1;
+}
+
+// Whether a prefill takes the three steps instead of the one pass's expected
+// `us`: they read the inputs twice, 3 us per million elements, and take some 8 us
+// for two launches and the chain.
+bool lru_three(const LruIO& io, double us) {
+  return io.T > GDN_LRU_SMALL && 8.0 + 3e-6 * static_cast<double>(io.T) * io.D < us;
 }
 
 // Checks and resolves what the packed calls share.
@@ -472,16 +810,40 @@ int lru_common(const gdn_lru_shape_t* shape, int32_t n_seqs, const int32_t* cu_d
   return GDN_OK;
 }
 
+// Workspace of the three steps: A, B, for the trainer Q, and a cache's A and B.
+size_t lru_ws_bytes(int64_t D, int64_t N, int64_t T, bool grad) {
+  const int64_t floats = gdn::lru_slots(T, N) * D * (grad ? 3 : 2) + (grad ? 0 : 2 * N * D);
+  return (static_cast<size_t>(floats) * sizeof(float) / gdn::kAlign + 4) * gdn::kAlign;
+}
+void lru_ws(LruIO* io, void* ws, bool grad) {
+  io->slots = gdn::lru_slots(io->T, io->N);
+  const int64_t step = (io->slots * io->D + 63) / 64 * 64;  // floats, 256 bytes
+  io->wA = static_cast<float*>(ws);
+  io->wB = io->wA + step;
+  io->wQ = grad ? io->wB + step : nullptr;
+  io->keep = grad ? nullptr : io->wB + step;
+}
+// Lanes over channels and blocks of the steps over all chunks.
+int64_t lru_units(LruIO* io) {
+  io->cw = 64;
+  while (io->cw < 256 && io->cw < io->D) io->cw *= 2;
+  const int64_t per = 256 / io->cw, groups = (io->D + io->cw - 1) / io->cw;
+  return (io->slots + per - 1) / per * groups;
+}
+int64_t lru_chain_blocks(const LruIO& io) { return io.N * static_cast<int64_t>((io.D + kChainW - 1) / kChainW); }
+// A launch holds fewer than 2^32 threads.
+bool lru_fits(int64_t threads) { return threads < (int64_t{1} << 32); }
+
 int lru_prefill_entry(const gdn_lru_shape_t* shape, int32_t n_seqs, const int32_t* cu_dev, const int32_t* cu_host,
                       const void* x, int64_t ldx, const void* g, int64_t ldg, const float* h0, void* o, int64_t ldo,
-                      float* hT, gdn_lru_cache_t* cache, bool resume, void* stream) {
+                      float* hT, gdn_lru_cache_t* cache, bool resume, void* ws, size_t ws_bytes, void* stream) {
   hipStream_t st = static_cast<hipStream_t>(stream);
   LruIO io{};
   std::vector<int32_t> buf;
   int64_t longest = 0;
   int rc = gdn::check_lru_shape(shape);
   if (rc != GDN_OK) return rc;
-  if (!gdn::aligned16({x, g, h0, o, hT})) return GDN_ERR_INVALID_ARG;
+  if (!gdn::aligned16({x, g, h0, o, hT, ws})) return GDN_ERR_INVALID_ARG;
   if ((cache || resume) && (rc = gdn::check_lru_cache(cache)) != GDN_OK) return rc;
   io.ldx = gdn::row_stride(ldx, shape->D);
   io.ldg = gdn::row_stride(ldg, shape->D);
@@ -489,24 +851,43 @@ int lru_prefill_entry(const gdn_lru_shape_t* shape, int32_t n_seqs, const int32_
   if (io.ldx < 0 || io.ldg < 0 || io.ldo < 0) return GDN_ERR_INVALID_ARG;
   if ((rc = lru_common(shape, n_seqs, cu_dev, &cu_host, buf, st, &io, &longest)) != GDN_OK) return rc;
   if (io.T > 0 && (!x || !g || !o)) return GDN_ERR_INVALID_ARG;
+  const bool small = io.T <= GDN_LRU_SMALL;
+  if (!small && (!ws || ws_bytes < lru_ws_bytes(shape->D, n_seqs, io.T, false))) return GDN_ERR_WORKSPACE;
   if (n_seqs == 0) return GDN_OK;
   io.x = x; io.g = g; io.h0 = h0; io.o = o; io.hT = hT; io.resume = resume;
   if (cache) io.cache = *cache;
-  const bool f32 = shape->in_dtype == GDN_F32 && shape->g_dtype == GDN_F32;
-  const bool even = shape->D % 2 == 0 && io.ldx % 2 == 0 && io.ldg % 2 == 0 && io.ldo % 2 == 0;
-  const int V = !f32 && even ? 2 : 1;
-  int threads;
-  lru_tiling(io, V, longest, &io.lps, &threads);
-  io.tiles = (io.D + io.lps * V - 1) / (io.lps * V);
-  const int64_t blocks = lru_blocks(n_seqs, io.tiles);
-  if (blocks > INT32_MAX) return GDN_ERR_UNSUPPORTED;
-  lru_dispatch(shape, [&]<typename TX, typename TG>() {
-    Timed t_("k_lru_fwd", st);
+  const LruTiling tiling = lru_tiling(io, cu_host, longest);
+  const bool three = lru_three(io, tiling.us);
+  int threads = 256;
+  int64_t blocks;
+  if (three) {
+    lru_ws(&io, ws, false);
+    blocks = lru_units(&io);
+  } else {
+    threads = tiling.threads;
+    io.lps = tiling.lps;
+    io.tiles = (io.D + io.lps - 1) / io.lps;
+    lru_pack(&io, cu_host, threads);
+    blocks = lru_blocks(io.units, io.tiles);
+  }
+  if (!lru_fits(blocks * threads) || (three && !lru_fits(lru_chain_blocks(io) * 256))) return GDN_ERR_UNSUPPORTED;
+  lru_dispatch(shape, [&]<typename TX, typename TG, int GATE>() {
     const dim3 grid(static_cast<unsigned>(blocks)), block(threads);
-    if (V == 2)
-      hipLaunchKernelGGL((k_lru_fwd<TX, TG, 2>), grid, block, 0, st, io);
-    else
-      hipLaunchKernelGGL((k_lru_fwd<TX, TG, 1>), grid, block, 0, st, io);
+    if (!three) {
+      Timed t_("k_lru_fwd", st);
+      hipLaunchKernelGGL((k_lru_fwd<TX, TG, GATE>), grid, block, 0, st, io);
+      return GDN_OK;
+    }
+    {
+      Timed t_("k_lru_fold", st);
+      hipLaunchKernelGGL((k_lru_fold<TX, TG, GATE, false>), grid, block, 0, st, io);
+    }
+    {
+      Timed t_("k_lru_chain", st);
+      hipLaunchKernelGGL(k_lru_chain, dim3(static_cast<unsigned>(lru_chain_blocks(io))), block, 0, st, io);
+    }
+    Timed t_("k_lru_apply", st);
+    hipLaunchKernelGGL((k_lru_apply<TX, TG, GATE>), grid, block, 0, st, io);
     return GDN_OK;
   });
   if (cache) {
@@ -530,8 +911,7 @@ int gdn_lru_cache_init(const gdn_lru_shape_t* shape, int32_t n_seqs, const float
   if (n_seqs == 0) return GDN_OK;
   LruIO io{};
   io.N = n_seqs; io.D = shape->D; io.h0 = h0; io.cache = *cache;
-  const int64_t blocks = (static_cast<int64_t>(n_seqs) * shape->D + 255) / 256;
-  if (blocks > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+  const int64_t want = (static_cast<int64_t>(n_seqs) * shape->D + 255) / 256, blocks = want < 65536 ? want : 65536;
   hipStream_t st = static_cast<hipStream_t>(stream);
   Timed t_("k_lru_cache_init", st);
   hipLaunchKernelGGL(k_lru_cache_init, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, io);
@@ -540,16 +920,18 @@ int gdn_lru_cache_init(const gdn_lru_shape_t* shape, int32_t n_seqs, const float
 
 int gdn_lru_prefill(const gdn_lru_shape_t* shape, int32_t n_seqs, const int32_t* cu_seqlens_dev,
                     const int32_t* cu_seqlens_host, const void* x, int64_t ldx, const void* g, int64_t ldg,
-                    const float* h0, void* o, int64_t ldo, float* hT, gdn_lru_cache_t* cache, void* stream) {
+                    const float* h0, void* o, int64_t ldo, float* hT, gdn_lru_cache_t* cache, void* ws, size_t ws_bytes,
+                    void* stream) {
   return lru_prefill_entry(shape, n_seqs, cu_seqlens_dev, cu_seqlens_host, x, ldx, g, ldg, h0, o, ldo, hT, cache, false,
-                           stream);
+                           ws, ws_bytes, stream);
 }
 
 int gdn_lru_prefill_continue(const gdn_lru_shape_t* shape, int32_t n_seqs, const int32_t* cu_seqlens_dev,
                              const int32_t* cu_seqlens_host, const void* x, int64_t ldx, const void* g, int64_t ldg,
-                             gdn_lru_cache_t* cache, void* o, int64_t ldo, float* hT, void* stream) {
+                             gdn_lru_cache_t* cache, void* o, int64_t ldo, float* hT, void* ws, size_t ws_bytes,
+                             void* stream) {
   return lru_prefill_entry(shape, n_seqs, cu_seqlens_dev, cu_seqlens_host, x, ldx, g, ldg, nullptr, o, ldo, hT, cache,
-                           true, stream);
+                           true, ws, ws_bytes, stream);
 }
 
 int gdn_lru_decode_step(const gdn_lru_shape_t* shape, int32_t n_seqs, const void* x, int64_t ldx, const void* g,
@@ -569,18 +951,18 @@ int gdn_lru_decode_step(const gdn_lru_shape_t* shape, int32_t n_seqs, const void
   io.x = x; io.g = g; io.o = o; io.cache = *cache;
   io.N = n_seqs; io.D = shape->D; io.gate = shape->gate;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  return lru_dispatch(shape, [&]<typename TX, typename TG>() {
+  return lru_dispatch(shape, [&]<typename TX, typename TG, int GATE>() {
     Timed t_("k_lru_decode", st);
     const dim3 grid((io.D + gdn::kLruGroup - 1) / gdn::kLruGroup, n_seqs);
-    hipLaunchKernelGGL((k_lru_decode<TX, TG>), grid, dim3(64), 0, st, io);
+    hipLaunchKernelGGL((k_lru_decode<TX, TG, GATE>), grid, dim3(64), 0, st, io);
     return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_HIP;
   });
 }
 
-size_t gdn_lru_workspace_bytes(const gdn_lru_shape_t* shape, int32_t n_seqs, int64_t total_tokens) {
+size_t gdn_lru_workspace_bytes(const gdn_lru_shape_t* shape, int32_t n_seqs, int64_t total_tokens, int32_t op) {
   if (gdn::check_lru_shape(shape) != GDN_OK || n_seqs < 0 || total_tokens < 0 || total_tokens > INT32_MAX) return 0;
-  return (static_cast<size_t>(gdn::lru_slots(total_tokens, n_seqs)) * shape->D * sizeof(float) + gdn::kAlign) /
-         gdn::kAlign * gdn::kAlign;
+  if (op != GDN_OP_PREFILL && op != GDN_OP_PREFILL_CONTINUE && op != GDN_OP_FWD_BWD) return 0;
+  return lru_ws_bytes(shape->D, n_seqs, total_tokens, op == GDN_OP_FWD_BWD);
 }
 
 int gdn_lru_fwd_bwd(const gdn_lru_shape_t* shape, int32_t n_seqs, const int32_t* cu_seqlens_dev,
@@ -605,18 +987,24 @@ int gdn_lru_fwd_bwd(const gdn_lru_shape_t* shape, int32_t n_seqs, const int32_t*
   if (io.ldx < 0 || io.ldg < 0 || io.ldo < 0 || io.lddo < 0 || io.lddx < 0 || io.lddg < 0) return GDN_ERR_INVALID_ARG;
   if ((rc = lru_common(shape, n_seqs, cu_seqlens_dev, &cu_seqlens_host, buf, st, &io, &longest)) != GDN_OK) return rc;
   if (io.T > 0 && (!x || !g || !dO || !dx || !dg)) return GDN_ERR_INVALID_ARG;
-  if (!ws || ws_bytes < gdn_lru_workspace_bytes(shape, n_seqs, io.T)) return GDN_ERR_WORKSPACE;
+  if (!ws || ws_bytes < lru_ws_bytes(shape->D, n_seqs, io.T, true)) return GDN_ERR_WORKSPACE;
   if (n_seqs == 0) return GDN_OK;
   io.x = x; io.g = g; io.h0 = h0; io.dO = dO; io.dhT = dhT; io.o = o; io.hT = hT; io.dx = dx; io.dg = dg; io.dh0 = dh0;
-  io.states = static_cast<float*>(ws);
-  int threads;
-  lru_tiling(io, 1, longest, &io.lps, &threads);
-  io.tiles = (io.D + io.lps - 1) / io.lps;
-  const int64_t blocks = lru_blocks(n_seqs, io.tiles);
-  if (blocks > INT32_MAX) return GDN_ERR_UNSUPPORTED;
-  return lru_dispatch(shape, [&]<typename TX, typename TG>() {
-    Timed t_("k_lru_bwd", st);
-    hipLaunchKernelGGL((k_lru_bwd<TX, TG>), dim3(static_cast<unsigned>(blocks)), dim3(threads), 0, st, io);
+  lru_ws(&io, ws, true);
+  const int64_t blocks = lru_units(&io);
+  if (!lru_fits(blocks * 256) || !lru_fits(2 * lru_chain_blocks(io) * 256)) return GDN_ERR_UNSUPPORTED;
+  return lru_dispatch(shape, [&]<typename TX, typename TG, int GATE>() {
+    const dim3 grid(static_cast<unsigned>(blocks)), block(256);
+    {
+      Timed t_("k_lru_fold", st);
+      hipLaunchKernelGGL((k_lru_fold<TX, TG, GATE, true>), grid, block, 0, st, io);
+    }
+    {
+      Timed t_("k_lru_chain", st);
+      hipLaunchKernelGGL(k_lru_chain, dim3(static_cast<unsigned>(lru_chain_blocks(io)), 2), block, 0, st, io);
+    }
+    Timed t_("k_lru_grad", st);
+    hipLaunchKernelGGL((k_lru_grad<TX, TG, GATE>), grid, block, 0, st, io);
     return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_HIP;
   });
 }

@@ -84,9 +84,9 @@ int check_lru_shape(const gdn_lru_shape_t* s);
 int check_lru_cache(const gdn_lru_cache_t* c);
 // A row distance as given (0 = dense): the distance, or -1 if it is too small.
 int64_t row_stride(int64_t ld, int64_t row);
-// Chunk slots that the backward keeps states for: T / 32 + N bounds every
-// split of T tokens into N sequences.
-inline int64_t lru_slots(int64_t T, int64_t N) { return T / GDN_LRU_CHUNK + N; }
+// Chunk slots of T tokens in N sequences, whatever their lengths and whichever
+// of them begin inside a chunk.
+inline int64_t lru_slots(int64_t T, int64_t N) { return T / GDN_LRU_CHUNK + 2 * N; }
 
 // Norms of q and k with rotary positions.
 int check_qk_shape(const gdn_qk_shape_t* s);

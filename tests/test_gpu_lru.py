@@ -72,6 +72,7 @@ def prefill(p, **kw):
 SHAPES = [
     ([1], 1), ([5], 2), ([31], 3), ([32], 16), ([33], 17), ([0, 64, 0], 130), ([65, 1, 0, 97], 257), ([700], 64),
     ([40, 333], 520), ([2100], 24), ([1] * 70, 8), ([5000], 6),
+    ([9000, 0, 40, 1], 33), ([3, 4200, 0, 2500], 40), ([300] * 12 + [7, 0, 1100], 100),
 ]
 
 
@@ -180,6 +181,49 @@ def test_prefill_cache_equals_decoded_cache_and_empty_sequences():
     assert same(h[2], hT[2])
     r = B.gdn_lru_fwd_bwd(p["shape"], d["x"], d["g"], d["cu"], d["dO"], h0=d["h0"], dhT=d["dhT"])
     assert same(r["dh0"][0], d["dhT"][0]) and same(r["hT"][3], d["h0"][3])
+
+
+def kernels(call):
+    """The names' launch counts of the library kernels that `call` runs, and what it returns."""
+    B.profile_enable(True)
+    try:
+        r = call()
+        torch.cuda.synchronize()
+        names = ("k_lru_fwd", "k_lru_fold", "k_lru_chain", "k_lru_apply", "k_lru_grad", "k_lru_pos")
+        return {k: B.profile_read(k)[1] for k in names}, r
+    finally:
+        B.profile_enable(False)
+
+
+@pytest.mark.parametrize("D,gate", [(40, "norm"), (300, "none")])
+def test_both_schedules_continue_to_the_same_bits(D, gate):
+    """One long sequence of few channels takes the three steps, short ones the one pass; continued from caches that stand
+    inside chunks, with sequences that bring no token, both equal one prefill."""
+    lens, cut = [6000 * (1 if D == 300 else 2), 45, 100, 32], [17, 45, 64, 32]
+    p = make(lens, D, "bf16", "bf16", gate, seed=60, resets=True)
+    d, cu = dev(p), p["cu"].tolist()
+    n, (o, hT) = kernels(lambda: prefill(p))
+    assert n["k_lru_fold"] == n["k_lru_chain"] == n["k_lru_apply"] == 1 and n["k_lru_fwd"] == 0
+    rows = lambda a, b: torch.cat([torch.arange(cu[i] + a[i], cu[i] + b[i]) for i in range(4)]).cuda()  # noqa: E731
+    count = lambda a, b: torch.tensor([0] + list(np.cumsum([j - i for i, j in zip(a, b)])), dtype=torch.int32)  # noqa: E731
+    cache, r = B.LruCache(D, 4, "cuda"), rows([0] * 4, cut)
+    n, (first, _) = kernels(lambda: B.gdn_lru_prefill(p["shape"], d["x"][r], d["g"][r], count([0] * 4, cut).cuda(), h0=d["h0"],
+                                                      cache=cache))
+    assert n["k_lru_fwd"] == 1 and n["k_lru_fold"] == 0 and same(first, o[r])
+    r = rows(cut, lens)
+    n, (rest, last) = kernels(lambda: B.gdn_lru_prefill_continue(p["shape"], d["x"][r], d["g"][r], count(cut, lens).cuda(), cache))
+    assert n["k_lru_fold"] == 1 and same(rest, o[r])
+    full = B.LruCache(D, 4, "cuda")
+    prefill(p, cache=full)
+    for a, b in zip(cache.tensors(), full.tensors()):
+        assert torch.equal(a.view(torch.int32), b.view(torch.int32))
+    assert same(last[0], hT[0]) and same(last[1], cache.state()[1])
+    # the same long sequence next to as many others as let the one pass have it
+    many = make(lens[:1] * 40, 300, "bf16", "bf16", gate, seed=61)
+    if D == 300:
+        many["x"][:6000], many["g"][:6000], many["h0"][0] = p["x"][:6000], p["g"][:6000], p["h0"][0]
+        n, (om, hm) = kernels(lambda: prefill(many))
+        assert n["k_lru_fwd"] == 1 and n["k_lru_fold"] == 0 and same(om[:6000], o[:6000]) and same(hm[0], hT[0])
 
 
 def test_batch_composition_does_not_change_bits():
@@ -299,9 +343,10 @@ def test_null_host_copy():
     d = dev(p)
     want, _ = prefill(p)
     o = torch.empty_like(d["x"])
+    ws = torch.empty(B.lru_workspace_bytes(p["shape"], 2, 53, B.OP_PREFILL), dtype=torch.uint8, device="cuda")
     st = B.lib().gdn_lru_prefill(ctypes.byref(p["shape"]), 2, d["cu"].data_ptr(), None, d["x"].data_ptr(), 0,
                                  d["g"].data_ptr(), 0, d["h0"].data_ptr(), o.data_ptr(), 0, None, None,
-                                 torch.cuda.current_stream().cuda_stream)
+                                 ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
     assert st == B.GDN_OK and same(o, want)
 
 

@@ -24,10 +24,11 @@ def lru_shape(**kw):
     return B.LruShape(*[base[k] for k in ("D", "in_dtype", "g_dtype", "gate")])
 
 
-def lru_prefill(s, cu, x=P, ldx=0, g=P, ldg=0, h0=None, o=P, ldo=0, hT=None, cache=None, cu_dev=P):
+def lru_prefill(s, cu, x=P, ldx=0, g=P, ldg=0, h0=None, o=P, ldo=0, hT=None, cache=None, cu_dev=P, ws=P,
+                ws_bytes=1 << 40):
     host = (ctypes.c_int32 * len(cu))(*cu)
     return B.lib().gdn_lru_prefill(ctypes.byref(s), len(cu) - 1, cu_dev, host, x, ldx, g, ldg, h0, o, ldo, hT,
-                                   cache, None)
+                                   cache, ws, ws_bytes, None)
 
 
 @pytest.mark.parametrize("kw,want", [
@@ -46,7 +47,7 @@ def test_lru_shape_claims(kw, want):
     assert L.gdn_lru_decode_step(ctypes.byref(s), 1, P, 0, P, 0, ctypes.byref(cache), P, 0, None) == want
     assert L.gdn_lru_fwd_bwd(ctypes.byref(s), 1, P, cu, P, 0, P, 0, None, P, 0, None, P, 0, P, P, 0, P, 0, P, P,
                              1 << 40, None) == want
-    assert L.gdn_lru_workspace_bytes(ctypes.byref(s), 1, 5) == 0
+    assert L.gdn_lru_workspace_bytes(ctypes.byref(s), 1, 5, B.OP_PREFILL) == 0
 
 
 def test_lru_argument_checks():
@@ -63,12 +64,16 @@ def test_lru_argument_checks():
     assert lru_prefill(s, [0, 5], cu_dev=None) == bad
     assert lru_prefill(s, [0, 5], cache=ctypes.byref(B.LruCacheStruct(16, 16, None, 16))) == bad
     assert lru_prefill(s, [0, 5], cache=ctypes.byref(B.LruCacheStruct(16, 16, 20, 16))) == bad
+    need = L.gdn_lru_workspace_bytes(ctypes.byref(s), 1, 2049, B.OP_PREFILL)
+    assert lru_prefill(s, [0, 2049], ws=None) == B.GDN_ERR_WORKSPACE
+    assert lru_prefill(s, [0, 2049], ws_bytes=need - 1) == B.GDN_ERR_WORKSPACE
+    assert lru_prefill(s, [0, 5], ws=ODD) == bad
     assert lru_prefill(s, [0]) == B.GDN_OK                # no sequence, nothing to do
     cache = B.LruCacheStruct(16, 16, 16, 16)
     cb = ctypes.byref(cache)
     cu = (ctypes.c_int32 * 2)(0, 5)
-    assert L.gdn_lru_prefill_continue(ctypes.byref(s), 1, P, cu, P, 0, P, 0, None, P, 0, None, None) == bad
-    assert L.gdn_lru_prefill_continue(ctypes.byref(s), -1, P, cu, P, 0, P, 0, cb, P, 0, None, None) == bad
+    assert L.gdn_lru_prefill_continue(ctypes.byref(s), 1, P, cu, P, 0, P, 0, None, P, 0, None, P, 1 << 40, None) == bad
+    assert L.gdn_lru_prefill_continue(ctypes.byref(s), -1, P, cu, P, 0, P, 0, cb, P, 0, None, P, 1 << 40, None) == bad
     step = L.gdn_lru_decode_step
     assert step(ctypes.byref(s), 1, P, 0, P, 0, cb, None, 0, None) == bad
     assert step(ctypes.byref(s), 1, P, 4, P, 0, cb, P, 0, None) == bad
@@ -86,15 +91,15 @@ def test_lru_trainer_checks():
     def call(ws=P, ws_bytes=1 << 40, dO=P, dx=P, dg=P, dh0=P, lddx=0, lddo=0):
         return L.gdn_lru_fwd_bwd(ctypes.byref(s), 1, P, cu, P, 0, P, 0, None, dO, lddo, None, None, 0, None, dx, lddx,
                                  dg, 0, dh0, ws, ws_bytes, None)
-    need = L.gdn_lru_workspace_bytes(ctypes.byref(s), 1, 100)
-    assert need >= (100 // 32 + 1) * 8 * 4
+    size = lambda n, t, op=B.OP_FWD_BWD: L.gdn_lru_workspace_bytes(ctypes.byref(s), n, t, op)  # noqa: E731
+    need = size(1, 100)
+    assert need >= (100 // 32 + 2) * 8 * 4 * 3
     assert call(ws=None) == B.GDN_ERR_WORKSPACE
     assert call(ws_bytes=need - 1) == B.GDN_ERR_WORKSPACE
     for kw in (dict(dO=None), dict(dx=None), dict(dg=None), dict(dh0=None), dict(dx=ODD), dict(lddx=3), dict(lddo=-1)):
         assert call(**kw) == B.GDN_ERR_INVALID_ARG, kw
-    assert L.gdn_lru_workspace_bytes(ctypes.byref(s), -1, 5) == 0
-    assert L.gdn_lru_workspace_bytes(ctypes.byref(s), 1, -5) == 0
-    assert L.gdn_lru_workspace_bytes(ctypes.byref(s), 1, 0) > 0
+    assert size(-1, 5) == 0 and size(1, -5) == 0 and size(1, 5, B.OP_DECODE) == 0
+    assert size(1, 0) > 0 and size(3, 100) > size(1, 100)
 
 
 def qk_shape(**kw):
