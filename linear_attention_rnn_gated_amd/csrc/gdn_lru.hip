@@ -167,28 +167,44 @@ __device__ __forceinline__ void lru_empty(const LruIO& io, int64_t e) {
   }
 }
 
-// The chain over a round's m slots for one channel: start[s] = S, S = a S + b,
-// the maps eight at a time out of LDS so that their latency is paid once.
-// Where a sequence begins (begin[s]) S is the state that its lanes left in
-// start[s].
-__device__ __forceinline__ float lru_chain(const float2* agg, float* start, const int* begin, int W, int m, float S) {
-  for (int s0 = 0; s0 < m; s0 += 8) {
-    float2 ab[8];
-    float h0[8];
-    int fresh[8];
+// Marks a map (mark, S) that gives S whatever was before it: a sequence's first
+// chunk, whose lanes know their start.  (Were a chunk's own product this NaN, its
+// B would be a NaN too, which is then the state by either rule.)
+constexpr uint32_t kLruMark = 0xffc0deadu;
+
+// The chain S -> a S + b over m maps in LDS, W entries apart, for one channel;
+// put(s, S) takes the state in front of map s (none in front of a marked one).
+// U maps at a time, the next U read before the U fma's, so that a step costs its
+// fma and not a round trip to LDS.
+template <bool MARKS, int U, typename Put>
+__device__ __forceinline__ float lru_chain(const float2* agg, int W, int maps, float S, Put&& put) {
+  const int m = __builtin_amdgcn_readfirstlane(maps);  // the same for the whole block: scalar branches
+  float2 ab[U], next[U];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int s = s0 + j < m ? s0 + j : m - 1;
-      ab[j] = agg[s * W];
-      h0[j] = start[s * W];
-      fresh[j] = begin[s];
+  for (int j = 0; j < U; ++j) ab[j] = agg[(j < m ? j : m - 1) * W];
+  int s0 = 0;
+  for (; s0 + U <= m; s0 += U) {
+#pragma unroll
+    for (int j = 0; j < U; ++j) next[j] = agg[(s0 + U + j < m ? s0 + U + j : m - 1) * W];
+    float before[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      before[j] = S;
+      const float to = fmaf(ab[j].x, S, ab[j].y);
+      S = MARKS && __float_as_uint(ab[j].x) == kLruMark ? ab[j].y : to;
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (s0 + j >= m) break;
-      S = fresh[j] ? h0[j] : S;
-      start[(s0 + j) * W] = S;
-      S = fmaf(ab[j].x, S, ab[j].y);
+    for (int j = 0; j < U; ++j) {
+      if (!(MARKS && __float_as_uint(ab[j].x) == kLruMark)) put(s0 + j, before[j]);
+      ab[j] = next[j];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < U - 1; ++j) {
+    if (s0 + j < m) {
+      const bool mark = MARKS && __float_as_uint(ab[j].x) == kLruMark;
+      if (!mark) put(s0 + j, S);
+      S = mark ? ab[j].y : fmaf(ab[j].x, S, ab[j].y);
     }
   }
   return S;
@@ -198,7 +214,6 @@ template <typename TX, typename TG, int GATE>
 __global__ __launch_bounds__(kLruThreads) void k_lru_fwd(LruIO io) {
   __shared__ float2 agg[kLruThreads];  // [slot][channel of the tile]
   __shared__ float start[kLruThreads];
-  __shared__ int begin[kLruThreads / 8];
   __shared__ int64_t chunk0[kLruPack + 1];  // chunks of the unit before each of its sequences
   int unit, tile;
   if (!lru_item(io, unit, tile)) return;
@@ -258,18 +273,24 @@ __global__ __launch_bounds__(kLruThreads) void k_lru_fwd(LruIO io) {
       const TX* x = static_cast<const TX*>(io.x) + cc;
       const TG* g = static_cast<const TG*>(io.g) + cc;
       float a = 1.0f, b = 0.0f;
+      // sixteen rows' loads at a time: all of them at once spilled registers, and
+      // four waves a SIMD keep enough in flight (32 ragged x 2048: 454 -> 436 us)
       if (lo == 0 && hi == kLruC) {
 #pragma unroll
-        for (int j = 0; j < kLruC; ++j) {
-          A[j] = ldin(g + (row + j) * io.ldg);
-          B[j] = ldin(x + (row + j) * io.ldx);
-        }
+        for (int half = 0; half < kLruC; half += kLruC / 2) {
 #pragma unroll
-        for (int j = 0; j < kLruC; ++j) {
-          float al;
-          const float u = lru_input<GATE>(A[j], B[j], al);
-          A[j] = a = al * a;
-          B[j] = b = fmaf(al, b, u);
+          for (int j = half; j < half + kLruC / 2; ++j) {
+            A[j] = ldin(g + (row + j) * io.ldg);
+            B[j] = ldin(x + (row + j) * io.ldx);
+          }
+#pragma unroll
+          for (int j = half; j < half + kLruC / 2; ++j) {
+            float al;
+            const float u = lru_input<GATE>(A[j], B[j], al);
+            A[j] = a = al * a;
+            B[j] = b = fmaf(al, b, u);
+          }
+          __builtin_amdgcn_sched_barrier(0);
         }
       } else {
         if (lo > 0) {
@@ -277,31 +298,39 @@ __global__ __launch_bounds__(kLruThreads) void k_lru_fwd(LruIO io) {
           b = io.cache.B[sn + cc];
         }
 #pragma unroll
-        for (int j = 0; j < kLruC; ++j) {
-          const int64_t t = row + (j < lo ? lo : (j >= hi ? hi - 1 : j));  // a row of this chunk
-          A[j] = ldin(g + t * io.ldg);
-          B[j] = ldin(x + t * io.ldx);
-        }
+        for (int half = 0; half < kLruC; half += kLruC / 2) {
 #pragma unroll
-        for (int j = 0; j < kLruC; ++j) {
-          float al;
-          float u = lru_input<GATE>(A[j], B[j], al);
-          // places outside the rows change nothing: 1 a = a, fma(1, b, -0) = b
-          const bool in = j >= lo && j < hi;
-          al = in ? al : 1.0f;
-          u = in ? u : -0.0f;
-          A[j] = a = al * a;
-          B[j] = b = fmaf(al, b, u);
+          for (int j = half; j < half + kLruC / 2; ++j) {
+            const int64_t t = row + (j < lo ? lo : (j >= hi ? hi - 1 : j));  // a row of this chunk
+            A[j] = ldin(g + t * io.ldg);
+            B[j] = ldin(x + t * io.ldx);
+          }
+#pragma unroll
+          for (int j = half; j < half + kLruC / 2; ++j) {
+            float al;
+            float u = lru_input<GATE>(A[j], B[j], al);
+            // places outside the rows change nothing: 1 a = a, fma(1, b, -0) = b
+            const bool in = j >= lo && j < hi;
+            al = in ? al : 1.0f;
+            u = in ? u : -0.0f;
+            A[j] = a = al * a;
+            B[j] = b = fmaf(al, b, u);
+          }
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
-      agg[threadIdx.x] = float2{a, b};
-      if (ch == 0) start[threadIdx.x] = io.resume ? io.cache.S[sn + cc] : (io.h0 ? io.h0[sn + cc] : 0.0f);
-      if (static_cast<int>(threadIdx.x) == slot * W) begin[slot] = ch == 0;
+      if (ch == 0) {
+        const float S0 = io.resume ? io.cache.S[sn + cc] : (io.h0 ? io.h0[sn + cc] : 0.0f);
+        start[threadIdx.x] = S0;
+        agg[threadIdx.x] = float2{__uint_as_float(kLruMark), fmaf(a, S0, b)};
+      } else {
+        agg[threadIdx.x] = float2{a, b};
+      }
     }
     __syncthreads();
     if (folds)
-      S = lru_chain(agg + threadIdx.x, start + threadIdx.x, begin, W,
-                    static_cast<int>(nch - cb < slots ? nch - cb : slots), S);
+      S = lru_chain<true, 4>(agg + threadIdx.x, W, static_cast<int>(nch - cb < slots ? nch - cb : slots), S,
+                          [&](int s, float v) { start[s * W + threadIdx.x] = v; });
     __syncthreads();
     if (has && live) {
       const float st = start[threadIdx.x];
@@ -492,7 +521,7 @@ __global__ __launch_bounds__(256) void k_lru_fold(LruIO io) {
 // chunks' starts), backward (grid.y = 1) K -> A K + Q (wQ then holds the
 // gradients of the states behind the chunks' ends).  Also what a sequence ends
 // with: hT, the cache, dh0.
-constexpr int kChainW = 32, kChainRows = 256;
+constexpr int kChainW = 32, kChainRows = 128;
 __global__ __launch_bounds__(256) void k_lru_chain(LruIO io) {
   __shared__ float2 agg[kChainRows * kChainW];
   const int tiles = (io.D + kChainW - 1) / kChainW;
@@ -513,43 +542,47 @@ __global__ __launch_bounds__(256) void k_lru_chain(LruIO io) {
   const bool folds = row == 0 && live;
   if (folds) S = up ? (io.resume ? io.cache.S[sn + c] : (io.h0 ? io.h0[sn + c] : 0.0f)) : (io.dhT ? io.dhT[sn + c] : 0.0f);
   float before = S;  // the state at the start of the last chunk
-  for (int64_t r0 = 0; r0 < nch; r0 += kChainRows) {
-    const int m = static_cast<int>(nch - r0 < kChainRows ? nch - r0 : kChainRows);
-    // rows in the chain's order: from the first chunk up, or from the last down
-    if (live) {
-#pragma unroll 8
-      for (int r = row; r < m; r += 256 / kChainW) {
-        const int64_t at = base + (up ? r0 + r : nch - 1 - r0 - r) * io.D;
-        agg[r * kChainW + col] = float2{io.wA[at], w[at]};
+  constexpr int kRowsStep = 256 / kChainW, kPer = kChainRows / kRowsStep;
+  float2 in[kPer];
+  // rows in the chain's order: from the first chunk up, or from the last down
+  auto load = [&](int64_t r0) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int64_t r = r0 + row + i * kRowsStep;
+      if (live && r < nch) {
+        const int64_t at = base + (up ? r : nch - 1 - r) * io.D;
+        in[i] = float2{io.wA[at], w[at]};
       }
     }
-    __syncthreads();
-    if (folds) {
-      for (int s0 = 0; s0 < m; s0 += 8) {
-        float2 ab[8];
+  };
+  load(0);
+  for (int64_t r0 = 0; r0 < nch; r0 += kChainRows) {
+    const int m = static_cast<int>(nch - r0 < kChainRows ? nch - r0 : kChainRows);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ab[j] = agg[(s0 + j < m ? s0 + j : m - 1) * kChainW + col];
+    for (int i = 0; i < kPer; ++i) agg[(row + i * kRowsStep) * kChainW + col] = in[i];
+    if (up && live && r0 + m == nch && io.cache.S) {
+      // the last chunk as the cache keeps it
+      const bool full = (p0 + L) % kLruC == 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (s0 + j >= m) break;
-          agg[(s0 + j) * kChainW + col].x = S;
-          before = S;
-          S = fmaf(ab[j].x, S, ab[j].y);
+      for (int i = 0; i < kPer; ++i) {
+        if (row + i * kRowsStep == m - 1) {
+          io.cache.A[sn + c] = full ? 1.0f : in[i].x;
+          io.cache.B[sn + c] = full ? 0.0f : in[i].y;
         }
       }
     }
     __syncthreads();
-    if (live) {
-      if (up && r0 + m == nch && io.cache.S && row == (m - 1) % (256 / kChainW)) {
-        // the last chunk as the cache keeps it; wB's own thread, before it is overwritten
-        const int64_t at = base + (nch - 1) * io.D;
-        const bool full = (p0 + L) % kLruC == 0;
-        io.cache.A[sn + c] = full ? 1.0f : io.wA[at];
-        io.cache.B[sn + c] = full ? 0.0f : io.wB[at];
-      }
-#pragma unroll 8
-      for (int r = row; r < m; r += 256 / kChainW)
-        w[base + (up ? r0 + r : nch - 1 - r0 - r) * io.D] = agg[r * kChainW + col].x;
+    load(r0 + kChainRows);  // in flight beside the chain
+    if (folds)
+      S = lru_chain<false, 8>(agg + col, kChainW, m, S, [&](int s, float v) {
+        agg[s * kChainW + col].x = v;
+        before = v;
+      });
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int64_t r = r0 + row + i * kRowsStep;
+      if (live && r < nch) w[base + (up ? r : nch - 1 - r) * io.D] = agg[(row + i * kRowsStep) * kChainW + col].x;
     }
     __syncthreads();
   }

@@ -160,6 +160,8 @@ int check_qk_shape(const gdn_qk_shape_t* s) {
 int64_t qk_bwd_blocks(const gdn_qk_shape_t* s, int64_t T) {
   (void)s;
   const int64_t b = (T + 3) / 4;  // a wave takes one token at a time, a block has four
+  // as many as are resident at once, so that each block writes its sums once
+  // (trainer 8x4096, 32 heads: 165 us; 768 blocks 170, 2048 169, 512 213)
   return b < 1024 ? b : 1024;
 }
 
