@@ -3,7 +3,6 @@
 // timing of the first.
 #include "gdn_kernels.hip"
 
-#include <cmath>
 #include <new>
 
 #include "gdn_lru.hip"

@@ -27,8 +27,8 @@
 namespace {
 
 constexpr int kLruC = GDN_LRU_CHUNK;
-constexpr int kLruPack = 64;     // most sequences that the host packs into units
-constexpr int kLruThreads = 1024;  // most threads of a scan block
+constexpr int kLruPack = gdn::kLruPack;
+constexpr int kLruThreads = gdn::kLruThreads; 
 
 struct LruIO {
   const void* x;
@@ -42,12 +42,8 @@ struct LruIO {
   int N, D, gate;
   int64_t T, ldx, ldg, ldo;
   // one pass
-  int lps;    // lanes per chunk = channels of a block's tile
+  gdn::LruPlan plan;
   int tiles;  // channel tiles
-  int units;  // sequences or, packed, groups of sequences that a block takes
-  int packed; // 1: unit u is the sequences seq[first[u]] .. seq[first[u + 1] - 1]
-  uint8_t seq[kLruPack];
-  uint8_t first[kLruPack + 1];
   // three steps
   int cw;        // lanes of a block over channels; 256 / cw chunks a block
   int64_t slots; // chunk slots
@@ -145,7 +141,7 @@ __device__ __forceinline__ bool lru_item(const LruIO& io, int& unit, int& tile) 
   const int64_t u = group / gpu;
   tile = static_cast<int>(group - u * gpu) * 4 + static_cast<int>(j & 3);
   unit = static_cast<int>(u);
-  return u < io.units && tile < io.tiles;
+  return u < io.plan.units && tile < io.tiles;
 }
 int64_t lru_blocks(int64_t units, int tiles) {
   const int64_t groups = units * ((tiles + 3) / 4);
@@ -217,19 +213,19 @@ __global__ __launch_bounds__(kLruThreads) void k_lru_fwd(LruIO io) {
   __shared__ int64_t chunk0[kLruPack + 1];  // chunks of the unit before each of its sequences
   int unit, tile;
   if (!lru_item(io, unit, tile)) return;
-  const int W = io.lps;
+  const int W = io.plan.lps;
   const int slots = blockDim.x / W;
   const int slot = threadIdx.x / W;
   const int c = tile * W + static_cast<int>(threadIdx.x) - slot * W;
   const bool live = c < io.D;
   const int cc = live ? c : io.D - 1;
   const bool folds = slot == 0 && live;  // these threads hold the chain of one channel each
-  const int i0 = io.packed ? io.first[unit] : 0;
-  const int count = io.packed ? io.first[unit + 1] - i0 : 1;
+  const int i0 = io.plan.packed ? io.plan.first[unit] : 0;
+  const int count = io.plan.packed ? io.plan.first[unit + 1] - i0 : 1;
   if (threadIdx.x < 64) {
     int64_t t0, L = 0, chunks = 0;
     if (static_cast<int>(threadIdx.x) < count) {
-      const int n = io.packed ? io.seq[i0 + threadIdx.x] : unit;
+      const int n = io.plan.packed ? io.plan.seq[i0 + threadIdx.x] : unit;
       lru_rows(io, n, t0, L);
       if (L > 0) chunks = ((io.resume ? lru_pos(io, n, 0) : 0) + L + kLruC - 1) / kLruC;
     }
@@ -246,7 +242,7 @@ __global__ __launch_bounds__(kLruThreads) void k_lru_fwd(LruIO io) {
   if (folds) {
     for (int i = 0; i < count; ++i)
       if (chunk0[i + 1] == chunk0[i])
-        lru_empty(io, static_cast<int64_t>(io.packed ? io.seq[i0 + i] : unit) * io.D + c);
+        lru_empty(io, static_cast<int64_t>(io.plan.packed ? io.plan.seq[i0 + i] : unit) * io.D + c);
   }
   const int64_t nch = chunk0[count];
   float S = 0.0f;
@@ -260,7 +256,7 @@ __global__ __launch_bounds__(kLruThreads) void k_lru_fwd(LruIO io) {
       int i = 0;
       for (int d = kLruPack / 2; d >= 1; d >>= 1)  // the last sequence that begins at or before the slot's chunk
         if (i + d < count && chunk0[i + d] <= cb + slot) i += d;
-      const int n = io.packed ? io.seq[i0 + i] : unit;
+      const int n = io.plan.packed ? io.plan.seq[i0 + i] : unit;
       int64_t t0, L;
       lru_rows(io, n, t0, L);
       sn = static_cast<int64_t>(n) * io.D;
@@ -516,24 +512,25 @@ __global__ __launch_bounds__(256) void k_lru_fold(LruIO io) {
     lru_fold<TX, TG, GATE, GRAD, false>(io, k, slot, c);
 }
 
-// The chains over a sequence's chunks, 32 channels a block, up to 256 chunks at
+// The chains over a sequence's chunks, up to ROWS chunks of W channels a block at
 // a time through LDS: forward S -> A S + B (wB then holds the states at the
-// chunks' starts), backward (grid.y = 1) K -> A K + Q (wQ then holds the
-// gradients of the states behind the chunks' ends).  Also what a sequence ends
-// with: hT, the cache, dh0.
-constexpr int kChainW = 32, kChainRows = 128;
+// chunks' starts), backward (grid.y = 1) K -> A K + Q (wQ then holds the gradients
+// of the states behind the chunks' ends).  Also what a sequence ends with: hT,
+// the cache, dh0.  Bound by latency: a round is a trip to memory and back, and
+// ROWS dependent fma's.
+template <int W, int ROWS>
 __global__ __launch_bounds__(256) void k_lru_chain(LruIO io) {
-  __shared__ float2 agg[kChainRows * kChainW];
-  const int tiles = (io.D + kChainW - 1) / kChainW;
+  __shared__ float2 agg[ROWS * W];
+  const int tiles = (io.D + W - 1) / W;
   const int n = blockIdx.x / tiles;
-  const int c0 = (blockIdx.x % tiles) * kChainW;
+  const int c0 = (blockIdx.x % tiles) * W;
   int64_t t0, L;
   lru_rows(io, n, t0, L);
   const int64_t sn = static_cast<int64_t>(n) * io.D;
   const bool up = blockIdx.y == 0;
   const int p0 = io.resume ? lru_pos(io, n, c0) : 0;
   const int64_t nch = L > 0 ? (p0 + L + kLruC - 1) / kLruC : 0;
-  const int col = threadIdx.x & (kChainW - 1), row = threadIdx.x / kChainW;
+  const int col = threadIdx.x & (W - 1), row = threadIdx.x / W;
   const int c = c0 + col;
   const bool live = c < io.D;
   const int64_t base = lru_slot0(io, n) * io.D + c;
@@ -542,7 +539,7 @@ __global__ __launch_bounds__(256) void k_lru_chain(LruIO io) {
   const bool folds = row == 0 && live;
   if (folds) S = up ? (io.resume ? io.cache.S[sn + c] : (io.h0 ? io.h0[sn + c] : 0.0f)) : (io.dhT ? io.dhT[sn + c] : 0.0f);
   float before = S;  // the state at the start of the last chunk
-  constexpr int kRowsStep = 256 / kChainW, kPer = kChainRows / kRowsStep;
+  constexpr int kRowsStep = 256 / W, kPer = ROWS / kRowsStep;
   float2 in[kPer];
   // rows in the chain's order: from the first chunk up, or from the last down
   auto load = [&](int64_t r0) {
@@ -556,10 +553,10 @@ __global__ __launch_bounds__(256) void k_lru_chain(LruIO io) {
     }
   };
   load(0);
-  for (int64_t r0 = 0; r0 < nch; r0 += kChainRows) {
-    const int m = static_cast<int>(nch - r0 < kChainRows ? nch - r0 : kChainRows);
+  for (int64_t r0 = 0; r0 < nch; r0 += ROWS) {
+    const int m = static_cast<int>(nch - r0 < ROWS ? nch - r0 : ROWS);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) agg[(row + i * kRowsStep) * kChainW + col] = in[i];
+    for (int i = 0; i < kPer; ++i) agg[(row + i * kRowsStep) * W + col] = in[i];
     if (up && live && r0 + m == nch && io.cache.S) {
       // the last chunk as the cache keeps it
       const bool full = (p0 + L) % kLruC == 0;
@@ -572,17 +569,17 @@ __global__ __launch_bounds__(256) void k_lru_chain(LruIO io) {
       }
     }
     __syncthreads();
-    load(r0 + kChainRows);  // in flight beside the chain
+    load(r0 + ROWS);  // in flight beside the chain
     if (folds)
-      S = lru_chain<false, 8>(agg + col, kChainW, m, S, [&](int s, float v) {
-        agg[s * kChainW + col].x = v;
+      S = lru_chain<false, 8>(agg + col, W, m, S, [&](int s, float v) {
+        agg[s * W + col].x = v;
         before = v;
       });
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int64_t r = r0 + row + i * kRowsStep;
-      if (live && r < nch) w[base + (up ? r : nch - 1 - r) * io.D] = agg[(row + i * kRowsStep) * kChainW + col].x;
+      if (live && r < nch) w[base + (up ? r : nch - 1 - r) * io.D] = agg[(row + i * kRowsStep) * W + col].x;
     }
     __syncthreads();
   }
@@ -717,104 +714,6 @@ int lru_dispatch(const gdn_lru_shape_t* s, F&& f) {
   return s->g_dtype == GDN_BF16 ? lru_dispatch_gate<float, bf16_t>(s, f) : lru_dispatch_gate<float, float>(s, f);
 }
 
-// The one pass's tile, threads and units.
-//
-// A block goes over its unit in rounds of threads / tile chunks, one block of
-// 1024 threads a CU, so a pass takes the larger of the longest unit's rounds
-// and the rounds of all units and tiles over 256 CUs, times a round's time.
-// That one is longer with narrow tiles, whose rows are 16- or 32-byte pieces of
-// a cache line, so that L2's request rate bounds them; measured with all CUs at
-// work (bf16 x, fp32 g, norm gate): 33, 20, 16 and 13.5 us a round at tiles of 8,
-// 16, 32 and 64 channels.  The tile with the least time is taken.
-//
-// Up to kLruPack sequences are packed: those shorter than a round share units
-// of up to a round (first fit, longest first), and the longest units begin
-// first.  More sequences are units of their own.
-//
-// Blocks of 512 threads, two a CU, where all tiles and units keep them busy: one
-// block's loads then overlap the other's chain (16 x 2048 tokens x 2048 channels:
-// 119 us against 125; with half as many blocks 122 against 108 us).
-struct LruTiling {
-  int lps = 64, threads = 1024;
-  double us = 0;  // expected
-};
-LruTiling lru_tiling(const LruIO& io, const int32_t* cu_host, int64_t longest) {
-  static constexpr int kTile[4] = {64, 32, 16, 8};
-  static constexpr double kRound[4] = {13.5, 16.0, 20.0, 33.0};
-  LruTiling best;
-  for (int k = 0; k < 4; ++k) {
-    const int l = kTile[k];
-    const int64_t round = static_cast<int64_t>(kLruThreads) / l * kLruC;
-    double rounds = 0;
-    if (io.N <= kLruPack) {
-      int64_t shorts = 0;
-      for (int32_t n = 0; n < io.N; ++n) {
-        const int64_t len = static_cast<int64_t>(cu_host[n + 1]) - cu_host[n];
-        if (len >= round) rounds += static_cast<double>((len + round - 1) / round);
-        else shorts += len;
-      }
-      rounds += static_cast<double>((shorts + round - 1) / round);
-    } else {
-      rounds = static_cast<double>(io.T / round + io.N);
-    }
-    const double all = std::ceil(rounds * ((io.D + l - 1) / l) / 256.0);
-    const double one = static_cast<double>((longest + round - 1) / round);
-    const double us = (all > one ? all : one) * kRound[k];
-    if (best.us == 0 || us < best.us) {
-      best.us = us;
-      best.lps = l;
-    }
-  }
-  const int64_t blocks = longest > 0 ? io.T * ((io.D + 63) / 64) / longest : 0;
-  const int64_t most = blocks >= 400 ? 512 : kLruThreads;
-  const int64_t t = ((longest / kLruC + 2) * best.lps + 63) / 64 * 64;
-  best.threads = static_cast<int>(t < most ? t : most);
-  return best;
-}
-
-// Packs the sequences into units of at most a round.
-void lru_pack(LruIO* io, const int32_t* cu_host, int threads) {
-  io->units = io->N;
-  io->packed = 0;
-  if (io->N > kLruPack) return;
-  const int64_t round = static_cast<int64_t>(threads) / io->lps * kLruC;
-  const int N = io->N;
-  int order[kLruPack], unit[kLruPack], units = 0;
-  int64_t len[kLruPack], sum[kLruPack];
-  for (int n = 0; n < N; ++n) {
-    len[n] = static_cast<int64_t>(cu_host[n + 1]) - cu_host[n];
-    int at = n;
-    for (; at > 0 && len[order[at - 1]] < len[n]; --at) order[at] = order[at - 1];
-    order[at] = n;
-  }
-  for (int i = 0; i < N; ++i) {
-    const int n = order[i];
-    // a chunk more for the places before a resumed sequence's first token
-    const int64_t need = (len[n] + (io->resume ? 2 * kLruC - 1 : kLruC - 1)) / kLruC * kLruC;
-    int u = 0;
-    while (u < units && sum[u] + need > round) ++u;
-    if (u == units) sum[units++] = 0;
-    sum[u] += need;
-    unit[i] = u;
-  }
-  int at = 0;
-  for (int u = 0; u < units; ++u) {
-    io->first[u] = static_cast<uint8_t>(at);
-    for (int i = 0; i < N; ++i)
-      if (unit[i] == u) io->seq[at++] = static_cast<uint8_t>(order[i]);
-  }
-  io->first[units] = static_cast<uint8_t>(at);
-  io->units = units;
-  io->packed = 1;
-}
-
-// Whether a prefill takes the three steps instead of the one pass's expected
-// `us`: they read the inputs twice, 3 us per million elements, and take some 8 us
-// for two launches and the chain.
-bool lru_three(const LruIO& io, double us) {
-  return io.T > GDN_LRU_SMALL && 8.0 + 3e-6 * static_cast<double>(io.T) * io.D < us;
-}
-
 // Checks and resolves what the packed calls share.
 int lru_common(const gdn_lru_shape_t* shape, int32_t n_seqs, const int32_t* cu_dev, const int32_t** cu_host,
                std::vector<int32_t>& buf, hipStream_t st, LruIO* io, int64_t* longest) {
@@ -863,7 +762,26 @@ int64_t lru_units(LruIO* io) {
   const int64_t per = 256 / io->cw, groups = (io->D + io->cw - 1) / io->cw;
   return (io->slots + per - 1) / per * groups;
 }
-int64_t lru_chain_blocks(const LruIO& io) { return io.N * static_cast<int64_t>((io.D + kChainW - 1) / kChainW); }
+// The chain's launch: rounds of 128 chunks x 32 channels in 32 KB of LDS, five
+// blocks a CU, or, for longer sequences in no more blocks than CUs, where each
+// round's latency is what counts, of 512 chunks x 16 channels (whole prefills, us:
+// 12 sequences to 14162 tokens x 200 channels 41 against 45, 16 to 14617 x 109 33
+// against 38; but 15 to 4475 x 972 in 915 blocks 58 against 52).
+int64_t lru_chain_blocks(const LruIO& io, bool deep) {
+  const int w = deep ? 16 : 32;
+  return io.N * static_cast<int64_t>((io.D + w - 1) / w);
+}
+bool lru_deep(const LruIO& io, int64_t longest) {
+  return longest > 128 * kLruC && lru_chain_blocks(io, true) <= 256;
+}
+void lru_launch_chain(const LruIO& io, bool deep, int directions, hipStream_t st) {
+  const dim3 grid(static_cast<unsigned>(lru_chain_blocks(io, deep)), directions);
+  Timed t_("k_lru_chain", st);
+  if (deep)
+    hipLaunchKernelGGL((k_lru_chain<16, 512>), grid, dim3(256), 0, st, io);
+  else
+    hipLaunchKernelGGL((k_lru_chain<32, 128>), grid, dim3(256), 0, st, io);
+}
 // A launch holds fewer than 2^32 threads.
 bool lru_fits(int64_t threads) { return threads < (int64_t{1} << 32); }
 
@@ -884,26 +802,22 @@ int lru_prefill_entry(const gdn_lru_shape_t* shape, int32_t n_seqs, const int32_
   if (io.ldx < 0 || io.ldg < 0 || io.ldo < 0) return GDN_ERR_INVALID_ARG;
   if ((rc = lru_common(shape, n_seqs, cu_dev, &cu_host, buf, st, &io, &longest)) != GDN_OK) return rc;
   if (io.T > 0 && (!x || !g || !o)) return GDN_ERR_INVALID_ARG;
-  const bool small = io.T <= GDN_LRU_SMALL;
-  if (!small && (!ws || ws_bytes < lru_ws_bytes(shape->D, n_seqs, io.T, false))) return GDN_ERR_WORKSPACE;
+  if (io.T > GDN_LRU_SMALL && (!ws || ws_bytes < lru_ws_bytes(shape->D, n_seqs, io.T, false))) return GDN_ERR_WORKSPACE;
   if (n_seqs == 0) return GDN_OK;
   io.x = x; io.g = g; io.h0 = h0; io.o = o; io.hT = hT; io.resume = resume;
   if (cache) io.cache = *cache;
-  const LruTiling tiling = lru_tiling(io, cu_host, longest);
-  const bool three = lru_three(io, tiling.us);
+  const bool three = gdn::lru_plan(cu_host, n_seqs, io.D, longest, resume, &io.plan);
   int threads = 256;
   int64_t blocks;
   if (three) {
     lru_ws(&io, ws, false);
     blocks = lru_units(&io);
   } else {
-    threads = tiling.threads;
-    io.lps = tiling.lps;
-    io.tiles = (io.D + io.lps - 1) / io.lps;
-    lru_pack(&io, cu_host, threads);
-    blocks = lru_blocks(io.units, io.tiles);
+    threads = io.plan.threads;
+    io.tiles = (io.D + io.plan.lps - 1) / io.plan.lps;
+    blocks = lru_blocks(io.plan.units, io.tiles);
   }
-  if (!lru_fits(blocks * threads) || (three && !lru_fits(lru_chain_blocks(io) * 256))) return GDN_ERR_UNSUPPORTED;
+  if (!lru_fits(blocks * threads) || (three && !lru_fits(lru_chain_blocks(io, true) * 256))) return GDN_ERR_UNSUPPORTED;
   lru_dispatch(shape, [&]<typename TX, typename TG, int GATE>() {
     const dim3 grid(static_cast<unsigned>(blocks)), block(threads);
     if (!three) {
@@ -915,10 +829,7 @@ int lru_prefill_entry(const gdn_lru_shape_t* shape, int32_t n_seqs, const int32_
       Timed t_("k_lru_fold", st);
       hipLaunchKernelGGL((k_lru_fold<TX, TG, GATE, false>), grid, block, 0, st, io);
     }
-    {
-      Timed t_("k_lru_chain", st);
-      hipLaunchKernelGGL(k_lru_chain, dim3(static_cast<unsigned>(lru_chain_blocks(io))), block, 0, st, io);
-    }
+    lru_launch_chain(io, lru_deep(io, longest), 1, st);
     Timed t_("k_lru_apply", st);
     hipLaunchKernelGGL((k_lru_apply<TX, TG, GATE>), grid, block, 0, st, io);
     return GDN_OK;
@@ -1025,17 +936,14 @@ int gdn_lru_fwd_bwd(const gdn_lru_shape_t* shape, int32_t n_seqs, const int32_t*
   io.x = x; io.g = g; io.h0 = h0; io.dO = dO; io.dhT = dhT; io.o = o; io.hT = hT; io.dx = dx; io.dg = dg; io.dh0 = dh0;
   lru_ws(&io, ws, true);
   const int64_t blocks = lru_units(&io);
-  if (!lru_fits(blocks * 256) || !lru_fits(2 * lru_chain_blocks(io) * 256)) return GDN_ERR_UNSUPPORTED;
+  if (!lru_fits(blocks * 256) || !lru_fits(2 * lru_chain_blocks(io, true) * 256)) return GDN_ERR_UNSUPPORTED;
   return lru_dispatch(shape, [&]<typename TX, typename TG, int GATE>() {
     const dim3 grid(static_cast<unsigned>(blocks)), block(256);
     {
       Timed t_("k_lru_fold", st);
       hipLaunchKernelGGL((k_lru_fold<TX, TG, GATE, true>), grid, block, 0, st, io);
     }
-    {
-      Timed t_("k_lru_chain", st);
-      hipLaunchKernelGGL(k_lru_chain, dim3(static_cast<unsigned>(lru_chain_blocks(io)), 2), block, 0, st, io);
-    }
+    lru_launch_chain(io, lru_deep(io, longest), 2, st);
     Timed t_("k_lru_grad", st);
     hipLaunchKernelGGL((k_lru_grad<TX, TG, GATE>), grid, block, 0, st, io);
     return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_HIP;

@@ -143,6 +143,111 @@ int64_t row_stride(int64_t ld, int64_t row) {
   return ld >= row && ld <= (int64_t{1} << 40) ? ld : -1;
 }
 
+// The one pass's tile, threads and units.
+//
+// A block goes over its unit in rounds of threads / tile chunks, one block of
+// 1024 threads a CU, so a pass takes the larger of the longest unit's rounds
+// and the rounds of all units and tiles over 256 CUs, times a round's time.
+// That one is longer with narrow tiles, whose rows are 16- or 32-byte pieces of
+// a cache line, so that L2's request rate bounds them; measured (bf16 x, fp32 g,
+// norm gate) at tiles of 8, 16, 32 and 64 channels: 33, 20, 16 and 13.5 us a round
+// with all CUs at work, 27, 16.5, 12 and 10.5 with a part of them.  The tile with
+// the least time is taken.
+//
+// Up to kLruPack sequences are packed: those shorter than a round share units
+// of up to a round (first fit, longest first), and the longest units begin
+// first (19 sequences of 1 to 1508 tokens x 3447 channels: 40 us, unpacked 75;
+// 32 of 128 to 8192 x 2048: 448 us, unpacked 504).  More sequences are units of
+// their own.
+//
+// Blocks of 512 threads, two a CU, where all tiles and units keep them busy: one
+// block's loads then overlap the other's chain (16 x 2048 tokens x 2048 channels:
+// 119 us against 125; with half as many blocks 122 against 108 us).
+static void lru_tile(const int32_t* cu, int32_t N, int64_t T, int32_t D, int64_t longest, LruPlan* plan, double* us) {
+  static constexpr int kTile[4] = {64, 32, 16, 8};
+  static constexpr double kRound[4] = {13.5, 16.0, 20.0, 33.0}, kAlone[4] = {10.5, 12.0, 16.5, 27.0};
+  *us = 0;
+  for (int k = 0; k < 4; ++k) {
+    const int l = kTile[k];
+    const int64_t round = static_cast<int64_t>(kLruThreads) / l * GDN_LRU_CHUNK;
+    double rounds = 0;
+    if (N <= kLruPack) {
+      int64_t shorts = 0;
+      for (int32_t n = 0; n < N; ++n) {
+        const int64_t len = static_cast<int64_t>(cu[n + 1]) - cu[n];
+        if (len >= round)
+          rounds += static_cast<double>((len + round - 1) / round);
+        else
+          shorts += len;
+      }
+      rounds += static_cast<double>((shorts + round - 1) / round);
+    } else {
+      rounds = static_cast<double>(T / round + N);
+    }
+    const double share = rounds * ((D + l - 1) / l) / 256.0;
+    const double all = (share > 1.0 ? std::ceil(share) : share) * kRound[k];
+    const double one = static_cast<double>((longest + round - 1) / round) * kAlone[k];
+    const double t = all > one ? all : one;
+    if (k == 0 || t < *us) {
+      *us = t;
+      plan->lps = l;
+    }
+  }
+  const int64_t blocks = longest > 0 ? T * ((D + 63) / 64) / longest : 0;
+  const int64_t most = blocks >= 400 ? 512 : kLruThreads;
+  const int64_t t = ((longest / GDN_LRU_CHUNK + 2) * plan->lps + 63) / 64 * 64;
+  plan->threads = static_cast<int32_t>(t < most ? t : most);
+}
+
+static void lru_pack(const int32_t* cu, int32_t N, bool resume, LruPlan* plan) {
+  plan->units = N;
+  plan->packed = 0;
+  if (N > kLruPack) return;
+  const int64_t round = static_cast<int64_t>(plan->threads) / plan->lps * GDN_LRU_CHUNK;
+  int order[kLruPack], unit[kLruPack], units = 0;
+  int64_t len[kLruPack], sum[kLruPack];
+  for (int n = 0; n < N; ++n) {
+    len[n] = static_cast<int64_t>(cu[n + 1]) - cu[n];
+    int at = n;
+    for (; at > 0 && len[order[at - 1]] < len[n]; --at) order[at] = order[at - 1];
+    order[at] = n;
+  }
+  int size[kLruPack] = {};  // sequences of each unit
+  for (int i = 0; i < N; ++i) {
+    // whole chunks, one more for the places before a resumed sequence's first token
+    const int64_t need = (len[order[i]] + (resume ? 2 : 1) * GDN_LRU_CHUNK - 1) / GDN_LRU_CHUNK * GDN_LRU_CHUNK;
+    int u = 0;
+    while (u < units && sum[u] + need > round) ++u;
+    if (u == units) sum[units++] = 0;
+    sum[u] += need;
+    ++size[u];
+    unit[i] = u;
+  }
+  int at = 0, next[kLruPack];
+  for (int u = 0; u < units; ++u) {
+    plan->first[u] = static_cast<uint8_t>(at);
+    next[u] = at;
+    at += size[u];
+  }
+  plan->first[units] = static_cast<uint8_t>(at);
+  for (int i = 0; i < N; ++i) plan->seq[next[unit[i]]++] = static_cast<uint8_t>(order[i]);
+  plan->units = units;
+  plan->packed = 1;
+}
+
+// The three steps read the inputs twice, 3 us per million elements, and take
+// some 8 us for two launches and the chain (us, one pass / three steps: 512
+// channels x 8192 tokens 42 / 30, 1024 x 4096 24 / 25, 1024 x 16384 110 / 70, 2048
+// x 4096 27 / 34, 2048 x 16384 132 / 111, 4096 x 16384 163 / 201).
+bool lru_plan(const int32_t* cu, int32_t N, int32_t D, int64_t longest, bool resume, LruPlan* plan) {
+  const int64_t T = N > 0 ? cu[N] : 0;
+  double us;
+  lru_tile(cu, N, T, D, longest, plan, &us);
+  if (T > GDN_LRU_SMALL && 8.0 + 3e-6 * static_cast<double>(T) * D < us) return true;
+  lru_pack(cu, N, resume, plan);
+  return false;
+}
+
 int check_qk_shape(const gdn_qk_shape_t* s) {
   if (!s || s->H_q <= 0 || s->H_k < 0 || s->d <= 0 || s->r < 0 || s->r > s->d) return GDN_ERR_INVALID_ARG;
   if (s->norm != GDN_NORM_NONE && s->norm != GDN_NORM_L2 && s->norm != GDN_NORM_RMS) return GDN_ERR_INVALID_ARG;

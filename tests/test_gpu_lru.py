@@ -276,6 +276,25 @@ def test_wide_rows_in_place_and_rows_behind():
     assert bool((dec[:, :40] == 5).all()) and bool((dec[:, 88:] == 5).all())
 
 
+def test_long_rows_in_place_and_rows_behind():
+    """The three steps over slices of wider rows: o over x, NaN behind the last sequence left alone and not read."""
+    T, D = 7000, 40
+    p = make([T], D, "bf16", "bf16", "norm", seed=16)
+    d = dev(p)
+    want, hT = prefill(p)
+    grads = B.gdn_lru_fwd_bwd(p["shape"], d["x"], d["g"], d["cu"], d["dO"], h0=d["h0"])
+    wide = torch.full((T + 33, 200), float("nan"), dtype=BF16, device="cuda")
+    wide[:T, 8:48], wide[:T, 64:104], wide[:T, 120:160] = d["x"], d["g"], d["dO"]
+    x, g, dO = wide[:, 8:48], wide[:, 64:104], wide[:, 120:160]
+    out = {k: torch.full((T + 33, 64), 7.0, dtype=BF16, device="cuda")[:, 8:48] for k in ("o", "dx", "dg")}
+    r = B.gdn_lru_fwd_bwd(p["shape"], x, g, d["cu"], dO, h0=d["h0"], out=out)
+    for k in out:
+        assert same(r[k][:T], grads[k]) and bool((r[k][T:] == 7).all()), k
+    n, (o, h) = kernels(lambda: B.gdn_lru_prefill(p["shape"], x, g, d["cu"], h0=d["h0"], out=x))
+    assert n["k_lru_fold"] == 1 and same(wide[:T, 8:48], want) and same(h, hT)
+    assert bool(wide[T:].isnan().all()) and bool(wide[:, 48:64].isnan().all())
+
+
 def test_offsets_past_32_bits():
     """Rows 2^21 elements apart: 1500 of them span 3e9 elements, 6 GB."""
     p = make([900, 600], 32, "bf16", "bf16", "norm", seed=10)
@@ -365,6 +384,35 @@ def test_streams():
     torch.cuda.synchronize()
     for (o, h), (ro, rh) in zip(got, want):
         assert same(o, ro) and same(h, rh)
+
+
+def test_two_graphs_share_a_workspace():
+    """Two captured trainer steps (and a captured long prefill) on one workspace, replayed in turn."""
+    ps = [make([3000, 40], 48, "bf16", "f32", "norm", seed=32), make([100, 2500], 48, "bf16", "f32", "none", seed=33)]
+    ds = [dev(p) for p in ps]
+    ws = torch.empty(max(B.lru_workspace_bytes(p["shape"], 2, sum(p["lens"])) for p in ps), dtype=torch.uint8, device="cuda")
+
+    def step(p, d):
+        r = B.gdn_lru_fwd_bwd(p["shape"], d["x"], d["g"], d["cu"], d["dO"], h0=d["h0"], ws=ws, cu_seqlens_host=p["cu"])
+        o, h = B.gdn_lru_prefill(p["shape"], d["x"], d["g"], d["cu"], h0=d["h0"], ws=ws, cu_seqlens_host=p["cu"])
+        return [*(r[k] for k in sorted(r)), o, h]
+    want = [[t.clone() for t in step(p, d)] for p, d in zip(ps, ds)]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for p, d in zip(ps, ds):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(step(p, d))
+        graphs.append(g)
+    for order in ((0, 1), (1, 0), (1, 1), (0, 0)):
+        for i in order:
+            for t in outs[i]:
+                t.zero_()
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in set(order):
+            for a, b in zip(outs[i], want[i]):
+                assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), (order, i)
 
 
 def test_captured_in_a_graph():

@@ -201,6 +201,36 @@ def test_binding_checks_strides_and_shapes():
         B._packed(torch.tensor([0, 9], dtype=torch.int32), False, dev, 9)
 
 
+def test_calls_run_on_their_tensors_gpu(monkeypatch):
+    """_launch makes the tensors' GPU current for the call where another one is, and takes that GPU's current stream."""
+    log = []
+
+    class Guard:
+        def __init__(self, dev):
+            self.dev = dev
+
+        def __enter__(self):
+            log.append(("enter", self.dev.index))
+
+        def __exit__(self, *a):
+            log.append(("exit", self.dev.index))
+
+    class Lib:
+        @staticmethod
+        def gdn_lru_decode_step(*args):
+            log.append(("call", args))
+            return B.GDN_OK
+    monkeypatch.setattr(B, "_lib", Lib)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 100 + i, raising=False)
+    monkeypatch.setattr(torch.cuda, "device", Guard)
+    B._launch("gdn_lru_decode_step", torch.device("cuda", 0), 1)
+    assert log == [("call", (1, 100))]
+    log.clear()
+    B._launch("gdn_lru_decode_step", torch.device("cuda", 1), 1)
+    assert log == [("enter", 1), ("call", (1, 101)), ("exit", 1)]
+
+
 # ---- rotary frequencies: the formulas written out ------------------------------
 
 
