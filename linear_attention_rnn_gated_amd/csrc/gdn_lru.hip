@@ -12,23 +12,29 @@
 // needs no state either.
 //
 // Two schedules give these operations, and the same bits:
-//   one pass     k_lru_fwd: a block holds a channel tile of one sequence, its
-//                waves one chunk each, and goes over the sequence in rounds;
-//                inputs are read once.  Prefill with enough sequences and
-//                channels to fill the chip.
+//   one pass     k_lru_fwd: a block takes a channel tile of one sequence, or of
+//                several short ones, and goes over their chunks in rounds, a
+//                few lanes to a chunk; inputs are read once.  Prefill with
+//                enough sequences and channels to fill the chip.
 //   three steps  k_lru_fold (every chunk's A, B and Q), k_lru_chain (the states
 //                and gradients at the chunks' edges), k_lru_apply or k_lru_grad
 //                (outputs): every step runs over all chunks at once, and the
-//                inputs are read twice.  Prefill of few sequences, and the
-//                trainer.
+//                inputs are read twice.  Prefill of long sequences of few
+//                channels, and the trainer.
+// Measured (bf16 x, norm gate, one MI355X): one pass, 4 x 2048 tokens x 4096
+// channels, fp32 g 59 us = 4.6 TB/s; 32 x 128..8192 x 2048, bf16 g, complement
+// gate 433 us = 4.2 TB/s; trainer, 8 x 4096 x 4096, fp32 g 600 us: fold 214 (5.0
+// TB/s), chain 26, grad 360 (6.0 TB/s), 24 bytes an element where one reading
+// would be 16.  Running the trainer a sequence at a time, so that the second
+// reading could come out of the last-level cache, took 750 us.
 //
-// Bound: HBM.  An element takes 6 to 16 bytes and 20 to 40 vector instructions.
+// Bound: HBM.  An element takes 6 to 24 bytes and 20 to 40 vector instructions.
 
 namespace {
 
 constexpr int kLruC = GDN_LRU_CHUNK;
 constexpr int kLruPack = gdn::kLruPack;
-constexpr int kLruThreads = gdn::kLruThreads; 
+constexpr int kLruThreads = gdn::kLruThreads;
 
 struct LruIO {
   const void* x;
@@ -79,7 +85,7 @@ __device__ __forceinline__ LruExp lru_exp(float g) {
   float c = __builtin_amdgcn_fmed3f(g, -104.0f, 89.0f);
   c = g != g ? g : c;
   const float n = rintf(c * 1.44269504f);
-  float f = fmaf(n, -0.693145751953125f, c);  // 17 bits of ln 2: the product is exact
+  float f = fmaf(n, -0.693145751953125f, c);  // 15 bits of ln 2: the product is exact
   f = fmaf(n, -1.42860677e-06f, f);
   float q = 0.0013882518978789449f;
   q = fmaf(q, f, 0.008366530761122704f);
@@ -164,9 +170,9 @@ __device__ __forceinline__ void lru_empty(const LruIO& io, int64_t e) {
 }
 
 // Marks a map (mark, S) that gives S whatever was before it: a sequence's first
-// chunk, whose lanes know their start.  (Were a chunk's own product this NaN, its
-// B would be a NaN too, which is then the state by either rule.)
-constexpr uint32_t kLruMark = 0xffc0deadu;
+// chunk, whose lanes know their start.  A product that is a NaN goes into the
+// chain as the plain one, so that no input's NaN can look like the mark.
+constexpr uint32_t kLruMark = 0xffc0deadu, kPlainNaN = 0x7fc00000u;
 
 // The chain S -> a S + b over m maps in LDS, W entries apart, for one channel;
 // put(s, S) takes the state in front of map s (none in front of a marked one).
@@ -320,13 +326,13 @@ __global__ __launch_bounds__(kLruThreads) void k_lru_fwd(LruIO io) {
         start[threadIdx.x] = S0;
         agg[threadIdx.x] = float2{__uint_as_float(kLruMark), fmaf(a, S0, b)};
       } else {
-        agg[threadIdx.x] = float2{a, b};
+        agg[threadIdx.x] = float2{a != a ? __uint_as_float(kPlainNaN) : a, b};
       }
     }
     __syncthreads();
     if (folds)
       S = lru_chain<true, 4>(agg + threadIdx.x, W, static_cast<int>(nch - cb < slots ? nch - cb : slots), S,
-                          [&](int s, float v) { start[s * W + threadIdx.x] = v; });
+                             [&](int s, float v) { start[s * W + threadIdx.x] = v; });
     __syncthreads();
     if (has && live) {
       const float st = start[threadIdx.x];
@@ -528,7 +534,7 @@ __global__ __launch_bounds__(256) void k_lru_chain(LruIO io) {
   lru_rows(io, n, t0, L);
   const int64_t sn = static_cast<int64_t>(n) * io.D;
   const bool up = blockIdx.y == 0;
-  const int p0 = io.resume ? lru_pos(io, n, c0) : 0;
+  const int p0 = io.resume ? lru_pos(io, n, 0) : 0;
   const int64_t nch = L > 0 ? (p0 + L + kLruC - 1) / kLruC : 0;
   const int col = threadIdx.x & (W - 1), row = threadIdx.x / W;
   const int c = c0 + col;

@@ -328,6 +328,27 @@ def test_growth_infinities_and_nan_stay_in_their_channel():
     check(oc, ro, eo, "o")
 
 
+@pytest.mark.parametrize("long", [False, True])
+def test_no_nan_crosses_into_another_sequence(long):
+    """Sequences that share a block's round, after ones whose states are NaN or infinite, and a NaN of every payload as g."""
+    lens = [70, 40, 33, 64, 100] + ([9000] if long else [])
+    p = make(lens, 6, "f32", "f32", "norm", seed=17)
+    cu = p["cu"].tolist()
+    want, wh = prefill(p)
+    bad = dict(p, x=p["x"].clone(), g=p["g"].clone())
+    bad["x"][cu[0] + 5], bad["x"][cu[2] + 1] = float("nan"), float("inf")
+    payload = torch.tensor([0xffc0dead - (1 << 32), 0x7fc00000, 0xffc0dead - (1 << 32), 0x7f800001, -1, 0x7fffffff], dtype=torch.int32)
+    bad["g"][cu[1] + 36] = payload.view(F32)
+    bad["g"][cu[4] + 66] = payload.view(F32)
+    o, h = prefill(bad)
+    for n in (3, 5)[:1 + long]:
+        assert same(o[cu[n]:cu[n + 1]], want[cu[n]:cu[n + 1]]) and same(h[n], wh[n]), n
+    for n, t in ((0, 5), (1, 36), (2, 1), (4, 66)):   # until then as without it
+        assert same(o[cu[n]:cu[n] + t], want[cu[n]:cu[n] + t]), n
+    for n, t in ((0, 5), (1, 36), (4, 66)):
+        assert bool(o[cu[n] + t:cu[n + 1]].isnan().all()) and bool(h[n].isnan().all())
+
+
 def test_many_sequences_and_longest_channel_count():
     p = make([2] * 70000, 5, "bf16", "f32", "none", seed=12)
     o, hT = prefill(p)
