@@ -386,7 +386,9 @@ __global__ void k_lru_cache_init(LruIO io) {
 }
 
 // One token of one sequence, 256 channels a block of one wave, which alone
-// reads and advances their position counter.
+// reads and advances their position counter.  Bound by HBM where large (1024
+// sequences x 4096 channels, fp32 g: 18.5 us for 117 MB, 6.3 TB/s), by the launch
+// where small (64 x 4096: 3.8 us).
 template <typename TX, typename TG, int GATE>
 __global__ __launch_bounds__(64) void k_lru_decode(LruIO io) {
   const int n = blockIdx.y;

@@ -9,6 +9,10 @@
 // sine and cosine are formed once per token and lane.
 //
 // Bound: HBM (4 to 12 bytes and about 12 vector instructions per element).
+// Measured (bf16, one MI355X): L2 norm and full rotation of 8192 tokens x 32 heads
+// of 128 29 us = 4.6 TB/s (rotation alone 26, neither 25); rotation of 148175
+// tokens x 40 heads 552 us = 5.5 TB/s; gradient of the RMS norm and rotation,
+// 32768 tokens x 32 heads, 160 us = 5.0 TB/s, and 5 us to add the weights' sums.
 
 namespace {
 
