@@ -136,23 +136,22 @@ __device__ __forceinline__ int lru_pos(const LruIO& io, int n, int c) {
   return p < 0 ? 0 : (p >= kLruC ? kLruC - 1 : p);
 }
 
-// Block -> (unit, channel tile).  Groups of four neighbouring tiles of a unit
-// go to one XCD (blocks are dealt to the eight XCDs in turn), where tiles
-// narrower than a cache line share it in that XCD's L2.
+// Block -> (unit, channel tile).  Runs of four items (neighbouring tiles of a
+// unit, mostly) go to one XCD (blocks are dealt to the eight XCDs in turn), where
+// tiles narrower than a cache line share it in that XCD's L2.  No item is left
+// out inside a run: an XCD deals its blocks to its four shader engines in turn, so
+// runs with idle places would leave whole engines idle (80 x 3000 tokens x 64
+// channels, two tiles: 73 us with runs padded to four, 41 without).
 __device__ __forceinline__ bool lru_item(const LruIO& io, int& unit, int& tile) {
   const int64_t b = blockIdx.x;
   const int64_t xcd = b & 7, j = b >> 3;
-  const int64_t group = (j >> 2) * 8 + xcd;
-  const int gpu = (io.tiles + 3) >> 2;  // groups per unit
-  const int64_t u = group / gpu;
-  tile = static_cast<int>(group - u * gpu) * 4 + static_cast<int>(j & 3);
+  const int64_t item = ((j >> 2) * 8 + xcd) * 4 + (j & 3);
+  const int64_t u = item / io.tiles;
+  tile = static_cast<int>(item - u * io.tiles);
   unit = static_cast<int>(u);
-  return u < io.plan.units && tile < io.tiles;
+  return u < io.plan.units;
 }
-int64_t lru_blocks(int64_t units, int tiles) {
-  const int64_t groups = units * ((tiles + 3) / 4);
-  return (groups + 7) / 8 * 8 * 4;
-}
+int64_t lru_blocks(int64_t units, int tiles) { return (units * tiles + 31) / 32 * 32; }
 
 // What an empty sequence's channel e = n D + c ends with: where it began.
 __device__ __forceinline__ void lru_empty(const LruIO& io, int64_t e) {
@@ -226,12 +225,14 @@ __global__ __launch_bounds__(kLruThreads) void k_lru_fwd(LruIO io) {
   const bool live = c < io.D;
   const int cc = live ? c : io.D - 1;
   const bool folds = slot == 0 && live;  // these threads hold the chain of one channel each
-  const int i0 = io.plan.packed ? io.plan.first[unit] : 0;
-  const int count = io.plan.packed ? io.plan.first[unit + 1] - i0 : 1;
+  const int per = io.plan.per;
+  const int i0 = per ? unit * per : io.plan.first[unit];
+  const int count = per ? (io.N - i0 < per ? io.N - i0 : per) : io.plan.first[unit + 1] - i0;
+  auto sequence = [&](int i) { return per ? i0 + i : static_cast<int>(io.plan.seq[i0 + i]); };
   if (threadIdx.x < 64) {
     int64_t t0, L = 0, chunks = 0;
     if (static_cast<int>(threadIdx.x) < count) {
-      const int n = io.plan.packed ? io.plan.seq[i0 + threadIdx.x] : unit;
+      const int n = sequence(threadIdx.x);
       lru_rows(io, n, t0, L);
       if (L > 0) chunks = ((io.resume ? lru_pos(io, n, 0) : 0) + L + kLruC - 1) / kLruC;
     }
@@ -248,7 +249,7 @@ __global__ __launch_bounds__(kLruThreads) void k_lru_fwd(LruIO io) {
   if (folds) {
     for (int i = 0; i < count; ++i)
       if (chunk0[i + 1] == chunk0[i])
-        lru_empty(io, static_cast<int64_t>(io.plan.packed ? io.plan.seq[i0 + i] : unit) * io.D + c);
+        lru_empty(io, static_cast<int64_t>(sequence(i)) * io.D + c);
   }
   const int64_t nch = chunk0[count];
   float S = 0.0f;
@@ -257,12 +258,12 @@ __global__ __launch_bounds__(kLruThreads) void k_lru_fwd(LruIO io) {
     int lo = 0, hi = 0;
     bool last = false;
     int64_t row = 0, sn = 0;  // row of the chunk's place 0, the sequence's states
-    float A[kLruC], B[kLruC];
+    float A[kLruC], B[kLruC], ae = 1.0f, be = 0.0f;  // the chunk's composition at every place, and whole
     if (has) {
       int i = 0;
       for (int d = kLruPack / 2; d >= 1; d >>= 1)  // the last sequence that begins at or before the slot's chunk
         if (i + d < count && chunk0[i + d] <= cb + slot) i += d;
-      const int n = io.plan.packed ? io.plan.seq[i0 + i] : unit;
+      const int n = sequence(i);
       int64_t t0, L;
       lru_rows(io, n, t0, L);
       sn = static_cast<int64_t>(n) * io.D;
@@ -299,28 +300,33 @@ __global__ __launch_bounds__(kLruThreads) void k_lru_fwd(LruIO io) {
           a = io.cache.A[sn + cc];
           b = io.cache.B[sn + cc];
         }
+        // eight rows at a time, those that no lane of the wave has left out
 #pragma unroll
-        for (int half = 0; half < kLruC; half += kLruC / 2) {
+        for (int j0 = 0; j0 < kLruC; j0 += 8) {
+          if (__any(j0 < hi && j0 + 8 > lo)) {
 #pragma unroll
-          for (int j = half; j < half + kLruC / 2; ++j) {
-            const int64_t t = row + (j < lo ? lo : (j >= hi ? hi - 1 : j));  // a row of this chunk
-            A[j] = ldin(g + t * io.ldg);
-            B[j] = ldin(x + t * io.ldx);
-          }
+            for (int j = j0; j < j0 + 8; ++j) {
+              const int64_t t = row + (j < lo ? lo : (j >= hi ? hi - 1 : j));  // a row of this chunk
+              A[j] = ldin(g + t * io.ldg);
+              B[j] = ldin(x + t * io.ldx);
+            }
 #pragma unroll
-          for (int j = half; j < half + kLruC / 2; ++j) {
-            float al;
-            float u = lru_input<GATE>(A[j], B[j], al);
-            // places outside the rows change nothing: 1 a = a, fma(1, b, -0) = b
-            const bool in = j >= lo && j < hi;
-            al = in ? al : 1.0f;
-            u = in ? u : -0.0f;
-            A[j] = a = al * a;
-            B[j] = b = fmaf(al, b, u);
+            for (int j = j0; j < j0 + 8; ++j) {
+              float al;
+              float u = lru_input<GATE>(A[j], B[j], al);
+              // places outside the rows change nothing: 1 a = a, fma(1, b, -0) = b
+              const bool in = j >= lo && j < hi;
+              al = in ? al : 1.0f;
+              u = in ? u : -0.0f;
+              A[j] = a = al * a;
+              B[j] = b = fmaf(al, b, u);
+            }
           }
           __builtin_amdgcn_sched_barrier(0);
         }
       }
+      ae = a;
+      be = b;
       if (ch == 0) {
         const float S0 = io.resume ? io.cache.S[sn + cc] : (io.h0 ? io.h0[sn + cc] : 0.0f);
         start[threadIdx.x] = S0;
@@ -346,14 +352,13 @@ __global__ __launch_bounds__(kLruThreads) void k_lru_fwd(LruIO io) {
           if (j >= lo && j < hi) stout(o + (row + j) * io.ldo, fmaf(A[j], st, B[j]));
       }
       if (last) {
-        const float al = A[kLruC - 1], bl = B[kLruC - 1];
-        const float h = fmaf(al, st, bl);
+        const float h = fmaf(ae, st, be);
         if (io.hT) io.hT[sn + c] = h;
         if (io.cache.S) {
           const bool full = hi == kLruC;
           io.cache.S[sn + c] = full ? h : st;
-          io.cache.A[sn + c] = full ? 1.0f : al;
-          io.cache.B[sn + c] = full ? 0.0f : bl;
+          io.cache.A[sn + c] = full ? 1.0f : ae;
+          io.cache.B[sn + c] = full ? 0.0f : be;
         }
       }
     }
@@ -724,7 +729,7 @@ int lru_dispatch(const gdn_lru_shape_t* s, F&& f) {
 
 // Checks and resolves what the packed calls share.
 int lru_common(const gdn_lru_shape_t* shape, int32_t n_seqs, const int32_t* cu_dev, const int32_t** cu_host,
-               std::vector<int32_t>& buf, hipStream_t st, LruIO* io, int64_t* longest) {
+               std::vector<int32_t>& buf, hipStream_t st, LruIO* io, int64_t* longest, int64_t* chunks) {
   int rc = gdn::check_lru_shape(shape);
   if (rc != GDN_OK) return rc;
   if (n_seqs < 0 || !cu_dev) return GDN_ERR_INVALID_ARG;
@@ -742,6 +747,7 @@ int lru_common(const gdn_lru_shape_t* shape, int32_t n_seqs, const int32_t* cu_d
     most = len > most ? len : most;
   }
   *longest = most;
+  *chunks = cnt.chunks;
   io->cu = cu_dev;
   io->N = n_seqs;
   io->D = shape->D;
@@ -799,7 +805,7 @@ int lru_prefill_entry(const gdn_lru_shape_t* shape, int32_t n_seqs, const int32_
   hipStream_t st = static_cast<hipStream_t>(stream);
   LruIO io{};
   std::vector<int32_t> buf;
-  int64_t longest = 0;
+  int64_t longest = 0, chunks = 0;
   int rc = gdn::check_lru_shape(shape);
   if (rc != GDN_OK) return rc;
   if (!gdn::aligned16({x, g, h0, o, hT, ws})) return GDN_ERR_INVALID_ARG;
@@ -808,13 +814,13 @@ int lru_prefill_entry(const gdn_lru_shape_t* shape, int32_t n_seqs, const int32_
   io.ldg = gdn::row_stride(ldg, shape->D);
   io.ldo = gdn::row_stride(ldo, shape->D);
   if (io.ldx < 0 || io.ldg < 0 || io.ldo < 0) return GDN_ERR_INVALID_ARG;
-  if ((rc = lru_common(shape, n_seqs, cu_dev, &cu_host, buf, st, &io, &longest)) != GDN_OK) return rc;
+  if ((rc = lru_common(shape, n_seqs, cu_dev, &cu_host, buf, st, &io, &longest, &chunks)) != GDN_OK) return rc;
   if (io.T > 0 && (!x || !g || !o)) return GDN_ERR_INVALID_ARG;
   if (io.T > GDN_LRU_SMALL && (!ws || ws_bytes < lru_ws_bytes(shape->D, n_seqs, io.T, false))) return GDN_ERR_WORKSPACE;
   if (n_seqs == 0) return GDN_OK;
   io.x = x; io.g = g; io.h0 = h0; io.o = o; io.hT = hT; io.resume = resume;
   if (cache) io.cache = *cache;
-  const bool three = gdn::lru_plan(cu_host, n_seqs, io.D, longest, resume, &io.plan);
+  const bool three = gdn::lru_plan(cu_host, n_seqs, chunks, io.D, longest, resume, &io.plan);
   int threads = 256;
   int64_t blocks;
   if (three) {
@@ -925,7 +931,7 @@ int gdn_lru_fwd_bwd(const gdn_lru_shape_t* shape, int32_t n_seqs, const int32_t*
   hipStream_t st = static_cast<hipStream_t>(stream);
   LruIO io{};
   std::vector<int32_t> buf;
-  int64_t longest = 0;
+  int64_t longest = 0, chunks = 0;
   int rc = gdn::check_lru_shape(shape);
   if (rc != GDN_OK) return rc;
   if (!gdn::aligned16({x, g, h0, dO, dhT, o, hT, dx, dg, dh0, ws})) return GDN_ERR_INVALID_ARG;
@@ -937,7 +943,7 @@ int gdn_lru_fwd_bwd(const gdn_lru_shape_t* shape, int32_t n_seqs, const int32_t*
   io.lddx = gdn::row_stride(lddx, shape->D);
   io.lddg = gdn::row_stride(lddg, shape->D);
   if (io.ldx < 0 || io.ldg < 0 || io.ldo < 0 || io.lddo < 0 || io.lddx < 0 || io.lddg < 0) return GDN_ERR_INVALID_ARG;
-  if ((rc = lru_common(shape, n_seqs, cu_seqlens_dev, &cu_seqlens_host, buf, st, &io, &longest)) != GDN_OK) return rc;
+  if ((rc = lru_common(shape, n_seqs, cu_seqlens_dev, &cu_seqlens_host, buf, st, &io, &longest, &chunks)) != GDN_OK) return rc;
   if (io.T > 0 && (!x || !g || !dO || !dx || !dg)) return GDN_ERR_INVALID_ARG;
   if (!ws || ws_bytes < lru_ws_bytes(shape->D, n_seqs, io.T, true)) return GDN_ERR_WORKSPACE;
   if (n_seqs == 0) return GDN_OK;

@@ -154,56 +154,71 @@ int64_t row_stride(int64_t ld, int64_t row) {
 // with all CUs at work, 27, 16.5, 12 and 10.5 with a part of them.  The tile with
 // the least time is taken.
 //
-// Up to kLruPack sequences are packed: those shorter than a round share units
-// of up to a round (first fit, longest first), and the longest units begin
-// first (19 sequences of 1 to 1508 tokens x 3447 channels: 40 us, unpacked 75;
-// 32 of 128 to 8192 x 2048: 448 us, unpacked 504).  More sequences are units of
-// their own.
+// Short sequences share units of up to a round: up to kLruPack sequences first
+// fit, longest first, and the longest units begin first (19 sequences of 1 to 1508
+// tokens x 3447 channels: 31 us, unpacked 75; 32 of 128 to 8192 x 2048: 433 us,
+// unpacked 504); of more sequences, as many neighbours as fill a round on average
+// (1000 of 20 tokens x 1024 channels: 66 us, a unit each 132; 2000 of 3 x 512: 30
+// against 83).
 //
 // Blocks of 512 threads, two a CU, where all tiles and units keep them busy: one
 // block's loads then overlap the other's chain (16 x 2048 tokens x 2048 channels:
-// 119 us against 125; with half as many blocks 122 against 108 us).
-static void lru_tile(const int32_t* cu, int32_t N, int64_t T, int32_t D, int64_t longest, LruPlan* plan, double* us) {
+// 119 us against 125; 80 x 3000 x 256: 122 against 140; with half as many blocks
+// 122 against 108 us).  Smaller blocks where the batch is so small that fewer than
+// 256 would be left.
+static void lru_tile(const int32_t* cu, int32_t N, int64_t chunks, int32_t D, int64_t longest, LruPlan* plan,
+                     double* us) {
   static constexpr int kTile[4] = {64, 32, 16, 8};
   static constexpr double kRound[4] = {13.5, 16.0, 20.0, 33.0}, kAlone[4] = {10.5, 12.0, 16.5, 27.0};
   *us = 0;
   for (int k = 0; k < 4; ++k) {
     const int l = kTile[k];
-    const int64_t round = static_cast<int64_t>(kLruThreads) / l * GDN_LRU_CHUNK;
+    const int64_t slots = kLruThreads / l;
     double rounds = 0;
     if (N <= kLruPack) {
       int64_t shorts = 0;
       for (int32_t n = 0; n < N; ++n) {
-        const int64_t len = static_cast<int64_t>(cu[n + 1]) - cu[n];
-        if (len >= round)
-          rounds += static_cast<double>((len + round - 1) / round);
+        const int64_t c = (static_cast<int64_t>(cu[n + 1]) - cu[n] + GDN_LRU_CHUNK - 1) / GDN_LRU_CHUNK;
+        if (c >= slots)
+          rounds += static_cast<double>((c + slots - 1) / slots);
         else
-          shorts += len;
+          shorts += c;
       }
-      rounds += static_cast<double>((shorts + round - 1) / round);
+      rounds += static_cast<double>((shorts + slots - 1) / slots);
     } else {
-      rounds = static_cast<double>(T / round + N);
+      const int64_t mean = (chunks + N - 1) / N;
+      rounds = mean < slots ? static_cast<double>(chunks) / slots
+                            : static_cast<double>(N) * static_cast<double>((mean + slots - 1) / slots);
     }
     const double share = rounds * ((D + l - 1) / l) / 256.0;
     const double all = (share > 1.0 ? std::ceil(share) : share) * kRound[k];
-    const double one = static_cast<double>((longest + round - 1) / round) * kAlone[k];
+    const double one =
+        static_cast<double>(((longest + GDN_LRU_CHUNK - 1) / GDN_LRU_CHUNK + slots - 1) / slots) * kAlone[k];
     const double t = all > one ? all : one;
     if (k == 0 || t < *us) {
       *us = t;
       plan->lps = l;
     }
   }
-  const int64_t blocks = longest > 0 ? T * ((D + 63) / 64) / longest : 0;
-  const int64_t most = blocks >= 400 ? 512 : kLruThreads;
-  const int64_t t = ((longest / GDN_LRU_CHUNK + 2) * plan->lps + 63) / 64 * 64;
+  const int64_t tiles64 = (D + 63) / 64;
+  const int64_t most = longest > 0 && chunks * GDN_LRU_CHUNK * tiles64 / longest > 256 ? 512 : kLruThreads;
+  const int64_t one = (longest / GDN_LRU_CHUNK + 2) * plan->lps;                    // the longest in one round
+  const int64_t share = chunks * ((D + plan->lps - 1) / plan->lps) * plan->lps / 256;  // 256 blocks of the batch
+  const int64_t t = ((one > share ? one : share) + 63) / 64 * 64;
   plan->threads = static_cast<int32_t>(t < most ? t : most);
 }
 
-static void lru_pack(const int32_t* cu, int32_t N, bool resume, LruPlan* plan) {
-  plan->units = N;
-  plan->packed = 0;
-  if (N > kLruPack) return;
-  const int64_t round = static_cast<int64_t>(plan->threads) / plan->lps * GDN_LRU_CHUNK;
+static void lru_pack(const int32_t* cu, int32_t N, int64_t chunks, bool resume, LruPlan* plan) {
+  const int64_t slots = plan->threads / plan->lps;
+  if (N > kLruPack) {
+    // a resumed sequence may take a chunk more than its tokens do
+    const int64_t mean = (chunks + N - 1) / N + (resume ? 1 : 0);
+    const int64_t per = mean > 0 ? slots / mean : kLruPack;
+    plan->per = static_cast<int32_t>(per < 1 ? 1 : per > kLruPack ? kLruPack : per);
+    plan->units = (N + plan->per - 1) / plan->per;
+    return;
+  }
+  plan->per = 0;
   int order[kLruPack], unit[kLruPack], units = 0;
   int64_t len[kLruPack], sum[kLruPack];
   for (int n = 0; n < N; ++n) {
@@ -214,10 +229,10 @@ static void lru_pack(const int32_t* cu, int32_t N, bool resume, LruPlan* plan) {
   }
   int size[kLruPack] = {};  // sequences of each unit
   for (int i = 0; i < N; ++i) {
-    // whole chunks, one more for the places before a resumed sequence's first token
-    const int64_t need = (len[order[i]] + (resume ? 2 : 1) * GDN_LRU_CHUNK - 1) / GDN_LRU_CHUNK * GDN_LRU_CHUNK;
+    // chunks, one more for the places before a resumed sequence's first token
+    const int64_t need = (len[order[i]] + (resume ? 2 : 1) * GDN_LRU_CHUNK - 1) / GDN_LRU_CHUNK;
     int u = 0;
-    while (u < units && sum[u] + need > round) ++u;
+    while (u < units && sum[u] + need > slots) ++u;
     if (u == units) sum[units++] = 0;
     sum[u] += need;
     ++size[u];
@@ -232,19 +247,20 @@ static void lru_pack(const int32_t* cu, int32_t N, bool resume, LruPlan* plan) {
   plan->first[units] = static_cast<uint8_t>(at);
   for (int i = 0; i < N; ++i) plan->seq[next[unit[i]]++] = static_cast<uint8_t>(order[i]);
   plan->units = units;
-  plan->packed = 1;
 }
 
 // The three steps read the inputs twice, 3 us per million elements, and take
 // some 8 us for two launches and the chain (us, one pass / three steps: 512
 // channels x 8192 tokens 42 / 30, 1024 x 4096 24 / 25, 1024 x 16384 110 / 70, 2048
 // x 4096 27 / 34, 2048 x 16384 132 / 111, 4096 x 16384 163 / 201).
-bool lru_plan(const int32_t* cu, int32_t N, int32_t D, int64_t longest, bool resume, LruPlan* plan) {
+bool lru_plan(const int32_t* cu, int32_t N, int64_t chunks, int32_t D, int64_t longest, bool resume, LruPlan* plan) {
   const int64_t T = N > 0 ? cu[N] : 0;
   double us;
-  lru_tile(cu, N, T, D, longest, plan, &us);
-  if (T > GDN_LRU_SMALL && 8.0 + 3e-6 * static_cast<double>(T) * D < us) return true;
-  lru_pack(cu, N, resume, plan);
+  lru_tile(cu, N, chunks, D, longest, plan, &us);
+  // over the chunks' places and whole waves, which is what the steps run over
+  const double twice = 8.0 + 3e-6 * static_cast<double>(chunks * GDN_LRU_CHUNK) * ((D + 63) / 64 * 64);
+  if (T > GDN_LRU_SMALL && twice < us) return true;
+  lru_pack(cu, N, chunks, resume, plan);
   return false;
 }
 

@@ -89,19 +89,22 @@ int64_t row_stride(int64_t ld, int64_t row);
 inline int64_t lru_slots(int64_t T, int64_t N) { return T / GDN_LRU_CHUNK + 2 * N; }
 
 // How a prefill runs (see gdn_lru.hip).
-constexpr int kLruPack = 64;       // most sequences that are packed into units
+constexpr int kLruPack = 64;       // most sequences of a unit, and those that are sorted into units
 constexpr int kLruThreads = 1024;  // most threads of a one-pass block
 struct LruPlan {
   int32_t lps = 64;       // lanes per chunk = channels of a block's tile: 8, 16, 32 or 64
   int32_t threads = 64;   // of a block: a multiple of 64
-  int32_t units = 0;      // sequences or, packed, groups of sequences that a block takes
-  int32_t packed = 0;     // 1: unit u is the sequences seq[first[u]] .. seq[first[u + 1] - 1]
+  int32_t units = 0;      // groups of sequences that a block takes
+  int32_t per = 0;        // 0: unit u is the sequences seq[first[u]] .. seq[first[u + 1] - 1];
+                          // else it is `per` neighbours, those from u per on
   uint8_t seq[kLruPack] = {};
   uint8_t first[kLruPack + 1] = {};
 };
-// Fills the plan of the one pass from a validated cu_seqlens; true where the
-// three steps are expected to be faster.
-bool lru_plan(const int32_t* cu_host, int32_t n_seqs, int32_t D, int64_t longest, bool resume, LruPlan* plan);
+// Fills the plan of the one pass from a validated cu_seqlens with its count of
+// chunks (each sequence's from its first token) and its longest length; true
+// where the three steps are expected to be faster.
+bool lru_plan(const int32_t* cu_host, int32_t n_seqs, int64_t chunks, int32_t D, int64_t longest, bool resume,
+              LruPlan* plan);
 
 // Norms of q and k with rotary positions.
 int check_qk_shape(const gdn_qk_shape_t* s);

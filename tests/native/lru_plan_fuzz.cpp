@@ -22,23 +22,25 @@ int main() {
     const int N = static_cast<int>(pick(0, 3) ? pick(0, 64) : pick(65, 300));
     const int64_t most = pick(0, 2) == 0 ? 40 : pick(0, 1) ? 3000 : 100000;
     std::vector<int32_t> cu(static_cast<size_t>(N) + 1, 0);
-    int64_t longest = 0;
+    int64_t longest = 0, chunks = 0;
     for (int n = 0; n < N; ++n) {
       const int64_t len = pick(0, 4) == 0 ? 0 : pick(0, most);
       cu[n + 1] = static_cast<int32_t>(cu[n] + len);
       longest = len > longest ? len : longest;
+      chunks += (len + 31) / 32;
     }
     const int32_t D = static_cast<int32_t>(pick(0, 9) == 0 ? pick(1, 1 << 20) : pick(1, 9000));
     const bool resume = pick(0, 1);
     gdn::LruPlan p;
-    const bool three = gdn::lru_plan(cu.data(), N, D, longest, resume, &p);
+    const bool three = gdn::lru_plan(cu.data(), N, chunks, D, longest, resume, &p);
     if (three && cu[N] <= GDN_LRU_SMALL) return fail("three steps without a workspace", it);
     if (p.lps != 8 && p.lps != 16 && p.lps != 32 && p.lps != 64) return fail("tile", it);
     if (p.threads < 64 || p.threads > gdn::kLruThreads || p.threads % 64 != 0 || p.threads < p.lps)
       return fail("threads", it);
     if (three) continue;
-    if (!p.packed) {
-      if (p.units != N) return fail("units", it);
+    if (p.per) {
+      if (N <= gdn::kLruPack || p.per < 0 || p.per > gdn::kLruPack || p.units != (N + p.per - 1) / p.per)
+        return fail("neighbours", it);
       continue;
     }
     if (N > gdn::kLruPack || p.units > N || p.first[0] != 0 || p.first[p.units] != N) return fail("packing", it);

@@ -328,6 +328,52 @@ def test_growth_infinities_and_nan_stay_in_their_channel():
     check(oc, ro, eo, "o")
 
 
+@pytest.mark.parametrize("most,D", [(6, 40), (90, 130), (400, 17)])
+def test_many_sequences_continue(most, D):
+    """More sequences than are packed by length, empty ones among them: a prefix, two continuations and a decode step equal
+    one prefill of each."""
+    N = 150
+    gen = torch.Generator().manual_seed(most)
+    lens = [int(v) for v in torch.randint(0, most, (N,), generator=gen)]
+    p = make(lens, D, "bf16", "f32", "complement", seed=most)
+    d, cu = dev(p), p["cu"].tolist()
+    o, hT = prefill(p)
+    ro, rh, eo, eh = lru_fwd(np64(p["x"]), np64(p["g"]), cu, "complement", np64(p["h0"]))
+    check(o, ro, eo, "o")
+    check(hT, rh, eh, "hT")
+    cache, at = B.gdn_lru_cache_init(p["shape"], N, "cuda", h0=d["h0"]), [0] * N
+    for step in range(3):
+        to = [n if step == 2 else int(torch.randint(a, n + 1, (1,), generator=gen)) for a, n in zip(at, lens)]
+        rows = torch.cat([torch.arange(cu[n] + at[n], cu[n] + to[n]) for n in range(N)]).cuda()
+        c = torch.tensor([0] + list(np.cumsum([b - a for a, b in zip(at, to)])), dtype=torch.int32, device="cuda")
+        got, last = B.gdn_lru_prefill_continue(p["shape"], d["x"][rows], d["g"][rows], c, cache)
+        assert same(got, o[rows]), step
+        at = to
+    assert same(last, hT)
+    full = B.LruCache(D, N, "cuda")
+    prefill(p, cache=full)
+    for a, b in zip(cache.tensors(), full.tensors()):
+        assert torch.equal(a.view(torch.int32), b.view(torch.int32))
+
+
+def test_positions_outside_a_chunk_are_clamped():
+    p = make([40, 3, 2500], 300, seed=18)
+    d = dev(p)
+    for bad in (-3, 99, 32, -(1 << 31), (1 << 31) - 1):
+        for lens in ([40, 3, 0], [40, 3, 2500]):
+            cache = B.gdn_lru_cache_init(p["shape"], 3, "cuda", h0=d["h0"])
+            cache.pos.fill_(bad)
+            T = sum(lens)
+            cu = torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int32, device="cuda")
+            out = torch.full((T + 40, 300), 3.0, dtype=BF16, device="cuda")
+            pad = lambda t: torch.cat([t[:T], t[:40]])  # noqa: E731
+            B.gdn_lru_prefill_continue(p["shape"], pad(d["x"]), pad(d["g"]), cu, cache, out=out)
+            assert bool((out[T:] == 3).all()) and bool((cache.pos >= 0).all()) and bool((cache.pos < 32).all())
+            cache.pos.fill_(bad)
+            B.gdn_lru_decode_step(p["shape"], d["x"][:3], d["g"][:3], cache)
+            assert bool((cache.pos >= 0).all()) and bool((cache.pos < 32).all())
+
+
 @pytest.mark.parametrize("long", [False, True])
 def test_no_nan_crosses_into_another_sequence(long):
     """Sequences that share a block's round, after ones whose states are NaN or infinite, and a NaN of every payload as g."""
