@@ -352,16 +352,18 @@ __global__ __launch_bounds__(256) void k_qk_bwd(QkIO io) {
         if (io.norm != GDN_NORM_NONE) {
           const float n = qk_inverse_norm(io, x);
           if (io.norm == GDN_NORM_RMS) {
-            const float nq = is_q ? n : 0.0f, nk = is_q ? 0.0f : n;
             float m[8];
             if (l.active) qk_weight(l, w[is_q ? 0 : 1], m);
+            // branches, not factors of zero: 0 x NaN would take a q head's NaN into k's sum
+            if (is_q) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float yx = y[e] * x[e];
-              gq[e] = fmaf(yx, nq, gq[e]);
-              gk[e] = fmaf(yx, nk, gk[e]);
-              y[e] = l.active ? y[e] * m[e] : 0.0f;
+              for (int e = 0; e < 8; ++e) gq[e] = fmaf(y[e] * x[e], n, gq[e]);
+            } else if (h < H) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) gk[e] = fmaf(y[e] * x[e], n, gk[e]);
             }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = l.active ? y[e] * m[e] : 0.0f;
           }
           float e4[4];
 #pragma unroll

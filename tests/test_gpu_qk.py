@@ -81,6 +81,9 @@ CASES = [
     (4, 1, 2, 504, 16, "bf16", "f32", "rms", "interleaved"),
     (11, 4, 4, 128, 0, "bf16", "bf16", "rms", "half"),
     (300, 40, 8, 64, 32, "bf16", "bf16", "none", "interleaved"),
+    (2, 4000, 96, 8, 8, "bf16", "bf16", "rms", "half"),
+    (3, 65, 1, 24, 8, "f32", "f32", "l2", "interleaved"),
+    (2100, 1, 1, 512, 256, "bf16", "bf16", "rms", "interleaved"),
 ]
 
 
@@ -207,6 +210,31 @@ def test_zero_vectors_and_no_weights():
     none = B.gdn_qk_rotary_bwd(p["shape"], g["q"][:0], g["k"][:0], g["dq"][:0], g["dk"][:0], g["inv_freq"],
                                pos=g["pos"][:0], w_q=g["w_q"], w_k=g["w_k"])
     assert bool((none["dw_q"] == 0).all()) and none["dq"].shape == (0, 2, 64)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("d", [8, 96, 128])
+def test_weight_gradients_keep_q_and_k_apart(d, bad):
+    """A NaN or an infinity in a head of q reaches dw_q and that head alone, and eps = 0 with more places in a wave than
+    there are heads reaches nothing."""
+    p = make(5, 2, 1, d, 8, "f32", seed=9)
+    p["shape"] = B.make_qk_shape(2, 1, d, 8, F32, norm="rms", eps=0.0, weight_offset=p["offset"])
+    g = on_gpu(p)
+    args = (p["shape"], g["q"], g["k"], g["dq"], g["dk"], g["inv_freq"])
+    kw = dict(pos=g["pos"], w_q=g["w_q"], w_k=g["w_k"])
+    clean = B.gdn_qk_rotary_bwd(*args, **kw)
+    assert all(torch.isfinite(t).all() for t in clean.values())
+    for name, other in (("q", "k"), ("k", "q")):
+        keep = g[name].clone()
+        g[name][2, 0, 3] = bad
+        got = B.gdn_qk_rotary_bwd(*args, **kw)
+        g[name].copy_(keep)
+        assert torch.equal(got["dw_" + other], clean["dw_" + other])
+        assert torch.equal(got["d" + other], clean["d" + other])
+        assert not torch.isfinite(got["d" + name][2, 0]).all() and not torch.isfinite(got["dw_" + name]).all()
+        rest = torch.ones(5, g[name].shape[1], dtype=torch.bool, device="cuda")
+        rest[2, 0] = False
+        assert torch.equal(got["d" + name][rest], clean["d" + name][rest])
 
 
 def test_captured_in_a_graph_and_on_a_stream():
