@@ -375,7 +375,8 @@ int gdn_lru_prefill_continue(const gdn_lru_shape_t* shape, int32_t n_seqs,
                              gdn_lru_cache_t* cache, void* o, int64_t ldo, float* hT, void* ws,
                              size_t ws_bytes, void* stream);
 
-/* One token for each of n_seqs sequences: x, o and g hold n_seqs rows. */
+/* One token for each of n_seqs sequences (at most 65535): x, o and g hold
+ * n_seqs rows. */
 int gdn_lru_decode_step(const gdn_lru_shape_t* shape, int32_t n_seqs, const void* x, int64_t ldx,
                         const void* g, int64_t ldg, gdn_lru_cache_t* cache, void* o, int64_t ldo,
                         void* stream);
