@@ -15,12 +15,13 @@
 //   one pass     k_lru_fwd: a block takes a channel tile of one sequence, or of
 //                several short ones, and goes over their chunks in rounds, a
 //                few lanes to a chunk; inputs are read once.  Prefill with
-//                enough sequences and channels to fill the chip.
+//                enough sequences and channels to fill the chip.  k_lru_train
+//                is the trainer's, of sequences that fit one round.
 //   three steps  k_lru_fold (every chunk's A, B and Q), k_lru_chain (the states
 //                and gradients at the chunks' edges), k_lru_apply or k_lru_grad
 //                (outputs): every step runs over all chunks at once, and the
 //                inputs are read twice.  Prefill of long sequences of few
-//                channels, and the trainer.
+//                channels, and the trainer's longer sequences.
 // Measured (bf16 x, norm gate, one MI355X): one pass, 4 x 2048 tokens x 4096
 // channels, fp32 g 59 us = 4.6 TB/s; 32 x 128..8192 x 2048, bf16 g, complement
 // gate 433 us = 4.2 TB/s; trainer, 8 x 4096 x 4096, fp32 g 600 us: fold 214 (5.0
@@ -35,6 +36,7 @@ namespace {
 constexpr int kLruC = GDN_LRU_CHUNK;
 constexpr int kLruPack = gdn::kLruPack;
 constexpr int kLruThreads = gdn::kLruThreads;
+constexpr int kLruTrain = gdn::kLruTrain;
 
 struct LruIO {
   const void* x;
@@ -211,6 +213,45 @@ __device__ __forceinline__ float lru_chain(const float2* agg, int W, int maps, f
   return S;
 }
 
+// The sequences of a unit; chunk0[i] counts the chunks before its i-th.
+struct LruUnit {
+  int i0, count;
+  __device__ __forceinline__ int sequence(const LruIO& io, int i) const {
+    return io.plan.per ? i0 + i : static_cast<int>(io.plan.seq[i0 + i]);
+  }
+  // the last sequence that begins at or before a chunk
+  __device__ __forceinline__ int find(const int64_t* chunk0, int64_t chunk) const {
+    int i = 0;
+    for (int d = kLruPack / 2; d >= 1; d >>= 1)
+      if (i + d < count && chunk0[i + d] <= chunk) i += d;
+    return i;
+  }
+};
+__device__ __forceinline__ LruUnit lru_open(const LruIO& io, int unit, int64_t* chunk0) {
+  const int per = io.plan.per;
+  LruUnit of;
+  of.i0 = per ? unit * per : io.plan.first[unit];
+  of.count = per ? (io.N - of.i0 < per ? io.N - of.i0 : per) : io.plan.first[unit + 1] - of.i0;
+  if (threadIdx.x < 64) {
+    int64_t t0, L = 0, chunks = 0;
+    if (static_cast<int>(threadIdx.x) < of.count) {
+      const int n = of.sequence(io, threadIdx.x);
+      lru_rows(io, n, t0, L);
+      if (L > 0) chunks = ((io.resume ? lru_pos(io, n, 0) : 0) + L + kLruC - 1) / kLruC;
+    }
+    int64_t before = chunks;
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+      const int64_t up = __shfl_up(before, m, 64);
+      if (static_cast<int>(threadIdx.x) >= m) before += up;
+    }
+    chunk0[threadIdx.x + 1] = before;
+    if (threadIdx.x == 0) chunk0[0] = 0;
+  }
+  __syncthreads();
+  return of;
+}
+
 template <typename TX, typename TG, int GATE>
 __global__ __launch_bounds__(kLruThreads) void k_lru_fwd(LruIO io) {
   __shared__ float2 agg[kLruThreads];  // [slot][channel of the tile]
@@ -225,33 +266,12 @@ __global__ __launch_bounds__(kLruThreads) void k_lru_fwd(LruIO io) {
   const bool live = c < io.D;
   const int cc = live ? c : io.D - 1;
   const bool folds = slot == 0 && live;  // these threads hold the chain of one channel each
-  const int per = io.plan.per;
-  const int i0 = per ? unit * per : io.plan.first[unit];
-  const int count = per ? (io.N - i0 < per ? io.N - i0 : per) : io.plan.first[unit + 1] - i0;
-  auto sequence = [&](int i) { return per ? i0 + i : static_cast<int>(io.plan.seq[i0 + i]); };
-  if (threadIdx.x < 64) {
-    int64_t t0, L = 0, chunks = 0;
-    if (static_cast<int>(threadIdx.x) < count) {
-      const int n = sequence(threadIdx.x);
-      lru_rows(io, n, t0, L);
-      if (L > 0) chunks = ((io.resume ? lru_pos(io, n, 0) : 0) + L + kLruC - 1) / kLruC;
-    }
-    int64_t before = chunks;
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-      const int64_t up = __shfl_up(before, m, 64);
-      if (static_cast<int>(threadIdx.x) >= m) before += up;
-    }
-    chunk0[threadIdx.x + 1] = before;
-    if (threadIdx.x == 0) chunk0[0] = 0;
-  }
-  __syncthreads();
+  const LruUnit of = lru_open(io, unit, chunk0);
   if (folds) {
-    for (int i = 0; i < count; ++i)
-      if (chunk0[i + 1] == chunk0[i])
-        lru_empty(io, static_cast<int64_t>(sequence(i)) * io.D + c);
+    for (int i = 0; i < of.count; ++i)
+      if (chunk0[i + 1] == chunk0[i]) lru_empty(io, static_cast<int64_t>(of.sequence(io, i)) * io.D + c);
   }
-  const int64_t nch = chunk0[count];
+  const int64_t nch = chunk0[of.count];
   float S = 0.0f;
   for (int64_t cb = 0; cb < nch; cb += slots) {
     const bool has = cb + slot < nch;
@@ -260,10 +280,8 @@ __global__ __launch_bounds__(kLruThreads) void k_lru_fwd(LruIO io) {
     int64_t row = 0, sn = 0;  // row of the chunk's place 0, the sequence's states
     float A[kLruC], B[kLruC], ae = 1.0f, be = 0.0f;  // the chunk's composition at every place, and whole
     if (has) {
-      int i = 0;
-      for (int d = kLruPack / 2; d >= 1; d >>= 1)  // the last sequence that begins at or before the slot's chunk
-        if (i + d < count && chunk0[i + d] <= cb + slot) i += d;
-      const int n = sequence(i);
+      const int i = of.find(chunk0, cb + slot);
+      const int n = of.sequence(io, i);
       int64_t t0, L;
       lru_rows(io, n, t0, L);
       sn = static_cast<int64_t>(n) * io.D;
@@ -278,7 +296,7 @@ __global__ __launch_bounds__(kLruThreads) void k_lru_fwd(LruIO io) {
       float a = 1.0f, b = 0.0f;
       // sixteen rows' loads at a time: all of them at once spilled registers, and
       // four waves a SIMD keep enough in flight (32 ragged x 2048: 454 -> 436 us)
-      if (lo == 0 && hi == kLruC) {
+      if (__all(lo == 0 && hi == kLruC)) {  // one way for all chunks of a wave
 #pragma unroll
         for (int half = 0; half < kLruC; half += kLruC / 2) {
 #pragma unroll
@@ -343,7 +361,7 @@ __global__ __launch_bounds__(kLruThreads) void k_lru_fwd(LruIO io) {
     if (has && live) {
       const float st = start[threadIdx.x];
       TX* o = static_cast<TX*>(io.o) + c;
-      if (lo == 0 && hi == kLruC) {
+      if (__all(lo == 0 && hi == kLruC)) {
 #pragma unroll
         for (int j = 0; j < kLruC; ++j) stout(o + (row + j) * io.ldo, fmaf(A[j], st, B[j]));
       } else {
@@ -363,6 +381,178 @@ __global__ __launch_bounds__(kLruThreads) void k_lru_fwd(LruIO io) {
       }
     }
   }
+}
+
+// Outputs and gradients of one chunk of one channel from alpha, x, dO and, in w,
+// the input's weight: forward for h and
+//     e_i = alpha_i h_{i-1} + b'_i x_i      (dg_i = delta_i e_i)
+// in the place of x, then backward for delta.  S is the state in front of the
+// chunk, K the gradient of the one behind it; places from hi on are not written
+// (WHOLE: there are none).
+template <int GATE, bool WHOLE, typename TX, typename TG>
+__device__ __forceinline__ void lru_outputs(const float* al, float* x, const float* dy, const float* w, float S, float K,
+                                            int hi, int64_t row, TX* o, int64_t ldo, TX* dx, int64_t lddx, TG* dg,
+                                            int64_t lddg) {
+  float a = 1.0f, b = 0.0f, hp = S;
+  TX* po = o ? o + row * ldo : nullptr;
+#pragma unroll
+  for (int i = 0; i < kLruC; ++i) {
+    const float xi = x[i];
+    const float u = GATE == GDN_LRU_GATE_NONE ? xi : w[i] * xi;
+    a = al[i] * a;
+    b = fmaf(al[i], b, u);
+    const float h = fmaf(a, S, b);
+    if (o && (WHOLE || i < hi)) stout(po, h);
+    po += ldo;
+    float e = al[i] * hp;
+    if constexpr (GATE == GDN_LRU_GATE_COMPLEMENT) e = fmaf(-al[i], xi, e);
+    // b' = -alpha^2 / b, the reciprocal the hardware's (1 ulp)
+    if constexpr (GATE == GDN_LRU_GATE_NORM)
+      e = fmaf(w[i] > 0.0f ? -(al[i] * al[i]) * __builtin_amdgcn_rcpf(w[i]) : 0.0f, xi, e);
+    x[i] = e;
+    hp = h;
+  }
+  dx += (row + kLruC - 1) * lddx;
+  dg += (row + kLruC - 1) * lddg;
+#pragma unroll
+  for (int i = kLruC - 1; i >= 0; --i) {
+    if (WHOLE || i < hi) {
+      const float d = dy[i] + K;
+      K = al[i] * d;
+      stout(dx, GATE == GDN_LRU_GATE_NONE ? d : w[i] * d);
+      stout(dg, d * x[i]);
+    }
+    dx -= lddx;
+    dg -= lddg;
+  }
+}
+
+// The trainer of units that fit one round: a chunk's inputs stay in its lanes'
+// registers from the composition to the gradients, so they are read once.  Bound
+// by HBM where large: 64 x 256 tokens x 4096 channels, norm gate, bf16 and fp32 g 255
+// us = 4.2 TB/s, all fp32 316 us = 5.1 TB/s (three steps: 358 and 488).  171
+// registers, two waves a SIMD; held to 168 for three it spilled and took 273 us.
+template <typename TX, typename TG, int GATE>
+__global__ __launch_bounds__(kLruTrain) void k_lru_train(LruIO io) {
+  __shared__ float2 up[kLruTrain], down[kLruTrain];  // [slot][channel of the tile]: (A, B) and (A, Q)
+  __shared__ float start[kLruTrain], behind[kLruTrain];
+  __shared__ int64_t chunk0[kLruPack + 1];
+  int unit, tile;
+  if (!lru_item(io, unit, tile)) return;
+  const int W = io.plan.lps;
+  const int slots = blockDim.x / W;
+  const int slot = threadIdx.x / W;
+  const int col = static_cast<int>(threadIdx.x) - slot * W;
+  const int c = tile * W + col;
+  const bool live = c < io.D;
+  const int cc = live ? c : io.D - 1;
+  const LruUnit of = lru_open(io, unit, chunk0);
+  if (slot == 0 && live) {
+    for (int i = 0; i < of.count; ++i)
+      if (chunk0[i + 1] == chunk0[i]) {
+        const int64_t e = static_cast<int64_t>(of.sequence(io, i)) * io.D + c;
+        lru_empty(io, e);
+        io.dh0[e] = io.dhT ? io.dhT[e] : 0.0f;
+      }
+  }
+  // a device copy of cu_seqlens that disagrees with the host's may need more than a round: left out
+  const int nch = static_cast<int>(chunk0[of.count] < slots ? chunk0[of.count] : slots);
+  if (nch == 0) return;
+  const bool has = slot < nch;
+  int hi = 0;
+  bool first = false, last = false;
+  int64_t row = 0, e = 0;
+  float al[kLruC], x[kLruC], dy[kLruC], w[GATE == GDN_LRU_GATE_NONE ? 1 : kLruC];
+  float a = 1.0f, b = 0.0f, q = 0.0f;
+  if (has) {
+    const int i = of.find(chunk0, slot);
+    const int n = of.sequence(io, i);
+    int64_t t0, L;
+    lru_rows(io, n, t0, L);
+    const int64_t ch = slot - chunk0[i], tb = ch * kLruC;
+    row = t0 + tb;
+    hi = L - tb < kLruC ? static_cast<int>(L - tb) : kLruC;
+    first = ch == 0;
+    last = slot + 1 == chunk0[i + 1];
+    e = static_cast<int64_t>(n) * io.D + c;
+    const TX* px = static_cast<const TX*>(io.x) + cc;
+    const TG* pg = static_cast<const TG*>(io.g) + cc;
+    const TX* py = static_cast<const TX*>(io.dO) + cc;
+    // all rows' loads first; eight rows that no lane of the wave has are left out.
+    // Places behind the last token change nothing: 1 a = a, fma(1, b, -0) = b
+    if (__all(hi == kLruC)) {  // one way for all chunks of a wave
+#pragma unroll
+      for (int j = 0; j < kLruC; ++j) {
+        al[j] = ldin(pg + (row + j) * io.ldg);
+        x[j] = ldin(px + (row + j) * io.ldx);
+        dy[j] = ldin(py + (row + j) * io.lddo);
+      }
+#pragma unroll
+      for (int j = 0; j < kLruC; ++j) {
+        const float wj = lru_weight<GATE>(al[j], al[j]);
+        if constexpr (GATE != GDN_LRU_GATE_NONE) w[j] = wj;
+      }
+    } else {
+#pragma unroll
+      for (int j0 = 0; j0 < kLruC; j0 += 8) {
+        if (__any(j0 < hi)) {
+#pragma unroll
+          for (int j = j0; j < j0 + 8; ++j) {
+            const int64_t t = row + (j < hi ? j : hi - 1);
+            al[j] = ldin(pg + t * io.ldg);
+            x[j] = ldin(px + t * io.ldx);
+            dy[j] = ldin(py + t * io.lddo);
+          }
+        } else {
+#pragma unroll
+          for (int j = j0; j < j0 + 8; ++j) al[j] = x[j] = dy[j] = 0.0f;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kLruC; ++j) {
+        const float wj = lru_weight<GATE>(al[j], al[j]);
+        const bool in = j < hi;
+        al[j] = in ? al[j] : 1.0f;
+        x[j] = in ? x[j] : -0.0f;
+        dy[j] = in ? dy[j] : -0.0f;
+        if constexpr (GATE != GDN_LRU_GATE_NONE) w[j] = in ? wj : 1.0f;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kLruC; ++j) {
+      a = al[j] * a;
+      b = fmaf(al[j], b, GATE == GDN_LRU_GATE_NONE ? x[j] : w[j] * x[j]);
+      q = fmaf(a, dy[j], q);
+    }
+    const float am = a != a ? __uint_as_float(kPlainNaN) : a, mark = __uint_as_float(kLruMark);
+    const float S0 = first && io.h0 && live ? io.h0[e] : 0.0f, K0 = last && io.dhT && live ? io.dhT[e] : 0.0f;
+    start[threadIdx.x] = S0;
+    behind[threadIdx.x] = K0;
+    up[threadIdx.x] = first ? float2{mark, fmaf(a, S0, b)} : float2{am, b};
+    down[threadIdx.x] = last ? float2{mark, fmaf(a, K0, q)} : float2{am, q};
+  }
+  __syncthreads();
+  // the chains: up by the first slot's threads, down by the last slot's
+  if (slot == 0)
+    lru_chain<true, 4>(up + col, W, nch, 0.0f, [&](int s, float v) { start[s * W + col] = v; });
+  if (slot == slots - 1)
+    lru_chain<true, 4>(down + (nch - 1) * W + col, -W, nch, 0.0f,
+                       [&](int s, float v) { behind[(nch - 1 - s) * W + col] = v; });
+  __syncthreads();
+  if (!has || !live) return;
+  if constexpr (GATE != GDN_LRU_GATE_NONE) {
+    // products w x are formed again rather than held over the chains in 32 registers more
+#pragma unroll
+    for (int j = 0; j < kLruC; ++j) asm volatile("" : "+v"(w[j]));
+  }
+  const float S = start[threadIdx.x];
+  float K = behind[threadIdx.x];
+  if (last && io.hT) io.hT[e] = fmaf(a, S, b);
+  if (first) io.dh0[e] = fmaf(a, K, q);
+  TX* o = io.o ? static_cast<TX*>(io.o) + c : nullptr;
+  TX* dx = static_cast<TX*>(io.dx) + c;
+  TG* dg = static_cast<TG*>(io.dg) + c;
+  lru_outputs<GATE, false>(al, x, dy, w, S, K, hi, row, o, io.ldo, dx, io.lddx, dg, io.lddg);
 }
 
 // The cache's positions after a prefill (from 0) or a continuation: a launch
@@ -650,9 +840,6 @@ __global__ __launch_bounds__(256) void k_lru_apply(LruIO io) {
     lru_apply<TX, TG, GATE, false>(io, k, slot, c);
 }
 
-// Outputs and gradients of one chunk of one channel: forward for h and
-//     e_i = alpha_i h_{i-1} + b'_i x_i      (dg_i = delta_i e_i)
-// then backward for delta.
 template <typename TX, typename TG, int GATE, bool WHOLE>
 __device__ __forceinline__ void lru_grad(const LruIO& io, const LruChunk& k, int64_t slot, int c) {
   const TX* x = static_cast<const TX*>(io.x) + c;
@@ -662,7 +849,7 @@ __device__ __forceinline__ void lru_grad(const LruIO& io, const LruChunk& k, int
   TX* dx = static_cast<TX*>(io.dx) + c;
   TG* dg = static_cast<TG*>(io.dg) + c;
   const float S = io.wB[slot * io.D + c];
-  float K = io.wQ[slot * io.D + c];
+  const float K = io.wQ[slot * io.D + c];
   float al[kLruC], e[kLruC], dy[kLruC], w[GATE == GDN_LRU_GATE_NONE ? 1 : kLruC];
 #pragma unroll
   for (int i = 0; i < kLruC; ++i) {
@@ -671,33 +858,12 @@ __device__ __forceinline__ void lru_grad(const LruIO& io, const LruChunk& k, int
     e[i] = ldin(x + t * io.ldx);
     dy[i] = ldin(dO + t * io.lddo);
   }
-  float a = 1.0f, b = 0.0f, hp = S;
 #pragma unroll
   for (int i = 0; i < kLruC; ++i) {
-    const float xi = e[i];
     const float wi = lru_weight<GATE>(al[i], al[i]);
-    const float u = GATE == GDN_LRU_GATE_NONE ? xi : wi * xi;
-    a = al[i] * a;
-    b = fmaf(al[i], b, u);
-    const float h = fmaf(a, S, b);
-    if (o && (WHOLE || i < k.hi)) stout(o + (k.row + i) * io.ldo, h);
-    e[i] = al[i] * hp;
-    if constexpr (GATE == GDN_LRU_GATE_COMPLEMENT) e[i] = fmaf(-al[i], xi, e[i]);
-    // b' = -alpha^2 / b, the reciprocal the hardware's (1 ulp)
-    if constexpr (GATE == GDN_LRU_GATE_NORM)
-      e[i] = fmaf(wi > 0.0f ? -(al[i] * al[i]) * __builtin_amdgcn_rcpf(wi) : 0.0f, xi, e[i]);
     if constexpr (GATE != GDN_LRU_GATE_NONE) w[i] = wi;
-    hp = h;
   }
-#pragma unroll
-  for (int i = kLruC - 1; i >= 0; --i) {
-    if (WHOLE || i < k.hi) {
-      const float d = dy[i] + K;
-      K = al[i] * d;
-      stout(dx + (k.row + i) * io.lddx, GATE == GDN_LRU_GATE_NONE ? d : w[i] * d);
-      stout(dg + (k.row + i) * io.lddg, d * e[i]);
-    }
-  }
+  lru_outputs<GATE, WHOLE>(al, e, dy, w, S, K, k.hi, k.row, o, io.ldo, dx, io.lddx, dg, io.lddg);
 }
 template <typename TX, typename TG, int GATE>
 __global__ __launch_bounds__(256) void k_lru_grad(LruIO io) {
@@ -948,6 +1114,16 @@ int gdn_lru_fwd_bwd(const gdn_lru_shape_t* shape, int32_t n_seqs, const int32_t*
   if (!ws || ws_bytes < lru_ws_bytes(shape->D, n_seqs, io.T, true)) return GDN_ERR_WORKSPACE;
   if (n_seqs == 0) return GDN_OK;
   io.x = x; io.g = g; io.h0 = h0; io.dO = dO; io.dhT = dhT; io.o = o; io.hT = hT; io.dx = dx; io.dg = dg; io.dh0 = dh0;
+  if (gdn::lru_train_plan(cu_seqlens_host, n_seqs, chunks, io.D, longest, &io.plan)) {
+    io.tiles = (io.D + io.plan.lps - 1) / io.plan.lps;
+    const int64_t items = lru_blocks(io.plan.units, io.tiles);
+    if (!lru_fits(items * io.plan.threads)) return GDN_ERR_UNSUPPORTED;
+    return lru_dispatch(shape, [&]<typename TX, typename TG, int GATE>() {
+      Timed t_("k_lru_train", st);
+      hipLaunchKernelGGL((k_lru_train<TX, TG, GATE>), dim3(static_cast<unsigned>(items)), dim3(io.plan.threads), 0, st, io);
+      return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_HIP;
+    });
+  }
   lru_ws(&io, ws, true);
   const int64_t blocks = lru_units(&io);
   if (!lru_fits(blocks * 256) || !lru_fits(2 * lru_chain_blocks(io, true) * 256)) return GDN_ERR_UNSUPPORTED;

@@ -208,12 +208,12 @@ static void lru_tile(const int32_t* cu, int32_t N, int64_t chunks, int32_t D, in
   plan->threads = static_cast<int32_t>(t < most ? t : most);
 }
 
-static void lru_pack(const int32_t* cu, int32_t N, int64_t chunks, bool resume, LruPlan* plan) {
+// Units for the plan's tile and threads; of more than kLruPack sequences as many
+// neighbours as fit a round with `each` chunks each.
+static void lru_pack(const int32_t* cu, int32_t N, int64_t each, bool resume, LruPlan* plan) {
   const int64_t slots = plan->threads / plan->lps;
   if (N > kLruPack) {
-    // a resumed sequence may take a chunk more than its tokens do
-    const int64_t mean = (chunks + N - 1) / N + (resume ? 1 : 0);
-    const int64_t per = mean > 0 ? slots / mean : kLruPack;
+    const int64_t per = each > 0 ? slots / each : kLruPack;
     plan->per = static_cast<int32_t>(per < 1 ? 1 : per > kLruPack ? kLruPack : per);
     plan->units = (N + plan->per - 1) / plan->per;
     return;
@@ -260,8 +260,32 @@ bool lru_plan(const int32_t* cu, int32_t N, int64_t chunks, int32_t D, int64_t l
   // over the chunks' places and whole waves, which is what the steps run over
   const double twice = 8.0 + 3e-6 * static_cast<double>(chunks * GDN_LRU_CHUNK) * ((D + 63) / 64 * 64);
   if (T > GDN_LRU_SMALL && twice < us) return true;
-  lru_pack(cu, N, chunks, resume, plan);
+  // on average, and a resumed sequence may take a chunk more than its tokens do
+  lru_pack(cu, N, N > 0 ? (chunks + N - 1) / N + (resume ? 1 : 0) : 0, resume, plan);
   return false;
+}
+
+// The trainer's one pass where the longest sequence fits a round of 512 threads:
+// up to 256 tokens with 64 lanes a chunk (64 x 256 tokens x 4096 channels, bf16, fp32
+// g: 255 us, three steps 358; 400 x 40 x 1024: 71 against 190), to 512 with 32 (16 x
+// 512 x 4096 141 against 180) and to 1024 with 16, where rows are narrow, in batches
+// of up to 2^24 elements (8 x 1024 x 2048 86 against 93; 32 x 1024 x 4096 698 against
+// 617).  Wider tiles are faster than narrower ones throughout, and narrower ones
+// still, 8 lanes, lose to the three steps (4 x 2048 x 1024: 50 against 48).
+// Batches of more than kLruPack sequences fill rounds for the longest one: those
+// that would leave two thirds of the places empty take the three steps (500 tokens
+// and 100 x 50, 2048 channels, seven eighths empty: 266 against 111; 250 and 300 x
+// 100, 1024 channels, half empty: 175 against 233).
+bool lru_train_plan(const int32_t* cu, int32_t N, int64_t chunks, int32_t D, int64_t longest, LruPlan* plan) {
+  int64_t each = (longest + GDN_LRU_CHUNK - 1) / GDN_LRU_CHUNK;
+  each = each > 0 ? each : 1;
+  if (each > kLruTrain / 16) return false;
+  plan->lps = each <= kLruTrain / 64 ? 64 : each <= kLruTrain / 32 ? 32 : 16;
+  if (plan->lps == 16 && chunks * GDN_LRU_CHUNK * D > 1 << 24) return false;
+  plan->threads = static_cast<int32_t>((each * plan->lps + 63) / 64 * 64);
+  lru_pack(cu, N, each, false, plan);
+  const int64_t slots = plan->threads / plan->lps;
+  return plan->per == 0 || plan->units * slots <= 3 * chunks + slots;
 }
 
 int check_qk_shape(const gdn_qk_shape_t* s) {

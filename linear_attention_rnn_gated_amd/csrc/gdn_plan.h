@@ -91,6 +91,7 @@ inline int64_t lru_slots(int64_t T, int64_t N) { return T / GDN_LRU_CHUNK + 2 * 
 // How a prefill runs (see gdn_lru.hip).
 constexpr int kLruPack = 64;       // most sequences of a unit, and those that are sorted into units
 constexpr int kLruThreads = 1024;  // most threads of a one-pass block
+constexpr int kLruTrain = 512;     // and of the trainer's
 struct LruPlan {
   int32_t lps = 64;       // lanes per chunk = channels of a block's tile: 8, 16, 32 or 64
   int32_t threads = 64;   // of a block: a multiple of 64
@@ -105,6 +106,10 @@ struct LruPlan {
 // where the three steps are expected to be faster.
 bool lru_plan(const int32_t* cu_host, int32_t n_seqs, int64_t chunks, int32_t D, int64_t longest, bool resume,
               LruPlan* plan);
+
+// Fills the plan of the trainer's one pass; false where the three steps are
+// expected to be faster or a sequence does not fit one round.
+bool lru_train_plan(const int32_t* cu_host, int32_t n_seqs, int64_t chunks, int32_t D, int64_t longest, LruPlan* plan);
 
 // Norms of q and k with rotary positions.
 int check_qk_shape(const gdn_qk_shape_t* s);

@@ -189,7 +189,7 @@ def kernels(call):
     try:
         r = call()
         torch.cuda.synchronize()
-        names = ("k_lru_fwd", "k_lru_fold", "k_lru_chain", "k_lru_apply", "k_lru_grad", "k_lru_pos")
+        names = ("k_lru_fwd", "k_lru_fold", "k_lru_chain", "k_lru_apply", "k_lru_grad", "k_lru_pos", "k_lru_train")
         return {k: B.profile_read(k)[1] for k in names}, r
     finally:
         B.profile_enable(False)
@@ -247,6 +247,53 @@ def test_batch_composition_does_not_change_bits():
     part = B.make_lru_shape(31, BF16, BF16, "norm")
     o2, _ = B.gdn_lru_prefill(part, d["x"][:, 16:47], d["g"][:, 16:47], d["cu"], h0=d["h0"][:, 16:47].contiguous())
     assert same(o2, o[:, 16:47])
+
+
+@pytest.mark.parametrize("lens,D,x,g,gate", [
+    ([100, 256, 0, 1, 33, 64], 130, "bf16", "f32", "norm"),
+    ([512, 31, 257, 32, 0, 300], 70, "f32", "bf16", "complement"),
+    ([1000, 640, 1, 90, 1024], 33, "bf16", "bf16", "none"),
+    ([0, 5, 40, 2, 64] * 20, 65, "f32", "f32", "norm"),
+    ([0, 0], 7, "f32", "f32", "none"),
+])
+def test_both_trainer_schedules_give_the_same_bits(lens, D, x, g, gate):
+    """Sequences that fit a round take one pass; with a longer one in the batch all take the three steps."""
+    p = make(lens + [1025], D, x, g, gate, seed=23)
+    d, T, N = dev(p), sum(lens), len(lens)
+
+    def run(n, T):
+        c, r = kernels(lambda: B.gdn_lru_fwd_bwd(p["shape"], d["x"][:T], d["g"][:T], d["cu"][:n + 1], d["dO"][:T],
+                                                 h0=d["h0"][:n], dhT=d["dhT"][:n]))
+        return r, (c["k_lru_train"], c["k_lru_grad"])
+    three, k = run(N + 1, T + 1025)
+    assert k == (0, 1)
+    one, k = run(N, T)
+    assert k == (1, 0)
+    for key, t in one.items():
+        assert same(t, three[key][:t.shape[0]]), key
+    bw = B.gdn_lru_fwd_bwd(p["shape"], d["x"][:T], d["g"][:T], d["cu"][:N + 1], d["dO"][:T], h0=d["h0"][:N],
+                           dhT=d["dhT"][:N], want_o=False)
+    assert all(same(t, one[key]) for key, t in bw.items())
+
+
+def test_no_nan_crosses_into_another_sequences_gradient():
+    lens = [70, 40, 33, 64, 100, 20]
+    p = make(lens, 6, "f32", "f32", "norm", seed=18)
+    cu, d = p["cu"].tolist(), dev(p)
+    train = lambda: B.gdn_lru_fwd_bwd(p["shape"], d["x"], d["g"], d["cu"], d["dO"], h0=d["h0"], dhT=d["dhT"])  # noqa: E731
+    want = train()
+    payload = torch.tensor([0xffc0dead - (1 << 32), 0x7fc00000, 0xffc0dead - (1 << 32), 0x7f800001, -1, 0x7fffffff], dtype=torch.int32)
+    d["x"][cu[0] + 5], d["dO"][cu[2] + 1] = float("nan"), float("inf")
+    d["g"][cu[1] + 36] = d["g"][cu[4] + 66] = payload.view(F32).cuda()
+    got = train()
+    for n in (3, 5):
+        for k in ("o", "dx", "dg"):
+            assert same(got[k][cu[n]:cu[n + 1]], want[k][cu[n]:cu[n + 1]]), (n, k)
+        assert same(got["hT"][n], want["hT"][n]) and same(got["dh0"][n], want["dh0"][n])
+    for n, t in ((1, 36), (4, 66)):  # states behind the NaN, gradients in front of it
+        assert bool(got["o"][cu[n] + t:cu[n + 1]].isnan().all()) and bool(got["dx"][cu[n]:cu[n] + t].isnan().all())
+        assert same(got["o"][cu[n]:cu[n] + t], want["o"][cu[n]:cu[n] + t])
+        assert same(got["dx"][cu[n] + t + 1:cu[n + 1]], want["dx"][cu[n] + t + 1:cu[n + 1]])
 
 
 def test_wide_rows_in_place_and_rows_behind():
@@ -420,6 +467,10 @@ def test_host_copy_that_disagrees_stays_inside():
     bad = torch.tensor([-5, 95, 30], dtype=torch.int32, device="cuda")
     B.gdn_lru_prefill(p["shape"], pad(x), pad(g), bad, h0=d["h0"], out=out, cu_seqlens_host=p["cu"])
     assert bool((out[80:] == 3).all())
+    dx, dg = torch.full((100, 16), 3.0, dtype=BF16, device="cuda"), torch.full((100, 16), 3.0, device="cuda")
+    B.gdn_lru_fwd_bwd(p["shape"], pad(x), pad(g), bad, pad(d["dO"]), h0=d["h0"], out=dict(o=out, dx=dx, dg=dg),
+                      cu_seqlens_host=p["cu"])
+    assert bool((out[80:] == 3).all()) and bool((dx[80:] == 3).all()) and bool((dg[80:] == 3).all())
 
 
 def test_null_host_copy():
