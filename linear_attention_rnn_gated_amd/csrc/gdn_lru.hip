@@ -630,10 +630,16 @@ struct LruChunk {
   int64_t row;
 };
 __device__ __forceinline__ bool lru_chunk(const LruIO& io, int64_t slot, LruChunk& k) {
-  int lo = 0, hi = io.N - 1;  // the last sequence that starts at or before the slot
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (lru_slot0(io, mid) <= slot) lo = mid; else hi = mid - 1;
+  // the last sequence that starts at or before the slot, by a whole wave: a place
+  // for each lane, so that 64 sequences take one trip to memory and 4096 two
+  const int lane = threadIdx.x & 63;
+  int lo = 0;
+  for (int n = io.N; n > 1;) {
+    const int step = (n + 63) >> 6, at = lane * step;
+    const int starts = __popcll(__ballot(at < n && lru_slot0(io, lo + at) <= slot));
+    const int skip = starts > 1 ? (starts - 1) * step : 0;
+    lo += skip;
+    n = n - skip < step ? n - skip : step;
   }
   k.n = lo;
   int64_t t0, L;
@@ -651,15 +657,15 @@ __device__ __forceinline__ int64_t lru_row(const LruChunk& k, int i) {
   return k.row + (WHOLE ? i : (i < k.lo ? k.lo : (i >= k.hi ? k.hi - 1 : i)));
 }
 
-// The block's slot and the lane's first channel; false past the ends.
+// The wave's slot and the lane's channel; false past the slots.
 __device__ __forceinline__ bool lru_unit(const LruIO& io, int64_t& slot, int& c) {
   const int per = 256 / io.cw;
   const int groups = (io.D + io.cw - 1) / io.cw;
   const int64_t b = blockIdx.x;
-  const int sub = threadIdx.x / io.cw;
+  const int sub = __builtin_amdgcn_readfirstlane(threadIdx.x) / io.cw;  // io.cw is 64 at least
   slot = b / groups * per + sub;
   c = static_cast<int>(b % groups) * io.cw + static_cast<int>(threadIdx.x) - sub * io.cw;
-  return slot < io.slots && c < io.D;
+  return slot < io.slots;
 }
 
 template <typename TX, typename TG, int GATE, bool GRAD, bool WHOLE>
@@ -708,7 +714,7 @@ __global__ __launch_bounds__(256) void k_lru_fold(LruIO io) {
   int64_t slot;
   int c;
   LruChunk k;
-  if (!lru_unit(io, slot, c) || !lru_chunk(io, slot, k)) return;
+  if (!lru_unit(io, slot, c) || !lru_chunk(io, slot, k) || c >= io.D) return;
   if (k.lo == 0 && k.hi == kLruC)
     lru_fold<TX, TG, GATE, GRAD, true>(io, k, slot, c);
   else
@@ -833,7 +839,7 @@ __global__ __launch_bounds__(256) void k_lru_apply(LruIO io) {
   int64_t slot;
   int c;
   LruChunk k;
-  if (!lru_unit(io, slot, c) || !lru_chunk(io, slot, k)) return;
+  if (!lru_unit(io, slot, c) || !lru_chunk(io, slot, k) || c >= io.D) return;
   if (k.lo == 0 && k.hi == kLruC)
     lru_apply<TX, TG, GATE, true>(io, k, slot, c);
   else
@@ -870,7 +876,7 @@ __global__ __launch_bounds__(256) void k_lru_grad(LruIO io) {
   int64_t slot;
   int c;
   LruChunk k;
-  if (!lru_unit(io, slot, c) || !lru_chunk(io, slot, k)) return;
+  if (!lru_unit(io, slot, c) || !lru_chunk(io, slot, k) || c >= io.D) return;
   if (k.hi == kLruC)
     lru_grad<TX, TG, GATE, true>(io, k, slot, c);
   else
@@ -946,21 +952,21 @@ int64_t lru_units(LruIO* io) {
 // blocks a CU, or, for longer sequences in no more blocks than CUs, where each
 // round's latency is what counts, of 512 chunks x 16 channels (whole prefills, us:
 // 12 sequences to 14162 tokens x 200 channels 41 against 45, 16 to 14617 x 109 33
-// against 38; but 15 to 4475 x 972 in 915 blocks 58 against 52).
-int64_t lru_chain_blocks(const LruIO& io, bool deep) {
-  const int w = deep ? 16 : 32;
-  return io.N * static_cast<int64_t>((io.D + w - 1) / w);
-}
-bool lru_deep(const LruIO& io, int64_t longest) {
-  return longest > 128 * kLruC && lru_chain_blocks(io, true) <= 256;
-}
-void lru_launch_chain(const LruIO& io, bool deep, int directions, hipStream_t st) {
-  const dim3 grid(static_cast<unsigned>(lru_chain_blocks(io, deep)), directions);
+// against 38; but 15 to 4475 x 972 in 915 blocks 58 against 52), or, for many
+// sequences of up to 64 chunks, where blocks are what counts, of 8 x 256 (whole
+// training calls: one of 1000 tokens and 1000 of 30, 1024 channels 206 against 368;
+// 2000 and 100 x 100, 2048 channels, 6464 blocks of 32 143 against 167; 2000 and 30
+// x 100 in 1984 blocks 69 against 69; 41 of 2000 x 512 in 656 blocks 216 against 214).
+int64_t lru_chain_blocks(const LruIO& io, int w) { return io.N * static_cast<int64_t>((io.D + w - 1) / w); }
+void lru_launch_chain(const LruIO& io, int64_t longest, int directions, hipStream_t st) {
   Timed t_("k_lru_chain", st);
-  if (deep)
-    hipLaunchKernelGGL((k_lru_chain<16, 512>), grid, dim3(256), 0, st, io);
+  auto grid = [&](int w) { return dim3(static_cast<unsigned>(lru_chain_blocks(io, w)), directions); };
+  if (longest > 128 * kLruC && lru_chain_blocks(io, 16) <= 256)
+    hipLaunchKernelGGL((k_lru_chain<16, 512>), grid(16), dim3(256), 0, st, io);
+  else if (longest <= 64 * kLruC && lru_chain_blocks(io, 32) > 2048)
+    hipLaunchKernelGGL((k_lru_chain<256, 8>), grid(256), dim3(256), 0, st, io);
   else
-    hipLaunchKernelGGL((k_lru_chain<32, 128>), grid, dim3(256), 0, st, io);
+    hipLaunchKernelGGL((k_lru_chain<32, 128>), grid(32), dim3(256), 0, st, io);
 }
 // A launch holds fewer than 2^32 threads.
 bool lru_fits(int64_t threads) { return threads < (int64_t{1} << 32); }
@@ -997,7 +1003,7 @@ int lru_prefill_entry(const gdn_lru_shape_t* shape, int32_t n_seqs, const int32_
     io.tiles = (io.D + io.plan.lps - 1) / io.plan.lps;
     blocks = lru_blocks(io.plan.units, io.tiles);
   }
-  if (!lru_fits(blocks * threads) || (three && !lru_fits(lru_chain_blocks(io, true) * 256))) return GDN_ERR_UNSUPPORTED;
+  if (!lru_fits(blocks * threads) || (three && !lru_fits(lru_chain_blocks(io, 16) * 256))) return GDN_ERR_UNSUPPORTED;
   lru_dispatch(shape, [&]<typename TX, typename TG, int GATE>() {
     const dim3 grid(static_cast<unsigned>(blocks)), block(threads);
     if (!three) {
@@ -1009,7 +1015,7 @@ int lru_prefill_entry(const gdn_lru_shape_t* shape, int32_t n_seqs, const int32_
       Timed t_("k_lru_fold", st);
       hipLaunchKernelGGL((k_lru_fold<TX, TG, GATE, false>), grid, block, 0, st, io);
     }
-    lru_launch_chain(io, lru_deep(io, longest), 1, st);
+    lru_launch_chain(io, longest, 1, st);
     Timed t_("k_lru_apply", st);
     hipLaunchKernelGGL((k_lru_apply<TX, TG, GATE>), grid, block, 0, st, io);
     return GDN_OK;
@@ -1126,14 +1132,14 @@ int gdn_lru_fwd_bwd(const gdn_lru_shape_t* shape, int32_t n_seqs, const int32_t*
   }
   lru_ws(&io, ws, true);
   const int64_t blocks = lru_units(&io);
-  if (!lru_fits(blocks * 256) || !lru_fits(2 * lru_chain_blocks(io, true) * 256)) return GDN_ERR_UNSUPPORTED;
+  if (!lru_fits(blocks * 256) || !lru_fits(2 * lru_chain_blocks(io, 16) * 256)) return GDN_ERR_UNSUPPORTED;
   return lru_dispatch(shape, [&]<typename TX, typename TG, int GATE>() {
     const dim3 grid(static_cast<unsigned>(blocks)), block(256);
     {
       Timed t_("k_lru_fold", st);
       hipLaunchKernelGGL((k_lru_fold<TX, TG, GATE, true>), grid, block, 0, st, io);
     }
-    lru_launch_chain(io, lru_deep(io, longest), 2, st);
+    lru_launch_chain(io, longest, 2, st);
     Timed t_("k_lru_grad", st);
     hipLaunchKernelGGL((k_lru_grad<TX, TG, GATE>), grid, block, 0, st, io);
     return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_HIP;

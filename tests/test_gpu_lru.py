@@ -276,6 +276,22 @@ def test_both_trainer_schedules_give_the_same_bits(lens, D, x, g, gate):
     assert all(same(t, one[key]) for key, t in bw.items())
 
 
+def test_trainer_of_many_sequences_next_to_a_long_one():
+    """Enough sequences for the chains to go over many channels a block; the first four of them alone give the same bits."""
+    lens = [1300] + [20, 0, 33] * 70
+    p = make(lens, 330, "bf16", "f32", "norm", seed=29)
+    d, T = dev(p), int(p["cu"][4])
+    many = B.gdn_lru_fwd_bwd(p["shape"], d["x"], d["g"], d["cu"], d["dO"], h0=d["h0"], dhT=d["dhT"])
+    few = B.gdn_lru_fwd_bwd(p["shape"], d["x"][:T], d["g"][:T], d["cu"][:5], d["dO"][:T], h0=d["h0"][:4], dhT=d["dhT"][:4])
+    for key, t in few.items():
+        assert same(t, many[key][:t.shape[0]]), key
+    last = lambda name, n: d[name][-n:].clone()  # noqa: E731
+    one = B.gdn_lru_fwd_bwd(p["shape"], last("x", 33), last("g", 33), torch.tensor([0, 33], dtype=torch.int32, device="cuda"),
+                            last("dO", 33), h0=last("h0", 1), dhT=last("dhT", 1))
+    for key, t in one.items():
+        assert same(t, many[key][-t.shape[0]:]), key
+
+
 def test_no_nan_crosses_into_another_sequences_gradient():
     lens = [70, 40, 33, 64, 100, 20]
     p = make(lens, 6, "f32", "f32", "norm", seed=18)
