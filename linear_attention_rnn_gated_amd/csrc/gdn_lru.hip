@@ -644,8 +644,11 @@ __device__ __forceinline__ bool lru_chunk(const LruIO& io, int64_t slot, LruChun
   k.n = lo;
   int64_t t0, L;
   lru_rows(io, lo, t0, L);
-  const int64_t tb = (slot - lru_slot0(io, lo)) * kLruC - (io.resume ? lru_pos(io, lo, 0) : 0);
-  if (L == 0 || tb >= L) return false;  // (an empty sequence may stand inside a chunk: tb < 0)
+  const int p0 = io.resume ? lru_pos(io, lo, 0) : 0;
+  const int64_t tb = (slot - lru_slot0(io, lo)) * kLruC - p0;
+  // An empty sequence may stand inside a chunk (tb < 0); a slot in front of its sequence's first (tb < -p0) comes from
+  // a device copy of cu_seqlens that is not the host's: one that starts behind row 0 or steps back.
+  if (L == 0 || tb < -p0 || tb >= L) return false;
   k.row = t0 + tb;
   k.lo = tb < 0 ? static_cast<int>(-tb) : 0;
   k.hi = L - tb < kLruC ? static_cast<int>(L - tb) : kLruC;

@@ -631,3 +631,33 @@ def test_kernel_timing_names():
         assert n == 2 and ms > 0
     finally:
         B.profile_enable(False)
+
+
+STRAY = [[100, 6000, 6045], [-5, 7000, 30], [6045, 0, 6045], [3000, 3000, 3000], [6044, 6045, 1 << 30], [-(1 << 31), -1, 0]]
+
+
+@pytest.mark.parametrize("stray", STRAY)
+def test_host_copy_that_disagrees_stays_inside_three_steps(stray):
+    """The schedules that keep chunks in the workspace, whose places follow from the device copy: a copy that starts behind
+    row 0, steps back or ends elsewhere reads no cache that is not there and touches only the rows [0, T)."""
+    lens, D, T = [6000, 45], 40, 6045
+    p = make(lens, D, seed=62)
+    d = dev(p)
+    pad = lambda t: torch.cat([t, t[:60]])  # noqa: E731
+    fresh = lambda dt=BF16: torch.full((T + 60, D), 3.0, dtype=dt, device="cuda")  # noqa: E731
+    bad = torch.tensor(stray, dtype=torch.int32, device="cuda")
+    x, g, dO = pad(d["x"]), pad(d["g"]), pad(d["dO"])
+    cache = B.gdn_lru_cache_init(p["shape"], 2, "cuda", h0=d["h0"])
+    cache.pos.fill_(17)
+    for call in (lambda o: B.gdn_lru_prefill(p["shape"], x, g, bad, h0=d["h0"], out=o, cu_seqlens_host=p["cu"]),
+                 lambda o: B.gdn_lru_prefill_continue(p["shape"], x, g, bad, cache, out=o, cu_seqlens_host=p["cu"])):
+        out = fresh()
+        n, (_, hT) = kernels(lambda: call(out))
+        assert n["k_lru_fold"] == n["k_lru_apply"] == 1 and hT.shape == (2, D)
+        assert bool((out[T:] == 3).all())
+    out = dict(o=fresh(), dx=fresh(), dg=fresh(F32))
+    n, _ = kernels(lambda: B.gdn_lru_fwd_bwd(p["shape"], x, g, bad, dO, h0=d["h0"], out=out, cu_seqlens_host=p["cu"]))
+    assert n["k_lru_fold"] == n["k_lru_grad"] == 1
+    assert all(bool((t[T:] == 3).all()) for t in out.values())
+    # the right copy gives the right bits after it
+    assert same(prefill(p)[0], B.gdn_lru_fwd_bwd(p["shape"], d["x"], d["g"], d["cu"], d["dO"], h0=d["h0"])["o"])
