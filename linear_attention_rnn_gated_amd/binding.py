@@ -610,9 +610,23 @@ def lru_workspace_bytes(shape, n_seqs, total_tokens, op=OP_FWD_BWD):
     return int(lib().gdn_lru_workspace_bytes(ctypes.byref(shape), n_seqs, total_tokens, op))
 
 
+def _cache_tensor(name):
+    """A tensor attribute of LruCache: assigning another one drops the struct of addresses."""
+    held = "_" + name
+
+    def get(self):
+        return getattr(self, held)
+
+    def put(self, t):
+        setattr(self, held, t)
+        self._struct = None
+    return property(get, put)
+
+
 class LruCache:
     """Decode cache (gdn_lru_cache_t) of n sequences of D channels, owned by
-    torch tensors."""
+    torch tensors.  S, A, B and pos may be assigned (a reordered batch, say); the
+    next call checks and takes the tensors that are there then."""
 
     def __init__(self, D, n, device):
         f32 = dict(dtype=torch.float32, device=device)
@@ -624,37 +638,47 @@ class LruCache:
         """A cache over existing tensors: S, A, B fp32 [n, D], pos int32
         [n, ceil(D / 256)]."""
         c = object.__new__(cls)
-        n, D = S.shape
-        dev = _gpu(S, "S")
-        for t, name in ((S, "S"), (A, "A"), (B, "B")):
-            _dense(t, torch.float32, (n, D), dev, name)
-        _dense(pos, torch.int32, (n, -(-D // LRU_GROUP)), dev, "pos")
+        _gpu(S, "S")
         c._hold(S, A, B, pos)
+        c.struct()
         return c
+
+    S, A, B, pos = (_cache_tensor(name) for name in ("S", "A", "B", "pos"))
+    n = property(lambda self: self._S.shape[0])
+    D = property(lambda self: self._S.shape[1])
+    device = property(lambda self: self._S.device)
 
     def _hold(self, S, A, B, pos):
         self.S, self.A, self.B, self.pos = S, A, B, pos
-        self.n, self.D = S.shape
-        self.device = S.device
-        self._struct = LruCacheStruct(S.data_ptr(), A.data_ptr(), B.data_ptr(), pos.data_ptr())
 
     def struct(self):
+        # an assignment drops the struct; a tensor given other memory in place moves its address
+        at = (self._S.data_ptr(), self._A.data_ptr(), self._B.data_ptr(), self._pos.data_ptr())
+        if self._struct is None or at != self._at:
+            (n, D), dev = self._S.shape, self._S.device
+            for t, name in ((self._S, "S"), (self._A, "A"), (self._B, "B")):
+                _dense(t, torch.float32, (n, D), dev, name)
+            _dense(self._pos, torch.int32, (n, -(-D // LRU_GROUP)), dev, "pos")
+            self._at, self._fits, self._struct = at, (n, D, dev), LruCacheStruct(*at)
         return self._struct
 
     def tensors(self):
-        return [self.S, self.A, self.B, self.pos]
+        return [self._S, self._A, self._B, self._pos]
 
     def state(self):
         """The states now, [n, D]: A S + B."""
-        return self.A * self.S + self.B
+        return self._A * self._S + self._B
 
     def clone(self):
         return LruCache.of(*[t.clone() for t in self.tensors()])
 
     def check(self, shape, n, dev):
-        if self.n != n or self.D != shape.D or self.device != dev:
+        """The struct, after checking that it is one of n sequences on dev."""
+        struct = self.struct()
+        if self._fits != (n, shape.D, dev):
             raise ValueError(f"cache: expected {n} sequences of {shape.D} channels on {dev}, got "
                              f"{self.n} of {self.D} on {self.device}")
+        return struct
 
 
 def gdn_lru_cache_init(shape, n, device, h0=None):
@@ -680,9 +704,7 @@ def _lru_prefill(name, shape, x, g, cu_seqlens, h0, cache, want_hT, ws, out, hT_
     if hT is None and want_hT:
         hT = torch.empty(n, D, dtype=torch.float32, device=dev)
     p_hT = _optional(hT, torch.float32, (n, D), dev, "hT_out")
-    if cache is not None:
-        cache.check(shape, n, dev)
-    cs = None if cache is None else ctypes.byref(cache.struct())
+    cs = None if cache is None else ctypes.byref(cache.check(shape, n, dev))
     tail = (None, 0)
     if T > LRU_SMALL:
         ws = _scratch(ws, lru_workspace_bytes(shape, n, T, OP_PREFILL), dev,
@@ -724,9 +746,9 @@ def gdn_lru_decode_step(shape, x, g, cache, out=None):
     ldg = _rows(g, _DTYPES.get(shape.g_dtype), n, D, dev, "g")
     o = torch.empty(n, D, dtype=xt, device=dev) if out is None else out
     ldo = _rows(o, xt, n, D, dev, "out")
-    cache.check(shape, n, dev)
+    cs = cache.check(shape, n, dev)
     _launch("gdn_lru_decode_step", dev, ctypes.byref(shape), n, x.data_ptr(), ldx, g.data_ptr(),
-            ldg, ctypes.byref(cache.struct()), o.data_ptr(), ldo)
+            ldg, ctypes.byref(cs), o.data_ptr(), ldo)
     return o
 
 

@@ -661,3 +661,31 @@ def test_host_copy_that_disagrees_stays_inside_three_steps(stray):
     assert all(bool((t[T:] == 3).all()) for t in out.values())
     # the right copy gives the right bits after it
     assert same(prefill(p)[0], B.gdn_lru_fwd_bwd(p["shape"], d["x"], d["g"], d["cu"], d["dO"], h0=d["h0"])["o"])
+
+
+def test_a_reordered_cache_continues_its_sequences():
+    """A batch whose cache tensors are assigned in another order, then cut: decode and continuation go on with what was
+    assigned."""
+    lens, D = [40, 7, 64, 33], 300
+    p = make(lens, D, seed=63)
+    d = dev(p)
+    cache = B.LruCache(D, 4, "cuda")
+    prefill(p, cache=cache)
+    fixed, step = cache.clone(), make([1] * 4, D, seed=64)
+    x, g = step["x"].cuda(), step["g"].cuda()
+    want = B.gdn_lru_decode_step(p["shape"], x, g, fixed)
+    order = torch.tensor([2, 0, 3, 1], device="cuda")
+    cache.S, cache.A, cache.B, cache.pos = (t[order] for t in cache.tensors())
+    assert same(B.gdn_lru_decode_step(p["shape"], x[order], g[order], cache), want[order])
+    for a, b in zip(cache.tensors(), fixed.tensors()):
+        assert torch.equal(a.view(torch.int32), b[order].view(torch.int32))
+    cache.S, cache.A, cache.B, cache.pos = (t[1:3].clone() for t in cache.tensors())
+    cu = torch.tensor([0, 5, 12], dtype=torch.int32, device="cuda")
+    some = fixed.clone()
+    some = B.LruCache.of(*[t[order[1:3]].contiguous() for t in some.tensors()])
+    a, _ = B.gdn_lru_prefill_continue(p["shape"], d["x"][:12], d["g"][:12], cu, cache)
+    b, _ = B.gdn_lru_prefill_continue(p["shape"], d["x"][:12], d["g"][:12], cu, some)
+    assert same(a, b) and all(torch.equal(s.view(torch.int32), t.view(torch.int32)) for s, t in zip(cache.tensors(), some.tensors()))
+    cache.A = cache.A[:1]
+    with pytest.raises(ValueError):
+        B.gdn_lru_decode_step(p["shape"], x[:2], g[:2], cache)

@@ -364,3 +364,40 @@ def test_qk_oracle_rotation_is_relative():
     for layout in ("half", "interleaved"):
         y = lambda v, p: qk_fwd(v, "none", layout, 8, [p], freq)[0]  # noqa: E731
         assert abs((y(a, 5) * y(b, 2)).sum() - (y(a, 1005) * y(b, 1002)).sum()) < 1e-12
+
+
+# ---- the cache's tensors -------------------------------------------------------
+
+
+def test_cache_follows_assigned_tensors():
+    """The struct of addresses is that of the tensors which the cache holds at the call."""
+    c = B.LruCache(300, 4, "cpu")
+    at = lambda: tuple(getattr(c.struct(), k) for k in ("S", "A", "B", "pos"))  # noqa: E731
+    now = lambda: tuple(t.data_ptr() for t in c.tensors())  # noqa: E731
+    assert at() == now() and c.struct() is c.struct()
+    for name in ("S", "A", "B", "pos"):
+        old = getattr(c, name)
+        setattr(c, name, old[[2, 0, 3, 1]])
+        assert getattr(c, name).data_ptr() != old.data_ptr() and at() == now(), name
+    c.B.set_(torch.zeros(4, 300))            # other memory under the same tensor
+    assert at() == now()
+    order = torch.tensor([1, 3])
+    c.S, c.A, c.B, c.pos = (t[order] for t in c.tensors())
+    c.check(B.make_lru_shape(300, torch.float32), 2, torch.device("cpu"))
+    assert (c.n, c.D) == (2, 300) and at() == now()
+    c.S, c.A, c.B, c.pos = (t[:1] for t in c.tensors())     # the same addresses, fewer sequences
+    assert at() == now() and c.n == 1
+    with pytest.raises(ValueError):
+        c.check(B.make_lru_shape(300, torch.float32), 2, torch.device("cpu"))
+
+
+@pytest.mark.parametrize("name,bad", [
+    ("A", torch.zeros(3, 8)), ("B", torch.zeros(4, 9)), ("S", torch.zeros(4, 16)[:, ::2]), ("A", torch.zeros(4, 8).double()),
+    ("pos", torch.zeros(4, 2, dtype=torch.int32)), ("pos", torch.zeros(4, 1, dtype=torch.int64)),
+    ("B", torch.zeros(8, 4).t()), ("S", torch.zeros(5, 8)),
+])
+def test_cache_refuses_tensors_that_do_not_fit(name, bad):
+    c = B.LruCache(8, 4, "cpu")
+    setattr(c, name, bad)
+    with pytest.raises(ValueError):
+        c.struct()
