@@ -113,7 +113,8 @@ __device__ __forceinline__ float lru_weight(float g, float& a) {
   a = r.a;
   if constexpr (GATE == GDN_LRU_GATE_NONE) return 1.0f;
   if constexpr (GATE == GDN_LRU_GATE_COMPLEMENT) return r.m;
-  return __builtin_amdgcn_sqrtf(fmaxf(r.m * (1.0f + r.a), 0.0f));
+  const float w = r.m * (1.0f + r.a);
+  return __builtin_amdgcn_sqrtf(w < 0.0f ? 0.0f : w);  // (a maximum would turn a NaN into 0)
 }
 // u = b x; without a gate x itself.
 template <int GATE>

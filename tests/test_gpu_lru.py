@@ -689,3 +689,22 @@ def test_a_reordered_cache_continues_its_sequences():
     cache.A = cache.A[:1]
     with pytest.raises(ValueError):
         B.gdn_lru_decode_step(p["shape"], x[:2], g[:2], cache)
+
+
+@pytest.mark.parametrize("gate", ["none", "complement", "norm"])
+@pytest.mark.parametrize("lens", [[70, 40], [1100, 40]])
+def test_a_nan_decay_reaches_its_own_tokens_gradient(lens, gate):
+    """Both trainer schedules: a NaN in g makes dx at that token NaN where its weight depends on g, and dg always; the last
+    token's dx without a gate is dO + dhT."""
+    p = make(lens, 6, "f32", "f32", gate, seed=65)
+    d, t = dev(p), lens[0] - 1
+    at = [t, 33, sum(lens) - 1]
+    d["g"][at[0], 1], d["g"][at[1], 2], d["g"][at[2], 3] = (float("nan"),) * 3
+    n, r = kernels(lambda: B.gdn_lru_fwd_bwd(p["shape"], d["x"], d["g"], d["cu"], d["dO"], h0=d["h0"], dhT=d["dhT"]))
+    assert n["k_lru_train"] == (lens[0] < 1024) and n["k_lru_grad"] == (lens[0] > 1024)
+    for row, c in zip(at, (1, 2, 3)):
+        assert bool(r["dg"][row, c].isnan()) and bool(r["o"][row, c].isnan())
+        assert bool(r["dx"][row, c].isnan()) == (gate != "none"), (row, c)
+    want, _ = lru_bwd(np64(d["x"]), np64(d["g"]), p["cu"].tolist(), gate, np64(d["dO"]), np64(d["h0"]), np64(d["dhT"]))
+    for k in ("dx", "dg", "dh0"):
+        assert np.array_equal(np.isnan(np64(r[k])), np.isnan(want[k])), k
