@@ -298,8 +298,8 @@ int gdn_decode_step_native(const gdn_shape_t* shape, int32_t n_seqs, const void*
  *     o_t     = h_t
  *
  * with b_t = 1 (GDN_LRU_GATE_NONE), 1 - alpha_t (GDN_LRU_GATE_COMPLEMENT) or
- * sqrt(max(0, 1 - alpha_t^2)) (GDN_LRU_GATE_NORM).  g_t = -inf resets the
- * state; g_t <= 0 is meant, larger values follow the same formulas.
+ * sqrt(max(0, 1 - alpha_t^2)) (GDN_LRU_GATE_NORM; 0 where 1 - alpha_t^2 <
+ * 2^-126, that is for g_t above -2^-127).  g_t = -inf resets a finite state.
  *
  * As above, chunks are counted from each sequence's first token, here of
  * GDN_LRU_CHUNK tokens, whatever the batch.  Within a chunk
@@ -309,6 +309,14 @@ int gdn_decode_step_native(const gdn_shape_t* shape, int32_t n_seqs, const void*
  * starts from its last h.  Prefill, continuation, decode and the trainer's
  * forward run these operations in this order, so they give bit-identical o and
  * states, for any batch composition.
+ *
+ * Range: g_t <= 0 is meant.  Where g_t > 0, the sum of g over a chunk's tokens
+ * up to any of them has to stay below 88.7: past that A_p is infinite in fp32,
+ * and A_p S is NaN (S = 0) or infinite whatever the state.  At the other end
+ * A_p has fewer bits below 2^-126 and none below 2^-150, so that what is left
+ * of a state S that a chunk takes down so far is off by up to 2^-145 |S|: for
+ * |S| < 2^19 less than fp32's smallest normal number.  The gradient's products
+ * are these A_p too.
  *
  * Rows: x, o, dO and dx hold D channels in in_dtype, g and dg in g_dtype; ldx,
  * ldg, ... is the distance between tokens' rows in elements (0 = D, and at

@@ -602,7 +602,8 @@ def _packed(cu_seqlens, cu_seqlens_host, dev, T):
 def make_lru_shape(D, in_dtype, g_dtype=torch.float32, gate="none"):
     """Shape of a gated linear recurrence of D channels: x, o in in_dtype, the
     log decay g in g_dtype; gate "none", "complement" or "norm" gives the
-    input's weight 1, 1 - alpha or sqrt(1 - alpha^2)."""
+    input's weight 1, 1 - alpha or sqrt(1 - alpha^2).  g <= 0 is meant; the sum
+    of larger ones over 32 tokens has to stay below 88.7 (see include/gdn.h)."""
     return LruShape(D, _DTYPE_CODES[in_dtype], _DTYPE_CODES[g_dtype], LRU_GATES[gate])
 
 

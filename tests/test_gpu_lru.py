@@ -708,3 +708,66 @@ def test_a_nan_decay_reaches_its_own_tokens_gradient(lens, gate):
     want, _ = lru_bwd(np64(d["x"]), np64(d["g"]), p["cu"].tolist(), gate, np64(d["dO"]), np64(d["h0"]), np64(d["dhT"]))
     for k in ("dx", "dg", "dh0"):
         assert np.array_equal(np.isnan(np64(r[k])), np.isnan(want[k])), k
+
+
+@pytest.mark.parametrize("T", [64 * 3 + 5, 12000])
+def test_growth_and_decay_to_the_ends_of_the_range(T):
+    """Chunks whose sums of g go up to 88 and down by 88, in both schedules: within the oracle's bound, and 2^-145 of the
+    largest state for what a chunk takes down below fp32's normal numbers (32 products, each off by 2^-150 at most)."""
+    p = make([T], 40, "f32", "f32", "none", h0=False, seed=66)
+    rise = (torch.arange(T) // 32 % 2 == 0)[:, None]
+    p["g"] = torch.where(rise, 2.75, -2.75).expand(T, 40).contiguous()
+    p["x"] = p["x"] * 1e-3
+    p["x"][:31, 5] = 0.0                # a zero state and a zero sum up to the chunk's last token
+    n, (o, hT) = kernels(lambda: prefill(p))
+    assert n["k_lru_fold"] == (T > 2048)
+    ro, rh, eo, eh = lru_fwd(np64(p["x"]), np64(p["g"]), [0, T], "none")
+    lost = 2.0 ** -145 * np.abs(ro).max(0)
+    check(o, ro, eo + lost, "o")
+    check(hT, rh, eh + lost, "hT")
+    assert float(o[:31, 5].abs().max()) == 0.0 and same(o[31, 5], p["x"][31, 5].cuda())
+    assert float(o.abs().max()) > 1e33
+
+
+@pytest.mark.parametrize("long", [False, True])
+def test_gradient_of_a_growing_chunk(long):
+    """One chunk whose g sums to 88, alone and next to a sequence past a round, in both trainer schedules."""
+    lens = [32] + ([1100] if long else [])
+    p = make(lens, 8, "f32", "f32", "none", seed=67)
+    p["g"][:32] = 2.75
+    for k in ("x", "dO", "h0", "dhT"):
+        p[k] = p[k] * 1e-3
+    d = dev(p)
+    n, r = kernels(lambda: B.gdn_lru_fwd_bwd(p["shape"], d["x"], d["g"], d["cu"], d["dO"], h0=d["h0"], dhT=d["dhT"]))
+    assert n["k_lru_grad"] == long
+    want, bound = lru_bwd(np64(p["x"]), np64(p["g"]), p["cu"].tolist(), "none", np64(p["dO"]), np64(p["h0"]), np64(p["dhT"]))
+    for k in ("dx", "dg", "dh0"):
+        check(r[k], want[k], bound[k], k)
+    assert float(r["dh0"][0].abs().max()) > 1e32
+
+
+def test_a_state_that_a_chunk_takes_below_the_normal_numbers():
+    p = make([32], 4, "f32", "f32", "none", seed=68)
+    p["g"].fill_(float(np.log(0.03)))
+    p["x"].zero_()
+    p["h0"] = torch.tensor([[1e30, -1e25, 1.0, 3e38]])
+    o, _ = prefill(p)
+    ro, _, eo, _ = lru_fwd(np64(p["x"]), np64(p["g"]), [0, 32], "none", np64(p["h0"]))
+    check(o, ro, eo + 2.0 ** -145 * np.abs(np64(p["h0"])), "o")
+
+
+def test_weights_at_the_smallest_decays():
+    """b = 1 - alpha and sqrt(1 - alpha^2) for |g| down to 2^-126; the root's is 0 for the few values below."""
+    g = -torch.tensor([[2.0 ** -126, 1.5 * 2.0 ** -126, 1e-37, 1e-30, 1e-20, 1e-8, 3e-5, 0.01]])
+    cu = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    x, gd = torch.ones(1, 8, device="cuda"), g.cuda()
+    for gate in ("complement", "norm"):
+        o, _ = B.gdn_lru_prefill(B.make_lru_shape(8, F32, F32, gate), x, gd, cu)
+        ro, _, eo, _ = lru_fwd(np.ones((1, 8)), np64(g), [0, 1], gate)
+        off = np.abs(np64(o) - ro)
+        assert (off <= eo + 2.0 ** -24 * ro + 2.0 ** -148).all(), (gate, off / ro)
+    tiny = -torch.tensor([[0.0, 1e-45, 1e-40, 2.0 ** -128]]).repeat(1, 2).cuda()
+    s = B.make_lru_shape(8, F32, F32, "norm")
+    o, _ = B.gdn_lru_prefill(s, x, tiny, cu)
+    r = B.gdn_lru_fwd_bwd(s, x, tiny, cu, x)
+    assert bool((o == 0).all()) and bool((r["dg"] == 0).all()) and bool((r["dx"] == 0).all())
