@@ -326,6 +326,9 @@ int gdn_decode_step_native(const gdn_shape_t* shape, int32_t n_seqs, const void*
  * conventions at the top hold (16-byte aligned starts, cu_seqlens in a device
  * and a host copy, host copy nullable); a host copy that disagrees with the
  * device copy gives wrong values, never an access outside the rows [0, T).
+ * A batch whose launches would hold 2^32 threads is refused
+ * (GDN_ERR_UNSUPPORTED); none is where N max(D, 64) <= 2^24 and T max(D, 64)
+ * <= 2^35.
  */
 #define GDN_LRU_CHUNK 32
 
@@ -436,7 +439,7 @@ int gdn_lru_fwd_bwd(const gdn_lru_shape_t* shape, int32_t n_seqs, const int32_t*
  *
  * Supported: d a multiple of 8 up to 512, r a multiple of 8 up to d (0: no
  * rotation, inv_freq may be NULL), H_q >= 1, H_k >= 0 (0: k is not touched),
- * fp32 or bf16 on either side.
+ * together at most 4096, fp32 or bf16 on either side.
  */
 typedef enum { GDN_NORM_NONE = 0, GDN_NORM_L2 = 1, GDN_NORM_RMS = 2 } gdn_norm_t;
 typedef enum { GDN_ROPE_HALF = 0, GDN_ROPE_INTERLEAVED = 1 } gdn_rope_layout_t;

@@ -952,28 +952,18 @@ int64_t lru_units(LruIO* io) {
   const int64_t per = 256 / io->cw, groups = (io->D + io->cw - 1) / io->cw;
   return (io->slots + per - 1) / per * groups;
 }
-// The chain's launch: rounds of 128 chunks x 32 channels in 32 KB of LDS, five
-// blocks a CU, or, for longer sequences in no more blocks than CUs, where each
-// round's latency is what counts, of 512 chunks x 16 channels (whole prefills, us:
-// 12 sequences to 14162 tokens x 200 channels 41 against 45, 16 to 14617 x 109 33
-// against 38; but 15 to 4475 x 972 in 915 blocks 58 against 52), or, for many
-// sequences of up to 64 chunks, where blocks are what counts, of 8 x 256 (whole
-// training calls: one of 1000 tokens and 1000 of 30, 1024 channels 206 against 368;
-// 2000 and 100 x 100, 2048 channels, 6464 blocks of 32 143 against 167; 2000 and 30
-// x 100 in 1984 blocks 69 against 69; 41 of 2000 x 512 in 656 blocks 216 against 214).
-int64_t lru_chain_blocks(const LruIO& io, int w) { return io.N * static_cast<int64_t>((io.D + w - 1) / w); }
-void lru_launch_chain(const LruIO& io, int64_t longest, int directions, hipStream_t st) {
+// The chain's launch, of the width that gdn::lru_chain_width gives.
+void lru_launch_chain(const LruIO& io, int width, int directions, hipStream_t st) {
   Timed t_("k_lru_chain", st);
-  auto grid = [&](int w) { return dim3(static_cast<unsigned>(lru_chain_blocks(io, w)), directions); };
-  if (longest > 128 * kLruC && lru_chain_blocks(io, 16) <= 256)
-    hipLaunchKernelGGL((k_lru_chain<16, 512>), grid(16), dim3(256), 0, st, io);
-  else if (longest <= 64 * kLruC && lru_chain_blocks(io, 32) > 2048)
-    hipLaunchKernelGGL((k_lru_chain<256, 8>), grid(256), dim3(256), 0, st, io);
+  const dim3 grid(static_cast<unsigned>(gdn::lru_chain_blocks(io.N, io.D, width)), directions);
+  if (width == 16)
+    hipLaunchKernelGGL((k_lru_chain<16, 512>), grid, dim3(256), 0, st, io);
+  else if (width == 256)
+    hipLaunchKernelGGL((k_lru_chain<256, 8>), grid, dim3(256), 0, st, io);
   else
-    hipLaunchKernelGGL((k_lru_chain<32, 128>), grid(32), dim3(256), 0, st, io);
+    hipLaunchKernelGGL((k_lru_chain<32, 128>), grid, dim3(256), 0, st, io);
 }
-// A launch holds fewer than 2^32 threads.
-bool lru_fits(int64_t threads) { return threads < (int64_t{1} << 32); }
+bool lru_fits(int64_t threads) { return threads < gdn::kLaunchThreads; }
 
 int lru_prefill_entry(const gdn_lru_shape_t* shape, int32_t n_seqs, const int32_t* cu_dev, const int32_t* cu_host,
                       const void* x, int64_t ldx, const void* g, int64_t ldg, const float* h0, void* o, int64_t ldo,
@@ -997,17 +987,18 @@ int lru_prefill_entry(const gdn_lru_shape_t* shape, int32_t n_seqs, const int32_
   io.x = x; io.g = g; io.h0 = h0; io.o = o; io.hT = hT; io.resume = resume;
   if (cache) io.cache = *cache;
   const bool three = gdn::lru_plan(cu_host, n_seqs, chunks, io.D, longest, resume, &io.plan);
-  int threads = 256;
+  int threads = 256, width = 0;
   int64_t blocks;
   if (three) {
     lru_ws(&io, ws, false);
     blocks = lru_units(&io);
+    width = gdn::lru_chain_width(n_seqs, io.D, longest, 1);
   } else {
     threads = io.plan.threads;
     io.tiles = (io.D + io.plan.lps - 1) / io.plan.lps;
     blocks = lru_blocks(io.plan.units, io.tiles);
   }
-  if (!lru_fits(blocks * threads) || (three && !lru_fits(lru_chain_blocks(io, 16) * 256))) return GDN_ERR_UNSUPPORTED;
+  if (!lru_fits(blocks * threads) || (three && !width)) return GDN_ERR_UNSUPPORTED;
   lru_dispatch(shape, [&]<typename TX, typename TG, int GATE>() {
     const dim3 grid(static_cast<unsigned>(blocks)), block(threads);
     if (!three) {
@@ -1019,7 +1010,7 @@ int lru_prefill_entry(const gdn_lru_shape_t* shape, int32_t n_seqs, const int32_
       Timed t_("k_lru_fold", st);
       hipLaunchKernelGGL((k_lru_fold<TX, TG, GATE, false>), grid, block, 0, st, io);
     }
-    lru_launch_chain(io, longest, 1, st);
+    lru_launch_chain(io, width, 1, st);
     Timed t_("k_lru_apply", st);
     hipLaunchKernelGGL((k_lru_apply<TX, TG, GATE>), grid, block, 0, st, io);
     return GDN_OK;
@@ -1136,14 +1127,15 @@ int gdn_lru_fwd_bwd(const gdn_lru_shape_t* shape, int32_t n_seqs, const int32_t*
   }
   lru_ws(&io, ws, true);
   const int64_t blocks = lru_units(&io);
-  if (!lru_fits(blocks * 256) || !lru_fits(2 * lru_chain_blocks(io, 16) * 256)) return GDN_ERR_UNSUPPORTED;
+  const int width = gdn::lru_chain_width(n_seqs, io.D, longest, 2);
+  if (!lru_fits(blocks * 256) || !width) return GDN_ERR_UNSUPPORTED;
   return lru_dispatch(shape, [&]<typename TX, typename TG, int GATE>() {
     const dim3 grid(static_cast<unsigned>(blocks)), block(256);
     {
       Timed t_("k_lru_fold", st);
       hipLaunchKernelGGL((k_lru_fold<TX, TG, GATE, true>), grid, block, 0, st, io);
     }
-    lru_launch_chain(io, longest, 2, st);
+    lru_launch_chain(io, width, 2, st);
     Timed t_("k_lru_grad", st);
     hipLaunchKernelGGL((k_lru_grad<TX, TG, GATE>), grid, block, 0, st, io);
     return hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_HIP;

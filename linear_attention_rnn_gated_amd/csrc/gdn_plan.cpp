@@ -265,6 +265,24 @@ bool lru_plan(const int32_t* cu, int32_t N, int64_t chunks, int32_t D, int64_t l
   return false;
 }
 
+// The chain's rounds: 128 chunks x 32 channels in 32 KB of LDS, five blocks a CU,
+// or, for longer sequences in no more blocks than CUs, where each round's latency
+// is what counts, 512 chunks x 16 channels (whole prefills, us: 12 sequences to
+// 14162 tokens x 200 channels 41 against 45, 16 to 14617 x 109 33 against 38; but 15
+// to 4475 x 972 in 915 blocks 58 against 52), or, for many sequences of up to 64
+// chunks, where blocks are what counts, 8 x 256 (whole training calls: one of 1000
+// tokens and 1000 of 30, 1024 channels 206 against 368; 2000 and 100 x 100, 2048
+// channels, 6464 blocks of 32 143 against 167; 2000 and 30 x 100 in 1984 blocks 69
+// against 69; 41 of 2000 x 512 in 656 blocks 216 against 214).  The last also where
+// blocks of 32 channels would take a launch past its threads.
+int lru_chain_width(int32_t N, int32_t D, int64_t longest, int directions) {
+  if (longest > 128 * GDN_LRU_CHUNK && lru_chain_blocks(N, D, 16) <= 256) return 16;
+  auto fits = [&](int w) { return lru_chain_blocks(N, D, w) * directions * 256 < kLaunchThreads; };
+  const bool many = longest <= 64 * GDN_LRU_CHUNK && lru_chain_blocks(N, D, 32) > 2048;
+  if (!many && fits(32)) return 32;
+  return fits(256) ? 256 : 0;
+}
+
 // The trainer's one pass where the longest sequence fits a round of 512 threads:
 // up to 256 tokens with 64 lanes a chunk (64 x 256 tokens x 4096 channels, bf16, fp32
 // g: 255 us, three steps 358; 400 x 40 x 1024: 71 against 190), to 512 with 32 (16 x

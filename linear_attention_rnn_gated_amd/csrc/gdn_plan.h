@@ -107,6 +107,13 @@ struct LruPlan {
 bool lru_plan(const int32_t* cu_host, int32_t n_seqs, int64_t chunks, int32_t D, int64_t longest, bool resume,
               LruPlan* plan);
 
+// A launch holds fewer threads than this.
+constexpr int64_t kLaunchThreads = int64_t{1} << 32;
+// Blocks of a chain of `width` channels a block, and the width to launch in one
+// or two directions: 16, 32 or 256, or 0 where no launch holds it.
+inline int64_t lru_chain_blocks(int64_t N, int64_t D, int width) { return N * ((D + width - 1) / width); }
+int lru_chain_width(int32_t n_seqs, int32_t D, int64_t longest, int directions);
+
 // Fills the plan of the trainer's one pass; false where the three steps are
 // expected to be faster or a sequence does not fit one round.
 bool lru_train_plan(const int32_t* cu_host, int32_t n_seqs, int64_t chunks, int32_t D, int64_t longest, LruPlan* plan);

@@ -771,3 +771,26 @@ def test_weights_at_the_smallest_decays():
     o, _ = B.gdn_lru_prefill(s, x, tiny, cu)
     r = B.gdn_lru_fwd_bwd(s, x, tiny, cu, x)
     assert bool((o == 0).all()) and bool((r["dg"] == 0).all()) and bool((r["dx"] == 0).all())
+
+
+def test_trainer_of_more_sequences_and_channels_than_narrow_chains_hold():
+    """32768 sequences x 4096 channels, whose chains take 256 channels a block: the long one and its neighbours alone, and the
+    last ones, give the same bits."""
+    N, D = 32768, 4096
+    lens = [1100] + [1] * (N - 1)
+    T = sum(lens)
+    gen = torch.Generator(device="cuda").manual_seed(69)
+    rn = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    x, g, dO, h0, dhT = rn(T, D).bfloat16(), -rn(T, D).abs().bfloat16(), rn(T, D).bfloat16(), rn(N, D), rn(N, D)
+    cu = torch.zeros(N + 1, dtype=torch.int32)
+    cu[1:] = torch.cumsum(torch.tensor(lens, dtype=torch.int64), 0)
+    s = B.make_lru_shape(D, BF16, BF16, "norm")
+    n, many = kernels(lambda: B.gdn_lru_fwd_bwd(s, x, g, cu.cuda(), dO, h0=h0, dhT=dhT, cu_seqlens_host=cu))
+    assert n["k_lru_chain"] == n["k_lru_grad"] == 1
+    few = B.gdn_lru_fwd_bwd(s, x[:1103], g[:1103], cu[:5].cuda(), dO[:1103], h0=h0[:4], dhT=dhT[:4])
+    for key, t in few.items():
+        assert same(t, many[key][:t.shape[0]]), key
+    end = torch.tensor([0, 1, 2, 3], dtype=torch.int32, device="cuda")
+    last = B.gdn_lru_fwd_bwd(s, x[-3:].clone(), g[-3:].clone(), end, dO[-3:].clone(), h0=h0[-3:].clone(), dhT=dhT[-3:].clone())
+    for key, t in last.items():
+        assert same(t, many[key][-3:]), key
