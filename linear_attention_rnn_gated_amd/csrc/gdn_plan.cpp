@@ -166,10 +166,10 @@ int64_t row_stride(int64_t ld, int64_t row) {
 // 119 us against 125; 80 x 3000 x 256: 122 against 140; with half as many blocks
 // 122 against 108 us).  Smaller blocks where the batch is so small that fewer than
 // 256 would be left.
+static constexpr int kTile[4] = {64, 32, 16, 8};
+static constexpr double kRound[4] = {13.5, 16.0, 20.0, 33.0}, kAlone[4] = {10.5, 12.0, 16.5, 27.0};
 static void lru_tile(const int32_t* cu, int32_t N, int64_t chunks, int32_t D, int64_t longest, LruPlan* plan,
                      double* us) {
-  static constexpr int kTile[4] = {64, 32, 16, 8};
-  static constexpr double kRound[4] = {13.5, 16.0, 20.0, 33.0}, kAlone[4] = {10.5, 12.0, 16.5, 27.0};
   *us = 0;
   for (int k = 0; k < 4; ++k) {
     const int l = kTile[k];
@@ -208,16 +208,64 @@ static void lru_tile(const int32_t* cu, int32_t N, int64_t chunks, int32_t D, in
   plan->threads = static_cast<int32_t>(t < most ? t : most);
 }
 
-// Units for the plan's tile and threads; of more than kLruPack sequences as many
-// neighbours as fit a round with `each` chunks each.
-static void lru_pack(const int32_t* cu, int32_t N, int64_t each, bool resume, LruPlan* plan) {
-  const int64_t slots = plan->threads / plan->lps;
-  if (N > kLruPack) {
-    const int64_t per = each > 0 ? slots / each : kLruPack;
-    plan->per = static_cast<int32_t>(per < 1 ? 1 : per > kLruPack ? kLruPack : per);
-    plan->units = (N + plan->per - 1) / plan->per;
-    return;
+// More than kLruPack sequences: as many neighbours a unit as fit a round with
+// `each` chunks each.
+static void lru_neighbours(int32_t N, int64_t each, LruPlan* plan) {
+  const int64_t slots = plan->threads / plan->lps, per = each > 0 ? slots / each : kLruPack;
+  plan->per = static_cast<int32_t>(per < 1 ? 1 : per > kLruPack ? kLruPack : per);
+  plan->units = static_cast<int32_t>((int64_t{N} + plan->per - 1) / plan->per);
+}
+
+// Rounds of all those units and of the longest of them.
+static void lru_rounds(const int32_t* cu, int32_t N, bool resume, const LruPlan& plan, int64_t* all, int64_t* worst) {
+  const int64_t slots = plan.threads / plan.lps, lead = (resume ? 2 : 1) * GDN_LRU_CHUNK - 1;
+  *all = *worst = 0;
+  for (int64_t n0 = 0; n0 < N; n0 += plan.per) {
+    const int64_t n1 = n0 + plan.per < N ? n0 + plan.per : N;
+    int64_t held = 0;
+    for (int64_t n = n0; n < n1; ++n) {
+      const int64_t len = int64_t{cu[n + 1]} - cu[n];
+      held += len > 0 ? (len + lead) / GDN_LRU_CHUNK : 0;
+    }
+    const int64_t r = (held + slots - 1) / slots;
+    *all += r;
+    *worst = r > *worst ? r : *worst;
   }
+}
+
+// Neighbours that are not alike can give a unit several long sequences one after
+// another, which lru_tile's cost does not know.  Where that takes a unit more than
+// twice the rounds of the longest sequence alone, the units' own time counts, with
+// as many neighbours as take the least of it, the number halved for as long as that
+// helps (us, without this / with it: 5000 x 1 and 10 x 8000 tokens x 512 channels
+// 1196 / 532, 200 x 20 and 8 x 2000 x 256 108 / 32, both now in three steps; at up to
+// twice the rounds the costs are too close: 649 of up to 298 x 2403 293 / 321).
+static void lru_uneven(const int32_t* cu, int32_t N, bool resume, int32_t D, int64_t longest, LruPlan* plan, double* us) {
+  int k = 0;
+  while (kTile[k] != plan->lps) ++k;
+  const int64_t slots = plan->threads / plan->lps;
+  const int64_t alone = ((longest + (resume ? 2 : 1) * GDN_LRU_CHUNK - 1) / GDN_LRU_CHUNK + slots - 1) / slots;
+  const double blocks = 256.0 * kLruThreads / plan->threads;  // at once
+  double best = 0;
+  for (int32_t per = plan->per; per >= 1; per /= 2) {
+    LruPlan p = *plan;
+    p.per = per;
+    p.units = static_cast<int32_t>((int64_t{N} + per - 1) / per);
+    int64_t all, worst;
+    lru_rounds(cu, N, resume, p, &all, &worst);
+    if (best == 0 && worst <= 2 * (alone > 1 ? alone : 1)) return;
+    const double share = std::ceil(static_cast<double>(all) * ((D + p.lps - 1) / p.lps) / blocks) * kRound[k];
+    const double one = static_cast<double>(worst) * kAlone[k], t = share > one ? share : one;
+    if (best > 0 && t >= best) break;
+    best = t;
+    *plan = p;
+  }
+  *us = best > *us ? best : *us;
+}
+
+// Units of up to kLruPack sequences for the plan's tile and threads.
+static void lru_pack(const int32_t* cu, int32_t N, bool resume, LruPlan* plan) {
+  const int64_t slots = plan->threads / plan->lps;
   plan->per = 0;
   int order[kLruPack], unit[kLruPack], units = 0;
   int64_t len[kLruPack], sum[kLruPack];
@@ -259,9 +307,13 @@ bool lru_plan(const int32_t* cu, int32_t N, int64_t chunks, int32_t D, int64_t l
   lru_tile(cu, N, chunks, D, longest, plan, &us);
   // over the chunks' places and whole waves, which is what the steps run over
   const double twice = 8.0 + 3e-6 * static_cast<double>(chunks * GDN_LRU_CHUNK) * ((D + 63) / 64 * 64);
+  if (N > kLruPack) {
+    // on average, and a resumed sequence may take a chunk more than its tokens do
+    lru_neighbours(N, (chunks + N - 1) / N + (resume ? 1 : 0), plan);
+    lru_uneven(cu, N, resume, D, longest, plan, &us);
+  }
   if (T > GDN_LRU_SMALL && twice < us) return true;
-  // on average, and a resumed sequence may take a chunk more than its tokens do
-  lru_pack(cu, N, N > 0 ? (chunks + N - 1) / N + (resume ? 1 : 0) : 0, resume, plan);
+  if (N <= kLruPack) lru_pack(cu, N, resume, plan);
   return false;
 }
 
@@ -301,7 +353,10 @@ bool lru_train_plan(const int32_t* cu, int32_t N, int64_t chunks, int32_t D, int
   plan->lps = each <= kLruTrain / 64 ? 64 : each <= kLruTrain / 32 ? 32 : 16;
   if (plan->lps == 16 && chunks * GDN_LRU_CHUNK * D > 1 << 24) return false;
   plan->threads = static_cast<int32_t>((each * plan->lps + 63) / 64 * 64);
-  lru_pack(cu, N, each, false, plan);
+  if (N > kLruPack)
+    lru_neighbours(N, each, plan);
+  else
+    lru_pack(cu, N, false, plan);
   const int64_t slots = plan->threads / plan->lps;
   return plan->per == 0 || plan->units * slots <= 3 * chunks + slots;
 }

@@ -794,3 +794,25 @@ def test_trainer_of_more_sequences_and_channels_than_narrow_chains_hold():
     last = B.gdn_lru_fwd_bwd(s, x[-3:].clone(), g[-3:].clone(), end, dO[-3:].clone(), h0=h0[-3:].clone(), dhT=dhT[-3:].clone())
     for key, t in last.items():
         assert same(t, many[key][-3:]), key
+
+
+def test_short_sequences_next_to_long_ones_in_a_row():
+    """Many short sequences with long neighbours, whose one pass would run them one after another: the same bits as in three
+    batches, from the start and continued."""
+    lens, D = [20] * 200 + [2000] * 8 + [0, 7], 96
+    p = make(lens, D, "bf16", "f32", "complement", seed=70)
+    d, cu, N = dev(p), p["cu"].tolist(), len(lens)
+    n, (o, hT) = kernels(lambda: prefill(p))
+    assert n["k_lru_fold"] == 1 and n["k_lru_fwd"] == 0
+    for a, b in ((0, 40), (200, 203), (205, N)):
+        r = slice(cu[a], cu[b])
+        c = torch.tensor([v - cu[a] for v in cu[a:b + 1]], dtype=torch.int32, device="cuda")
+        o1, h1 = B.gdn_lru_prefill(p["shape"], d["x"][r].clone(), d["g"][r].clone(), c, h0=d["h0"][a:b].clone())
+        assert same(o1, o[r]) and same(h1, hT[a:b]), (a, b)
+    cache, cut = B.gdn_lru_cache_init(p["shape"], N, "cuda", h0=d["h0"]), [min(v, 11 * (i % 5)) for i, v in enumerate(lens)]
+    for at, to in (([0] * N, cut), (cut, lens)):
+        rows = torch.cat([torch.arange(cu[i] + at[i], cu[i] + to[i]) for i in range(N)]).cuda()
+        c = torch.tensor([0] + list(np.cumsum([j - i for i, j in zip(at, to)])), dtype=torch.int32, device="cuda")
+        got, last = B.gdn_lru_prefill_continue(p["shape"], d["x"][rows], d["g"][rows], c, cache)
+        assert same(got, o[rows])
+    assert same(last, hT)

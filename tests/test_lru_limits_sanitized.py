@@ -1,6 +1,6 @@
-"""The sizes that the gated linear recurrence takes: its host-side plan (pure
+"""The sizes that the gated linear recurrence takes and how it groups many sequences: its host-side plan (pure
 C++) built with g++ under AddressSanitizer and UndefinedBehaviorSanitizer and run
-against randomised sizes (tests/native/lru_limits_fuzz.cpp)."""
+against randomised sizes and batches (tests/native/lru_limits_fuzz.cpp, lru_units_fuzz.cpp)."""
 
 import os
 import shutil
@@ -13,7 +13,7 @@ CSRC = os.path.join(ROOT, "linear_attention_rnn_gated_amd", "csrc")
 
 
 @pytest.mark.skipif(shutil.which("g++") is None, reason="g++ not available")
-@pytest.mark.parametrize("name", ["lru_limits_fuzz"])
+@pytest.mark.parametrize("name", ["lru_limits_fuzz", "lru_units_fuzz"])
 def test_lru_limits_under_asan_ubsan(tmp_path, name):
     exe = str(tmp_path / name)
     cmd = ["g++", "-std=c++17", "-O1", "-g", "-fno-omit-frame-pointer",
