@@ -599,6 +599,12 @@ def _packed(cu_seqlens, cu_seqlens_host, dev, T):
     return n, cu_dev, cu_host
 
 
+def _host_copy(cu_seqlens_host):
+    """cu_seqlens_host as _packed takes it.  False, as gdn_prefill takes it, has the
+    device copy read back: here by the binding, whose check of the rows needs it."""
+    return None if cu_seqlens_host is False else cu_seqlens_host
+
+
 def make_lru_shape(D, in_dtype, g_dtype=torch.float32, gate="none"):
     """Shape of a gated linear recurrence of D channels: x, o in in_dtype, the
     log decay g in g_dtype; gate "none", "complement" or "norm" gives the
@@ -698,7 +704,7 @@ def _lru_prefill(name, shape, x, g, cu_seqlens, h0, cache, want_hT, ws, out, hT_
     xt = _DTYPES.get(shape.in_dtype)
     ldx = _rows(x, xt, T, D, dev, "x")
     ldg = _rows(g, _DTYPES.get(shape.g_dtype), T, D, dev, "g")
-    n, cu_dev, cu_host = _packed(cu_seqlens, cu_seqlens_host, dev, T)
+    n, cu_dev, cu_host = _packed(cu_seqlens, _host_copy(cu_seqlens_host), dev, T)
     o = torch.empty(T, D, dtype=xt, device=dev) if out is None else out
     ldo = _rows(o, xt, T, D, dev, "out")
     hT = hT_out
@@ -765,7 +771,7 @@ def gdn_lru_fwd_bwd(shape, x, g, cu_seqlens, dO, h0=None, dhT=None, ws=None, wan
     ldx = _rows(x, xt, T, D, dev, "x")
     ldg = _rows(g, gt, T, D, dev, "g")
     lddo = _rows(dO, xt, T, D, dev, "dO")
-    n, cu_dev, cu_host = _packed(cu_seqlens, cu_seqlens_host, dev, T)
+    n, cu_dev, cu_host = _packed(cu_seqlens, _host_copy(cu_seqlens_host), dev, T)
     kinds = {"o": (xt, T), "hT": (torch.float32, n), "dx": (xt, T), "dg": (gt, T),
              "dh0": (torch.float32, n)}
     if not want_o:

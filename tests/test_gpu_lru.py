@@ -816,3 +816,15 @@ def test_short_sequences_next_to_long_ones_in_a_row():
         got, last = B.gdn_lru_prefill_continue(p["shape"], d["x"][rows], d["g"][rows], c, cache)
         assert same(got, o[rows])
     assert same(last, hT)
+
+
+def test_no_host_copy():
+    """cu_seqlens_host=False, as gdn_prefill takes it."""
+    p = make([33, 0, 2500], 16, seed=71)
+    d = dev(p)
+    want, hT = prefill(p, cu_seqlens_host=p["cu"])
+    o, h = prefill(p, cu_seqlens_host=False)
+    r = B.gdn_lru_fwd_bwd(p["shape"], d["x"], d["g"], d["cu"], d["dO"], h0=d["h0"], cu_seqlens_host=False)
+    assert same(o, want) and same(h, hT) and same(r["o"], want)
+    cache = B.gdn_lru_cache_init(p["shape"], 3, "cuda", h0=d["h0"])
+    assert same(B.gdn_lru_prefill_continue(p["shape"], d["x"], d["g"], d["cu"], cache, cu_seqlens_host=False)[0], want)

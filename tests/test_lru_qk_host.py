@@ -401,3 +401,19 @@ def test_cache_refuses_tensors_that_do_not_fit(name, bad):
     setattr(c, name, bad)
     with pytest.raises(ValueError):
         c.struct()
+
+
+def test_no_host_copy_reads_the_device_copy_back(monkeypatch):
+    """cu_seqlens_host=False, as gdn_prefill takes it: the calls go on with a copy that they read back and check."""
+    seen = []
+    x, g = torch.zeros(5, 8), torch.zeros(5, 8)
+    cu, s = torch.tensor([0, 2, 5], dtype=torch.int32), B.make_lru_shape(8, torch.float32)
+    monkeypatch.setattr(B, "_gpu", lambda t, name: t.device)
+    monkeypatch.setattr(B, "_launch", lambda name, dev, *args: seen.append((name, args[1], args[3])))
+    for host in (False, None, cu.clone()):
+        B.gdn_lru_prefill(s, x, g, cu, cu_seqlens_host=host)
+        B.gdn_lru_prefill_continue(s, x, g, cu, B.LruCache(8, 2, "cpu"), cu_seqlens_host=host)
+        B.gdn_lru_fwd_bwd(s, x, g, cu, x, cu_seqlens_host=host)
+        with pytest.raises(ValueError, match="past the 4 rows"):
+            B.gdn_lru_prefill(s, x[:4], g[:4], cu, cu_seqlens_host=host)
+    assert len(seen) == 9 and all(n == 2 and p for _, n, p in seen)
