@@ -673,7 +673,9 @@ class LruCache:
         return [self._S, self._A, self._B, self._pos]
 
     def state(self):
-        """The states now, [n, D]: A S + B."""
+        """The states now, [n, D]: A S + B, rounded twice.  The calls' o and hT are
+        one fma and may differ in the last place; hT of a continuation without
+        tokens (a cu_seqlens of zeros) is that fma."""
         return self._A * self._S + self._B
 
     def clone(self):

@@ -828,3 +828,32 @@ def test_no_host_copy():
     assert same(o, want) and same(h, hT) and same(r["o"], want)
     cache = B.gdn_lru_cache_init(p["shape"], 3, "cuda", h0=d["h0"])
     assert same(B.gdn_lru_prefill_continue(p["shape"], d["x"], d["g"], d["cu"], cache, cu_seqlens_host=False)[0], want)
+
+
+@pytest.mark.parametrize("x,g,gate,D", [("bf16", "f32", "norm", 300), ("f32", "f32", "none", 33), ("bf16", "bf16", "complement", 64)])
+def test_decoded_states_are_the_prefills(x, g, gate, D):
+    """A continuation without tokens gives the states: after token-by-token decode, after a prefill into a cache and by that
+    prefill itself the same bits; A S + B in two roundings is next to them."""
+    lens = [1, 40, 97, 32, 64, 130]
+    p = make(lens, D, x, g, gate, seed=72)
+    p["g"] = (p["g"].float() / 16).to(DT[g])     # slow decays: A S counts in the sum
+    d, cu, N = dev(p), p["cu"].tolist(), len(lens)
+    none, zeros = torch.zeros(N + 1, dtype=torch.int32, device="cuda"), (d["x"][:0], d["g"][:0])
+    filled = B.LruCache(D, N, "cuda")
+    _, hT = prefill(p, cache=filled)
+    assert same(B.gdn_lru_prefill_continue(p["shape"], *zeros, none, filled)[1], hT)
+    cache, seen = B.gdn_lru_cache_init(p["shape"], N, "cuda", h0=d["h0"]), 0
+    for t in range(max(lens)):
+        rows = torch.tensor([min(cu[n] + t, cu[n + 1] - 1) for n in range(N)], device="cuda")
+        o = B.gdn_lru_decode_step(p["shape"], d["x"][rows], d["g"][rows], cache)
+        _, now = B.gdn_lru_prefill_continue(p["shape"], *zeros, none, cache)
+        if x == "f32":
+            assert same(now, o), t
+        for n in range(N):
+            if t == lens[n] - 1:
+                assert same(now[n], hT[n]), n
+                seen += 1
+        two = cache.A.double().abs() * cache.S.double().abs() + cache.B.double().abs()
+        # a product, a sum and the fma, each off by 2^-24 of at most |A S| + |B| (and of the roundings before)
+        assert bool(((cache.state().double() - now.double()).abs() <= 3.001 * 2.0 ** -24 * two + 2.0 ** -126).all()), t
+    assert seen == N
