@@ -857,3 +857,128 @@ def test_decoded_states_are_the_prefills(x, g, gate, D):
         # a product, a sum and the fma, each off by 2^-24 of at most |A S| + |B| (and of the roundings before)
         assert bool(((cache.state().double() - now.double()).abs() <= 3.001 * 2.0 ** -24 * two + 2.0 ** -126).all()), t
     assert seen == N
+
+
+# ---- both schedules: [6000, 45] tokens x 40 channels takes the three steps, [40, 45] the one pass ----
+BOTH = [([40, 45], False), ([6000, 45], True)]
+
+
+def launched(long, n, forward, train):
+    """Whether n's launches are those of the three steps (long) or of the one pass, for the calls that ran."""
+    want = dict.fromkeys(n, 0)
+    if long:
+        want.update(k_lru_fold=forward + train, k_lru_chain=forward + train, k_lru_apply=forward, k_lru_grad=train)
+    else:
+        want.update(k_lru_fwd=forward, k_lru_train=train)
+    want["k_lru_pos"] = n["k_lru_pos"]
+    return n == want
+
+
+@pytest.mark.parametrize("lens,long", BOTH)
+def test_poisoned_buffers_in_both_schedules(lens, long):
+    p = make(lens, 40, "bf16", "f32", "norm", seed=73)
+    d, T, N = dev(p), sum(lens), len(lens)
+    begin = B.LruCache(40, N, "cuda")
+    prefill(dict(p, x=p["x"][:50], g=p["g"][:50], cu=torch.tensor([0, 17, 50], dtype=torch.int32)), cache=begin)
+    res = []
+    for fill in (0xFF, 0x00, 0x7F):
+        ws = lambda op: torch.full((B.lru_workspace_bytes(p["shape"], N, T, op),), fill, dtype=torch.uint8, device="cuda")  # noqa: E731
+        cache, go = B.LruCache(40, N, "cuda"), begin.clone()
+        for t in cache.tensors():
+            t.view(torch.uint8).fill_(fill)
+        out = torch.empty_like(d["x"])
+        out.view(torch.uint8).fill_(fill)
+        n, (o, h) = kernels(lambda: prefill(p, cache=cache, ws=ws(B.OP_PREFILL), out=out))
+        assert launched(long, n, 1, 0)
+        n, (c, hc) = kernels(lambda: B.gdn_lru_prefill_continue(p["shape"], d["x"], d["g"], d["cu"], go,
+                                                                ws=ws(B.OP_PREFILL_CONTINUE)))
+        assert launched(long, n, 1, 0)
+        n, r = kernels(lambda: B.gdn_lru_fwd_bwd(p["shape"], d["x"], d["g"], d["cu"], d["dO"], h0=d["h0"], ws=ws(B.OP_FWD_BWD)))
+        assert launched(long, n, 0, 1)
+        res.append([o, h, c, hc, *cache.tensors(), *go.tensors(), *[r[k] for k in sorted(r)]])
+    for other in res[1:]:
+        for a, b in zip(res[0], other):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("lens,long", BOTH)
+def test_offsets_past_32_bits_in_both_schedules(lens, long):
+    """Rows that span more than 2^32 elements, for every row that the prefill, the continuation, the trainer and a decode step
+    take."""
+    p = make(lens, 40, "bf16", "bf16", "norm", seed=74)
+    d, T = dev(p), sum(lens)
+    ld = (1 << 20) if long else (1 << 26)
+    big = torch.empty(T, ld, dtype=BF16, device="cuda")
+    assert (T - 1) * ld > 1 << 32
+    cols = {k: big[:, i * 64:i * 64 + 40] for i, k in enumerate(("x", "g", "dO", "o", "dx", "dg"))}
+    for k in ("x", "g", "dO"):
+        cols[k].copy_(d[k])
+    caches = [B.LruCache(40, 2, "cuda") for _ in range(2)]
+    n, (o, h) = kernels(lambda: B.gdn_lru_prefill(p["shape"], cols["x"], cols["g"], d["cu"], h0=d["h0"], cache=caches[0],
+                                                  out=cols["o"]))
+    assert launched(long, n, 1, 0)
+    want, hT = prefill(p, cache=caches[1])
+    assert same(o, want) and same(h, hT)
+    n, (o, h) = kernels(lambda: B.gdn_lru_prefill_continue(p["shape"], cols["x"], cols["g"], d["cu"], caches[0], out=cols["o"]))
+    assert launched(long, n, 1, 0)
+    want, hT = B.gdn_lru_prefill_continue(p["shape"], d["x"], d["g"], d["cu"], caches[1])
+    assert same(o, want) and same(h, hT)
+    for a, b in zip(*(c.tensors() for c in caches)):
+        assert torch.equal(a.view(torch.int32), b.view(torch.int32))
+    want = B.gdn_lru_fwd_bwd(p["shape"], d["x"], d["g"], d["cu"], d["dO"], h0=d["h0"])
+    n, r = kernels(lambda: B.gdn_lru_fwd_bwd(p["shape"], cols["x"], cols["g"], d["cu"], cols["dO"], h0=d["h0"],
+                                             out={k: cols[k] for k in ("o", "dx", "dg")}))
+    assert launched(long, n, 0, 1)
+    for k in ("o", "dx", "dg", "hT", "dh0"):
+        assert same(r[k], want[k]), k
+    one, two = (B.gdn_lru_cache_init(p["shape"], T, "cuda") for _ in range(2))
+    assert same(B.gdn_lru_decode_step(p["shape"], cols["x"], cols["g"], one, out=cols["o"]),
+                B.gdn_lru_decode_step(p["shape"], d["x"], d["g"], two))
+
+
+@pytest.mark.parametrize("long", [False, True])
+def test_no_nan_crosses_into_another_sequences_gradient_in_both_schedules(long):
+    lens = [70, 40, 33, 64, 100, 20] + ([1100] if long else [])
+    p = make(lens, 6, "f32", "f32", "complement", seed=75)
+    cu, d = p["cu"].tolist(), dev(p)
+
+    def train():
+        n, r = kernels(lambda: B.gdn_lru_fwd_bwd(p["shape"], d["x"], d["g"], d["cu"], d["dO"], h0=d["h0"], dhT=d["dhT"]))
+        assert launched(long, n, 0, 1)
+        return r
+    want = train()
+    payload = torch.tensor([0xffc0dead - (1 << 32), 0x7fc00000, 0xffc0dead - (1 << 32), 0x7f800001, -1, 0x7fffffff], dtype=torch.int32)
+    d["x"][cu[0] + 5], d["dO"][cu[2] + 1] = float("nan"), float("inf")
+    d["g"][cu[1] + 36] = d["g"][cu[4] + 66] = payload.view(F32).cuda()
+    got = train()
+    for n in (3, 5, 6)[:2 + long]:
+        for k in ("o", "dx", "dg"):
+            assert same(got[k][cu[n]:cu[n + 1]], want[k][cu[n]:cu[n + 1]]), (n, k)
+        assert same(got["hT"][n], want["hT"][n]) and same(got["dh0"][n], want["dh0"][n])
+    for n, t in ((1, 36), (4, 66)):  # states from the NaN on, gradients up to it
+        assert bool(got["o"][cu[n] + t:cu[n + 1]].isnan().all()) and bool(got["dx"][cu[n]:cu[n] + t + 1].isnan().all())
+        assert bool(got["dg"][cu[n] + t].isnan().all()) and bool(got["dh0"][n].isnan().all())
+        assert same(got["o"][cu[n]:cu[n] + t], want["o"][cu[n]:cu[n] + t])
+        assert same(got["dx"][cu[n] + t + 1:cu[n + 1]], want["dx"][cu[n] + t + 1:cu[n + 1]])
+
+
+def test_both_schedules_on_their_own_streams():
+    """A call in three steps, one in one pass and a trainer call at once, each on its own stream, workspace and cache."""
+    ps = [make([6000, 45], 40, "bf16", "f32", "norm", seed=76), make([40, 45], 40, "bf16", "f32", "norm", seed=77)]
+    want = [prefill(p) for p in ps]
+    ds = [dev(p) for p in ps]
+    train = lambda d: B.gdn_lru_fwd_bwd(ps[0]["shape"], d["x"], d["g"], d["cu"], d["dO"], h0=d["h0"], cu_seqlens_host=ps[0]["cu"])  # noqa: E731
+    grads = train(ds[0])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(3):
+        got = []
+        for s, (p, d) in zip(streams, zip(ps, ds)):
+            with torch.cuda.stream(s):
+                got.append(B.gdn_lru_prefill(p["shape"], d["x"], d["g"], d["cu"], h0=d["h0"], cu_seqlens_host=p["cu"]))
+        with torch.cuda.stream(streams[2]):
+            r = train(ds[0])
+        torch.cuda.synchronize()
+        for (o, h), (ro, rh) in zip(got, want):
+            assert same(o, ro) and same(h, rh)
+        assert all(same(r[k], grads[k]) for k in r)
