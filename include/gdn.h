@@ -426,7 +426,8 @@ int gdn_lru_fwd_bwd(const gdn_lru_shape_t* shape, int32_t n_seqs, const int32_t*
  *     q is multiplied by `scale` besides.
  *
  * Angles are formed in fp64 and reduced there, so far positions lose nothing;
- * sums are fp32, and each output is rounded once.
+ * sums are fp32, and each output is rounded once.  With eps = 0 a head whose
+ * fp32 sum of squares is 0 has an infinite n.
  *
  * Rows: token t's heads are H_q (H_k) vectors of d elements one after another,
  * at q + t ldq (ld in elements; 0 = dense; a multiple of 8), so that q and k
@@ -471,6 +472,8 @@ size_t gdn_qk_workspace_bytes(const gdn_qk_shape_t* shape, int64_t n_tokens);
  * with dz the turned-back dy times scale, u = dz (weight_offset + w) and m = d
  * (RMS) or 1 (L2),
  *     dx = n (u - x (n^2 / m) sum(u x)),   dw = sum over tokens and heads of dz x n.
+ * n^2 has to be finite in fp32: with eps = 0 heads of elements below 1e-19 may
+ * get infinite or NaN gradients.
  * dw_q, dw_k: fp32 [d], RMS only, nullable; their sums run in a fixed order
  * for given sizes (no atomics). */
 int gdn_qk_rotary_bwd(const gdn_qk_shape_t* shape, int64_t n_tokens, const int32_t* pos,

@@ -327,3 +327,20 @@ def test_refusals_on_the_gpu():
         call(w_q=torch.ones(64, device="cuda"))
     with pytest.raises(B.GdnError):       # rows not a multiple of eight elements apart
         call(q=torch.zeros(4, 132, dtype=BF16, device="cuda")[:, :128].unflatten(1, (2, 64)))
+
+
+@pytest.mark.parametrize("norm", ["rms", "l2"])
+def test_smallest_heads_without_eps(norm):
+    """eps = 0 and heads whose mean square lies around and below fp32's normal numbers.  Each square and each of their sums
+    is off by 2^-150 there, so the sum of d = 64 squares of size s by 128 2^-150 / (64 s) of it, halved by the root, and the
+    mean once more by 2^-150 / s."""
+    sizes = [1e-10, 2e-19, 1.1e-19, 1e-19, 5e-20, 1e-20, 1e-21]
+    T, d = len(sizes), 64
+    gen = torch.Generator().manual_seed(20)
+    x = (1 + torch.rand(T, 2, d, generator=gen)) * torch.tensor(sizes)[:, None, None]
+    s = B.make_qk_shape(2, 0, d, 0, F32, norm=norm, eps=0.0, weight_offset=1.0)
+    y, _ = B.gdn_qk_rotary(s, x.cuda(), None, None, pos=torch.zeros(T, dtype=torch.int32, device="cuda"))
+    want, bound = qk_fwd(np64(x), norm=norm, layout="half", r=0, pos=np.zeros(T), inv_freq=np.zeros(0), eps=0.0,
+                         w=np.ones(d) if norm == "rms" else None)
+    low = 2 * 2.0 ** -150 / np.array(sizes)[:, None, None] ** 2
+    check(y, want, bound + low * np.abs(want), "y")
