@@ -982,3 +982,24 @@ def test_both_schedules_on_their_own_streams():
         for (o, h), (ro, rh) in zip(got, want):
             assert same(o, ro) and same(h, rh)
         assert all(same(r[k], grads[k]) for k in r)
+
+
+def test_accuracy_of_the_gates():
+    """alpha, 1 - alpha and sqrt(1 - alpha^2) over four million g, in units of 2^-24.  alpha: its last rounding 1, p's polynomial
+    0.3, p's and q's roundings 1.4 of at most 0.42 of it, f's rounding 0.25: 2.  1 - alpha: at n = 0 p's 1.7; at n = -1, where
+    it is 0.29 at least, p's 1.2, f's 0.6 and its own 1: 3.  The root: half of 1 - alpha's 3, of 1 + alpha's 2 and of the
+    product's 1, and the instruction's own 2: 5."""
+    D, worst = 1 << 20, {}
+    gen = torch.Generator().manual_seed(80)
+    g = -torch.cat([torch.exp(torch.rand(2, D, generator=gen) * 40 - 36), torch.rand(1, D, generator=gen) * 2,
+                    torch.rand(1, D, generator=gen) * 104])
+    cu = torch.arange(5, dtype=torch.int32, device="cuda")
+    gd = g.cuda()
+    ones, e = torch.ones(4, D, device="cuda"), gd.double()
+    for gate, want, units in (("none", e.exp(), 2), ("complement", -e.expm1(), 3), ("norm", (-(2 * e).expm1()).sqrt(), 5)):
+        s = B.make_lru_shape(D, F32, F32, gate)
+        o, _ = B.gdn_lru_prefill(s, ones * (gate != "none"), gd, cu, h0=ones * (gate == "none"), cu_seqlens_host=cu.cpu())
+        off = (o.double() - want).abs() - 2.0 ** -149         # a step of the denormal numbers
+        worst[gate] = float((off / want).max()) * 2 ** 24
+        assert worst[gate] <= units, worst
+    print("units of 2^-24:", worst)

@@ -417,3 +417,20 @@ def test_no_host_copy_reads_the_device_copy_back(monkeypatch):
         with pytest.raises(ValueError, match="past the 4 rows"):
             B.gdn_lru_prefill(s, x[:4], g[:4], cu, cu_seqlens_host=host)
     assert len(seen) == 9 and all(n == 2 and p for _, n, p in seen)
+
+
+def test_exp_polynomial():
+    """The recurrence's p(f) = f + f^2 q(f), with the coefficients that its source holds: within 2^-25.8 of e^f - 1."""
+    import os
+    import re
+    src = open(os.path.join(os.path.dirname(B.__file__), "csrc", "gdn_lru.hip")).read()
+    body = src[src.index("LruExp lru_exp(float g)"):]
+    first = float(re.search(r"float q = ([0-9.e-]+)f;", body).group(1))
+    rest = [float(v) for v in re.findall(r"q = fmaf\(q, f, ([0-9.e-]+)f\);", body)]
+    assert len(rest) == 4
+    f = np.linspace(-math.log(2) / 2, math.log(2) / 2, 400000)
+    q = np.full_like(f, float(np.float32(first)))
+    for c in rest:
+        q = q * f + float(np.float32(c))
+    off = np.abs((f + f * f * q) / np.expm1(f) - 1)
+    assert off.max() < 2.0 ** -25.8
