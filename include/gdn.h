@@ -363,7 +363,9 @@ int gdn_lru_cache_init(const gdn_lru_shape_t* shape, int32_t n_seqs, const float
 
 /* Bytes of workspace of `op` (GDN_OP_PREFILL, GDN_OP_PREFILL_CONTINUE or
  * GDN_OP_FWD_BWD); 0 for an invalid shape or another op.  A prefill or
- * continuation of at most GDN_LRU_SMALL tokens needs none: ws may be NULL. */
+ * continuation of at most GDN_LRU_SMALL tokens needs none: ws may be NULL.
+ * Above it the need follows from the sizes alone, and holds also where a call
+ * then runs in one pass and leaves the workspace untouched. */
 #define GDN_LRU_SMALL 2048
 size_t gdn_lru_workspace_bytes(const gdn_lru_shape_t* shape, int32_t n_seqs, int64_t total_tokens,
                                int32_t op);

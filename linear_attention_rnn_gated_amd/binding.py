@@ -515,6 +515,8 @@ def gdn_fwd_bwd(shape, q, k, v, beta, g, cu_seqlens, dO, h0=None, dhT=None, ws=N
 # These calls take rows with any distance between tokens (slices of wider
 # projections), check that every tensor lies on the first one's GPU, and run
 # there on that GPU's current stream, whichever GPU is current.
+# Rows behind the last sequence of cu_seqlens are not written: in an output that
+# the call makes itself they hold no values.
 
 
 def _gpu(t, name):
@@ -889,7 +891,8 @@ def gdn_qk_rotary(shape, q, k, inv_freq, pos=None, cu_seqlens=None, start=None, 
 def gdn_qk_rotary_bwd(shape, q, k, dq_out, dk_out, inv_freq, pos=None, cu_seqlens=None,
                       start=None, w_q=None, w_k=None, ws=None):
     """Gradient of gdn_qk_rotary: from the gradients of its outputs, dict(dq,
-    dk) in q's type and, with norm "rms", dw_q and dw_k (fp32 [d])."""
+    dk) in q's type and, with norm "rms", dw_q and dw_k (fp32 [d]).  dq and dk are
+    dense tensors of their own (the C entry takes rows of any distance)."""
     dev, args = _qk_args(shape, q, k, inv_freq, pos, cu_seqlens, start, w_q, w_k)
     T, d = q.shape[0], shape.d
     ot = _DTYPES.get(shape.out_dtype)

@@ -301,6 +301,13 @@ static void lru_pack(const int32_t* cu, int32_t N, bool resume, LruPlan* plan) {
 // some 8 us for two launches and the chain (us, one pass / three steps: 512
 // channels x 8192 tokens 42 / 30, 1024 x 4096 24 / 25, 1024 x 16384 110 / 70, 2048
 // x 4096 27 / 34, 2048 x 16384 132 / 111, 4096 x 16384 163 / 201).
+//
+// Those costs are bf16 x's and fp32 g's with the norm gate, and stand for every
+// type and gate.  fp32 x takes both ways longer alike (1024 x 16384 143 / 80, 2048 x
+// 4096 33 / 38, 4096 x 16384 226 / 270; the shorter is taken in all of 12 batches);
+// without a gate both are as with one.  With bf16 g the second reading costs less
+// than the rule takes it for: at most 9% are lost (4096 x 16384 166 / 152, 4096 x
+// 32768 319 / 289, in one pass).
 bool lru_plan(const int32_t* cu, int32_t N, int64_t chunks, int32_t D, int64_t longest, bool resume, LruPlan* plan) {
   const int64_t T = N > 0 ? cu[N] : 0;
   double us;
@@ -342,6 +349,8 @@ int lru_chain_width(int32_t N, int32_t D, int64_t longest, int directions) {
 // of up to 2^24 elements (8 x 1024 x 2048 86 against 93; 32 x 1024 x 4096 698 against
 // 617).  Wider tiles are faster than narrower ones throughout, and narrower ones
 // still, 8 lanes, lose to the three steps (4 x 2048 x 1024: 50 against 48).
+// All with bf16 x and fp32 g.  In fp32 one pass gains more (16 x 512 x 4096 184
+// against 244), with bf16 g less: 8 x 1024 x 2048, 88 against 74, loses by it.
 // Batches of more than kLruPack sequences fill rounds for the longest one: those
 // that would leave two thirds of the places empty take the three steps (500 tokens
 // and 100 x 50, 2048 channels, seven eighths empty: 266 against 111; 250 and 300 x
