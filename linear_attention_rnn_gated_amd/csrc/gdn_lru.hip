@@ -116,8 +116,8 @@ __device__ __forceinline__ float lru_weight(float g, float& a) {
   a = r.a;
   if constexpr (GATE == GDN_LRU_GATE_NONE) return 1.0f;
   if constexpr (GATE == GDN_LRU_GATE_COMPLEMENT) return r.m;
-  const float w = r.m * (1.0f + r.a);
-  return __builtin_amdgcn_sqrtf(w < 0.0f ? 0.0f : w);  // (a maximum would turn a NaN into 0)
+  // the maximum that keeps a NaN, and one instruction as fmaxf, which does not
+  return __builtin_amdgcn_sqrtf(__builtin_elementwise_maximum(r.m * (1.0f + r.a), 0.0f));
 }
 // u = b x; without a gate x itself.
 template <int GATE>
