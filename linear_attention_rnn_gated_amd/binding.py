@@ -671,6 +671,9 @@ class LruCache:
             self._at, self._fits, self._struct = at, (n, D, dev), LruCacheStruct(*at)
         return self._struct
 
+    def __getstate__(self):
+        return dict(self.__dict__, _struct=None)  # a copy or a restored cache has addresses of its own
+
     def tensors(self):
         return [self._S, self._A, self._B, self._pos]
 

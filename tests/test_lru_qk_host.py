@@ -434,3 +434,18 @@ def test_exp_polynomial():
         q = q * f + float(np.float32(c))
     off = np.abs((f + f * f * q) / np.expm1(f) - 1)
     assert off.max() < 2.0 ** -25.8
+
+
+def test_cache_is_copied_and_restored():
+    """As the other cache: deep copies and pickles hold tensors of their own, and their struct is of those."""
+    import copy
+    import pickle
+    c = B.LruCache(40, 3, "cpu")
+    for t in c.tensors()[:3]:
+        t.normal_()
+    for make in (copy.copy, copy.deepcopy, lambda c: pickle.loads(pickle.dumps(c))):
+        c.struct()
+        d = make(c)
+        assert tuple(getattr(d.struct(), k) for k in ("S", "A", "B", "pos")) == tuple(t.data_ptr() for t in d.tensors())
+        assert all(torch.equal(a, b) for a, b in zip(c.tensors(), d.tensors()))
+        assert make is copy.copy or all(a.data_ptr() != b.data_ptr() for a, b in zip(c.tensors(), d.tensors()))
