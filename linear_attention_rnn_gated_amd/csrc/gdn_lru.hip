@@ -433,8 +433,8 @@ __device__ __forceinline__ void lru_outputs(const float* al, float* x, const flo
 
 // The trainer of units that fit one round: a chunk's inputs stay in its lanes'
 // registers from the composition to the gradients, so they are read once.  Bound
-// by HBM where large: 64 x 256 tokens x 4096 channels, norm gate, bf16 and fp32 g 255
-// us = 4.2 TB/s, all fp32 316 us = 5.1 TB/s (three steps: 358 and 488).  171
+// by HBM where large: 64 x 256 tokens x 4096 channels, norm gate, bf16 and fp32 g 254
+// us = 4.2 TB/s, all fp32 318 us = 5.1 TB/s (three steps: 310 and 458).  171
 // registers, two waves a SIMD; held to 168 for three it spilled and took 273 us.
 template <typename TX, typename TG, int GATE>
 __global__ __launch_bounds__(kLruTrain) void k_lru_train(LruIO io) {

@@ -344,8 +344,8 @@ int lru_chain_width(int32_t N, int32_t D, int64_t longest, int directions) {
 
 // The trainer's one pass where the longest sequence fits a round of 512 threads:
 // up to 256 tokens with 64 lanes a chunk (64 x 256 tokens x 4096 channels, bf16, fp32
-// g: 255 us, three steps 358; 400 x 40 x 1024: 71 against 190), to 512 with 32 (16 x
-// 512 x 4096 141 against 180) and to 1024 with 16, where rows are narrow, in batches
+// g: 254 us, three steps 310; 400 x 40 x 1024: 71 against 116), to 512 with 32 (16 x
+// 512 x 4096 144 against 177) and to 1024 with 16, where rows are narrow, in batches
 // of up to 2^24 elements (8 x 1024 x 2048 86 against 93; 32 x 1024 x 4096 698 against
 // 617).  Wider tiles are faster than narrower ones throughout, and narrower ones
 // still, 8 lanes, lose to the three steps (4 x 2048 x 1024: 50 against 48).
