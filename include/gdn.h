@@ -402,8 +402,9 @@ int gdn_lru_decode_step(const gdn_lru_shape_t* shape, int32_t n_seqs, const void
  *     dx_t    = b_t delta_t
  *     dg_t    = delta_t (alpha_t h_{t-1} + b'_t x_t)
  *     dh0     = alpha_1 delta_1                        (dhT for an empty sequence)
- * where b' = db/dg is 0, -alpha or -alpha^2 / b (0 where b = 0, at g = 0,
- * where the derivative has no finite value).  No atomics: bitwise reproducible.
+ * where b' = db/dg is 0, -alpha or -alpha^2 / b (0 where b = 0: for g above
+ * -2^-127, and at g = 0 the derivative has no finite value).  No atomics:
+ * bitwise reproducible.
  */
 int gdn_lru_fwd_bwd(const gdn_lru_shape_t* shape, int32_t n_seqs, const int32_t* cu_seqlens_dev,
                     const int32_t* cu_seqlens_host, const void* x, int64_t ldx, const void* g,
