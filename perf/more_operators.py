@@ -139,7 +139,7 @@ def prepare(case, seed):
             from linear_attention_rnn_gated_amd import binding as lib
             s["shape"] = lib.make_attn_shape(Hq, Hkv, d, dt, scale=s["scale"])
             if case["op"] == "train":
-                s["ws"] = torch.empty(lib.attn_workspace_bytes(s["shape"], T), dtype=torch.uint8, device=DEV)
+                s["ws"] = torch.empty(lib.attn_workspace_bytes(s["shape"], T, T), dtype=torch.uint8, device=DEV)
         return s
 
     P, old, new = case["P"], _lens(case["old"], 5), _lens(case["new"])
@@ -264,15 +264,18 @@ def _plain_write(s, k, v, lens, first):
     front = t // BLOCK == begin // BLOCK
     keep[slot[front]] = (begin % BLOCK)[front]
     older = torch.arange(BLOCK, device=DEV) < keep[:, None]
+    live = older.clone()
+    live[slot, off] = True  # what stands behind the last token stays
     pg, bl = some // (P // BLOCK), some % (P // BLOCK)
     for x, codes, scales in ((k, s["kc"], s["ks"]), (v, s["vc"], s["vs"])):
         blocks = codes.view(pages, Hkv, P // BLOCK, BLOCK, d)
         sc = scales[pg, :, bl]
-        was = blocks.view(torch.uint8)[pg, :, bl].view(E4M3).float() * sc[..., None, None]
+        raw = blocks.view(torch.uint8)[pg, :, bl]
+        was = raw.view(E4M3).float() * sc[..., None, None]
         now = torch.where(older[:, None, :, None], was, 0)
         now[slot, :, off] = x.float()
         c, sc = _quantised(now, sc, (keep > 0)[:, None])
-        blocks.view(torch.uint8)[pg, :, bl] = c.view(torch.uint8)
+        blocks.view(torch.uint8)[pg, :, bl] = torch.where(live[:, None, :, None], c.view(torch.uint8), raw)
         scales[pg, :, bl] = sc
 
 
@@ -411,14 +414,16 @@ def _exact_write(s):
             was = _values(s, name, n, a)[first:] if a else s[name][:0].double()
             x = torch.cat([was, s[name][at:at + b].double()])
             at += b
-            x = torch.nn.functional.pad(x, (0, 0, 0, 0, 0, -len(x) % BLOCK)).unflatten(0, (-1, BLOCK)).permute(0, 2, 1, 3)
+            count = len(x)
+            x = torch.nn.functional.pad(x, (0, 0, 0, 0, 0, -count % BLOCK)).unflatten(0, (-1, BLOCK)).permute(0, 2, 1, 3)
             need = torch.exp2(torch.ceil(torch.log2(x.abs().amax((2, 3)) / 448)).clamp(min=-117))
             blk = torch.arange(first // BLOCK, first // BLOCK + len(x), device=DEV)
             page, slot = s["table"][n].long()[blk * BLOCK // P], blk % (P // BLOCK)
             if a > first:
                 need[0] = torch.maximum(need[0], scale[page[0], :, slot[0]])
             scale[page, :, slot] = need
-            pool[page, :, slot] = x / need[..., None, None]
+            there = (torch.arange(len(x) * BLOCK, device=DEV) < count).view(-1, 1, BLOCK, 1)
+            pool[page, :, slot] = torch.where(there, x / need[..., None, None], pool[page, :, slot])
         out[name], out[name + "_scale"] = pool.flatten(2, 3), scale
     return out
 
