@@ -521,6 +521,123 @@ int gdn_rope_freqs(int32_t r, double base, const gdn_rope_scaling_t* scaling, fl
                    float* rope_scale);
 
 /*
+ * ---- Softmax attention -------------------------------------------------------
+ *
+ * The other mixer of stacks that interleave it with the layers above.  Query head
+ * h reads key/value head h / (H_q / H_kv).  Sequence n has the queries [cu_q[n],
+ * cu_q[n+1]) and the keys [cu_k[n], cu_k[n+1]), aligned at their ends: query i of
+ * L_q sees keys j <= i + L_k - L_q, and
+ *
+ *     s_ij = scale q_i . k_j,  lse_i = log sum_j exp(s_ij),
+ *     o_i  = sum_j exp(s_ij - lse_i) v_j
+ *
+ * A query that sees nothing (L_k < L_q) has o = 0 and lse = -inf.  Products and
+ * sums are fp32; bf16 inputs go into the products as they are, and exp(s - max)
+ * is rounded to bf16 there (not in its own sum), with fp32 inputs nothing is.  A
+ * sequence's bits do not depend on the batch.
+ *
+ * Rows as for gdn_qk_rotary: token t's heads are d elements each, one after
+ * another, at q + t ldq (ld in elements; 0 = dense; a multiple of 8, at most 2^22).
+ * All cu_* are on the device and read there; they must start at 0 and be
+ * non-decreasing (values outside the T rows are clamped: wrong values, no access
+ * outside).  Rows past cu[n_seqs] are neither read nor written, and one
+ * sequence's infinities and NaN reach no other's rows; within the sequence they
+ * reach the rows that see them, forward, and any, in the gradient.
+ *
+ * Supported: d 64, 128 or 256; H_q a multiple of H_kv, at most 4096; scale > 0.
+ */
+typedef struct {
+  int32_t H_q, H_kv;
+  int32_t d;
+  int32_t in_dtype; /* gdn_dtype_t of q, k, v, o and the gradients */
+  float scale;
+} gdn_attn_shape_t;
+
+/* Prefill and the trainer's forward.  cu_k NULL: cu_q, and T_k = T_q.  lse fp32
+ * [T_q, H_q], nullable. */
+int gdn_attn_prefill(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t* cu_q,
+                     const int32_t* cu_k, int64_t T_q, int64_t T_k, const void* q, int64_t ldq,
+                     const void* k, int64_t ldk, const void* v, int64_t ldv, void* o, int64_t ldo,
+                     float* lse, void* stream);
+
+/* Bytes of workspace of gdn_attn_bwd; 0 for an invalid shape. */
+size_t gdn_attn_workspace_bytes(const gdn_attn_shape_t* shape, int64_t T_q, int64_t T_k);
+
+/* Its gradient, from what gdn_attn_prefill took and gave and the gradient dO of o
+ * (in in_dtype, as dq, dk, dv): with p = exp(s - lse),
+ *     dS_ij = p_ij (dO_i . v_j - dO_i . o_i),   dv_j = sum p_ij dO_i,
+ *     dq_i = scale sum_j dS_ij k_j,   dk_j = scale sum dS_ij q_i,
+ * the sums of dk and dv over the queries of all heads of the group.  Keys that no
+ * query sees get 0.  No atomics: bitwise reproducible.  All rows are dense but for
+ * their distances; no output may overlap an input. */
+int gdn_attn_bwd(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t* cu_q,
+                 const int32_t* cu_k, int64_t T_q, int64_t T_k, const void* q, int64_t ldq,
+                 const void* k, int64_t ldk, const void* v, int64_t ldv, const void* o,
+                 int64_t ldo, const float* lse, const void* dO, int64_t lddo, void* dq,
+                 int64_t lddq, void* dk, int64_t lddk, void* dv, int64_t lddv, void* ws,
+                 size_t ws_bytes, void* stream);
+
+/*
+ * Key/value cache in 8 bits, plain device memory owned by the caller: pages of
+ * page_tokens tokens (a multiple of GDN_KV_BLOCK), anywhere in one pool.  Token t
+ * of sequence n stands in page block_table[n * max_pages + t / page_tokens], place
+ * t % page_tokens.  An element is an e4m3 code (fn: no infinity) times the scale
+ * that GDN_KV_BLOCK neighbouring tokens of a head share, one for keys and one for
+ * values: the least power of two s >= 2^-117 with max |x| <= 448 s over the finite
+ * elements.  Codes are x / s rounded to nearest even; infinities and NaN become
+ * NaN.  (At s = 2^120 codes end at 240.)  Entries of block_table outside [0, pages)
+ * hold no tokens: writes to them are dropped, reads leave the rows as they are,
+ * attention passes over them.
+ */
+#define GDN_KV_BLOCK 32
+
+typedef struct {
+  void* k;             /* [pages, H_kv, page_tokens, d] e4m3                       */
+  void* v;
+  float* k_scale;      /* [pages, H_kv, page_tokens / GDN_KV_BLOCK], powers of two */
+  float* v_scale;
+  int32_t pages;
+  int32_t page_tokens; /* at most 2^20                                             */
+} gdn_kv_cache_t;
+
+/* Writes the next tokens of n_seqs sequences, k, v [T, H_kv, d] packed by
+ * cu_seqlens (device; NULL: one token a sequence, T = n_seqs), at the places
+ * start[n], start[n] + 1, ... (device; NULL: 0).  A block that already holds tokens
+ * before start[n] keeps its scale if it is the larger, else their codes go over to
+ * the new one (exact, but for codes that become subnormal, which are rounded
+ * again); places behind the written ones are left as they are and hold nothing.
+ * Writing the same tokens again changes nothing.  No two sequences may write to
+ * one page. */
+int gdn_kv_write(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t* cu_seqlens,
+                 const int32_t* start, int64_t T, const void* k, int64_t ldk, const void* v,
+                 int64_t ldv, const gdn_kv_cache_t* cache, const int32_t* block_table,
+                 int32_t max_pages, void* stream);
+
+/* Reads tokens back into rows of in_dtype, packed by cu_seqlens, from the places
+ * start[n] on (arguments as gdn_kv_write). */
+int gdn_kv_read(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t* cu_seqlens,
+                const int32_t* start, int64_t T, const gdn_kv_cache_t* cache,
+                const int32_t* block_table, int32_t max_pages, void* k, int64_t ldk, void* v,
+                int64_t ldv, void* stream);
+
+/* Attention of new tokens over the cache, which holds them already: q [T, H_q, d]
+ * packed by cu_seqlens (NULL: one token a sequence).  kv_len[n] (device) counts the
+ * sequence's cached tokens, its L_q new ones being the last of them; as above,
+ * query i sees the tokens up to kv_len - L_q + i.  max_len, at least every
+ * kv_len[n] (tokens past it are not seen), sizes the launches and the workspace:
+ * a captured call holds for lengths up to it.  lse fp32 [T, H_q], nullable.  The
+ * cache's values go into the products exactly, in bf16, with q and exp(s - max) in
+ * one bf16 part (bf16 q) or three that sum to them (fp32 q).  No atomics; a
+ * sequence's bits depend on neither batch, page size nor max_len. */
+size_t gdn_attn_decode_workspace_bytes(const gdn_attn_shape_t* shape, int32_t n_seqs,
+                                       int64_t T, int64_t max_len);
+int gdn_attn_decode(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t* cu_seqlens,
+                    int64_t T, const void* q, int64_t ldq, const gdn_kv_cache_t* cache,
+                    const int32_t* block_table, int32_t max_pages, const int32_t* kv_len,
+                    int64_t max_len, void* o, int64_t ldo, float* lse, void* ws,
+                    size_t ws_bytes, void* stream);
+
+/*
  * Kernel timing (instrumentation).  While enabled, every launch the entry
  * points make is bracketed by HIP events recorded on the call's stream.
  * gdn_profile_read waits for the recorded events, returns the summed
@@ -530,8 +647,8 @@ int gdn_rope_freqs(int32_t r, double base, const gdn_rope_scaling_t* scaling, fl
  * k_cache_init, k_chunk_o (gdn_prefill_chunked, gdn_fwd_bwd_chunked),
  * k_decode_native (gdn_decode_step_native), k_cont_plan, k_cont_gather,
  * k_cont_scatter (gdn_prefill_continue), the k_bwd_* kernels of gdn_fwd_bwd,
- * the k_lru_* kernels of gdn_lru_* and the k_qk_* kernels of gdn_qk_*.  Events
- * are created
+ * the k_lru_* kernels of gdn_lru_*, the k_qk_* kernels of gdn_qk_*, the k_attn_*
+ * kernels of gdn_attn_* and the k_kv_* kernels of gdn_kv_*.  Events are created
  * by the library on first use and reused; no device memory is allocated.
  * Thread-safe; records from concurrent calls are merged.
  */

@@ -29,11 +29,15 @@ EXPORTS = ["gdn_workspace_bytes", "gdn_cache_init", "gdn_prefill", "gdn_decode_s
            "gdn_fwd_bwd_chunked", "gdn_decode_step_native", "gdn_profile_filter",
            "gdn_lru_cache_init", "gdn_lru_prefill", "gdn_lru_prefill_continue",
            "gdn_lru_decode_step", "gdn_lru_workspace_bytes", "gdn_lru_fwd_bwd",
-           "gdn_qk_rotary", "gdn_qk_workspace_bytes", "gdn_qk_rotary_bwd", "gdn_rope_freqs"]
+           "gdn_qk_rotary", "gdn_qk_workspace_bytes", "gdn_qk_rotary_bwd", "gdn_rope_freqs",
+           "gdn_attn_prefill", "gdn_attn_workspace_bytes", "gdn_attn_bwd", "gdn_kv_write",
+           "gdn_kv_read", "gdn_attn_decode_workspace_bytes", "gdn_attn_decode"]
 
 LRU_CHUNK = 32    # tokens per chunk of the gated linear recurrence
 LRU_SMALL = 2048  # a prefill of at most so many tokens needs no workspace
 LRU_GROUP = 256   # channels per position counter of its cache
+KV_BLOCK = 32     # tokens of the 8-bit cache that share a scale
+KV_SPLIT = 512    # attention over no more cached tokens needs no workspace
 LRU_GATES = {"none": 0, "complement": 1, "norm": 2}
 QK_NORMS = {"none": 0, "l2": 1, "rms": 2}
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
@@ -71,6 +75,17 @@ class QkShape(ctypes.Structure):
                 ("out_dtype", ctypes.c_int32), ("norm", ctypes.c_int32),
                 ("layout", ctypes.c_int32), ("eps", ctypes.c_float), ("scale", ctypes.c_float),
                 ("rope_scale", ctypes.c_float), ("weight_offset", ctypes.c_float)]
+
+
+class AttnShape(ctypes.Structure):
+    _fields_ = [("H_q", ctypes.c_int32), ("H_kv", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("in_dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class KvCacheStruct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int32),
+                ("page_tokens", ctypes.c_int32)]
 
 
 class RopeScaling(ctypes.Structure):
@@ -149,10 +164,23 @@ def lib():
         L.gdn_qk_rotary_bwd.argtypes = [qs, i64, vp, i32, vp, vp, vp, vp, vp, vp, i64, vp, i64, vp,
                                         i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, sz, vp]
         L.gdn_rope_freqs.argtypes = [i32, ctypes.c_double, ctypes.POINTER(RopeScaling), vp, vp]
+        as_, kc = ctypes.POINTER(AttnShape), ctypes.POINTER(KvCacheStruct)
+        L.gdn_attn_prefill.argtypes = [as_, i32, vp, vp, i64, i64, vp, i64, vp, i64, vp, i64, vp,
+                                       i64, vp, vp]
+        L.gdn_attn_workspace_bytes.argtypes = [as_, i64, i64]
+        L.gdn_attn_bwd.argtypes = [as_, i32, vp, vp, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64,
+                                   vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, sz, vp]
+        L.gdn_kv_write.argtypes = [as_, i32, vp, vp, i64, vp, i64, vp, i64, kc, vp, i32, vp]
+        L.gdn_kv_read.argtypes = [as_, i32, vp, vp, i64, kc, vp, i32, vp, i64, vp, i64, vp]
+        L.gdn_attn_decode_workspace_bytes.argtypes = [as_, i32, i64, i64]
+        L.gdn_attn_decode.argtypes = [as_, i32, vp, i64, vp, i64, kc, vp, i32, vp, i64, vp, i64,
+                                      vp, vp, sz, vp]
         for name in ("lru_cache_init", "lru_prefill", "lru_prefill_continue", "lru_decode_step",
-                     "lru_fwd_bwd", "qk_rotary", "qk_rotary_bwd", "rope_freqs"):
+                     "lru_fwd_bwd", "qk_rotary", "qk_rotary_bwd", "rope_freqs", "attn_prefill",
+                     "attn_bwd", "kv_write", "kv_read", "attn_decode"):
             getattr(L, "gdn_" + name).restype = ctypes.c_int
         L.gdn_lru_workspace_bytes.restype = L.gdn_qk_workspace_bytes.restype = sz
+        L.gdn_attn_workspace_bytes.restype = L.gdn_attn_decode_workspace_bytes.restype = sz
         _lib = L
     return _lib
 
@@ -914,3 +942,227 @@ def gdn_qk_rotary_bwd(shape, q, k, dq_out, dk_out, inv_freq, pos=None, cu_seqlen
     _launch("gdn_qk_rotary_bwd", dev, *args, dq_out.data_ptr(), lddq, pdk, lddk,
             r["dq"].data_ptr(), 0, r["dk"].data_ptr(), 0, *p_dw, p_ws, ws_bytes)
     return r
+
+
+# ---- softmax attention and its 8-bit cache --------------------------------------
+
+
+def make_attn_shape(H_q, H_kv, d, in_dtype, scale=None):
+    """Shape of causal attention: H_q query heads over H_kv key/value heads of d
+    (64, 128 or 256) elements; scale multiplies q . k (None: d ** -0.5)."""
+    return AttnShape(H_q, H_kv, d, _DTYPE_CODES[in_dtype], d ** -0.5 if scale is None else scale)
+
+
+def attn_workspace_bytes(shape, T_q, T_k=None):
+    return int(lib().gdn_attn_workspace_bytes(ctypes.byref(shape), T_q, T_q if T_k is None else T_k))
+
+
+def attn_decode_workspace_bytes(shape, n_seqs, total_tokens, max_len):
+    return int(lib().gdn_attn_decode_workspace_bytes(ctypes.byref(shape), n_seqs, total_tokens,
+                                                     max_len))
+
+
+def _attn_packed(cu_q, cu_k, T_q, T_k, dev):
+    """(N, cu_q, cu_k) as the two calls take them."""
+    n = cu_q.numel() - 1
+    if n < 0 or (n == 0 and T_q > 0):
+        raise ValueError("cu_seqlens: expected N + 1 values")
+    p_q = _dense(cu_q, torch.int32, (n + 1,), dev, "cu_seqlens")
+    if cu_k is None:
+        if T_k != T_q:
+            raise ValueError(f"cu_seqlens_k: needed for {T_k} keys of {T_q} queries")
+        return n, p_q, None
+    return n, p_q, _dense(cu_k, torch.int32, (n + 1,), dev, "cu_seqlens_k")
+
+
+def _attn_args(shape, q, k, v, cu_seqlens, cu_seqlens_k):
+    dev = _gpu(q, "q")
+    T_q, T_k, d = q.shape[0], k.shape[0], shape.d
+    it = _DTYPES.get(shape.in_dtype)
+    ldq = _heads(q, it, T_q, shape.H_q, d, dev, "q")
+    ldk = _heads(k, it, T_k, shape.H_kv, d, dev, "k")
+    ldv = _heads(v, it, T_k, shape.H_kv, d, dev, "v")
+    n, p_q, p_k = _attn_packed(cu_seqlens, cu_seqlens_k, T_q, T_k, dev)
+    return dev, it, (ctypes.byref(shape), n, p_q, p_k, T_q, T_k, q.data_ptr(), ldq, k.data_ptr(),
+                     ldk, v.data_ptr(), ldv)
+
+
+def gdn_attn_prefill(shape, q, k, v, cu_seqlens, cu_seqlens_k=None, out=None, want_lse=True):
+    """Causal attention of packed sequences: q [T, H_q, d], k, v [T, H_kv, d]
+    (slices of wider rows are fine), cu_seqlens int32 GPU tensor [N + 1].  With
+    cu_seqlens_k the keys are packed by it instead, each sequence's queries being
+    its last tokens.  Returns (o [T, H_q, d] in q's type, lse fp32 [T, H_q] or
+    None)."""
+    dev, it, args = _attn_args(shape, q, k, v, cu_seqlens, cu_seqlens_k)
+    T = q.shape[0]
+    o = torch.empty(T, shape.H_q, shape.d, dtype=it, device=dev) if out is None else out
+    ldo = _heads(o, it, T, shape.H_q, shape.d, dev, "out")
+    lse = torch.empty(T, shape.H_q, dtype=torch.float32, device=dev) if want_lse else None
+    _launch("gdn_attn_prefill", dev, *args, o.data_ptr(), ldo,
+            None if lse is None else lse.data_ptr())
+    return o, lse
+
+
+def gdn_attn_bwd(shape, q, k, v, cu_seqlens, o, lse, dO, cu_seqlens_k=None, ws=None, out=None):
+    """Gradient of gdn_attn_prefill from its inputs, its o and lse and the gradient
+    dO of o.  Returns dict(dq, dk, dv) in q's type; out: optional dict of
+    caller-owned tensors for some of them."""
+    dev, it, args = _attn_args(shape, q, k, v, cu_seqlens, cu_seqlens_k)
+    T_q, T_k, d = q.shape[0], k.shape[0], shape.d
+    ldo = _heads(o, it, T_q, shape.H_q, d, dev, "o")
+    lddo = _heads(dO, it, T_q, shape.H_q, d, dev, "dO")
+    p_lse = _dense(lse, torch.float32, (T_q, shape.H_q), dev, "lse")
+    kinds = {"dq": (T_q, shape.H_q, d), "dk": (T_k, shape.H_kv, d), "dv": (T_k, shape.H_kv, d)}
+    out = out or {}
+    if not set(out) <= set(kinds):
+        raise ValueError(f"out: expected some of {sorted(kinds)}, got {sorted(out)}")
+    r = {key: out[key] if key in out else torch.empty(size, dtype=it, device=dev)
+         for key, size in kinds.items()}
+    ld = {key: _heads(r[key], it, *kinds[key], dev, f"out[{key!r}]") for key in kinds}
+    ws = _scratch(ws, attn_workspace_bytes(shape, T_q, T_k), dev, "gdn_attn_workspace_bytes")
+    _launch("gdn_attn_bwd", dev, *args, o.data_ptr(), ldo, p_lse, dO.data_ptr(), lddo,
+            r["dq"].data_ptr(), ld["dq"], r["dk"].data_ptr(), ld["dk"], r["dv"].data_ptr(),
+            ld["dv"], ws.data_ptr(), ws.numel())
+    return r
+
+
+class KvCache:
+    """Key/value cache in 8 bits (gdn_kv_cache_t), owned by torch tensors: k, v
+    float8_e4m3fn [pages, H_kv, page_tokens, d] and k_scale, v_scale fp32 [pages,
+    H_kv, page_tokens / 32].  A sequence is a row of a block table (int32 GPU
+    tensor [N, max_pages]) that names its pages in order."""
+
+    def __init__(self, shape, pages, page_tokens, device):
+        H, d = shape.H_kv, shape.d
+        if page_tokens % KV_BLOCK:
+            raise ValueError(f"page_tokens: expected a multiple of {KV_BLOCK}, got {page_tokens}")
+        kw = dict(dtype=torch.float8_e4m3fn, device=device)
+        f32 = dict(dtype=torch.float32, device=device)
+        self._hold(torch.empty(pages, H, page_tokens, d, **kw),
+                   torch.empty(pages, H, page_tokens // KV_BLOCK, **f32),
+                   torch.empty(pages, H, page_tokens, d, **kw),
+                   torch.empty(pages, H, page_tokens // KV_BLOCK, **f32))
+
+    @classmethod
+    def of(cls, k, k_scale, v, v_scale):
+        """A cache over existing tensors."""
+        c = object.__new__(cls)
+        _gpu(k, "k")
+        c._hold(k, k_scale, v, v_scale)
+        c.struct()
+        return c
+
+    k, k_scale, v, v_scale = (_cache_tensor(name) for name in ("k", "k_scale", "v", "v_scale"))
+    pages = property(lambda self: self._k.shape[0])
+    page_tokens = property(lambda self: self._k.shape[2])
+    device = property(lambda self: self._k.device)
+
+    def _hold(self, k, k_scale, v, v_scale):
+        self.k, self.k_scale, self.v, self.v_scale = k, k_scale, v, v_scale
+
+    def struct(self):
+        # an assignment drops the struct; a tensor given other memory in place moves its address
+        at = (self._k.data_ptr(), self._v.data_ptr(), self._k_scale.data_ptr(),
+              self._v_scale.data_ptr())
+        if self._struct is None or at != self._at:
+            if self._k.dim() != 4:
+                raise ValueError("k: expected [pages, H_kv, page_tokens, d]")
+            (pages, H, P, d), dev = self._k.shape, self._k.device
+            for t, name in ((self._k, "k"), (self._v, "v")):
+                _dense(t, torch.float8_e4m3fn, (pages, H, P, d), dev, name)
+            for t, name in ((self._k_scale, "k_scale"), (self._v_scale, "v_scale")):
+                _dense(t, torch.float32, (pages, H, P // KV_BLOCK), dev, name)
+            self._at, self._fits = at, (H, d, dev)
+            self._struct = KvCacheStruct(*at, pages, P)
+        return self._struct
+
+    def __getstate__(self):
+        return dict(self.__dict__, _struct=None)  # a copy or a restored cache has addresses of its own
+
+    def tensors(self):
+        return [self._k, self._k_scale, self._v, self._v_scale]
+
+    def clone(self):
+        return KvCache.of(*[t.clone() for t in self.tensors()])
+
+    def check(self, shape, dev):
+        """The struct, after checking that it is one of the shape's heads on dev."""
+        struct = self.struct()
+        if self._fits != (shape.H_kv, shape.d, dev):
+            raise ValueError(f"cache: expected {shape.H_kv} heads of {shape.d} on {dev}, got "
+                             f"{self._fits[0]} of {self._fits[1]} on {self.device}")
+        return struct
+
+
+def _kv_packed(cu_seqlens, block_table, T, dev):
+    """(N, cu_seqlens, block table, its width)."""
+    i32 = torch.int32
+    if block_table.dim() != 2:
+        raise ValueError("block_table: expected [N, max_pages]")
+    n, width = block_table.shape
+    p_table = _dense(block_table, i32, (n, width), dev, "block_table")
+    if cu_seqlens is None:
+        if T != n:
+            raise ValueError(f"cu_seqlens: needed for {T} tokens of {n} sequences")
+        return n, None, p_table, width
+    if n == 0 and T > 0:
+        raise ValueError("block_table: expected a row for each sequence")
+    return n, _dense(cu_seqlens, i32, (n + 1,), dev, "cu_seqlens"), p_table, width
+
+
+def gdn_kv_write(shape, k, v, cache, block_table, cu_seqlens=None, start=None):
+    """Quantises the next tokens k, v [T, H_kv, d] of the sequences of block_table
+    into their pages, from place start[n] (int32 GPU tensor [N]; None: 0) on.  Packed
+    by cu_seqlens (int32 GPU tensor [N + 1]); without it one token a sequence."""
+    dev = _gpu(k, "k")
+    T, it = k.shape[0], _DTYPES.get(shape.in_dtype)
+    ldk = _heads(k, it, T, shape.H_kv, shape.d, dev, "k")
+    ldv = _heads(v, it, T, shape.H_kv, shape.d, dev, "v")
+    n, p_cu, p_table, width = _kv_packed(cu_seqlens, block_table, T, dev)
+    _launch("gdn_kv_write", dev, ctypes.byref(shape), n, p_cu,
+            _optional(start, torch.int32, (n,), dev, "start"), T, k.data_ptr(), ldk, v.data_ptr(),
+            ldv, ctypes.byref(cache.check(shape, dev)), p_table, width)
+
+
+def gdn_kv_read(shape, cache, block_table, cu_seqlens, total_tokens, start=None, k_out=None,
+                v_out=None):
+    """Reads total_tokens tokens back, packed by cu_seqlens (None: one a sequence),
+    from place start[n] on.  Returns (k, v) [T, H_kv, d] in the shape's type."""
+    dev, T, it = cache.device, total_tokens, _DTYPES.get(shape.in_dtype)
+    size = (T, shape.H_kv, shape.d)
+    k = torch.empty(size, dtype=it, device=dev) if k_out is None else k_out
+    v = torch.empty(size, dtype=it, device=dev) if v_out is None else v_out
+    ldk = _heads(k, it, *size, dev, "k_out")
+    ldv = _heads(v, it, *size, dev, "v_out")
+    n, p_cu, p_table, width = _kv_packed(cu_seqlens, block_table, T, dev)
+    _launch("gdn_kv_read", dev, ctypes.byref(shape), n, p_cu,
+            _optional(start, torch.int32, (n,), dev, "start"), T,
+            ctypes.byref(cache.check(shape, dev)), p_table, width, k.data_ptr(), ldk,
+            v.data_ptr(), ldv)
+    return k, v
+
+
+def gdn_attn_decode(shape, q, cache, block_table, kv_len, max_len, cu_seqlens=None, out=None,
+                    want_lse=False, ws=None):
+    """Attention of new tokens q [T, H_q, d] over the cache that holds them already:
+    kv_len (int32 GPU tensor [N]) counts each sequence's cached tokens, the new ones
+    being the last of them; max_len is at least the largest of kv_len.  One token a
+    sequence, or several packed by cu_seqlens.  Returns o in q's type, with want_lse
+    (o, lse fp32 [T, H_q])."""
+    dev = _gpu(q, "q")
+    T, it, d = q.shape[0], _DTYPES.get(shape.in_dtype), shape.d
+    ldq = _heads(q, it, T, shape.H_q, d, dev, "q")
+    n, p_cu, p_table, width = _kv_packed(cu_seqlens, block_table, T, dev)
+    o = torch.empty(T, shape.H_q, d, dtype=it, device=dev) if out is None else out
+    ldo = _heads(o, it, T, shape.H_q, d, dev, "out")
+    lse = torch.empty(T, shape.H_q, dtype=torch.float32, device=dev) if want_lse else None
+    p_len = _dense(kv_len, torch.int32, (n,), dev, "kv_len")
+    tail = (None, 0)
+    if max_len > KV_SPLIT:
+        ws = _scratch(ws, attn_decode_workspace_bytes(shape, n, T, max_len), dev,
+                      "gdn_attn_decode_workspace_bytes")
+        tail = (ws.data_ptr(), ws.numel())
+    _launch("gdn_attn_decode", dev, ctypes.byref(shape), n, p_cu, T, q.data_ptr(), ldq,
+            ctypes.byref(cache.check(shape, dev)), p_table, width, p_len, max_len, o.data_ptr(),
+            ldo, None if lse is None else lse.data_ptr(), *tail)
+    return (o, lse) if want_lse else o

@@ -18,19 +18,10 @@
 // same fixed summation orders, and per-item work that never depends on the
 // launch's grid or on other items.  gdn_contract_id() names this contract.
 
-#include <hip/hip_runtime.h>
-
-#include <cstdint>
-#include <cstring>
-#include <mutex>
-#include <string>
-#include <vector>
-
 #ifndef GDN_SOURCE_DIGEST
 #define GDN_SOURCE_DIGEST "unversioned"
 #endif
-#include "gdn.h"
-#include "gdn_plan.h"
+#include "gdn_common.h"
 
 // Fixed device scratch of gdn_decode_step_noalloc (the resync's chunk factors),
 // for callers that cannot allocate device memory.  Each GPU the library runs
@@ -40,8 +31,6 @@
 static __device__ __align__(256) unsigned char scratch[GDN_NOALLOC_SCRATCH_BYTES];
 
 namespace {
-
-using bf16_t = uint16_t;
 
 // Read-only, wave-uniform operands are read through the constant address
 // space so the compiler issues scalar loads (the values land in SGPRs and feed
@@ -99,17 +88,6 @@ __device__ __forceinline__ float4 ldbuf4in(brsrc_t r, uint32_t voff, uint32_t so
   const auto x = __builtin_amdgcn_raw_buffer_load_b64(r, voff, soff, 0);
   return float4{__uint_as_float(x[0] << 16), __uint_as_float(x[0] & 0xffff0000u), __uint_as_float(x[1] << 16),
                 __uint_as_float(x[1] & 0xffff0000u)};
-}
-
-// Largest n in [0, N) with arr[n] <= x (arr non-decreasing, arr[0] = 0): the
-// sequence that owns slot x.  Uniform across the block.
-__device__ __forceinline__ int find_seq(const int32_t* __restrict__ arr, int N, int64_t x) {
-  int lo = 0, hi = N - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (arr[mid] <= x) lo = mid; else hi = mid - 1;
-  }
-  return lo;
 }
 
 // ---------------------------------------------------------------------------
@@ -652,16 +630,11 @@ __device__ __forceinline__ int64_t xcd_block(int64_t nb8) {
 // fp32 accumulator.  Parts are packed two per 32-bit word, the lower element
 // in the low half, and a lane's eight elements of one part fill four words.
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-typedef float f32x2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 struct Parts {
   u32x4_t p[3];  // hi, mid, lo
 };
 
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
-}
 __device__ __forceinline__ void split_pair(float x0, float x1, uint32_t& h, uint32_t& m, uint32_t& l) {
   h = pack_bf16(x0, x1);
   const float r0 = x0 - __uint_as_float(h << 16), r1 = x1 - __uint_as_float(h & 0xffff0000u);
@@ -3676,67 +3649,6 @@ __global__ void k_cache_init(const float* __restrict__ h0, float* __restrict__ S
        e += stride)
     pos[e] = 0;
 }
-
-// ---------------------------------------------------------------------------
-// Kernel timing: optional HIP events around every launch.
-struct ProfRec {
-  const char* name;
-  hipEvent_t a, b;
-};
-struct Profiler {
-  std::mutex mu;
-  bool on = false;
-  std::string filter;  // only launches whose name contains it (empty: all)
-  std::vector<ProfRec> recs;
-  std::vector<hipEvent_t> pool;
-  hipEvent_t get() {
-    if (!pool.empty()) {
-      hipEvent_t e = pool.back();
-      pool.pop_back();
-      return e;
-    }
-    // timing-only events: no system-scope fence (no cache writeback and
-    // invalidation around the timed launches); they are read only after the
-    // caller has synchronised the device
-    hipEvent_t e = nullptr;
-    if (hipEventCreateWithFlags(&e, hipEventDisableSystemFence) != hipSuccess) return nullptr;
-    return e;
-  }
-};
-Profiler& prof() {
-  static Profiler p;
-  return p;
-}
-
-// Brackets the launches made in its scope with events when timing is on.
-class Timed {
- public:
-  Timed(const char* name, hipStream_t st) : st_(st) {
-    Profiler& p = prof();
-    std::lock_guard<std::mutex> g(p.mu);
-    if (!p.on) return;
-    if (!p.filter.empty() && std::strstr(name, p.filter.c_str()) == nullptr) return;
-    rec_.name = name;
-    rec_.a = p.get();
-    rec_.b = p.get();
-    if (rec_.a && rec_.b) {
-      (void)hipEventRecord(rec_.a, st_);
-      active_ = true;
-    }
-  }
-  ~Timed() {
-    if (!active_) return;
-    (void)hipEventRecord(rec_.b, st_);
-    Profiler& p = prof();
-    std::lock_guard<std::mutex> g(p.mu);
-    p.recs.push_back(rec_);
-  }
-
- private:
-  hipStream_t st_;
-  ProfRec rec_{};
-  bool active_ = false;
-};
 
 // ---------------------------------------------------------------------------
 // Host orchestration.

@@ -1,0 +1,813 @@
+// The 8-bit key/value cache and attention over it (include/gdn.h): kernels and
+// C ABI.
+#include "gdn_mma.h"
+
+namespace {
+
+constexpr int kBlk = GDN_KV_BLOCK;  // tokens that share a scale
+static_assert(kBlk == 32);
+
+struct KvIO {
+  uint8_t* kc;  // [pages, H_kv, P, D]
+  uint8_t* vc;
+  float* ks;    // [pages, H_kv, P / 32]
+  float* vs;
+  const int32_t* table;  // [N, max_pages]
+  const int32_t* cu;     // [N + 1], nullptr: a token a sequence
+  const int32_t* start;  // [N], nullable
+  void* k;               // rows to write, or to read into
+  void* v;
+  int64_t T, ldk, ldv;
+  int N, H_kv, pages, max_pages, bpp;  // blocks per page
+};
+
+// The page that holds block b of sequence n, or -1.
+__device__ __forceinline__ int page_of(const int32_t* __restrict__ table, int max_pages, int pages, int bpp, int n, int b) {
+  const int i = b / bpp;
+  if (i >= max_pages) return -1;
+  const int p = table[static_cast<int64_t>(n) * max_pages + i];
+  return p >= 0 && p < pages ? p : -1;
+}
+
+// The cache block that a workgroup takes, and the packed rows that it holds.
+struct KvItem {
+  int64_t row0;    // packed row of the block's place 0 (may lie before the sequence's first)
+  int64_t blk;     // index of the block among [pages, H_kv, P / 32]
+  int lo, hi;      // places of the call's tokens
+  bool older;      // places before lo hold tokens
+};
+__device__ __forceinline__ bool kv_item(const KvIO& io, int h, KvItem* it) {
+  const int x = blockIdx.x;
+  int n, local;
+  int64_t c0, c1;
+  if (io.cu) {
+    // sequence n's slots begin at cu[n] / 32 + 2 n: its tokens lie in at most two
+    // blocks more than they fill
+    int lo = 0, hi = io.N - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (io.cu[mid] / kBlk + 2 * mid <= x) lo = mid; else hi = mid - 1;
+    }
+    n = lo;
+    local = x - (io.cu[n] / kBlk + 2 * n);
+    c0 = io.cu[n];
+    c1 = io.cu[n + 1];
+    c0 = c0 < 0 ? 0 : c0 > io.T ? io.T : c0;
+    c1 = c1 < c0 ? c0 : c1 > io.T ? io.T : c1;
+  } else {
+    n = x;
+    local = 0;
+    c0 = n;
+    c1 = n + 1;
+  }
+  const int64_t first = io.start ? (io.start[n] > 0 ? io.start[n] : 0) : 0, end = first + (c1 - c0);
+  const int64_t b = first / kBlk + local;
+  if (local < 0 || b * kBlk >= end || b >= (int64_t{1} << 30)) return false;
+  const int page = page_of(io.table, io.max_pages, io.pages, io.bpp, n, static_cast<int>(b));
+  if (page < 0) return false;
+  it->blk = (static_cast<int64_t>(page) * io.H_kv + h) * io.bpp + b % io.bpp;
+  it->lo = static_cast<int>(first > b * kBlk ? first - b * kBlk : 0);
+  it->hi = static_cast<int>(end - b * kBlk < kBlk ? end - b * kBlk : kBlk);
+  it->older = it->lo > 0;
+  it->row0 = c0 + b * kBlk - first;
+  return true;
+}
+
+// The least power of two s with most / s <= 448 = 1.75 2^8, at least 2^-117 (below
+// it the codes' smallest step is no normal number).
+__device__ __forceinline__ float scale_for(float most) {
+  const uint32_t u = __float_as_uint(most);
+  int e = static_cast<int>(u >> 23) - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+  e = e < 10 ? 10 : e;
+  return __uint_as_float(static_cast<uint32_t>(e) << 23);
+}
+// Four codes of x / s; what is not finite becomes NaN.  At the largest scale,
+// 2^120, codes over 240 would stand for more than fp32 holds.
+__device__ __forceinline__ uint32_t codes4(const float* x, float inv, float cap) {
+  float y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool fin = fabsf(x[i]) < INFINITY;
+    y[i] = fin ? fminf(fmaxf(x[i] * inv, -cap), cap) : __uint_as_float(0x7fc00000u);
+  }
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], w, true);
+  return static_cast<uint32_t>(w);
+}
+
+template <int E>
+__device__ __forceinline__ void load_row(const float* p, float* x) {
+#pragma unroll
+  for (int i = 0; i < E; i += 4) {
+    const v4f y = *reinterpret_cast<const v4f*>(p + i);
+    x[i] = y[0]; x[i + 1] = y[1]; x[i + 2] = y[2]; x[i + 3] = y[3];
+  }
+}
+template <int E>
+__device__ __forceinline__ void load_row(const bf16_t* p, float* x) {
+#pragma unroll
+  for (int i = 0; i < E; i += 8) {
+    const u32x4 y = *reinterpret_cast<const u32x4*>(p + i);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[i + 2 * e] = __uint_as_float(y[e] << 16);
+      x[i + 2 * e + 1] = __uint_as_float(y[e] & 0xffff0000u);
+    }
+  }
+}
+template <int E>
+__device__ __forceinline__ void load_codes(const uint8_t* p, uint32_t* c) {
+#pragma unroll
+  for (int i = 0; i < E / 4; i += 2) {
+    const u32x2 y = *reinterpret_cast<const u32x2*>(p + 4 * i);
+    c[i] = y[0];
+    c[i + 1] = y[1];
+  }
+}
+template <int E>
+__device__ __forceinline__ void store_codes(uint8_t* p, const uint32_t* c) {
+#pragma unroll
+  for (int i = 0; i < E / 4; i += 2) *reinterpret_cast<u32x2*>(p + 4 * i) = u32x2{c[i], c[i + 1]};
+}
+__device__ __forceinline__ void decode4(uint32_t c, float s, float* x) {
+  x[0] = __builtin_amdgcn_cvt_f32_fp8(c, 0) * s;
+  x[1] = __builtin_amdgcn_cvt_f32_fp8(c, 1) * s;
+  x[2] = __builtin_amdgcn_cvt_f32_fp8(c, 2) * s;
+  x[3] = __builtin_amdgcn_cvt_f32_fp8(c, 3) * s;
+}
+
+// One workgroup writes one block of one head: eight threads a token, first its
+// keys, then its values.
+template <typename T, int D>
+__global__ __launch_bounds__(256) void k_kv_write(KvIO io) {
+  constexpr int E = D / 8;  // elements of a thread
+  __shared__ float most[2][4];
+  const int h = blockIdx.y;
+  KvItem it;
+  if (!kv_item(io, h, &it)) return;
+  const int r = threadIdx.x >> 3, e0 = (threadIdx.x & 7) * E;
+  const bool fresh = r >= it.lo && r < it.hi;
+  float x[2][E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) x[0][i] = x[1][i] = 0.0f;
+  if (fresh) {
+    load_row<E>(static_cast<const T*>(io.k) + (it.row0 + r) * io.ldk + static_cast<int64_t>(h) * D + e0, x[0]);
+    load_row<E>(static_cast<const T*>(io.v) + (it.row0 + r) * io.ldv + static_cast<int64_t>(h) * D + e0, x[1]);
+  }
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const float a = fabsf(x[w][i]);
+      m = fmaxf(m, a < INFINITY ? a : 0.0f);
+    }
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
+    if ((threadIdx.x & 63) == 0) most[w][threadIdx.x >> 6] = m;
+  }
+  const float was[2] = {io.ks[it.blk], io.vs[it.blk]};
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const float m = fmaxf(fmaxf(most[w][0], most[w][1]), fmaxf(most[w][2], most[w][3]));
+    const float need = scale_for(m), s = it.older && was[w] > need ? was[w] : need;
+    const float inv = 1.0f / s, cap = s > 0x1p119f ? 240.0f : 448.0f;
+    uint8_t* at = (w ? io.vc : io.kc) + (it.blk * kBlk + r) * D + e0;
+    uint32_t c[E / 4];
+    if (fresh) {
+#pragma unroll
+      for (int i = 0; i < E / 4; ++i) c[i] = codes4(x[w] + 4 * i, inv, cap);
+      store_codes<E>(at, c);
+    } else if (r < it.lo && s != was[w]) {  // older tokens go over to the larger scale
+      load_codes<E>(at, c);
+#pragma unroll
+      for (int i = 0; i < E / 4; ++i) {
+        float y[4];
+        decode4(c[i], was[w], y);
+        c[i] = codes4(y, inv, cap);
+      }
+      store_codes<E>(at, c);
+    }
+    if (threadIdx.x == 0) (w ? io.vs : io.ks)[it.blk] = s;
+  }
+}
+
+template <typename T, int D>
+__global__ __launch_bounds__(256) void k_kv_read(KvIO io) {
+  constexpr int E = D / 8;
+  const int h = blockIdx.y;
+  const int r = threadIdx.x >> 3, e0 = (threadIdx.x & 7) * E;
+  KvItem it;
+  if (!kv_item(io, h, &it)) return;
+  if (r < it.lo || r >= it.hi) return;
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const float s = (w ? io.vs : io.ks)[it.blk];
+    uint32_t c[E / 4];
+    load_codes<E>((w ? io.vc : io.kc) + (it.blk * kBlk + r) * D + e0, c);
+    T* y = static_cast<T*>(w ? io.v : io.k) + (it.row0 + r) * (w ? io.ldv : io.ldk) + static_cast<int64_t>(h) * D + e0;
+#pragma unroll
+    for (int i = 0; i < E / 4; ++i) {
+      float x[4];
+      decode4(c[i], s, x);
+      store4(y + 4 * i, x);
+    }
+  }
+}
+
+// ---- attention over the cache ---------------------------------------------------
+//
+// Rows are the query heads of a group for one token after another; a workgroup
+// takes 16 MT of them for one key/value head and one split of the cache, its four
+// waves every fourth block of 32 tokens.  Codes go from memory into registers and
+// become bf16 there, exactly (the scale is a power of two): S^T = K Q^T on 16 x 16
+// x 32 products leaves a row in the lanes l % 16, and O^T = V^T P^T takes exp(S^T)
+// as it stands; the bytes of 4 tokens x 4 elements are transposed in registers.
+struct DecIO {
+  const uint8_t* kc;
+  const uint8_t* vc;
+  const float* ks;
+  const float* vs;
+  const int32_t* table;
+  const int32_t* cu;
+  const int32_t* len;
+  const void* q;
+  void* o;
+  float* lse;
+  float* part;  // [rows of partial results][D]
+  float* stat;  // [..][2]: maximum (of s log2 e) and sum
+  int64_t T, ldq, ldo, extra, rows;
+  int N, H_q, H_kv, G, pages, max_pages, bpp, max_len;
+  float c;
+};
+constexpr int kSplit = 512;    // tokens a split
+constexpr int kRowsSplit = 64;  // rows for which they are that many
+
+// Tokens a split of a sequence with `rows` rows a head: more where there are rows
+// enough to go round.  A function of the sequence alone, so that its bits do not
+// depend on the batch.
+__host__ __device__ inline int64_t split_tokens(int64_t rows) { return kSplit * ((rows + kRowsSplit - 1) / kRowsSplit); }
+
+struct DecSeq {
+  int64_t q0;
+  int n, Lq, Lk;  // Lk: cached tokens that are read
+  int64_t pos;    // of the first query
+  int64_t rows, split;
+  int splits;
+  // the last cached token that query token t sees, -1 for none
+  __device__ __forceinline__ int sees(int64_t t) const {
+    const int64_t p = pos + t < Lk - 1 ? pos + t : Lk - 1;
+    return static_cast<int>(p < -1 ? -1 : p);
+  }
+};
+__device__ __forceinline__ DecSeq dec_seq(const DecIO& io, int n) {
+  DecSeq s;
+  s.n = n;
+  s.q0 = n;
+  s.Lq = 1;
+  if (io.cu) {
+    int64_t c0 = io.cu[n], c1 = io.cu[n + 1];
+    c0 = c0 < 0 ? 0 : c0 > io.T ? io.T : c0;
+    c1 = c1 < c0 ? c0 : c1 > io.T ? io.T : c1;
+    s.q0 = c0;
+    s.Lq = static_cast<int>(c1 - c0);
+  }
+  int64_t len = io.len[n];
+  s.pos = len - s.Lq;
+  len = len < 0 ? 0 : len > io.max_len ? io.max_len : len;
+  s.Lk = static_cast<int>(len);
+  s.rows = static_cast<int64_t>(s.Lq) * io.G;
+  s.split = split_tokens(s.rows > 0 ? s.rows : 1);
+  s.splits = static_cast<int>((s.Lk + s.split - 1) / s.split);
+  if (s.splits < 1) s.splits = 1;
+  return s;
+}
+
+typedef float v4acc __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ v4acc mma16(u32x4 a, u32x4 b, v4acc c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+// Eight codes as bf16, times the power of two s.
+__device__ __forceinline__ u32x4 codes8(uint32_t lo, uint32_t hi, float s) {
+  u32x4 y;
+  y[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, false));
+  y[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, true));
+  y[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, false));
+  y[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, true));
+  return y;
+}
+// Eight fp32 values in NP bf16 parts that sum to them (exactly, with three).
+template <int NP>
+__device__ __forceinline__ void parts8(const float* x, u32x4* p) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float a = x[2 * e], b = x[2 * e + 1];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const uint32_t w = pack_bf16(a, b);
+      p[i][e] = w;
+      if (i + 1 < NP) {
+        a -= __uint_as_float(w << 16);
+        b -= __uint_as_float(w & 0xffff0000u);
+      }
+    }
+  }
+}
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t x) { return ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+// x of the lanes with the same l % 16: the largest, and the sum.
+__device__ __forceinline__ float max_rows(float x) {
+  x = fmaxf(x, __shfl_xor(x, 16, 64));
+  return fmaxf(x, __shfl_xor(x, 32, 64));
+}
+__device__ __forceinline__ float sum_rows(float x) {
+  x += __shfl_xor(x, 16, 64);
+  return x + __shfl_xor(x, 32, 64);
+}
+
+// A block of 32 tokens as loaded.  Keys: 16 bytes at 64 c + 16 (l / 16) of tokens
+// 16 t + l % 16.  Values: D / 16 bytes at (D / 16) (l % 16) of tokens 16 t + 4 (l /
+// 16) + i.
+template <int D>
+struct KvRegs {
+  static constexpr int W = D / 64;  // dwords of values a token
+  u32x4 k[2][D / 64];
+  uint32_t v[2][4][W];
+  float ks, vs;
+  bool there;
+  __device__ __forceinline__ void load(const DecIO& io, int n, int hk, int b, int lane) {
+    const int page = page_of(io.table, io.max_pages, io.pages, io.bpp, n, b);
+    there = page >= 0;
+    if (!there) return;
+    const int64_t blk = (static_cast<int64_t>(page) * io.H_kv + hk) * io.bpp + b % io.bpp;
+    ks = io.ks[blk];
+    vs = io.vs[blk];
+    const uint8_t* kp = io.kc + blk * (kBlk * D) + (lane & 15) * D + (lane >> 4) * 16;
+    const uint8_t* vp = io.vc + blk * (kBlk * D) + (lane >> 4) * 4 * D + (lane & 15) * (D / 16);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) k[t][c] = *reinterpret_cast<const u32x4*>(kp + t * 16 * D + c * 64);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(vp + (16 * t + i) * D);
+        if constexpr (W == 1) v[t][i][0] = src[0];
+        if constexpr (W == 2) {
+          const u32x2 y = *reinterpret_cast<const u32x2*>(src);
+          v[t][i][0] = y[0];
+          v[t][i][1] = y[1];
+        }
+        if constexpr (W == 4) {
+          const u32x4 y = *reinterpret_cast<const u32x4*>(src);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[t][i][e] = y[e];
+        }
+      }
+    }
+  }
+  // 4 tokens x 4 elements, tokens within a dword afterwards
+  __device__ __forceinline__ void transpose() {
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const uint32_t a = v[t][0][w], b = v[t][1][w], c = v[t][2][w], d = v[t][3][w];
+        const uint32_t ab0 = __builtin_amdgcn_perm(b, a, 0x05010400u), ab1 = __builtin_amdgcn_perm(b, a, 0x07030602u);
+        const uint32_t cd0 = __builtin_amdgcn_perm(d, c, 0x05010400u), cd1 = __builtin_amdgcn_perm(d, c, 0x07030602u);
+        v[t][0][w] = __builtin_amdgcn_perm(cd0, ab0, 0x05040100u);
+        v[t][1][w] = __builtin_amdgcn_perm(cd0, ab0, 0x07060302u);
+        v[t][2][w] = __builtin_amdgcn_perm(cd1, ab1, 0x05040100u);
+        v[t][3][w] = __builtin_amdgcn_perm(cd1, ab1, 0x07060302u);
+      }
+  }
+};
+
+template <typename T, int D, int MT>
+__global__ __launch_bounds__(256) void k_attn_decode(DecIO io) {
+  constexpr int NP = sizeof(T) == 2 ? 1 : 3, KC = D / 32, ND = D / 16, W = D / 64;
+  constexpr int PAD = D + 4;
+  __shared__ __align__(16) float sh_o[4][16][PAD];
+  __shared__ float sh_m[4][16], sh_l[4][16];
+  // Values that some row must not see, where they are NaN (0 x NaN would take them
+  // to it), count as 0, and odd[e] is the first token whose element e is one
+  // (odd[D] the first of all): a row that sees that token gets NaN in the end.
+  __shared__ int odd[D + 1];
+  const int hk = blockIdx.x % io.H_kv;
+  const int x = blockIdx.x / io.H_kv;
+  int tile, n;
+  if (io.cu) {
+    int lo = 0, hi = io.N - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (static_cast<int64_t>(io.cu[mid]) * io.G / (16 * MT) + mid <= x) lo = mid; else hi = mid - 1;
+    }
+    n = lo;
+    tile = static_cast<int>(x - (static_cast<int64_t>(io.cu[n]) * io.G / (16 * MT) + n));
+  } else {
+    const int per = (io.G + 16 * MT - 1) / (16 * MT);
+    n = x / per;
+    tile = x - n * per;
+  }
+  const DecSeq sq = dec_seq(io, n);
+  const int64_t r0 = static_cast<int64_t>(tile) * 16 * MT;
+  const int split = blockIdx.y;
+  if (tile < 0 || r0 >= sq.rows || split >= sq.splits) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4;
+
+  // queries: steps 2 c and 2 c + 1 hold elements 64 c + 16 g + j and + 8 + j
+  u32x4 q[MT][KC][NP];
+  int lim[MT];  // the last token that the row sees
+  int lim_lo = INT32_MAX;
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    const int64_t r = r0 + 16 * mt + (lane & 15);
+    const bool in = r < sq.rows;
+    const int64_t tok = in ? r / io.G : 0;
+    const int head = hk * io.G + static_cast<int>(in ? r - tok * io.G : 0);
+    lim[mt] = in ? sq.sees(tok) : -1;
+    if (in && lim[mt] < lim_lo) lim_lo = lim[mt];
+    const T* src = static_cast<const T*>(io.q) + (sq.q0 + tok) * io.ldq + static_cast<int64_t>(head) * D + 16 * g;
+#pragma unroll
+    for (int k = 0; k < KC; ++k) {
+      if constexpr (NP == 1) {
+        q[mt][k][0] = in ? *reinterpret_cast<const u32x4*>(src + 64 * (k / 2) + 8 * (k % 2)) : u32x4{0, 0, 0, 0};
+      } else {
+        float y[8];
+        load_row<8>(reinterpret_cast<const float*>(src) + 64 * (k / 2) + 8 * (k % 2), y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = in ? y[e] : 0.0f;
+        parts8<NP>(y, q[mt][k]);
+      }
+    }
+  }
+#pragma unroll
+  for (int m = 1; m < 16; m <<= 1) lim_lo = min(lim_lo, __shfl_xor(lim_lo, m, 64));
+  lim_lo = __builtin_amdgcn_readfirstlane(lim_lo);
+  const int64_t lastrow = (r0 + 16 * MT < sq.rows ? r0 + 16 * MT : sq.rows) - 1;
+  const int lim_hi = sq.sees(lastrow / io.G);
+
+  const int64_t t0 = sq.split * split, t1 = t0 + sq.split < lim_hi + 1 ? t0 + sq.split : lim_hi + 1;
+  const int b1 = static_cast<int>((t1 + kBlk - 1) / kBlk);
+  v4acc acc[MT][ND];
+  float m[MT], l[MT];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    m[mt] = -INFINITY;
+    l[mt] = 0.0f;
+#pragma unroll
+    for (int d = 0; d < ND; ++d) acc[mt][d] = v4acc{0, 0, 0, 0};
+  }
+  for (int e = threadIdx.x; e < D + 1; e += 256) odd[e] = INT32_MAX;
+  __syncthreads();
+  KvRegs<D> cur, nxt;
+  int b = static_cast<int>(t0 / kBlk) + wave;
+  if (b < b1) cur.load(io, n, hk, b, lane);
+  for (; b < b1; b += 4) {
+    if (b + 4 < b1) nxt.load(io, n, hk, b + 4, lane);
+    if (cur.there) {
+      const int j0 = b * kBlk;
+      const bool edge = j0 + kBlk - 1 > lim_lo;
+      v4acc s[MT][2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) s[mt][t] = v4acc{0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < KC; ++k) {
+          const u32x4 a = codes8(cur.k[t][k / 2][2 * (k % 2)], cur.k[t][k / 2][2 * (k % 2) + 1], cur.ks);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = NP - 1; i >= 0; --i) s[mt][t] = mma16(a, q[mt][k][i], s[mt][t]);
+        }
+      }
+      u32x4 p[MT][NP];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        float y[8];
+        float top = m[mt];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          y[e] = s[mt][e / 4][e % 4] * io.c;
+          if (edge && j0 + 16 * (e / 4) + 4 * g + e % 4 > lim[mt]) y[e] = -INFINITY;
+          top = fmaxf(top, y[e]);
+        }
+        top = max_rows(top);
+        if (__any(top > m[mt])) {
+          const float f = top > m[mt] ? __builtin_amdgcn_exp2f(m[mt] - top) : 1.0f;
+          m[mt] = top;
+          l[mt] *= f;
+#pragma unroll
+          for (int d = 0; d < ND; ++d) acc[mt][d] *= f;
+        }
+        const float mm = m[mt] == -INFINITY ? 0.0f : m[mt];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          y[e] = __builtin_amdgcn_exp2f(y[e] - mm);
+          l[mt] += y[e];
+        }
+        parts8<NP>(y, p[mt]);
+      }
+      if (edge) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int tok = j0 + 16 * t + 4 * g + i;
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+              uint32_t y = tok < sq.Lk ? cur.v[t][i][w] : 0u;  // nothing stands behind the last token
+              const uint32_t bad = nan_bytes(y);
+              if (bad) {
+                y &= ~((bad >> 7) * 0xffu);
+#pragma unroll 1
+                for (int e = 0; e < 4; ++e)
+                  if (bad >> (8 * e) & 0x80u) {
+                    atomicMin(&odd[(D / 16) * (lane & 15) + 4 * w + e], tok);
+                    atomicMin(&odd[D], tok);
+                  }
+              }
+              cur.v[t][i][w] = y;
+            }
+          }
+      }
+      cur.transpose();
+#pragma unroll
+      for (int d = 0; d < ND; ++d) {  // row l % 16 of tile d is element (D / 16) (l % 16) + d
+        const u32x4 a = codes8(cur.v[0][d % 4][d / 4], cur.v[1][d % 4][d / 4], cur.vs);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int i = NP - 1; i >= 0; --i) acc[mt][d] = mma16(a, p[mt][i], acc[mt][d]);
+      }
+    }
+    cur = nxt;
+  }
+
+  // the waves' results, joined in their order
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    const int row = lane & 15;
+    const float lw = sum_rows(l[mt]);
+    if (mt > 0) __syncthreads();
+    if (lane < 16) {
+      sh_m[wave][row] = m[mt];
+      sh_l[wave][row] = lw;
+    }
+    // lane (row, g) holds elements (D / 16) (4 g + i) + d
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int d = 0; d < ND; d += 4) {
+        const v4f y{acc[mt][d][i], acc[mt][d + 1][i], acc[mt][d + 2][i], acc[mt][d + 3][i]};
+        *reinterpret_cast<v4f*>(&sh_o[wave][row][(D / 16) * (4 * g + i) + d]) = y;
+      }
+    __syncthreads();
+    // 16 threads a row, D / 16 elements each
+    const int rr = threadIdx.x >> 4, e0 = (threadIdx.x & 15) * 4;
+    const int64_t r = r0 + 16 * mt + rr;
+    if (r < sq.rows) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) top = fmaxf(top, sh_m[w][rr]);
+      float f[4], sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        f[w] = sh_m[w][rr] == top && top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(sh_m[w][rr] - top);
+        sum += sh_l[w][rr] * f[w];
+      }
+      const int64_t tok = r / io.G;
+      const int head = hk * io.G + static_cast<int>(r - tok * io.G);
+      const bool whole = sq.splits == 1;
+      const float inv = !whole ? 1.0f : sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+      const int64_t pr = (sq.q0 * io.G + n * io.extra + r * sq.splits + split) * io.H_kv + hk;
+#pragma unroll
+      for (int e = e0; e < D; e += 64) {
+        float y[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const v4f z = *reinterpret_cast<const v4f*>(&sh_o[w][rr][e]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[i] = fmaf(z[i], f[w], y[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] *= inv;
+        if (odd[D] != INT32_MAX) {
+          const int sees = sq.sees(tok);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (sees >= odd[e + i]) y[i] = NAN;
+        }
+        if (whole)
+          store4(static_cast<T*>(io.o) + (sq.q0 + tok) * io.ldo + static_cast<int64_t>(head) * D + e, y);
+        else
+          store4(io.part + pr * D + e, y);
+      }
+      if (e0 == 0) {
+        if (!whole) {
+          io.stat[2 * pr] = top;
+          io.stat[2 * pr + 1] = sum;
+        } else if (io.lse) {
+          io.lse[(sq.q0 + tok) * io.H_q + head] = sum > 0.0f ? (top + __log2f(sum)) * kLn2 : sum != sum ? sum : -INFINITY;
+        }
+      }
+    }
+  }
+}
+
+// The splits of a row, joined in their order: a wave a row.
+template <typename T, int D>
+__global__ __launch_bounds__(256) void k_attn_join(DecIO io) {
+  const int lane = threadIdx.x & 63;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const int64_t tk = item / io.H_q;
+  const int head = static_cast<int>(item - tk * io.H_q);
+  if (tk >= io.T) return;
+  int n = static_cast<int>(tk);
+  if (io.cu) {
+    if (tk >= io.cu[io.N]) return;
+    n = find_seq(io.cu, io.N, tk);
+  }
+  const DecSeq sq = dec_seq(io, n);
+  if (sq.splits <= 1 || tk < sq.q0 || tk >= sq.q0 + sq.Lq) return;
+  const int hk = head / io.G;
+  const int64_t r = (tk - sq.q0) * io.G + head - hk * io.G;
+  const int64_t p0 = sq.q0 * io.G + n * io.extra + r * sq.splits;
+  float top = -INFINITY;
+  for (int i = lane; i < sq.splits; i += 64) top = fmaxf(top, io.stat[2 * ((p0 + i) * io.H_kv + hk)]);
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+  float sum = 0.0f, y[D / 64];
+#pragma unroll
+  for (int e = 0; e < D / 64; ++e) y[e] = 0.0f;
+  for (int i = 0; i < sq.splits; ++i) {
+    const int64_t pr = (p0 + i) * io.H_kv + hk;
+    const float mi = io.stat[2 * pr];
+    const float f = mi == -INFINITY && top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mi - top);
+    sum = fmaf(io.stat[2 * pr + 1], f, sum);
+#pragma unroll
+    for (int e = 0; e < D / 64; ++e) y[e] = fmaf(io.part[pr * D + lane + 64 * e], f, y[e]);
+  }
+  const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+  T* o = static_cast<T*>(io.o) + tk * io.ldo + static_cast<int64_t>(head) * D + lane;
+#pragma unroll
+  for (int e = 0; e < D / 64; ++e) {
+    if constexpr (sizeof(T) == 2)
+      o[64 * e] = static_cast<bf16_t>(pack_bf16(y[e] * inv, 0.0f));
+    else
+      o[64 * e] = y[e] * inv;
+  }
+  if (io.lse && lane == 0)
+    io.lse[tk * io.H_q + head] = sum > 0.0f ? (top + __log2f(sum)) * kLn2 : sum != sum ? sum : -INFINITY;
+}
+
+// ---- host side ----------------------------------------------------------------
+
+template <typename F>
+int kv_dispatch(const gdn_attn_shape_t* s, F&& f) {
+  if (s->in_dtype == GDN_BF16) {
+    if (s->d == 64) return f.template operator()<bf16_t, 64>();
+    if (s->d == 128) return f.template operator()<bf16_t, 128>();
+    return f.template operator()<bf16_t, 256>();
+  }
+  if (s->d == 64) return f.template operator()<float, 64>();
+  if (s->d == 128) return f.template operator()<float, 128>();
+  return f.template operator()<float, 256>();
+}
+
+// Checks what kv_write and kv_read share and fills io; *run = false: nothing to do.
+int kv_common(const gdn_attn_shape_t* s, int32_t N, const int32_t* cu, const int32_t* start, int64_t T, const void* k,
+              int64_t ldk, const void* v, int64_t ldv, const gdn_kv_cache_t* cache, const int32_t* table,
+              int32_t max_pages, KvIO* io) {
+  int rc = gdn::check_attn_shape(s);
+  if (rc != GDN_OK) return rc;
+  rc = gdn::check_kv_cache(cache);
+  if (rc != GDN_OK) return rc;
+  if (N < 0 || T < 0 || max_pages < 0) return GDN_ERR_INVALID_ARG;
+  if (!gdn::aligned16({cu, start, k, v, table})) return GDN_ERR_INVALID_ARG;
+  if (cu ? N == 0 && T > 0 : T != N) return GDN_ERR_INVALID_ARG;
+  if (T > 0 && (!k || !v || (max_pages > 0 && !table))) return GDN_ERR_INVALID_ARG;
+  if (T > INT32_MAX || s->H_kv > 65535) return GDN_ERR_UNSUPPORTED;
+  const int64_t w = static_cast<int64_t>(s->H_kv) * s->d;
+  rc = gdn::attn_rows({{ldk, w, &io->ldk}, {ldv, w, &io->ldv}});
+  if (rc != GDN_OK) return rc;
+  io->kc = static_cast<uint8_t*>(cache->k); io->vc = static_cast<uint8_t*>(cache->v);
+  io->ks = cache->k_scale; io->vs = cache->v_scale;
+  io->table = table; io->cu = cu; io->start = start;
+  io->k = const_cast<void*>(k); io->v = const_cast<void*>(v);
+  io->T = T; io->N = N; io->H_kv = s->H_kv; io->pages = cache->pages; io->max_pages = max_pages;
+  io->bpp = cache->page_tokens / kBlk;
+  return GDN_OK;
+}
+
+int64_t kv_slots(const KvIO& io) { return io.cu ? io.T / kBlk + 2 * static_cast<int64_t>(io.N) : io.N; }
+
+// Rows of partial results of each head beyond one a query: see split_tokens.
+int64_t decode_extra(int32_t G, bool one, int64_t max_len) {
+  const int64_t most = (max_len + kSplit - 1) / kSplit;
+  return (most > 1 ? most - 1 : 0) * (one && G <= kRowsSplit ? G : kRowsSplit);
+}
+
+}  // namespace
+
+extern "C" {
+
+int gdn_kv_write(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t* cu_seqlens, const int32_t* start,
+                 int64_t n_tokens, const void* k, int64_t ldk, const void* v, int64_t ldv, const gdn_kv_cache_t* cache,
+                 const int32_t* block_table, int32_t max_pages, void* stream) {
+  KvIO io{};
+  const int rc = kv_common(shape, n_seqs, cu_seqlens, start, n_tokens, k, ldk, v, ldv, cache, block_table, max_pages, &io);
+  if (rc != GDN_OK) return rc;
+  if (n_tokens == 0 || max_pages == 0) return GDN_OK;
+  if (kv_slots(io) * 256 >= gdn::kLaunchThreads / io.H_kv) return GDN_ERR_UNSUPPORTED;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return kv_dispatch(shape, [&]<typename T, int D>() {
+    Timed t_("k_kv_write", st);
+    hipLaunchKernelGGL((k_kv_write<T, D>), dim3(static_cast<unsigned>(kv_slots(io)), io.H_kv), dim3(256), 0, st, io);
+    return static_cast<int>(hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_HIP);
+  });
+}
+
+int gdn_kv_read(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t* cu_seqlens, const int32_t* start,
+                int64_t n_tokens, const gdn_kv_cache_t* cache, const int32_t* block_table, int32_t max_pages, void* k,
+                int64_t ldk, void* v, int64_t ldv, void* stream) {
+  KvIO io{};
+  const int rc = kv_common(shape, n_seqs, cu_seqlens, start, n_tokens, k, ldk, v, ldv, cache, block_table, max_pages, &io);
+  if (rc != GDN_OK) return rc;
+  if (n_tokens == 0 || max_pages == 0) return GDN_OK;
+  if (kv_slots(io) * 256 >= gdn::kLaunchThreads / io.H_kv) return GDN_ERR_UNSUPPORTED;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return kv_dispatch(shape, [&]<typename T, int D>() {
+    Timed t_("k_kv_read", st);
+    hipLaunchKernelGGL((k_kv_read<T, D>), dim3(static_cast<unsigned>(kv_slots(io)), io.H_kv), dim3(256), 0, st, io);
+    return static_cast<int>(hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_HIP);
+  });
+}
+
+size_t gdn_attn_decode_workspace_bytes(const gdn_attn_shape_t* shape, int32_t n_seqs, int64_t n_tokens, int64_t max_len) {
+  if (gdn::check_attn_shape(shape) != GDN_OK || n_seqs < 0 || n_tokens < 0 || max_len < 0) return 0;
+  if (n_tokens > INT32_MAX || max_len > INT32_MAX) return 0;
+  const int32_t G = shape->H_q / shape->H_kv;
+  const int64_t one = decode_extra(G, true, max_len), many = decode_extra(G, false, max_len);
+  const int64_t extra = n_tokens == n_seqs ? (one > many ? one : many) : many;
+  if (max_len <= kSplit) return gdn::kAlign;
+  const int64_t rows = (n_tokens * G + n_seqs * extra) * shape->H_kv;
+  const size_t bytes = static_cast<size_t>(rows) * (shape->d + 2) * sizeof(float);
+  return (bytes + gdn::kAlign) / gdn::kAlign * gdn::kAlign;
+}
+
+int gdn_attn_decode(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t* cu_seqlens, int64_t n_tokens,
+                    const void* q, int64_t ldq, const gdn_kv_cache_t* cache, const int32_t* block_table,
+                    int32_t max_pages, const int32_t* kv_len, int64_t max_len, void* o, int64_t ldo, float* lse,
+                    void* ws, size_t ws_bytes, void* stream) {
+  int rc = gdn::check_attn_shape(shape);
+  if (rc != GDN_OK) return rc;
+  rc = gdn::check_kv_cache(cache);
+  if (rc != GDN_OK) return rc;
+  if (n_seqs < 0 || n_tokens < 0 || max_pages < 0 || max_len < 0) return GDN_ERR_INVALID_ARG;
+  if (!gdn::aligned16({cu_seqlens, q, block_table, kv_len, o, lse, ws})) return GDN_ERR_INVALID_ARG;
+  if (cu_seqlens ? n_seqs == 0 && n_tokens > 0 : n_tokens != n_seqs) return GDN_ERR_INVALID_ARG;
+  if (n_tokens > 0 && (!q || !o || !kv_len || (max_pages > 0 && !block_table))) return GDN_ERR_INVALID_ARG;
+  if (n_tokens > INT32_MAX || max_len > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+  DecIO io{};
+  const int64_t w = static_cast<int64_t>(shape->H_q) * shape->d;
+  rc = gdn::attn_rows({{ldq, w, &io.ldq}, {ldo, w, &io.ldo}});
+  if (rc != GDN_OK) return rc;
+  const int64_t holds = static_cast<int64_t>(max_pages) * cache->page_tokens;
+  if (max_len > holds) max_len = holds;
+  const int32_t G = shape->H_q / shape->H_kv;
+  const int64_t splits = (max_len + kSplit - 1) / kSplit;
+  if (splits > 65535) return GDN_ERR_UNSUPPORTED;
+  io.extra = decode_extra(G, cu_seqlens == nullptr, max_len);
+  io.rows = (n_tokens * G + n_seqs * io.extra) * shape->H_kv;
+  if (splits > 1 && (!ws || ws_bytes < static_cast<size_t>(io.rows) * (shape->d + 2) * sizeof(float)))
+    return GDN_ERR_WORKSPACE;
+  if (n_tokens == 0) return GDN_OK;
+  io.kc = static_cast<const uint8_t*>(cache->k); io.vc = static_cast<const uint8_t*>(cache->v);
+  io.ks = cache->k_scale; io.vs = cache->v_scale;
+  io.table = block_table; io.cu = cu_seqlens; io.len = kv_len; io.q = q; io.o = o; io.lse = lse;
+  io.part = static_cast<float*>(ws);
+  io.stat = splits > 1 ? io.part + io.rows * shape->d : nullptr;
+  io.T = n_tokens; io.N = n_seqs; io.H_q = shape->H_q; io.H_kv = shape->H_kv; io.G = G;
+  io.pages = cache->pages; io.max_pages = max_pages; io.bpp = cache->page_tokens / kBlk;
+  io.max_len = static_cast<int>(max_len);
+  io.c = shape->scale * kLog2e;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  return kv_dispatch(shape, [&]<typename T, int D>() {
+    const int64_t tiles = cu_seqlens ? n_tokens * G / 16 + n_seqs : n_seqs * int64_t{(G + 15) / 16};
+    if (tiles * io.H_kv * 256 >= gdn::kLaunchThreads / (splits > 0 ? splits : 1)) return static_cast<int>(GDN_ERR_UNSUPPORTED);
+    {
+      Timed t_("k_attn_decode", st);
+      hipLaunchKernelGGL((k_attn_decode<T, D, 1>), dim3(static_cast<unsigned>(tiles * io.H_kv), static_cast<unsigned>(splits > 0 ? splits : 1)),
+                         dim3(256), 0, st, io);
+    }
+    if (splits > 1) {
+      Timed t_("k_attn_join", st);
+      hipLaunchKernelGGL((k_attn_join<T, D>), dim3(static_cast<unsigned>((n_tokens * io.H_q + 3) / 4)), dim3(256), 0, st, io);
+    }
+    return static_cast<int>(hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_HIP);
+  });
+}
+
+}  // extern "C"

@@ -1,6 +1,6 @@
-// The library's one device translation unit: every kernel is compiled together
-// with the same flags, and the parts below share the helpers and the kernel
-// timing of the first.
+// The translation unit of the recurrences and the q/k preparation: these kernels
+// are compiled together with the same flags, and the parts below share the
+// helpers of the first.
 #include "gdn_kernels.hip"
 
 #include <new>

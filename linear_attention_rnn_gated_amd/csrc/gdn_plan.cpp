@@ -392,4 +392,30 @@ int64_t qk_bwd_blocks(const gdn_qk_shape_t* s, int64_t T) {
   return b < 1024 ? b : 1024;
 }
 
+int check_attn_shape(const gdn_attn_shape_t* s) {
+  if (!s || s->H_q <= 0 || s->H_kv <= 0 || s->d <= 0) return GDN_ERR_INVALID_ARG;
+  if (!std::isfinite(s->scale) || !(s->scale > 0.0f)) return GDN_ERR_INVALID_ARG;
+  if (s->in_dtype != GDN_F32 && s->in_dtype != GDN_BF16) return GDN_ERR_UNSUPPORTED;
+  if (s->d != 64 && s->d != 128 && s->d != 256) return GDN_ERR_UNSUPPORTED;
+  if (s->H_q % s->H_kv != 0 || s->H_q > 4096) return GDN_ERR_UNSUPPORTED;
+  return GDN_OK;
+}
+
+int check_kv_cache(const gdn_kv_cache_t* c) {
+  if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale || c->pages <= 0 || c->page_tokens <= 0)
+    return GDN_ERR_INVALID_ARG;
+  if (!aligned16({c->k, c->v, c->k_scale, c->v_scale})) return GDN_ERR_INVALID_ARG;
+  if (c->page_tokens % GDN_KV_BLOCK != 0 || c->page_tokens > (1 << 20)) return GDN_ERR_UNSUPPORTED;
+  return GDN_OK;
+}
+
+int attn_rows(std::initializer_list<AttnRow> rows) {
+  for (const AttnRow& r : rows) {
+    *r.out = row_stride(r.ld, r.row);
+    if (*r.out < 0 || *r.out % 8 != 0) return GDN_ERR_INVALID_ARG;
+    if (*r.out > (int64_t{1} << 22)) return GDN_ERR_UNSUPPORTED;
+  }
+  return GDN_OK;
+}
+
 }  // namespace gdn

@@ -124,4 +124,15 @@ int check_qk_shape(const gdn_qk_shape_t* s);
 // the sizes alone).
 int64_t qk_bwd_blocks(const gdn_qk_shape_t* s, int64_t T);
 
+// Attention.
+int check_attn_shape(const gdn_attn_shape_t* s);
+int check_kv_cache(const gdn_kv_cache_t* c);
+struct AttnRow {
+  int64_t ld, row;  // as given, and elements of a dense row
+  int64_t* out;
+};
+// Distances of rows (0 = dense): multiples of 8 elements, at least the row, at
+// most 2^22 (a tile's offsets are 32 bits).
+int attn_rows(std::initializer_list<AttnRow> rows);
+
 }  // namespace gdn
