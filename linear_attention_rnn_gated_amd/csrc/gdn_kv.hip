@@ -115,20 +115,6 @@ __device__ __forceinline__ void load_row(const bf16_t* p, float* x) {
     }
   }
 }
-template <int E>
-__device__ __forceinline__ void load_codes(const uint8_t* p, uint32_t* c) {
-#pragma unroll
-  for (int i = 0; i < E / 4; i += 2) {
-    const u32x2 y = *reinterpret_cast<const u32x2*>(p + 4 * i);
-    c[i] = y[0];
-    c[i + 1] = y[1];
-  }
-}
-template <int E>
-__device__ __forceinline__ void store_codes(uint8_t* p, const uint32_t* c) {
-#pragma unroll
-  for (int i = 0; i < E / 4; i += 2) *reinterpret_cast<u32x2*>(p + 4 * i) = u32x2{c[i], c[i + 1]};
-}
 __device__ __forceinline__ void decode4(uint32_t c, float s, float* x) {
   x[0] = __builtin_amdgcn_cvt_f32_fp8(c, 0) * s;
   x[1] = __builtin_amdgcn_cvt_f32_fp8(c, 1) * s;
@@ -136,58 +122,67 @@ __device__ __forceinline__ void decode4(uint32_t c, float s, float* x) {
   x[3] = __builtin_amdgcn_cvt_f32_fp8(c, 3) * s;
 }
 
-// One workgroup writes one block of one head: eight threads a token, first its
-// keys, then its values.
+// A workgroup takes one block of one head, D / 8 lanes a token with eight elements
+// each, so that both the codes (8 bytes a lane) and the rows (16 or 32) of
+// neighbouring lanes lie side by side.
+template <int D>
+struct KvTile {
+  static constexpr int LANES = D / 8, ROWS = 256 / LANES, PASSES = kBlk / ROWS;
+};
+
 template <typename T, int D>
 __global__ __launch_bounds__(256) void k_kv_write(KvIO io) {
-  constexpr int E = D / 8;  // elements of a thread
+  using Tile = KvTile<D>;
   __shared__ float most[2][4];
   const int h = blockIdx.y;
   KvItem it;
   if (!kv_item(io, h, &it)) return;
-  const int r = threadIdx.x >> 3, e0 = (threadIdx.x & 7) * E;
-  const bool fresh = r >= it.lo && r < it.hi;
-  float x[2][E];
+  const int r0 = threadIdx.x / Tile::LANES, e0 = threadIdx.x % Tile::LANES * 8;
+  float x[2][Tile::PASSES][8];
 #pragma unroll
-  for (int i = 0; i < E; ++i) x[0][i] = x[1][i] = 0.0f;
-  if (fresh) {
-    load_row<E>(static_cast<const T*>(io.k) + (it.row0 + r) * io.ldk + static_cast<int64_t>(h) * D + e0, x[0]);
-    load_row<E>(static_cast<const T*>(io.v) + (it.row0 + r) * io.ldv + static_cast<int64_t>(h) * D + e0, x[1]);
+  for (int p = 0; p < Tile::PASSES; ++p) {
+    const int r = r0 + p * Tile::ROWS;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[0][p][i] = x[1][p][i] = 0.0f;
+    if (r >= it.lo && r < it.hi) {
+      load_row<8>(static_cast<const T*>(io.k) + (it.row0 + r) * io.ldk + static_cast<int64_t>(h) * D + e0, x[0][p]);
+      load_row<8>(static_cast<const T*>(io.v) + (it.row0 + r) * io.ldv + static_cast<int64_t>(h) * D + e0, x[1][p]);
+    }
   }
+  const float was[2] = {io.ks[it.blk], io.vs[it.blk]};
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
     float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const float a = fabsf(x[w][i]);
-      m = fmaxf(m, a < INFINITY ? a : 0.0f);
-    }
+    for (int p = 0; p < Tile::PASSES; ++p)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float a = fabsf(x[w][p][i]);
+        m = fmaxf(m, a < INFINITY ? a : 0.0f);
+      }
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
     if ((threadIdx.x & 63) == 0) most[w][threadIdx.x >> 6] = m;
   }
-  const float was[2] = {io.ks[it.blk], io.vs[it.blk]};
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
     const float m = fmaxf(fmaxf(most[w][0], most[w][1]), fmaxf(most[w][2], most[w][3]));
     const float need = scale_for(m), s = it.older && was[w] > need ? was[w] : need;
     const float inv = 1.0f / s, cap = s > 0x1p119f ? 240.0f : 448.0f;
-    uint8_t* at = (w ? io.vc : io.kc) + (it.blk * kBlk + r) * D + e0;
-    uint32_t c[E / 4];
-    if (fresh) {
 #pragma unroll
-      for (int i = 0; i < E / 4; ++i) c[i] = codes4(x[w] + 4 * i, inv, cap);
-      store_codes<E>(at, c);
-    } else if (r < it.lo && s != was[w]) {  // older tokens go over to the larger scale
-      load_codes<E>(at, c);
-#pragma unroll
-      for (int i = 0; i < E / 4; ++i) {
-        float y[4];
-        decode4(c[i], was[w], y);
-        c[i] = codes4(y, inv, cap);
+    for (int p = 0; p < Tile::PASSES; ++p) {
+      const int r = r0 + p * Tile::ROWS;
+      u32x2* at = reinterpret_cast<u32x2*>((w ? io.vc : io.kc) + (it.blk * kBlk + r) * D + e0);
+      if (r >= it.lo && r < it.hi) {
+        *at = u32x2{codes4(x[w][p], inv, cap), codes4(x[w][p] + 4, inv, cap)};
+      } else if (r < it.lo && s != was[w]) {  // older tokens go over to the larger scale
+        const u32x2 c = *at;
+        float y[8];
+        decode4(c[0], was[w], y);
+        decode4(c[1], was[w], y + 4);
+        *at = u32x2{codes4(y, inv, cap), codes4(y + 4, inv, cap)};
       }
-      store_codes<E>(at, c);
     }
     if (threadIdx.x == 0) (w ? io.vs : io.ks)[it.blk] = s;
   }
@@ -195,25 +190,29 @@ __global__ __launch_bounds__(256) void k_kv_write(KvIO io) {
 
 template <typename T, int D>
 __global__ __launch_bounds__(256) void k_kv_read(KvIO io) {
-  constexpr int E = D / 8;
+  using Tile = KvTile<D>;
   const int h = blockIdx.y;
-  const int r = threadIdx.x >> 3, e0 = (threadIdx.x & 7) * E;
   KvItem it;
   if (!kv_item(io, h, &it)) return;
-  if (r < it.lo || r >= it.hi) return;
+  const int r0 = threadIdx.x / Tile::LANES, e0 = threadIdx.x % Tile::LANES * 8;
+  const float s[2] = {io.ks[it.blk], io.vs[it.blk]};
+  u32x2 c[2][Tile::PASSES];
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const float s = (w ? io.vs : io.ks)[it.blk];
-    uint32_t c[E / 4];
-    load_codes<E>((w ? io.vc : io.kc) + (it.blk * kBlk + r) * D + e0, c);
-    T* y = static_cast<T*>(w ? io.v : io.k) + (it.row0 + r) * (w ? io.ldv : io.ldk) + static_cast<int64_t>(h) * D + e0;
+  for (int w = 0; w < 2; ++w)
 #pragma unroll
-    for (int i = 0; i < E / 4; ++i) {
-      float x[4];
-      decode4(c[i], s, x);
-      store4(y + 4 * i, x);
+    for (int p = 0; p < Tile::PASSES; ++p)
+      c[w][p] = *reinterpret_cast<const u32x2*>((w ? io.vc : io.kc) + (it.blk * kBlk + r0 + p * Tile::ROWS) * D + e0);
+#pragma unroll
+  for (int w = 0; w < 2; ++w)
+#pragma unroll
+    for (int p = 0; p < Tile::PASSES; ++p) {
+      const int r = r0 + p * Tile::ROWS;
+      if (r < it.lo || r >= it.hi) continue;
+      float y[8];
+      decode4(c[w][p][0], s[w], y);
+      decode4(c[w][p][1], s[w], y + 4);
+      store8(static_cast<T*>(w ? io.v : io.k) + (it.row0 + r) * (w ? io.ldv : io.ldk) + static_cast<int64_t>(h) * D + e0, y);
     }
-  }
 }
 
 // ---- attention over the cache ---------------------------------------------------
@@ -616,11 +615,18 @@ __global__ __launch_bounds__(256) void k_attn_decode(DecIO io) {
   }
 }
 
-// The splits of a row, joined in their order: a wave a row.
-template <typename T, int D>
-__global__ __launch_bounds__(256) void k_attn_join(DecIO io) {
-  const int lane = threadIdx.x & 63;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+// Joins the splits of a row: sixteen sums, of the splits i, i + 16, ..., each in
+// order, then those in order.  GROUPS 16: a block a row, D / 4 lanes for each of
+// the sums; GROUPS 1, for up to sixteen splits: D / 4 lanes a row, which gives the
+// same bits (products and sums are rounded apart).
+constexpr int kJoin = 16;
+template <typename T, int D, int GROUPS>
+__global__ __launch_bounds__(GROUPS == 1 ? 256 : D / 4 * kJoin) void k_attn_join(DecIO io) {
+  constexpr int LANES = D / 4, PER = GROUPS == 1 ? 256 / LANES : 1;  // rows a block
+  __shared__ __align__(16) float sh_y[GROUPS == 1 ? 1 : kJoin][D];
+  __shared__ float sh_s[kJoin];
+  const int e = threadIdx.x % LANES * 4, group = GROUPS == 1 ? 0 : threadIdx.x / LANES;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * PER + (GROUPS == 1 ? threadIdx.x / LANES : 0);
   const int64_t tk = item / io.H_q;
   const int head = static_cast<int>(item - tk * io.H_q);
   if (tk >= io.T) return;
@@ -634,31 +640,52 @@ __global__ __launch_bounds__(256) void k_attn_join(DecIO io) {
   const int hk = head / io.G;
   const int64_t r = (tk - sq.q0) * io.G + head - hk * io.G;
   const int64_t p0 = sq.q0 * io.G + n * io.extra + r * sq.splits;
+  const float* part = io.part + (p0 * io.H_kv + hk) * D + e;
+  const float* stat = io.stat + 2 * (p0 * io.H_kv + hk);
+  const int64_t dp = static_cast<int64_t>(io.H_kv) * D, ds = 2 * io.H_kv;
   float top = -INFINITY;
-  for (int i = lane; i < sq.splits; i += 64) top = fmaxf(top, io.stat[2 * ((p0 + i) * io.H_kv + hk)]);
+  for (int i = threadIdx.x % LANES; i < sq.splits; i += LANES) top = fmaxf(top, stat[i * ds]);
 #pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
-  float sum = 0.0f, y[D / 64];
+  for (int d = (LANES < 64 ? LANES : 64) / 2; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+  float sum = 0.0f;
+  v4f y{0, 0, 0, 0};
+  constexpr int STEP = GROUPS == 1 ? 1 : kJoin, U = 4;  // loads of U splits in flight
+  for (int i0 = group; i0 < sq.splits; i0 += U * STEP) {
+    v4f z[U];
+    float m[U], l[U];
 #pragma unroll
-  for (int e = 0; e < D / 64; ++e) y[e] = 0.0f;
-  for (int i = 0; i < sq.splits; ++i) {
-    const int64_t pr = (p0 + i) * io.H_kv + hk;
-    const float mi = io.stat[2 * pr];
-    const float f = mi == -INFINITY && top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mi - top);
-    sum = fmaf(io.stat[2 * pr + 1], f, sum);
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * STEP < sq.splits ? i0 + u * STEP : i0;
+      z[u] = *reinterpret_cast<const v4f*>(part + i * dp);
+      m[u] = stat[i * ds];
+      l[u] = stat[i * ds + 1];
+    }
 #pragma unroll
-    for (int e = 0; e < D / 64; ++e) y[e] = fmaf(io.part[pr * D + lane + 64 * e], f, y[e]);
+    for (int u = 0; u < U; ++u) {
+      if (i0 + u * STEP >= sq.splits) break;
+      const float f = m[u] == -INFINITY && top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(m[u] - top);
+      sum += l[u] * f;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) y[x] += z[u][x] * f;
+    }
+  }
+  if constexpr (GROUPS > 1) {
+    *reinterpret_cast<v4f*>(&sh_y[group][e]) = y;
+    if (e == 0) sh_s[group] = sum;
+    __syncthreads();
+    if (group) return;
+#pragma unroll
+    for (int g = 1; g < kJoin; ++g) {
+      const v4f z = *reinterpret_cast<const v4f*>(&sh_y[g][e]);
+      sum += sh_s[g];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) y[x] += z[x];
+    }
   }
   const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-  T* o = static_cast<T*>(io.o) + tk * io.ldo + static_cast<int64_t>(head) * D + lane;
-#pragma unroll
-  for (int e = 0; e < D / 64; ++e) {
-    if constexpr (sizeof(T) == 2)
-      o[64 * e] = static_cast<bf16_t>(pack_bf16(y[e] * inv, 0.0f));
-    else
-      o[64 * e] = y[e] * inv;
-  }
-  if (io.lse && lane == 0)
+  const float out[4] = {y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv};
+  store4(static_cast<T*>(io.o) + tk * io.ldo + static_cast<int64_t>(head) * D + e, out);
+  if (io.lse && e == 0)
     io.lse[tk * io.H_q + head] = sum > 0.0f ? (top + __log2f(sum)) * kLn2 : sum != sum ? sum : -INFINITY;
 }
 
@@ -795,16 +822,30 @@ int gdn_attn_decode(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t
   io.c = shape->scale * kLog2e;
   hipStream_t st = static_cast<hipStream_t>(stream);
   return kv_dispatch(shape, [&]<typename T, int D>() {
-    const int64_t tiles = cu_seqlens ? n_tokens * G / 16 + n_seqs : n_seqs * int64_t{(G + 15) / 16};
-    if (tiles * io.H_kv * 256 >= gdn::kLaunchThreads / (splits > 0 ? splits : 1)) return static_cast<int>(GDN_ERR_UNSUPPORTED);
+    constexpr int MT = sizeof(T) == 4 ? 1 : D <= 128 ? 4 : 2;
+    // many rows a sequence: tiles of MT times 16, so that a block of the cache is
+    // read and converted once for more of them (each row's bits are the same)
+    const bool wide = MT > 1 && cu_seqlens && n_tokens * G >= 32 * static_cast<int64_t>(n_seqs);
+    const int rows = wide ? 16 * MT : 16;
+    const int64_t tiles = cu_seqlens ? n_tokens * G / rows + n_seqs : n_seqs * int64_t{(G + 15) / 16};
+    if (tiles * io.H_kv * 256 >= gdn::kLaunchThreads / (splits > 0 ? splits : 1) ||
+        n_tokens * io.H_q >= gdn::kLaunchThreads / 1024)
+      return static_cast<int>(GDN_ERR_UNSUPPORTED);
+    const dim3 grid(static_cast<unsigned>(tiles * io.H_kv), static_cast<unsigned>(splits > 0 ? splits : 1));
     {
       Timed t_("k_attn_decode", st);
-      hipLaunchKernelGGL((k_attn_decode<T, D, 1>), dim3(static_cast<unsigned>(tiles * io.H_kv), static_cast<unsigned>(splits > 0 ? splits : 1)),
-                         dim3(256), 0, st, io);
+      if (wide)
+        hipLaunchKernelGGL((k_attn_decode<T, D, MT>), grid, dim3(256), 0, st, io);
+      else
+        hipLaunchKernelGGL((k_attn_decode<T, D, 1>), grid, dim3(256), 0, st, io);
     }
     if (splits > 1) {
       Timed t_("k_attn_join", st);
-      hipLaunchKernelGGL((k_attn_join<T, D>), dim3(static_cast<unsigned>((n_tokens * io.H_q + 3) / 4)), dim3(256), 0, st, io);
+      const int64_t items = n_tokens * io.H_q, per = 1024 / D;
+      if (splits <= kJoin)
+        hipLaunchKernelGGL((k_attn_join<T, D, 1>), dim3(static_cast<unsigned>((items + per - 1) / per)), dim3(256), 0, st, io);
+      else
+        hipLaunchKernelGGL((k_attn_join<T, D, kJoin>), dim3(static_cast<unsigned>(items)), dim3(D / 4 * kJoin), 0, st, io);
     }
     return static_cast<int>(hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_HIP);
   });

@@ -192,4 +192,12 @@ __device__ __forceinline__ void store4(bf16_t* p, const float* x) {
   *reinterpret_cast<u32x2*>(p) = u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
 }
 
+__device__ __forceinline__ void store8(float* p, const float* x) {
+  store4(p, x);
+  store4(p + 4, x + 4);
+}
+__device__ __forceinline__ void store8(bf16_t* p, const float* x) {
+  *reinterpret_cast<u32x4*>(p) = u32x4{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7])};
+}
+
 }  // namespace
