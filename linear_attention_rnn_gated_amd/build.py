@@ -19,7 +19,7 @@ LIB = os.path.join(PKG, "libgdn.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["gdn_library.hip", "gdn_attn.hip", "gdn_kv.hip", "gdn_plan.cpp", "gdn_rope.cpp"]
-INCLUDED = ["gdn_common.h", "gdn_plan.h", "gdn_kernels.hip", "gdn_lru.hip", "gdn_qk.hip"]  # by the sources
+INCLUDED = ["gdn_common.h", "gdn_mma.h", "gdn_attn_walk.h", "gdn_plan.h", "gdn_kernels.hip", "gdn_lru.hip", "gdn_qk.hip"]  # by the sources
 FLAGS = [
     "--offload-arch=gfx950",
     "-O3",

@@ -1,6 +1,6 @@
 // Causal attention over packed sequences with grouped heads (include/gdn.h):
 // kernels and C ABI.
-#include "gdn_mma.h"
+#include "gdn_attn_walk.h"
 
 namespace {
 
@@ -47,182 +47,86 @@ __device__ __forceinline__ int tile_seq(const int32_t* __restrict__ cu, int N, i
 inline int64_t tile_slots(int64_t T, int64_t N, int rows) { return T / rows + N; }
 
 // ---- forward ------------------------------------------------------------------
-//
-// A wave takes 32 query rows of one head, a block NW waves of them, and the
-// block goes over the keys and values BN tokens at a time.  The transposed
-// product S^T = K Q^T leaves one query row per lane (its other half in lane +
-// 32), so the softmax's maximum and sum are taken within the lane and once
-// across the halves, and exp(S^T) is the right operand of O^T = V^T P^T as it
-// stands: k runs over the tokens in the order in which the lane holds them, and
-// V^T is read from LDS in that order.
-template <typename T, int D>
-struct FwdTile {
-  static constexpr int BN = sizeof(T) == 2 && D <= 128 ? 64 : 32;  // keys a step
-  static constexpr int NW = 4;
-  static constexpr int BM = 32 * NW;
+
+// The query rows of a block: 32 for each wave.
+struct QueryTile {
+  Span sp;
+  int hk, hq;
+  int r0, row;  // the wave's first row, the lane's
+  int rows;     // of the wave that there are (0 or fewer: none)
+  int last;     // the last token that the block's rows see
+  AttnRows at;
+};
+template <int BM>
+__device__ __forceinline__ bool query_tile(const AttnIO& io, int wave, int lane, QueryTile* x) {
+  x->hk = blockIdx.x % io.H_kv;
+  const int y = blockIdx.x / io.H_kv;
+  x->hq = x->hk * io.G + y % io.G;
+  int tile;
+  const int n = tile_seq(io.cu_q, io.N, BM, y / io.G, &tile);
+  const Span sp = x->sp = span_of(io.cu_q, io.cu_k, io.T_q, io.T_k, n);
+  const int tiles = (sp.Lq + BM - 1) / BM;
+  if (tile < 0 || tile >= tiles) return false;
+  tile = tiles - 1 - tile;  // the longest first
+  const int off = sp.Lk - sp.Lq;  // row i sees keys up to i + off
+  x->r0 = tile * BM + wave * 32;
+  x->row = x->r0 + (lane & 31);
+  x->rows = sp.Lq - x->r0 < 32 ? sp.Lq - x->r0 : 32;
+  x->last = ((tile + 1) * BM < sp.Lq ? (tile + 1) * BM - 1 : sp.Lq - 1) + off;
+  x->at.lim = x->row < sp.Lq ? x->row + off : -1;
+  x->at.lo = x->r0 + off;
+  x->at.hi = x->rows > 0 ? x->r0 + x->rows - 1 + off : -1;
+  x->at.block_lo = tile * BM + off;
+  return true;
+}
+
+// Keys and values of one head as rows in memory.
+template <typename T, int D, int BN, int NW>
+struct RowStage {
+  static constexpr bool DIRECT = sizeof(T) == 2, GAPS = false;
+  const AttnIO& io;
+  const Span& sp;
+  int hk;
+  Stager<T, D, BN, NW> sk, sv;
+  __device__ __forceinline__ RowStage(const AttnIO& io, const Span& sp, int hk, int wave, int lane)
+      : io(io), sp(sp), hk(hk), sk(io.ldk, wave, lane), sv(io.ldv, wave, lane) {}
+  __device__ __forceinline__ void start(int j, char* kb, char* vb) {
+    const int rows = sp.Lk - j * BN < BN ? sp.Lk - j * BN : BN;
+    sk.start(rows_rsrc<T, D>(io.k, sp.k0 + j * BN, io.ldk, hk, rows), kb);
+    sv.start(rows_rsrc<T, D>(io.v, sp.k0 + j * BN, io.ldv, hk, rows), vb);
+  }
+  __device__ __forceinline__ void finish(char* kb, char* vb) const {
+    sk.finish(kb);
+    sv.finish(vb);
+  }
 };
 
-// Infinities and NaN of a tile of v that some row must not see (0 x inf would take
-// them to it): they become 0 in LDS, and odd[e] the first token whose element e
-// is one (odd[D] the first of all).  A row that sees that token sees all before
-// it, so its element e is NaN in the end.
-template <typename T, int D, int ROWS, int THREADS>
-__device__ __forceinline__ void set_aside(char* tile, int j0, int* odd) {
-  constexpr int RB = D * sizeof(T), CPR = RB / 16, E = 16 / sizeof(T);
-#pragma unroll 1
-  for (int c = threadIdx.x; c < ROWS * CPR; c += THREADS) {
-    u32x4* at = reinterpret_cast<u32x4*>(tile) + c;
-    const u32x4 x = *at;
-    constexpr uint32_t lo = sizeof(T) == 2 ? 0x7f80u : 0, hi = 0x7f800000u;
-    bool bad = false;
+template <typename T, int D>
+__device__ __forceinline__ void load_rows(const void* x, int64_t at, int64_t ld, int h, int rows, int lane,
+                                          Held<T, D> (&y)[D / 16]) {
+  const brsrc_t r = rows_rsrc<T, D>(x, at, ld, h, rows);
+  const uint32_t col = static_cast<uint32_t>((lane & 31) * ld * sizeof(T)) + 8 * (lane >> 5) * sizeof(T);
 #pragma unroll
-    for (int w = 0; w < 4; ++w) bad |= (x[w] & hi) == hi || (sizeof(T) == 2 && (x[w] & lo) == lo);
-    if (!bad) continue;
-    const int r = c / CPR, e0 = ((c % CPR) ^ swizzle<RB>(r)) * E;
-    T* y = reinterpret_cast<T*>(at);
-#pragma unroll 1
-    for (int e = 0; e < E; ++e) {
-      uint32_t u = sizeof(T) == 2 ? static_cast<uint32_t>(reinterpret_cast<uint16_t*>(y)[e]) << 16 : reinterpret_cast<uint32_t*>(y)[e];
-      if ((u & hi) != hi) continue;
-      y[e] = 0;
-      atomicMin(&odd[e0 + e], j0 + r);
-      atomicMin(&odd[D], j0 + r);
-    }
-  }
+  for (int ks = 0; ks < D / 16; ++ks) y[ks].load(r, col + 16 * ks * sizeof(T));
 }
 
 template <typename T, int D>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attn_fwd(AttnIO io) {
 #ifdef GDN_DEVICE_PASS
-  using Tile = FwdTile<T, D>;
-  constexpr int BN = Tile::BN, BM = Tile::BM, NW = Tile::NW, NS = BN / 32, KS = D / 16, ND = D / 32;
-  constexpr int RB = D * sizeof(T);
-  __shared__ __align__(1024) char kA[BN * RB], vA[BN * RB], kB[BN * RB], vB[BN * RB];
+  using Tile = AttnTile<T, D>;
   __shared__ int odd[D + 1];
-  const int hk = blockIdx.x % io.H_kv;
-  const int y = blockIdx.x / io.H_kv;
-  const int hq = hk * io.G + y % io.G;
-  int tile;
-  const int n = tile_seq(io.cu_q, io.N, BM, y / io.G, &tile);
-  const Span sp = span_of(io.cu_q, io.cu_k, io.T_q, io.T_k, n);
-  const int tiles = (sp.Lq + BM - 1) / BM;
-  if (tile < 0 || tile >= tiles) return;
-  tile = tiles - 1 - tile;  // the longest first
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r0 = tile * BM + wave * 32, row = r0 + (lane & 31);
-  const int off = sp.Lk - sp.Lq;  // row i sees keys up to i + off
-  const int last = (tile + 1) * BM < sp.Lq ? (tile + 1) * BM - 1 : sp.Lq - 1;
-  const int steps = last + off >= 0 ? (last + off) / BN + 1 : 0;
-  const int lim = row < sp.Lq ? row + off : -1;
-  const int wave_last = r0 + 31 < sp.Lq ? r0 + 31 : sp.Lq - 1;
-  const int lim_hi = r0 < sp.Lq ? wave_last + off : -1, lim_lo = r0 + off;  // of the wave's rows
-
-  Frag<T> q[KS];
-  {
-    const int rows = sp.Lq - r0 < 32 ? sp.Lq - r0 : 32;
-    const brsrc_t rq = rows_rsrc<T, D>(io.q, sp.q0 + (rows > 0 ? r0 : 0), io.ldq, hq, rows);
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) q[ks].load(rq, (lane & 31) * io.ldq * sizeof(T) + (16 * ks + 8 * (lane >> 5)) * sizeof(T));
-  }
-  const Stager<T, D, BN, NW> sk(io.ldk, wave, lane), sv(io.ldv, wave, lane);
-  auto fetch = [&](char* kb, char* vb, int j) {
-    const int rows = sp.Lk - j * BN < BN ? sp.Lk - j * BN : BN;
-    sk.start(rows_rsrc<T, D>(io.k, sp.k0 + j * BN, io.ldk, hk, rows), kb);
-    sv.start(rows_rsrc<T, D>(io.v, sp.k0 + j * BN, io.ldv, hk, rows), vb);
-  };
-
-  v16f acc[ND];
-#pragma unroll
-  for (int d = 0; d < ND; ++d) acc[d] = zero16();
-  float m = -INFINITY, l = 0.0f;
-  const int edge_lo = tile * BM + off;  // behind it places are masked for some row of the block
-  for (int e = threadIdx.x; e < D + 1; e += NW * 64) odd[e] = INT32_MAX;
-  __syncthreads();
-
-  auto step = [&](char* kb, char* vb, char* kn, char* vn, int j) {
-    wait_loads();
-    __syncthreads();
-    if (j + 1 < steps) fetch(kn, vn, j + 1);
-    const int j0 = j * BN;
-    if (j0 + BN - 1 > edge_lo) {
-      set_aside<T, D, BN, NW * 64>(vb, j0, odd);
-      __syncthreads();
-    }
-    if (j0 > lim_hi) return;
-    v16f s[NS];
-#pragma unroll
-    for (int t = 0; t < NS; ++t) {
-      s[t] = zero16();
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) s[t] = mma32(row_frag<T, RB>(kb, 32 * t, ks, lane), q[ks], s[t]);
-    }
-    const bool edge = j0 + BN - 1 > lim_lo;  // some place is masked for some row
-    if (edge) {
-#pragma unroll
-      for (int t = 0; t < NS; ++t)
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (j0 + 32 * t + c_row(i, lane) > lim) s[t][i] = -INFINITY;
-    }
-    float top = m;
-#pragma unroll
-    for (int t = 0; t < NS; ++t)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) top = fmaxf(top, s[t][i]);
-    top = fmaxf(top, other_half(top));
-    if (__any(top > m)) {
-      const float f = top > m ? __builtin_amdgcn_exp2f((m - top) * io.c) : 1.0f;  // 0 from m = -inf
-      m = top;
-      l *= f;
-#pragma unroll
-      for (int d = 0; d < ND; ++d) acc[d] *= f;
-    }
-    const float mc = m == -INFINITY ? 0.0f : m * io.c;
-    Frag<T> p[NS][2];
-#pragma unroll
-    for (int t = 0; t < NS; ++t) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        s[t][i] = __builtin_amdgcn_exp2f(fmaf(s[t][i], io.c, -mc));
-        l += s[t][i];
-      }
-      p[t][0].pack(s[t], 0);
-      p[t][1].pack(s[t], 8);
-    }
-#pragma unroll
-    for (int t = 0; t < NS; ++t)
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int d = 0; d < ND; ++d) acc[d] = mma32(col_frag<T, RB>(vb, 32 * t + 16 * u, d, lane), p[t][u], acc[d]);
-  };
-  if (steps > 0) fetch(kA, vA, 0);
-  for (int j = 0; j < steps; j += 2) {
-    step(kA, vA, kB, vB, j);
-    if (j + 1 < steps) step(kB, vB, kA, vA, j + 1);
-  }
-
-  l += other_half(l);
-  __syncthreads();
-  if (odd[D] != INT32_MAX) {
-#pragma unroll
-    for (int d = 0; d < ND; ++d)
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (lim >= odd[32 * d + c_row(i, lane)]) acc[d][i] = NAN;
-  }
-  const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;  // an empty row is 0
-  if (row < sp.Lq) {
-    T* o = static_cast<T*>(io.o) + (sp.q0 + row) * io.ldo + static_cast<int64_t>(hq) * D;
-#pragma unroll
-    for (int d = 0; d < ND; ++d)
-#pragma unroll
-      for (int a = 0; a < 4; ++a) {
-        const float x[4] = {acc[d][4 * a] * inv, acc[d][4 * a + 1] * inv, acc[d][4 * a + 2] * inv, acc[d][4 * a + 3] * inv};
-        store4(o + 32 * d + 8 * a + 4 * (lane >> 5), x);
-      }
-    if (io.lse && lane < 32)
-      io.lse[(sp.q0 + row) * io.H_q + hq] = l > 0.0f ? (m * io.c + __log2f(l)) * kLn2 : l != l ? l : -INFINITY;
+  QueryTile x;
+  if (!query_tile<Tile::BM>(io, wave, lane, &x)) return;
+  Held<T, D> q[D / 16];
+  load_rows<T, D>(io.q, x.sp.q0 + (x.rows > 0 ? x.r0 : 0), io.ldq, x.hq, x.rows, lane, q);
+  RowStage<T, D, Tile::BN, Tile::NW> st(io, x.sp, x.hk, wave, lane);
+  AttnState<D> a;
+  const int steps = x.last >= 0 ? x.last / Tile::BN + 1 : 0;
+  attn_walk<T, T, D, Tile::BN, Tile::NW>(st, q, 0, steps, x.at, io.c, lane, odd, a);
+  if (x.row < x.sp.Lq) {
+    store_row<D>(static_cast<T*>(io.o) + (x.sp.q0 + x.row) * io.ldo + static_cast<int64_t>(x.hq) * D, a.acc, inverse_sum(a.l), lane);
+    if (io.lse && lane < 32) io.lse[(x.sp.q0 + x.row) * io.H_q + x.hq] = lse_of(a.m * io.c, a.l);
   }
 #endif
 }
@@ -242,6 +146,8 @@ struct GradIO {
   void* dk;
   void* dv;
   float* stat;  // [H_q][T_q][2]: lse log2(e) and dO . o
+  float* part;  // [parts][2][T_k][H_kv][D] fp32 sums for dk and dv, where parts > 1
+  int parts;    // that a group's heads are cut into
   int64_t lddo, lddq, lddk, lddv;
   float scale;
 };
@@ -249,151 +155,157 @@ struct GradIO {
 template <typename T, int D>
 __global__ __launch_bounds__(256, sizeof(T) == 2 && D <= 128 ? 2 : 1) void k_attn_dq(GradIO g) {
 #ifdef GDN_DEVICE_PASS
-  constexpr int BN = 32, NW = 4, BM = 32 * NW, KS = D / 16, ND = D / 32, RB = D * sizeof(T);
-  __shared__ __align__(1024) char kA[BN * RB], vA[BN * RB], kB[BN * RB], vB[BN * RB];
+  constexpr int BN = 32, NW = 4, KS = D / 16, ND = D / 32;
+  using P = Plane<T, D, BN>;
+  constexpr bool TWO = 4 * P::TILE <= 144 * 1024;
+  __shared__ __align__(1024) char kA[P::TILE], vA[P::TILE], kB[TWO ? P::TILE : 16], vB[TWO ? P::TILE : 16];
   const AttnIO& io = g.a;
-  const int hk = blockIdx.x % io.H_kv;
-  const int y = blockIdx.x / io.H_kv;
-  const int hq = hk * io.G + y % io.G;
-  int tile;
-  const int n = tile_seq(io.cu_q, io.N, BM, y / io.G, &tile);
-  const Span sp = span_of(io.cu_q, io.cu_k, io.T_q, io.T_k, n);
-  const int tiles = (sp.Lq + BM - 1) / BM;
-  if (tile < 0 || tile >= tiles) return;
-  tile = tiles - 1 - tile;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r0 = tile * BM + wave * 32, row = r0 + (lane & 31);
-  const int off = sp.Lk - sp.Lq;
-  const int last = (tile + 1) * BM < sp.Lq ? (tile + 1) * BM - 1 : sp.Lq - 1;
-  const int steps = last + off >= 0 ? (last + off) / BN + 1 : 0;
-  const int lim = row < sp.Lq ? row + off : -1;
-  const int wave_last = r0 + 31 < sp.Lq ? r0 + 31 : sp.Lq - 1;
-  const int lim_hi = r0 < sp.Lq ? wave_last + off : -1, lim_lo = r0 + off;
-
-  Frag<T> q[KS], dO[KS];
+  QueryTile x;
+  if (!query_tile<32 * NW>(io, wave, lane, &x)) return;
+  const int64_t at = x.sp.q0 + (x.rows > 0 ? x.r0 : 0);
+  Held<T, D> q[KS], dO[KS];
+  load_rows<T, D>(io.q, at, io.ldq, x.hq, x.rows, lane, q);
+  load_rows<T, D>(g.dO, at, g.lddo, x.hq, x.rows, lane, dO);
   float lse2, dot = 0.0f;
   {
-    const int rows = sp.Lq - r0 < 32 ? sp.Lq - r0 : 32;
-    const int64_t at = sp.q0 + (rows > 0 ? r0 : 0);
-    const brsrc_t rq = rows_rsrc<T, D>(io.q, at, io.ldq, hq, rows);
-    const brsrc_t rd = rows_rsrc<T, D>(g.dO, at, g.lddo, hq, rows);
-    const brsrc_t ro = rows_rsrc<T, D>(io.o, at, io.ldo, hq, rows);
+    const brsrc_t rd = rows_rsrc<T, D>(g.dO, at, g.lddo, x.hq, x.rows);
+    const brsrc_t ro = rows_rsrc<T, D>(io.o, at, io.ldo, x.hq, x.rows);
     const uint32_t col = 8 * (lane >> 5) * sizeof(T), r = lane & 31;
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      q[ks].load(rq, static_cast<uint32_t>(r * io.ldq * sizeof(T)) + col + 16 * ks * sizeof(T));
-      dO[ks].load(rd, static_cast<uint32_t>(r * g.lddo * sizeof(T)) + col + 16 * ks * sizeof(T));
-      Frag<T> o;
-      o.load(ro, static_cast<uint32_t>(r * io.ldo * sizeof(T)) + col + 16 * ks * sizeof(T));
-      dot += o.dot(dO[ks]);
-    }
+    for (int ks = 0; ks < KS; ++ks)
+      dot = dot8<T>(rd, static_cast<uint32_t>(r * g.lddo * sizeof(T)) + col + 16 * ks * sizeof(T), ro,
+                    static_cast<uint32_t>(r * io.ldo * sizeof(T)) + col + 16 * ks * sizeof(T), dot);
     dot += other_half(dot);
-    lse2 = row < sp.Lq ? io.lse[(sp.q0 + row) * io.H_q + hq] * kLog2e : 0.0f;
-    if (row < sp.Lq && lane < 32) {
-      float* s = g.stat + 2 * (static_cast<int64_t>(hq) * io.T_q + sp.q0 + row);
+    lse2 = x.row < x.sp.Lq ? io.lse[(x.sp.q0 + x.row) * io.H_q + x.hq] * kLog2e : 0.0f;
+    if (x.row < x.sp.Lq && lane < 32) {
+      float* s = g.stat + 2 * (static_cast<int64_t>(x.hq) * io.T_q + x.sp.q0 + x.row);
       s[0] = lse2;
       s[1] = dot;
     }
   }
-  const Stager<T, D, BN, NW> sk(io.ldk, wave, lane), sv(io.ldv, wave, lane);
-  auto fetch = [&](char* kb, char* vb, int j) {
-    const int rows = sp.Lk - j * BN < BN ? sp.Lk - j * BN : BN;
-    sk.start(rows_rsrc<T, D>(io.k, sp.k0 + j * BN, io.ldk, hk, rows), kb);
-    sv.start(rows_rsrc<T, D>(io.v, sp.k0 + j * BN, io.ldv, hk, rows), vb);
-  };
+  RowStage<T, D, BN, NW> st(io, x.sp, x.hk, wave, lane);
   v16f acc[ND];
 #pragma unroll
   for (int d = 0; d < ND; ++d) acc[d] = zero16();
+  const int end = x.last >= 0 ? x.last / BN + 1 : 0;
   auto step = [&](char* kb, char* vb, char* kn, char* vn, int j) {
-    wait_loads();
+    if constexpr (st.DIRECT) wait_loads();
     __syncthreads();
-    if (j + 1 < steps) fetch(kn, vn, j + 1);
+    if (j + 1 < end) st.start(j + 1, kn, vn);
     const int j0 = j * BN;
-    if (j0 > lim_hi) return;
-    v16f s = zero16(), dp = zero16();
+    if (j0 <= x.at.hi) {
+      v16f s = zero16(), dp = zero16();
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      s = mma32(row_frag<T, RB>(kb, 0, ks, lane), q[ks], s);
-      dp = mma32(row_frag<T, RB>(vb, 0, ks, lane), dO[ks], dp);
+      for (int ks = 0; ks < KS; ++ks) {
+        s = mma32(row_frag<T, D, BN>(kb, 0, ks, lane), q[ks].get(), s);
+        dp = mma32(row_frag<T, D, BN>(vb, 0, ks, lane), dO[ks].get(), dp);
+      }
+      const bool edge = j0 + BN - 1 > x.at.lo;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float p = __builtin_amdgcn_exp2f(fmaf(s[i], io.c, -lse2));
+        s[i] = p * (dp[i] - dot);
+        if (edge && j0 + c_row(i, lane) > x.at.lim) s[i] = 0.0f;
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        Frag<T> ds;
+        ds.pack(s, 8 * u);
+#pragma unroll
+        for (int d = 0; d < ND; ++d) acc[d] = mma32(col_frag<T, D, BN>(kb, 16 * u, d, lane), ds, acc[d]);
+      }
     }
-    const bool edge = j0 + BN - 1 > lim_lo;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float p = __builtin_amdgcn_exp2f(fmaf(s[i], io.c, -lse2));
-      s[i] = p * (dp[i] - dot);
-      if (edge && j0 + c_row(i, lane) > lim) s[i] = 0.0f;
-    }
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      Frag<T> ds;
-      ds.pack(s, 8 * u);
-#pragma unroll
-      for (int d = 0; d < ND; ++d) acc[d] = mma32(col_frag<T, RB>(kb, 16 * u, d, lane), ds, acc[d]);
+    if constexpr (!st.DIRECT) {
+      if constexpr (!TWO) __syncthreads();
+      if (j + 1 < end) st.finish(kn, vn);
     }
   };
-  if (steps > 0) fetch(kA, vA, 0);
-  for (int j = 0; j < steps; j += 2) {
-    step(kA, vA, kB, vB, j);
-    if (j + 1 < steps) step(kB, vB, kA, vA, j + 1);
+  if (end > 0) {
+    st.start(0, kA, vA);
+    if constexpr (!st.DIRECT) st.finish(kA, vA);
   }
-  if (row < sp.Lq) {
-    T* o = static_cast<T*>(g.dq) + (sp.q0 + row) * g.lddq + static_cast<int64_t>(hq) * D;
-#pragma unroll
-    for (int d = 0; d < ND; ++d)
-#pragma unroll
-      for (int a = 0; a < 4; ++a) {
-        const float x[4] = {acc[d][4 * a] * g.scale, acc[d][4 * a + 1] * g.scale, acc[d][4 * a + 2] * g.scale,
-                            acc[d][4 * a + 3] * g.scale};
-        store4(o + 32 * d + 8 * a + 4 * (lane >> 5), x);
-      }
+  if constexpr (TWO) {
+    for (int j = 0; j < end; j += 2) {
+      step(kA, vA, kB, vB, j);
+      if (j + 1 < end) step(kB, vB, kA, vA, j + 1);
+    }
+  } else {
+    for (int j = 0; j < end; ++j) step(kA, vA, kA, vA, j);
   }
+  if (x.row < x.sp.Lq)
+    store_row<D>(static_cast<T*>(g.dq) + (x.sp.q0 + x.row) * g.lddq + static_cast<int64_t>(x.hq) * D, acc, g.scale, lane);
 #endif
 }
 
+// The keys of a block of k_attn_dkv, 32 for each wave, and the query tiles of BQ
+// rows that it goes over: those of each of its heads from the first that sees one
+// of the keys on.
+struct KeyTile {
+  Span sp;
+  int hk, h0, h1;   // key/value head, query heads
+  int j0, key;      // the wave's first key, the lane's
+  int off;          // query i sees keys up to i + off
+  int first, per;   // first query tile, tiles a head
+};
+
 // WHAT: 3 both gradients, 1 dk, 2 dv (rows of 512 bytes and more, whose two sums
 // and operands together pass the registers of a wave).
+//
+// The step is in two halves: the products S and dP of one tile of queries run
+// while p and dS of the tile before are formed, which leaves the matrix cores
+// without work only where a block has nothing else to put between (one wave a
+// SIMD: two gradients' sums and two operands take 192 of its registers at d =
+// 128).  Three buffers: the tile of the sums, that of the products, the next.
 template <typename T, int D, int WHAT>
 __global__ __launch_bounds__(256, 1) void k_attn_dkv(GradIO g) {
 #ifdef GDN_DEVICE_PASS
-  constexpr int BQ = 32, NW = 4, BK = 32 * NW, KS = D / 16, ND = D / 32, RB = D * sizeof(T);
+  constexpr int BQ = 32, NW = 4, BK = 32 * NW, KS = D / 16, ND = D / 32;
   constexpr bool DK = WHAT & 1, DV = WHAT & 2;
-  __shared__ __align__(1024) char qA[BQ * RB], oA[BQ * RB], qB[BQ * RB], oB[BQ * RB];
-  __shared__ __align__(1024) float sA[2 * BQ], sB[2 * BQ];
+  using P = Plane<T, D, BQ>;
+  constexpr int BUFS = sizeof(T) == 2 ? 3 : 4 * P::TILE <= 144 * 1024 ? 2 : 1;
+  constexpr int SB = BUFS > 1 ? P::TILE : 16, SC = BUFS > 2 ? P::TILE : 16;
+  __shared__ __align__(1024) char qA[P::TILE], oA[P::TILE], qB[SB], oB[SB], qC[SC], oC[SC];
+  __shared__ __align__(1024) float sA[2 * BQ], sB[2 * BQ], sC[2 * BQ];
   const AttnIO& io = g.a;
-  const int hk = blockIdx.x % io.H_kv;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  KeyTile x;
+  x.hk = blockIdx.x % io.H_kv;
   int tile;
   const int n = tile_seq(io.cu_k, io.N, BK, blockIdx.x / io.H_kv, &tile);
-  const Span sp = span_of(io.cu_q, io.cu_k, io.T_q, io.T_k, n);
-  if (tile < 0 || tile * BK >= sp.Lk) return;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int j0 = tile * BK + wave * 32, key = j0 + (lane & 31);
-  const int off = sp.Lk - sp.Lq;
-  // query tiles from the first that sees one of the block's keys on
-  const int first = tile * BK - off > 0 ? (tile * BK - off) / BQ : 0;
-  const int per = (sp.Lq + BQ - 1) / BQ - first, steps = per > 0 ? per * io.G : 0;
+  x.sp = span_of(io.cu_q, io.cu_k, io.T_q, io.T_k, n);
+  if (tile < 0 || tile * BK >= x.sp.Lk) return;
+  const int heads = (io.G + g.parts - 1) / g.parts;
+  x.h0 = blockIdx.y * heads;
+  x.h1 = x.h0 + heads < io.G ? x.h0 + heads : io.G;
+  x.j0 = tile * BK + wave * 32;
+  x.key = x.j0 + (lane & 31);
+  x.off = x.sp.Lk - x.sp.Lq;
+  x.first = tile * BK - x.off > 0 ? (tile * BK - x.off) / BQ : 0;
+  x.per = (x.sp.Lq + BQ - 1) / BQ - x.first;
+  const int steps = x.per > 0 && x.h1 > x.h0 ? x.per * (x.h1 - x.h0) : 0;
 
-  Frag<T> k[KS], v[DK ? KS : 1];
+  Held<T, D> k[KS], v[DK ? KS : 1];
   {
-    const int rows = sp.Lk - j0 < 32 ? sp.Lk - j0 : 32;
-    const int64_t at = sp.k0 + (rows > 0 ? j0 : 0);
-    const brsrc_t rk = rows_rsrc<T, D>(io.k, at, io.ldk, hk, rows), rv = rows_rsrc<T, D>(io.v, at, io.ldv, hk, rows);
-    const uint32_t col = 8 * (lane >> 5) * sizeof(T), r = lane & 31;
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      k[ks].load(rk, static_cast<uint32_t>(r * io.ldk * sizeof(T)) + col + 16 * ks * sizeof(T));
-      if constexpr (DK) v[ks].load(rv, static_cast<uint32_t>(r * io.ldv * sizeof(T)) + col + 16 * ks * sizeof(T));
-    }
+    const int rows = x.sp.Lk - x.j0 < 32 ? x.sp.Lk - x.j0 : 32;
+    const int64_t at = x.sp.k0 + (rows > 0 ? x.j0 : 0);
+    load_rows<T, D>(io.k, at, io.ldk, x.hk, rows, lane, k);
+    if constexpr (DK) load_rows<T, D>(io.v, at, io.ldv, x.hk, rows, lane, v);
   }
-  const Stager<T, D, BQ, NW> sq(io.ldq, wave, lane), so(g.lddo, wave, lane);
-  auto fetch = [&](char* qb, char* ob, float* sb, int x) {
-    const int h = hk * io.G + x / per, i0 = (first + x % per) * BQ;
-    const int rows = sp.Lq - i0 < BQ ? sp.Lq - i0 : BQ;
-    sq.start(rows_rsrc<T, D>(io.q, sp.q0 + i0, io.ldq, h, rows), qb);
-    so.start(rows_rsrc<T, D>(g.dO, sp.q0 + i0, g.lddo, h, rows), ob);
+  Stager<T, D, BQ, NW> sq(io.ldq, wave, lane), so(g.lddo, wave, lane);
+  int fh = x.hk * io.G + x.h0, ft = x.first;  // the next tile to fetch
+  auto start = [&](char* qb, char* ob, float* sb) {
+    const int i0 = ft * BQ, rows = x.sp.Lq - i0 < BQ ? x.sp.Lq - i0 : BQ;
+    sq.start(rows_rsrc<T, D>(io.q, x.sp.q0 + i0, io.ldq, fh, rows), qb);
+    so.start(rows_rsrc<T, D>(g.dO, x.sp.q0 + i0, g.lddo, fh, rows), ob);
     if (wave == 0) {
-      float* st = g.stat + 2 * (static_cast<int64_t>(h) * io.T_q + sp.q0 + i0);
+      float* st = g.stat + 2 * (static_cast<int64_t>(fh) * io.T_q + x.sp.q0 + i0);
       const brsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(st, static_cast<short>(0), rows * 8, 0x00020000);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (GDN_LDS void*)sb, 4, lane * 4, 0, 0, 0);
+    }
+    if (++ft == x.first + x.per) {
+      ft = x.first;
+      ++fh;
     }
   };
   v16f ak[DK ? ND : 1], av[DV ? ND : 1];
@@ -402,19 +314,20 @@ __global__ __launch_bounds__(256, 1) void k_attn_dkv(GradIO g) {
     if constexpr (DK) ak[d] = zero16();
     if constexpr (DV) av[d] = zero16();
   }
-  auto step = [&](char* qb, char* ob, float* sb, char* qn, char* on, float* sn, int x) {
-    wait_loads();
-    __syncthreads();
-    if (x + 1 < steps) fetch(qn, on, sn, x + 1);
-    const int i0 = (first + x % per) * BQ;
-    if (i0 + BQ - 1 + off < j0) return;  // the wave's keys are all behind the tile's queries
-    v16f s = zero16(), dp = zero16();
+  auto products = [&](const char* qb, const char* ob, v16f& s, v16f& dp) {
+    s = zero16();
+    dp = zero16();
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      s = mma32(row_frag<T, RB>(qb, 0, ks, lane), k[ks], s);
-      if constexpr (DK) dp = mma32(row_frag<T, RB>(ob, 0, ks, lane), v[ks], dp);
+      s = mma32(row_frag<T, D, BQ>(qb, 0, ks, lane), k[ks].get(), s);
+      if constexpr (DK) dp = mma32(row_frag<T, D, BQ>(ob, 0, ks, lane), v[ks].get(), dp);
     }
-    const bool edge = i0 + off < j0 + 31;
+  };
+  int ct = x.first;  // the tile of the sums
+  auto weights = [&](const float* sb, v16f& s, v16f& dp) {
+    const int i0 = ct * BQ;
+    if (++ct == x.first + x.per) ct = x.first;
+    const bool edge = i0 + x.off < x.j0 + 31;
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
       const float* st = sb + 2 * (8 * a + 4 * (lane >> 5));
@@ -423,50 +336,130 @@ __global__ __launch_bounds__(256, 1) void k_attn_dkv(GradIO g) {
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
         const int i = 4 * a + b;
-        float p = __builtin_amdgcn_exp2f(fmaf(s[i], io.c, -lse2[b]));
-        float ds = p * (dp[i] - dot[b]);
-        if (edge && i0 + c_row(i, lane) + off < key) p = ds = 0.0f;
-        s[i] = p;
-        dp[i] = ds;
+        s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], io.c, -lse2[b]));
+        dp[i] = s[i] * (dp[i] - dot[b]);
       }
     }
+    if (edge) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      Frag<T> p, ds;
-      p.pack(s, 8 * u);
-      ds.pack(dp, 8 * u);
-#pragma unroll
-      for (int d = 0; d < ND; ++d) {
-        if constexpr (DV) av[d] = mma32(col_frag<T, RB>(ob, 16 * u, d, lane), p, av[d]);
-        if constexpr (DK) ak[d] = mma32(col_frag<T, RB>(qb, 16 * u, d, lane), ds, ak[d]);
-      }
+      for (int i = 0; i < 16; ++i)
+        if (i0 + c_row(i, lane) + x.off < x.key) s[i] = dp[i] = 0.0f;
     }
   };
-  if (steps > 0) fetch(qA, oA, sA, 0);
-  for (int x = 0; x < steps; x += 2) {
-    step(qA, oA, sA, qB, oB, sB, x);
-    if (x + 1 < steps) step(qB, oB, sB, qA, oA, sA, x + 1);
-  }
-  if (key < sp.Lk) {
-    T* dk = static_cast<T*>(g.dk) + (sp.k0 + key) * g.lddk + static_cast<int64_t>(hk) * D;
-    T* dv = static_cast<T*>(g.dv) + (sp.k0 + key) * g.lddv + static_cast<int64_t>(hk) * D;
+  auto sums = [&](const char* qb, const char* ob, const Frag<T> (&p)[2], const Frag<T> (&ds)[2]) {
 #pragma unroll
-    for (int d = 0; d < ND; ++d)
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int a = 0; a < 4; ++a) {
-        const int e = 32 * d + 8 * a + 4 * (lane >> 5);
-        if constexpr (DK) {
-          const float x[4] = {ak[d][4 * a] * g.scale, ak[d][4 * a + 1] * g.scale, ak[d][4 * a + 2] * g.scale,
-                              ak[d][4 * a + 3] * g.scale};
-          store4(dk + e, x);
-        }
-        if constexpr (DV) {
-          const float x[4] = {av[d][4 * a], av[d][4 * a + 1], av[d][4 * a + 2], av[d][4 * a + 3]};
-          store4(dv + e, x);
+      for (int d = 0; d < ND; ++d) {
+        if constexpr (DV) av[d] = mma32(col_frag<T, D, BQ>(ob, 16 * u, d, lane), p[u], av[d]);
+        if constexpr (DK) ak[d] = mma32(col_frag<T, D, BQ>(qb, 16 * u, d, lane), ds[u], ak[d]);
+      }
+  };
+  auto packed = [&](const v16f& s, const v16f& dp, Frag<T> (&p)[2], Frag<T> (&ds)[2]) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if constexpr (DV) p[u].pack(s, 8 * u);
+      if constexpr (DK) ds[u].pack(dp, 8 * u);
+    }
+  };
+  v16f s, dp;
+  if constexpr (BUFS == 3) {
+    // 0: tile i of the sums, 1: i + 1 of the products, 2: i + 2 on its way
+    auto step = [&](char* q0, char* o0, float* s0, char* q1, char* o1, char* q2, char* o2, float* s2, int i) {
+      wait_loads();
+      __syncthreads();
+      if (i + 2 < steps) start(q2, o2, s2);
+      v16f sn, dpn;
+      products(q1, o1, sn, dpn);  // behind the last tile: of what the buffer held before, and unused
+      weights(s0, s, dp);
+      Frag<T> p[2], ds[2];
+      packed(s, dp, p, ds);
+      sums(q0, o0, p, ds);
+      s = sn;
+      dp = dpn;
+    };
+    if (steps > 0) {
+      start(qA, oA, sA);
+      if (steps > 1) start(qB, oB, sB);
+      wait_loads();
+      __syncthreads();
+      products(qA, oA, s, dp);
+    }
+    for (int i = 0; i < steps; i += 3) {
+      step(qA, oA, sA, qB, oB, qC, oC, sC, i);
+      if (i + 1 < steps) step(qB, oB, sB, qC, oC, qA, oA, sA, i + 1);
+      if (i + 2 < steps) step(qC, oC, sC, qA, oA, qB, oB, sB, i + 2);
+    }
+  } else {
+    if (steps > 0) {
+      start(qA, oA, sA);
+      if constexpr (!sq.DIRECT) {
+        sq.finish(qA);
+        so.finish(oA);
+      }
+    }
+    constexpr bool TWO = BUFS == 2;
+    auto step = [&](char* qb, char* ob, float* sb, char* qn, char* on, float* sn, int i) {
+      wait_loads();
+      __syncthreads();
+      const bool more = i + 1 < steps;
+      if (more) start(qn, on, sn);
+      products(qb, ob, s, dp);
+      weights(sb, s, dp);
+      Frag<T> p[2], ds[2];
+      packed(s, dp, p, ds);
+      sums(qb, ob, p, ds);
+      if constexpr (!sq.DIRECT) {
+        if constexpr (!TWO) __syncthreads();
+        if (more) {
+          sq.finish(qn);
+          so.finish(on);
         }
       }
+    };
+    if constexpr (TWO) {
+      for (int i = 0; i < steps; i += 2) {
+        step(qA, oA, sA, qB, oB, sB, i);
+        if (i + 1 < steps) step(qB, oB, sB, qA, oA, sA, i + 1);
+      }
+    } else {
+      for (int i = 0; i < steps; i += 2) {
+        step(qA, oA, sA, qA, oA, sB, i);
+        if (i + 1 < steps) step(qA, oA, sB, qA, oA, sA, i + 1);
+      }
+    }
+  }
+  if (x.key < x.sp.Lk) {
+    const int64_t row = x.sp.k0 + x.key;
+    if (g.parts == 1) {
+      if constexpr (DK) store_row<D>(static_cast<T*>(g.dk) + row * g.lddk + static_cast<int64_t>(x.hk) * D, ak, g.scale, lane);
+      if constexpr (DV) store_row<D>(static_cast<T*>(g.dv) + row * g.lddv + static_cast<int64_t>(x.hk) * D, av, 1.0f, lane);
+    } else {
+      const int64_t size = io.T_k * io.H_kv * D;
+      float* part = g.part + 2 * blockIdx.y * size + (row * io.H_kv + x.hk) * D;
+      if constexpr (DK) store_row<D>(part, ak, g.scale, lane);
+      if constexpr (DV) store_row<D>(part + size, av, 1.0f, lane);
+    }
   }
 #endif
+}
+
+// dk and dv from the sums of each part of the group's heads, added in order.
+template <typename T>
+__global__ __launch_bounds__(256) void k_attn_dkv_sum(GradIO g, int D) {
+  const AttnIO& io = g.a;
+  const int64_t size = io.T_k * io.H_kv * D, e = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  int64_t end = io.cu_k[io.N];
+  end = end < 0 ? 0 : end > io.T_k ? io.T_k : end;
+  if (e >= end * io.H_kv * D) return;
+  const int64_t row = e / (io.H_kv * D), col = e - row * io.H_kv * D;
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    v4f y = *reinterpret_cast<const v4f*>(g.part + w * size + e);
+    for (int i = 1; i < g.parts; ++i) y += *reinterpret_cast<const v4f*>(g.part + (2 * i + w) * size + e);
+    const float z[4] = {y[0], y[1], y[2], y[3]};
+    store4(static_cast<T*>(w ? g.dv : g.dk) + row * (w ? g.lddv : g.lddk) + col, z);
+  }
 }
 
 // ---- host side ----------------------------------------------------------------
@@ -474,8 +467,24 @@ __global__ __launch_bounds__(256, 1) void k_attn_dkv(GradIO g) {
 template <typename T, int D>
 void launch_dkv(const GradIO& g, unsigned blocks, hipStream_t st) {
   constexpr bool split = D * sizeof(T) >= 512;
-  hipLaunchKernelGGL((k_attn_dkv<T, D, split ? 1 : 3>), dim3(blocks), dim3(256), 0, st, g);
-  if constexpr (split) hipLaunchKernelGGL((k_attn_dkv<T, D, 2>), dim3(blocks), dim3(256), 0, st, g);
+  const dim3 grid(blocks, g.parts);
+  hipLaunchKernelGGL((k_attn_dkv<T, D, split ? 1 : 3>), grid, dim3(256), 0, st, g);
+  if constexpr (split) hipLaunchKernelGGL((k_attn_dkv<T, D, 2>), grid, dim3(256), 0, st, g);
+}
+
+// Parts that a group's heads are cut into for dk and dv: more where the blocks of
+// 128 keys would not fill the chip.
+int dkv_parts(const gdn_attn_shape_t* s, int64_t T_k) {
+  const int G = s->H_q / s->H_kv;
+  const int64_t blocks = (T_k + 127) / 128 * s->H_kv;
+  int parts = 1;
+  while (parts < G && blocks * parts < 256) ++parts;
+  const int heads = (G + parts - 1) / parts;
+  return (G + heads - 1) / heads;  // none without a head
+}
+size_t stat_bytes(const gdn_attn_shape_t* s, int64_t T_q) {
+  const size_t bytes = static_cast<size_t>(T_q) * s->H_q * 2 * sizeof(float);
+  return (bytes + gdn::kAlign) / gdn::kAlign * gdn::kAlign;
 }
 
 template <typename F>
@@ -530,7 +539,7 @@ int gdn_attn_prefill(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_
   io.o = o; io.lse = lse;
   hipStream_t st = static_cast<hipStream_t>(stream);
   return attn_dispatch(shape, [&]<typename T, int D>() {
-    using Tile = FwdTile<T, D>;
+    using Tile = AttnTile<T, D>;
     const int64_t blocks = tile_slots(T_q, n_seqs, Tile::BM) * io.H_q;
     if (blocks * Tile::NW * 64 >= gdn::kLaunchThreads) return static_cast<int>(GDN_ERR_UNSUPPORTED);
     Timed t_("k_attn_fwd", st);
@@ -541,8 +550,9 @@ int gdn_attn_prefill(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_
 
 size_t gdn_attn_workspace_bytes(const gdn_attn_shape_t* shape, int64_t T_q, int64_t T_k) {
   if (gdn::check_attn_shape(shape) != GDN_OK || T_q < 0 || T_k < 0 || T_q > INT32_MAX || T_k > INT32_MAX) return 0;
-  const size_t bytes = static_cast<size_t>(T_q) * shape->H_q * 2 * sizeof(float);
-  return (bytes + gdn::kAlign) / gdn::kAlign * gdn::kAlign;
+  const int parts = dkv_parts(shape, T_k);
+  const size_t sums = parts > 1 ? static_cast<size_t>(parts) * 2 * T_k * shape->H_kv * shape->d * sizeof(float) : 0;
+  return stat_bytes(shape, T_q) + (sums + gdn::kAlign - 1) / gdn::kAlign * gdn::kAlign;
 }
 
 int gdn_attn_bwd(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t* cu_q, const int32_t* cu_k, int64_t T_q,
@@ -562,11 +572,13 @@ int gdn_attn_bwd(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t* c
   g.a.o = const_cast<void*>(o); g.a.lse = const_cast<float*>(lse);
   g.dO = dO; g.dq = dq; g.dk = dk; g.dv = dv;
   g.stat = static_cast<float*>(ws);
+  g.parts = dkv_parts(shape, T_k);
+  g.part = g.parts > 1 ? g.stat + stat_bytes(shape, T_q) / sizeof(float) : nullptr;
   g.scale = shape->scale;
   hipStream_t st = static_cast<hipStream_t>(stream);
   return attn_dispatch(shape, [&]<typename T, int D>() {
     const int64_t nq = tile_slots(T_q, n_seqs, 128) * g.a.H_q, nk = tile_slots(T_k, n_seqs, 128) * g.a.H_kv;
-    if (nq * 256 >= gdn::kLaunchThreads || nk * 256 >= gdn::kLaunchThreads) return static_cast<int>(GDN_ERR_UNSUPPORTED);
+    if (nq * 256 >= gdn::kLaunchThreads || nk * 256 >= gdn::kLaunchThreads / g.parts) return static_cast<int>(GDN_ERR_UNSUPPORTED);
     if (T_q > 0) {
       Timed t_("k_attn_dq", st);
       hipLaunchKernelGGL((k_attn_dq<T, D>), dim3(static_cast<unsigned>(nq)), dim3(256), 0, st, g);
@@ -574,6 +586,11 @@ int gdn_attn_bwd(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t* c
     if (T_k > 0) {
       Timed t_("k_attn_dkv", st);
       launch_dkv<T, D>(g, static_cast<unsigned>(nk), st);
+    }
+    if (T_k > 0 && g.parts > 1) {
+      Timed t_("k_attn_dkv_sum", st);
+      const int64_t blocks = (T_k * g.a.H_kv * D / 4 + 255) / 256;
+      hipLaunchKernelGGL(k_attn_dkv_sum<T>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, g, D);
     }
     return static_cast<int>(hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_HIP);
   });

@@ -3,9 +3,9 @@
 //
 // One product step is C[32 x 32] += A[32 x 16] B[16 x 32].  Lane l holds A[l %
 // 32][8 (l / 32) + j] and B[8 (l / 32) + j][l % 32], j = 0..7, and C's rows 8 (i /
-// 4) + 4 (l / 32) + i % 4, i = 0..15, of column l % 32.  bf16: one
-// v_mfma_f32_32x32x16_bf16; fp32: eight v_mfma_f32_32x32x2_f32, the j-th over k = j
-// and 8 + j.  Either sums in fp32.
+// 4) + 4 (l / 32) + i % 4, i = 0..15, of column l % 32: v_mfma_f32_32x32x16_bf16,
+// which sums in fp32.  fp32 operands are three bf16 parts each and take six of them,
+// 192 cycles where v_mfma_f32_32x32x2_f32 would take 512.
 //
 // A tile in LDS is rows of RB bytes in 16-byte pieces; piece c of row r stands at
 // c ^ swizzle(r), so that neither the reads along rows (32 rows, one piece each)
@@ -54,26 +54,54 @@ struct Frag;
 template <>
 struct Frag<bf16_t> {
   u32x4 x;
-  __device__ __forceinline__ void load(brsrc_t r, uint32_t at) { x = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0)); }
   // c[i0 .. i0 + 7], rounded to nearest even
   __device__ __forceinline__ void pack(const v16f& c, int i0) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) x[e] = pack_bf16(c[i0 + 2 * e], c[i0 + 2 * e + 1]);
   }
-  __device__ __forceinline__ float dot(const Frag& y) const {
-    float s = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      s = fmaf(__uint_as_float(x[e] << 16), __uint_as_float(y.x[e] << 16), s);
-      s = fmaf(__uint_as_float(x[e] & 0xffff0000u), __uint_as_float(y.x[e] & 0xffff0000u), s);
-    }
-    return s;
-  }
 };
 template <>
 struct Frag<float> {
-  float x[8];
+  u32x4 p[3];
+  // x in three bf16 parts, which hold its 24 bits
+  __device__ __forceinline__ void split(const float* x) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float a = x[2 * e], b = x[2 * e + 1];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const uint32_t w = pack_bf16(a, b);
+        p[i][e] = w;
+        if (i < 2) {
+          a -= __uint_as_float(w << 16);
+          b -= __uint_as_float(w & 0xffff0000u);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void pack(const v16f& c, int i0) {
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = c[i0 + e];
+    split(x);
+  }
+};
+
+// An operand that a wave holds throughout: as loaded where its parts would take
+// too many registers (fp32 at d = 256), else ready for the products.
+template <typename T, int D>
+struct Held {
+  Frag<T> f;
   __device__ __forceinline__ void load(brsrc_t r, uint32_t at) {
+    if constexpr (sizeof(T) == 2) {
+      f.x = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
+    } else {
+      float x[8];
+      load8(r, at, x);
+      f.split(x);
+    }
+  }
+  static __device__ __forceinline__ void load8(brsrc_t r, uint32_t at, float* x) {
     const v4f a = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0));
     const v4f b = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(r, at + 16, 0, 0));
 #pragma unroll
@@ -82,26 +110,60 @@ struct Frag<float> {
       x[4 + e] = b[e];
     }
   }
-  __device__ __forceinline__ void pack(const v16f& c, int i0) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = c[i0 + e];
-  }
-  __device__ __forceinline__ float dot(const Frag& y) const {
-    float s = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s = fmaf(x[e], y.x[e], s);
-    return s;
+  __device__ __forceinline__ const Frag<T>& get() const { return f; }
+};
+template <>
+struct Held<float, 256> {
+  float x[8];
+  __device__ __forceinline__ void load(brsrc_t r, uint32_t at) { Held<float, 64>::load8(r, at, x); }
+  __device__ __forceinline__ Frag<float> get() const {
+    Frag<float> f;
+    f.split(x);
+    return f;
   }
 };
 
-__device__ __forceinline__ v16f mma32(const Frag<bf16_t>& a, const Frag<bf16_t>& b, v16f c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a.x), __builtin_bit_cast(bf16x8, b.x), c, 0, 0, 0);
-}
-__device__ __forceinline__ v16f mma32(const Frag<float>& a, const Frag<float>& b, v16f c) {
+// sum += a . b of eight elements read from two buffers.
+template <typename T>
+__device__ __forceinline__ float dot8(brsrc_t ra, uint32_t at_a, brsrc_t rb, uint32_t at_b, float sum) {
+  if constexpr (sizeof(T) == 2) {
+    const u32x4 a = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(ra, at_a, 0, 0));
+    const u32x4 b = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rb, at_b, 0, 0));
 #pragma unroll
-  for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a.x[j], b.x[j], c, 0, 0, 0);
-  return c;
+    for (int e = 0; e < 4; ++e) {
+      sum = fmaf(__uint_as_float(a[e] << 16), __uint_as_float(b[e] << 16), sum);
+      sum = fmaf(__uint_as_float(a[e] & 0xffff0000u), __uint_as_float(b[e] & 0xffff0000u), sum);
+    }
+  } else {
+    float a[8], b[8];
+    Held<float, 64>::load8(ra, at_a, a);
+    Held<float, 64>::load8(rb, at_b, b);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum = fmaf(a[e], b[e], sum);
+  }
+  return sum;
 }
+
+__device__ __forceinline__ v16f mma32(u32x4 a, u32x4 b, v16f c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ v16f mma32(const Frag<bf16_t>& a, const Frag<bf16_t>& b, v16f c) { return mma32(a.x, b.x, c); }
+// The products of parts down to 2^-16 of the largest, small ones first; those left
+// out are 2^-24 of it.
+__device__ __forceinline__ v16f mma32(const Frag<float>& a, const Frag<float>& b, v16f c) {
+  c = mma32(a.p[0], b.p[2], c);
+  c = mma32(a.p[2], b.p[0], c);
+  c = mma32(a.p[1], b.p[1], c);
+  c = mma32(a.p[0], b.p[1], c);
+  c = mma32(a.p[1], b.p[0], c);
+  return mma32(a.p[0], b.p[0], c);
+}
+
+// A tile of ROWS rows in LDS: one plane of bf16, or three of an fp32 tile's parts.
+template <typename T, int D, int ROWS>
+struct Plane {
+  static constexpr int N = sizeof(T) == 2 ? 1 : 3, RB = 2 * D, BYTES = ROWS * RB, TILE = N * BYTES;
+};
 
 template <int RB>
 __device__ __forceinline__ int swizzle(int r) {
@@ -109,50 +171,51 @@ __device__ __forceinline__ int swizzle(int r) {
 }
 
 // Row operand: element j is X[r0 + l % 32][16 ks + 8 (l / 32) + j].  r0 a multiple of 32.
-template <typename T, int RB>
-__device__ __forceinline__ Frag<T> row_frag(const char* lds, int r0, int ks, int lane) {
-  const int r = lane & 31, f = swizzle<RB>(r);
-  const char* at = lds + r0 * RB + r * RB;
-  Frag<T> a;
-  if constexpr (sizeof(T) == 2) {
-    a.x = *reinterpret_cast<const u32x4*>(at + (((2 * ks + (lane >> 5)) ^ f) << 4));
-  } else {
+template <int RB>
+__device__ __forceinline__ u32x4 row_plane(const char* lds, int r0, int ks, int lane) {
+  const int r = lane & 31;
+  return *reinterpret_cast<const u32x4*>(lds + r0 * RB + r * RB + (((2 * ks + (lane >> 5)) ^ swizzle<RB>(r)) << 4));
+}
+// Column operand: element j is X[r0 + c_row(j)][32 dt + l % 32], the rows in the
+// order in which C holds them.  r0 a multiple of 16.  A transposing read takes 4
+// rows x 16 columns for each 16 lanes: lane 4 r + c gives the address of row r's
+// columns 4 c, and lane i gets column i.
+template <int RB>
+__device__ __forceinline__ u32x4 col_plane(const char* lds, int r0, int dt, int lane) {
+  const int i = lane & 15, h = lane >> 5, g = lane >> 4 & 1;
+  u32x4 a;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const v4f y = *reinterpret_cast<const v4f*>(at + (((4 * ks + 2 * (lane >> 5) + e) ^ f) << 4));
-#pragma unroll
-      for (int i = 0; i < 4; ++i) a.x[4 * e + i] = y[i];
-    }
+  for (int e = 0; e < 2; ++e) {
+    const int r = 8 * e + 4 * h + (i >> 2);
+    const int piece = (4 * dt + 2 * g + (i >> 1 & 1)) ^ swizzle<RB>(r);
+    const char* at = lds + r0 * RB + r * RB + (piece << 4) + ((i & 1) << 3);
+    const u32x2 w = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((GDN_LDS s16x4*)(at)));
+    a[2 * e] = w[0];
+    a[2 * e + 1] = w[1];
   }
   return a;
 }
-
-// Column operand: element j is X[r0 + c_row(j)][32 dt + l % 32], the rows in the
-// order in which C holds them.  r0 a multiple of 16.
-template <typename T, int RB>
-__device__ __forceinline__ Frag<T> col_frag(const char* lds, int r0, int dt, int lane) {
+template <typename T, int D, int ROWS>
+__device__ __forceinline__ Frag<T> row_frag(const char* lds, int r0, int ks, int lane) {
+  using P = Plane<T, D, ROWS>;
   Frag<T> a;
-  if constexpr (sizeof(T) == 2) {
-    // a transposing read takes 4 rows x 16 columns for each 16 lanes: lane 4 r + c
-    // gives the address of row r's columns 4 c, and lane i gets column i
-    const int i = lane & 15, h = lane >> 5, g = lane >> 4 & 1;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = 8 * e + 4 * h + (i >> 2);
-      const int piece = (4 * dt + 2 * g + (i >> 1 & 1)) ^ swizzle<RB>(r);
-      const char* at = lds + r0 * RB + r * RB + (piece << 4) + ((i & 1) << 3);
-      const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((GDN_LDS s16x4*)(at));
-      const u32x2 w = __builtin_bit_cast(u32x2, y);
-      a.x[2 * e] = w[0];
-      a.x[2 * e + 1] = w[1];
-    }
+  if constexpr (P::N == 1) {
+    a.x = row_plane<P::RB>(lds, r0, ks, lane);
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int r = c_row(j, lane);
-      const int piece = (8 * dt + ((lane & 31) >> 2)) ^ swizzle<RB>(r);
-      a.x[j] = *reinterpret_cast<const float*>(lds + r0 * RB + r * RB + (piece << 4) + ((lane & 3) << 2));
-    }
+    for (int i = 0; i < 3; ++i) a.p[i] = row_plane<P::RB>(lds + i * P::BYTES, r0, ks, lane);
+  }
+  return a;
+}
+template <typename T, int D, int ROWS>
+__device__ __forceinline__ Frag<T> col_frag(const char* lds, int r0, int dt, int lane) {
+  using P = Plane<T, D, ROWS>;
+  Frag<T> a;
+  if constexpr (P::N == 1) {
+    a.x = col_plane<P::RB>(lds, r0, dt, lane);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) a.p[i] = col_plane<P::RB>(lds + i * P::BYTES, r0, dt, lane);
   }
   return a;
 }
@@ -166,24 +229,50 @@ __device__ __forceinline__ brsrc_t rows_rsrc(const void* x, int64_t at, int64_t 
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), static_cast<short>(0), bytes, 0x00020000);
 }
 
-// Loads of a tile of ROWS rows straight into LDS, 64 pieces a wave and step.
+// Moves a tile of ROWS rows into LDS.  bf16 rows go there straight from memory
+// (start), 64 pieces of 16 bytes a wave and step; fp32 rows through registers
+// (start), and their parts from there (finish).
 template <typename T, int D, int ROWS, int NW>
 struct Stager {
-  static constexpr int RB = D * sizeof(T), CPR = RB / 16, STEPS = ROWS * CPR / (64 * NW);
+  using P = Plane<T, D, ROWS>;
+  static constexpr bool DIRECT = sizeof(T) == 2;
+  static constexpr int CPR = P::RB / 16, STEPS = ROWS * CPR / (64 * NW);
   static_assert(ROWS * CPR % (64 * NW) == 0);
   uint32_t at[STEPS];
-  int wave;
-  __device__ __forceinline__ Stager(int64_t ld, int w, int lane) : wave(w) {
+  u32x4 held[DIRECT ? 1 : 2 * STEPS];
+  int wave, lane;
+  __device__ __forceinline__ Stager(int64_t ld, int w, int l) : wave(w), lane(l) {
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
-      const int c = (s * NW + w) * 64 + lane, r = c / CPR;
-      at[s] = static_cast<uint32_t>(r * ld * sizeof(T)) + (((c % CPR) ^ swizzle<RB>(r)) << 4);
+      const int c = (s * NW + w) * 64 + l, r = c / CPR;
+      at[s] = static_cast<uint32_t>(r * ld * sizeof(T)) + (((c % CPR) ^ swizzle<P::RB>(r)) * 8 * sizeof(T));
     }
   }
-  __device__ __forceinline__ void start(brsrc_t rsrc, char* lds) const {
+  __device__ __forceinline__ void start(brsrc_t rsrc, char* lds) {
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (GDN_LDS void*)(lds + (s * NW + wave) * 1024), 16, at[s], 0, 0, 0);
+    for (int s = 0; s < STEPS; ++s) {
+      if constexpr (DIRECT) {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (GDN_LDS void*)(lds + (s * NW + wave) * 1024), 16, at[s], 0, 0, 0);
+      } else {
+        held[2 * s] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at[s], 0, 0));
+        held[2 * s + 1] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at[s] + 16, 0, 0));
+      }
+    }
+  }
+  __device__ __forceinline__ void finish(char* lds) const {
+    if constexpr (!DIRECT) {
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s) {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(held[2 * s + e / 4][e % 4]);
+        Frag<float> f;
+        f.split(x);
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          *reinterpret_cast<u32x4*>(lds + i * P::BYTES + ((s * NW + wave) * 64 + lane) * 16) = f.p[i];
+      }
+    }
   }
 };
 
