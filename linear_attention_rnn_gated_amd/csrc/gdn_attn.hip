@@ -252,21 +252,19 @@ struct KeyTile {
 // WHAT: 3 both gradients, 1 dk, 2 dv (rows of 512 bytes and more, whose two sums
 // and operands together pass the registers of a wave).
 //
-// The step is in two halves: the products S and dP of one tile of queries run
-// while p and dS of the tile before are formed, which leaves the matrix cores
-// without work only where a block has nothing else to put between (one wave a
-// SIMD: two gradients' sums and two operands take 192 of its registers at d =
-// 128).  Three buffers: the tile of the sums, that of the products, the next.
+// One wave a SIMD (two gradients' sums and two operands take 192 of its registers
+// at d = 128), so a wave has to hide its own latencies: the products S and dP of
+// one tile of queries run while p and dS of the tile before are formed.
 template <typename T, int D, int WHAT>
 __global__ __launch_bounds__(256, 1) void k_attn_dkv(GradIO g) {
 #ifdef GDN_DEVICE_PASS
   constexpr int BQ = 32, NW = 4, BK = 32 * NW, KS = D / 16, ND = D / 32;
   constexpr bool DK = WHAT & 1, DV = WHAT & 2;
   using P = Plane<T, D, BQ>;
-  constexpr int BUFS = sizeof(T) == 2 ? 3 : 4 * P::TILE <= 144 * 1024 ? 2 : 1;
+  constexpr int BUFS = sizeof(T) == 2 ? 4 : 4 * P::TILE <= 144 * 1024 ? 2 : 1;
   constexpr int SB = BUFS > 1 ? P::TILE : 16, SC = BUFS > 2 ? P::TILE : 16;
-  __shared__ __align__(1024) char qA[P::TILE], oA[P::TILE], qB[SB], oB[SB], qC[SC], oC[SC];
-  __shared__ __align__(1024) float sA[2 * BQ], sB[2 * BQ], sC[2 * BQ];
+  __shared__ __align__(1024) char qA[P::TILE], oA[P::TILE], qB[SB], oB[SB], qC[SC], oC[SC], qD[SC], oD[SC];
+  __shared__ __align__(1024) float sA[2 * BQ], sB[2 * BQ], sC[2 * BQ], sD[2 * BQ];
   const AttnIO& io = g.a;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   KeyTile x;
@@ -325,9 +323,6 @@ __global__ __launch_bounds__(256, 1) void k_attn_dkv(GradIO g) {
   };
   int ct = x.first;  // the tile of the sums
   auto weights = [&](const float* sb, v16f& s, v16f& dp) {
-    const int i0 = ct * BQ;
-    if (++ct == x.first + x.per) ct = x.first;
-    const bool edge = i0 + x.off < x.j0 + 31;
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
       const float* st = sb + 2 * (8 * a + 4 * (lane >> 5));
@@ -340,7 +335,9 @@ __global__ __launch_bounds__(256, 1) void k_attn_dkv(GradIO g) {
         dp[i] = s[i] * (dp[i] - dot[b]);
       }
     }
-    if (edge) {
+  };
+  auto hide = [&](int i0, v16f& s, v16f& dp) {
+    if (i0 + x.off < x.j0 + 31) {
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         if (i0 + c_row(i, lane) + x.off < x.key) s[i] = dp[i] = 0.0f;
@@ -363,32 +360,99 @@ __global__ __launch_bounds__(256, 1) void k_attn_dkv(GradIO g) {
     }
   };
   v16f s, dp;
-  if constexpr (BUFS == 3) {
-    // 0: tile i of the sums, 1: i + 1 of the products, 2: i + 2 on its way
-    auto step = [&](char* q0, char* o0, float* s0, char* q1, char* o1, char* q2, char* o2, float* s2, int i) {
+  if constexpr (BUFS == 4) {
+    // Step i: first half, the products of tile i + 1 beside p and dS of tile i; then
+    // tile i + 2 has arrived and i + 3 sets out; second half, the sums of tile i.
+    // The halves are laid out in slots of one product each, with the LDS reads
+    // some slots (of 32 cycles) ahead of the products that take them (a read takes
+    // some 100).
+    constexpr int AHEAD = 4, M1 = KS * (DK ? 2 : 1), NF = ND * ((DK ? 1 : 0) + (DV ? 1 : 0));
+    Frag<T> rf[M1];  // the products' left operands: of q, and between them of dO
+    auto row_of = [&](const char* qb, const char* ob, int m) {
+      return DK && m % 2 ? row_frag<T, D, BQ>(ob, 0, m / 2, lane) : row_frag<T, D, BQ>(qb, 0, DK ? m / 2 : m, lane);
+    };
+    auto col_of = [&](const char* qb, const char* ob, int u, int f) {
+      if constexpr (DK && DV) return col_frag<T, D, BQ>(f % 2 ? qb : ob, 16 * u, f / 2, lane);
+      return col_frag<T, D, BQ>(DK ? qb : ob, 16 * u, f, lane);
+    };
+    auto step = [&](char* q0, char* o0, float* s0, char* q1, char* o1, char* q2, char* o2, char* q3, char* o3, float* s3, int i) {
+      const int i0 = ct * BQ;
+      if (++ct == x.first + x.per) ct = x.first;
+      v16f sn = zero16(), dpn = zero16();
+      Frag<T> f0[NF], f1[NF], p[2], ds[2];
+      v4f st[2][2];
+      auto stat = [&](int a) {
+        const float* at = s0 + 2 * (8 * a + 4 * (lane >> 5));
+        st[a % 2][0] = *reinterpret_cast<const v4f*>(at);
+        st[a % 2][1] = *reinterpret_cast<const v4f*>(at + 4);
+      };
+      stat(0);
+#pragma unroll
+      for (int m = 0; m < M1; ++m) {  // behind the last tile: of what the buffer held before, and unused
+        __builtin_amdgcn_sched_barrier(0);
+        if (m + AHEAD < M1) rf[m + AHEAD] = row_of(q1, o1, m + AHEAD);
+#pragma unroll
+        for (int f = m * NF / M1; f < (m + 1) * NF / M1; ++f) f0[f] = col_of(q0, o0, 0, f);
+        if (DK && m % 2)
+          dpn = mma32(rf[m], v[DK ? m / 2 : 0].get(), dpn);
+        else
+          sn = mma32(rf[m], k[DK ? m / 2 : m].get(), sn);
+#pragma unroll
+        for (int e = m * 16 / M1; e < (m + 1) * 16 / M1; ++e) {
+          const int a = e / 4, b = e % 4;
+          if (b == 0 && a < 3) stat(a + 1);
+          s[e] = __builtin_amdgcn_exp2f(fmaf(s[e], io.c, -st[a % 2][b / 2][2 * (b % 2)]));
+          if constexpr (DK) dp[e] = s[e] * (dp[e] - st[a % 2][b / 2][2 * (b % 2) + 1]);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      hide(i0, s, dp);
       wait_loads();
       __syncthreads();
-      if (i + 2 < steps) start(q2, o2, s2);
-      v16f sn, dpn;
-      products(q1, o1, sn, dpn);  // behind the last tile: of what the buffer held before, and unused
-      weights(s0, s, dp);
-      Frag<T> p[2], ds[2];
-      packed(s, dp, p, ds);
-      sums(q0, o0, p, ds);
+      if (i + 3 < steps) start(q3, o3, s3);
+      if constexpr (DV) p[0].pack(s, 0);
+      if constexpr (DK) ds[0].pack(dp, 0);
+#pragma unroll
+      for (int m = 0; m < 2 * NF; ++m) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (m < NF) f1[m] = col_of(q0, o0, 1, m);
+        if (m >= 2 * NF - AHEAD) rf[m - 2 * NF + AHEAD] = row_of(q2, o2, m - 2 * NF + AHEAD);
+        if (m == NF / 2) {
+          if constexpr (DV) p[1].pack(s, 8);
+          if constexpr (DK) ds[1].pack(dp, 8);
+        }
+        const int u = m / NF, f = m % NF;
+        const Frag<T>& left = u ? f1[f] : f0[f];
+        if (DK && DV) {
+          if (f % 2)
+            ak[f / 2] = mma32(left, ds[u], ak[f / 2]);
+          else
+            av[f / 2] = mma32(left, p[u], av[f / 2]);
+        } else if (DK) {
+          ak[f] = mma32(left, ds[u], ak[f]);
+        } else {
+          av[f] = mma32(left, p[u], av[f]);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
       s = sn;
       dp = dpn;
     };
     if (steps > 0) {
       start(qA, oA, sA);
       if (steps > 1) start(qB, oB, sB);
+      if (steps > 2) start(qC, oC, sC);
       wait_loads();
       __syncthreads();
       products(qA, oA, s, dp);
+#pragma unroll
+      for (int m = 0; m < AHEAD; ++m) rf[m] = row_of(qB, oB, m);
     }
-    for (int i = 0; i < steps; i += 3) {
-      step(qA, oA, sA, qB, oB, qC, oC, sC, i);
-      if (i + 1 < steps) step(qB, oB, sB, qC, oC, qA, oA, sA, i + 1);
-      if (i + 2 < steps) step(qC, oC, sC, qA, oA, qB, oB, sB, i + 2);
+    for (int i = 0; i < steps; i += 4) {
+      step(qA, oA, sA, qB, oB, qC, oC, qD, oD, sD, i);
+      if (i + 1 < steps) step(qB, oB, sB, qC, oC, qD, oD, qA, oA, sA, i + 1);
+      if (i + 2 < steps) step(qC, oC, sC, qD, oD, qA, oA, qB, oB, sB, i + 2);
+      if (i + 3 < steps) step(qD, oD, sD, qA, oA, qB, oB, qC, oC, sC, i + 3);
     }
   } else {
     if (steps > 0) {
@@ -406,6 +470,8 @@ __global__ __launch_bounds__(256, 1) void k_attn_dkv(GradIO g) {
       if (more) start(qn, on, sn);
       products(qb, ob, s, dp);
       weights(sb, s, dp);
+      hide(ct * BQ, s, dp);
+      if (++ct == x.first + x.per) ct = x.first;
       Frag<T> p[2], ds[2];
       packed(s, dp, p, ds);
       sums(qb, ob, p, ds);
