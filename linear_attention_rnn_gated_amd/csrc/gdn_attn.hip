@@ -90,14 +90,14 @@ struct RowStage {
   Stager<T, D, BN, NW> sk, sv;
   __device__ __forceinline__ RowStage(const AttnIO& io, const Span& sp, int hk, int wave, int lane)
       : io(io), sp(sp), hk(hk), sk(io.ldk, wave, lane), sv(io.ldv, wave, lane) {}
-  __device__ __forceinline__ void start(int j, char* kb, char* vb) {
-    const int rows = sp.Lk - j * BN < BN ? sp.Lk - j * BN : BN;
-    sk.start(rows_rsrc<T, D>(io.k, sp.k0 + j * BN, io.ldk, hk, rows), kb);
-    sv.start(rows_rsrc<T, D>(io.v, sp.k0 + j * BN, io.ldv, hk, rows), vb);
+  // keys of tile jk into kb and values of tile jv into vb, those that there are
+  __device__ __forceinline__ void start(int jk, char* kb, bool k, int jv, char* vb, bool v) {
+    if (k) sk.start(rows_rsrc<T, D>(io.k, sp.k0 + jk * BN, io.ldk, hk, sp.Lk - jk * BN < BN ? sp.Lk - jk * BN : BN), kb);
+    if (v) sv.start(rows_rsrc<T, D>(io.v, sp.k0 + jv * BN, io.ldv, hk, sp.Lk - jv * BN < BN ? sp.Lk - jv * BN : BN), vb);
   }
-  __device__ __forceinline__ void finish(char* kb, char* vb) const {
-    sk.finish(kb);
-    sv.finish(vb);
+  __device__ __forceinline__ void finish(char* kb, char* vb, bool k, bool v) const {
+    if (k) sk.finish(kb);
+    if (v) sv.finish(vb);
   }
 };
 
@@ -111,19 +111,18 @@ __device__ __forceinline__ void load_rows(const void* x, int64_t at, int64_t ld,
 }
 
 template <typename T, int D>
-__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void k_attn_fwd(AttnIO io) {
+__global__ __launch_bounds__(256, (kAttnOcc<T, D>)) void k_attn_fwd(AttnIO io) {
 #ifdef GDN_DEVICE_PASS
-  using Tile = AttnTile<T, D>;
   __shared__ int odd[D + 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   QueryTile x;
-  if (!query_tile<Tile::BM>(io, wave, lane, &x)) return;
+  if (!query_tile<kAttnRows>(io, wave, lane, &x)) return;
   Held<T, D> q[D / 16];
   load_rows<T, D>(io.q, x.sp.q0 + (x.rows > 0 ? x.r0 : 0), io.ldq, x.hq, x.rows, lane, q);
-  RowStage<T, D, Tile::BN, Tile::NW> st(io, x.sp, x.hk, wave, lane);
+  RowStage<T, D, kAttnStep, kAttnWaves> st(io, x.sp, x.hk, wave, lane);
   AttnState<D> a;
-  const int steps = x.last >= 0 ? x.last / Tile::BN + 1 : 0;
-  attn_walk<T, T, D, Tile::BN, Tile::NW>(st, q, 0, steps, x.at, io.c, lane, odd, a);
+  const int steps = x.last >= 0 ? x.last / kAttnStep + 1 : 0;
+  attn_walk<T, T, D, kAttnWaves>(st, q, 0, steps, x.at, io.c, lane, odd, a);
   if (x.row < x.sp.Lq) {
     store_row<D>(static_cast<T*>(io.o) + (x.sp.q0 + x.row) * io.ldo + static_cast<int64_t>(x.hq) * D, a.acc, inverse_sum(a.l), lane);
     if (io.lse && lane < 32) io.lse[(x.sp.q0 + x.row) * io.H_q + x.hq] = lse_of(a.m * io.c, a.l);
@@ -192,7 +191,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && D <= 128 ? 2 : 1) void k_att
   auto step = [&](char* kb, char* vb, char* kn, char* vn, int j) {
     if constexpr (st.DIRECT) wait_loads();
     __syncthreads();
-    if (j + 1 < end) st.start(j + 1, kn, vn);
+    st.start(j + 1, kn, j + 1 < end, j + 1, vn, j + 1 < end);
     const int j0 = j * BN;
     if (j0 <= x.at.hi) {
       v16f s = zero16(), dp = zero16();
@@ -218,12 +217,12 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && D <= 128 ? 2 : 1) void k_att
     }
     if constexpr (!st.DIRECT) {
       if constexpr (!TWO) __syncthreads();
-      if (j + 1 < end) st.finish(kn, vn);
+      st.finish(kn, vn, j + 1 < end, j + 1 < end);
     }
   };
   if (end > 0) {
-    st.start(0, kA, vA);
-    if constexpr (!st.DIRECT) st.finish(kA, vA);
+    st.start(0, kA, true, 0, vA, true);
+    if constexpr (!st.DIRECT) st.finish(kA, vA, true, true);
   }
   if constexpr (TWO) {
     for (int j = 0; j < end; j += 2) {
@@ -605,11 +604,10 @@ int gdn_attn_prefill(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_
   io.o = o; io.lse = lse;
   hipStream_t st = static_cast<hipStream_t>(stream);
   return attn_dispatch(shape, [&]<typename T, int D>() {
-    using Tile = AttnTile<T, D>;
-    const int64_t blocks = tile_slots(T_q, n_seqs, Tile::BM) * io.H_q;
-    if (blocks * Tile::NW * 64 >= gdn::kLaunchThreads) return static_cast<int>(GDN_ERR_UNSUPPORTED);
+    const int64_t blocks = tile_slots(T_q, n_seqs, kAttnRows) * io.H_q;
+    if (blocks * 256 >= gdn::kLaunchThreads) return static_cast<int>(GDN_ERR_UNSUPPORTED);
     Timed t_("k_attn_fwd", st);
-    hipLaunchKernelGGL((k_attn_fwd<T, D>), dim3(static_cast<unsigned>(blocks)), dim3(Tile::NW * 64), 0, st, io);
+    hipLaunchKernelGGL((k_attn_fwd<T, D>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, io);
     return static_cast<int>(hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_HIP);
   });
 }

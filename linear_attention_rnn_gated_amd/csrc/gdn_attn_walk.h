@@ -2,7 +2,7 @@
 // share.
 //
 // A wave takes 32 query rows, a block NW waves of them, and the block goes over
-// the keys and values BN tokens at a time.  The transposed product S^T = K Q^T
+// the keys and values 32 tokens at a time.  The transposed product S^T = K Q^T
 // leaves one query row per lane (its other half in lane + 32), so the softmax's
 // maximum and sum are taken within the lane and once across the halves, and
 // exp(S^T) is the right operand of O^T = V^T P^T as it stands: k runs over the
@@ -59,101 +59,167 @@ struct AttnRows {
   int block_lo;  // the least of the block's
 };
 
+constexpr int kAttnStep = 32;             // tokens a step
+constexpr int kAttnWaves = 4, kAttnRows = 32 * kAttnWaves;  // of a block
+// Waves a SIMD that the walk's registers leave room for.
 template <typename T, int D>
-struct AttnTile {
-  static constexpr int NW = 4, BM = 32 * NW;
-  static constexpr int BN = sizeof(T) == 2 && D <= 128 ? 64 : 32;  // tokens a step
-};
+constexpr int kAttnOcc = sizeof(T) == 2 ? (D <= 128 ? 2 : 1) : 1;
 
-// Steps [j, end) of BN tokens.  T: the rows' type, TK: the tiles'.
-template <typename T, typename TK, int D, int BN, int NW, class Stage>
+// Goes over tiles [j, end) of 32 tokens.  T: the rows' type, TK: the tiles'.
+//
+// Step j: first half, the products S of tile j + 1 beside the softmax of tile j;
+// then tile j + 2 of the keys and j + 1 of the values have arrived and the ones
+// behind them set out; second half, the products with the values of tile j.  The
+// halves are laid out in slots of one product each, with the LDS reads AHEAD slots
+// before the products that take them (a product is 32 cycles, a read some 100), so
+// that one wave a SIMD keeps the matrix cores busy.
+//
+// The running maximum moves only where a row's grows by more than 2^kLazy: until
+// then exp(s - m) is at most that, which costs no bits.
+constexpr float kLazy = 8.0f;
+template <typename T, typename TK, int D, int NW, class Stage>
 __device__ __forceinline__ void attn_walk(Stage& st, const Held<T, D> (&q)[D / 16], int j, int end, const AttnRows& rows,
                                           float c, int lane, int* odd, AttnState<D>& a) {
+  constexpr int BN = kAttnStep, KS = D / 16, ND = D / 32, AHEAD = sizeof(T) == 2 ? 4 : 2, TOP = KS / 4;
   using P = Plane<TK, D, BN>;
-  constexpr int NS = BN / 32, KS = D / 16, ND = D / 32;
-  constexpr bool TWO = 4 * P::TILE <= 144 * 1024;  // buffers
-  __shared__ __align__(1024) char kA[P::TILE], vA[P::TILE], kB[TWO ? P::TILE : 16], vB[TWO ? P::TILE : 16];
+  // fp32 tiles at d = 256 have room for one of each, and take the step's parts one
+  // after another
+  constexpr bool ONE = 6 * P::TILE > 152 * 1024;
+  constexpr int REST = ONE ? 16 : P::TILE;
+  __shared__ __align__(1024) char kA[P::TILE], kB[REST], kC[REST], vA[P::TILE], vB[REST], vC[REST];
   for (int e = threadIdx.x; e < D + 1; e += NW * 64) odd[e] = INT32_MAX;
-  auto step = [&](char* kb, char* vb, char* kn, char* vn, int j) {
-    if constexpr (Stage::DIRECT) wait_loads();
+  if (j >= end) {
     __syncthreads();
-    if (j + 1 < end) st.start(j + 1, kn, vn);
-    const int j0 = j * BN;
-    if (j0 + BN - 1 > rows.block_lo) {  // some place is masked for some row of the block
-      set_aside<TK, D, BN, NW * 64>(vb, j0, odd);
+    return;
+  }
+  auto clean = [&](char* vb, int j) {
+    if (j * BN + BN - 1 > rows.block_lo) {  // some place is masked for some row of the block
+      set_aside<TK, D, BN, NW * 64>(vb, j * BN, odd);
       __syncthreads();
     }
-    if (j0 <= rows.hi) {
-      v16f s[NS];
+  };
+  v16f s, sn;
+  auto hide = [&](int j0) {
+    if (j0 + BN - 1 > rows.lo) {
 #pragma unroll
-      for (int t = 0; t < NS; ++t) {
-        s[t] = zero16();
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) s[t] = mma32(row_frag<TK, D, BN>(kb, 32 * t, ks, lane), q[ks].get(), s[t]);
-      }
-      if (j0 + BN - 1 > rows.lo) {
-#pragma unroll
-        for (int t = 0; t < NS; ++t)
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (j0 + 32 * t + c_row(i, lane) > rows.lim) s[t][i] = -INFINITY;
-      }
-      if constexpr (Stage::GAPS) {
-#pragma unroll
-        for (int t = 0; t < NS; ++t)
-          if (st.gap(t)) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) s[t][i] = -INFINITY;
-          }
-      }
-      float top = a.m;
-#pragma unroll
-      for (int t = 0; t < NS; ++t)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) top = fmaxf(top, s[t][i]);
-      top = fmaxf(top, other_half(top));
-      if (__any(top > a.m)) {
-        const float f = top > a.m ? __builtin_amdgcn_exp2f((a.m - top) * c) : 1.0f;  // 0 from m = -inf
-        a.m = top;
-        a.l *= f;
-#pragma unroll
-        for (int d = 0; d < ND; ++d) a.acc[d] *= f;
-      }
-      const float mc = a.m == -INFINITY ? 0.0f : a.m * c;
-#pragma unroll
-      for (int t = 0; t < NS; ++t) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          s[t][i] = __builtin_amdgcn_exp2f(fmaf(s[t][i], c, -mc));
-          a.l += s[t][i];
-        }
-      }
-#pragma unroll
-      for (int t = 0; t < NS; ++t)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          Frag<T> p;
-          p.pack(s[t], 8 * u);
-#pragma unroll
-          for (int d = 0; d < ND; ++d) a.acc[d] = mma32(col_frag<TK, D, BN>(vb, 32 * t + 16 * u, d, lane), p, a.acc[d]);
-        }
+      for (int i = 0; i < 16; ++i)
+        if (j0 + c_row(i, lane) > rows.lim) s[i] = -INFINITY;
     }
-    if constexpr (!Stage::DIRECT) {
-      if constexpr (!TWO) __syncthreads();
-      if (j + 1 < end) st.finish(kn, vn);
+    if constexpr (Stage::GAPS) {
+      if (st.gap()) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] = -INFINITY;
+      }
     }
   };
-  if (j < end) {
-    st.start(j, kA, vA);
-    if constexpr (!Stage::DIRECT) st.finish(kA, vA);
-  }
-  if constexpr (TWO) {
-    for (; j < end; j += 2) {
-      step(kA, vA, kB, vB, j);
-      if (j + 1 < end) step(kB, vB, kA, vA, j + 1);
+  auto raise = [&](float top) {  // the maximum; what it is in log2 afterwards, 0 for none
+    top = fmaxf(top, other_half(top));
+    if (__any(top * c > a.m * c + kLazy)) {
+      const bool move = top * c > a.m * c + kLazy;
+      const float f = move ? __builtin_amdgcn_exp2f((a.m - top) * c) : 1.0f;  // 0 from m = -inf
+      a.m = move ? top : a.m;
+      a.l *= f;
+#pragma unroll
+      for (int d = 0; d < ND; ++d) a.acc[d] *= f;
+    }
+    return a.m == -INFINITY ? 0.0f : a.m * c;
+  };
+  if constexpr (ONE) {
+    st.start(j, kA, true, j, vA, true);
+    for (; j < end; ++j) {
+      st.finish(kA, vA, true, true);
+      __syncthreads();
+      st.start(j + 1, kA, j + 1 < end, j + 1, vA, j + 1 < end);
+      clean(vA, j);
+      s = zero16();
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) s = mma32(row_frag<TK, D, BN>(kA, 0, ks, lane), q[ks].get(), s);
+      hide(j * BN);
+      float top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, s[i]);
+      const float mc = raise(top);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -mc));
+        a.l += s[i];
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        Frag<T> p;
+        p.pack(s, 8 * u);
+#pragma unroll
+        for (int d = 0; d < ND; ++d) a.acc[d] = mma32(col_frag<TK, D, BN>(vA, 16 * u, d, lane), p, a.acc[d]);
+      }
+      __syncthreads();
     }
   } else {
-    for (; j < end; ++j) step(kA, vA, kA, vA, j);
+  Frag<TK> rf[KS], cf[2 * ND];
+  auto step = [&](char* v0, char* k1, char* v1, char* k2, char* v2, char* k3, int j) {
+    hide(j * BN);
+    sn = zero16();
+    auto product = [&](int m) {
+      if (m + AHEAD < KS) rf[m + AHEAD] = row_frag<TK, D, BN>(k1, 0, m + AHEAD, lane);
+      if (m >= KS - AHEAD) cf[m - KS + AHEAD] = col_frag<TK, D, BN>(v0, 16 * ((m - KS + AHEAD) / ND), (m - KS + AHEAD) % ND, lane);
+      sn = mma32(rf[m], q[m].get(), sn);
+    };
+    float top = -INFINITY;
+#pragma unroll
+    for (int m = 0; m < TOP; ++m) {
+      __builtin_amdgcn_sched_barrier(0);
+      product(m);
+#pragma unroll
+      for (int i = 16 * m / TOP; i < 16 * (m + 1) / TOP; ++i) top = fmaxf(top, s[i]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    const float mc = raise(top);
+    Frag<T> p[2];
+#pragma unroll
+    for (int m = TOP; m < KS; ++m) {
+      __builtin_amdgcn_sched_barrier(0);
+      product(m);
+#pragma unroll
+      for (int i = 16 * (m - TOP) / (KS - TOP); i < 16 * (m - TOP + 1) / (KS - TOP); ++i) {
+        s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -mc));
+        a.l += s[i];
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    p[0].pack(s, 0);
+    if constexpr (!Stage::DIRECT) st.finish(k2, v1, j + 2 < end, j + 1 < end);
+    wait_loads();
+    __syncthreads();
+    st.start(j + 3, k3, j + 3 < end, j + 2, v2, j + 2 < end);
+    if (j + 1 < end) clean(v1, j + 1);
+#pragma unroll
+    for (int f = 0; f < 2 * ND; ++f) {
+      __builtin_amdgcn_sched_barrier(0);
+      if (f + AHEAD < 2 * ND) cf[f + AHEAD] = col_frag<TK, D, BN>(v0, 16 * ((f + AHEAD) / ND), (f + AHEAD) % ND, lane);
+      if (f >= 2 * ND - AHEAD) rf[f - 2 * ND + AHEAD] = row_frag<TK, D, BN>(k2, 0, f - 2 * ND + AHEAD, lane);
+      if (f == ND / 2) p[1].pack(s, 8);
+      a.acc[f % ND] = mma32(cf[f], p[f / ND], a.acc[f % ND]);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    s = sn;
+  };
+  st.start(j, kA, true, j, vA, true);
+  if constexpr (!Stage::DIRECT) st.finish(kA, vA, true, true);
+  st.start(j + 1, kB, j + 1 < end, j, vA, false);
+  if constexpr (!Stage::DIRECT) st.finish(kB, vA, j + 1 < end, false);
+  wait_loads();
+  __syncthreads();
+  st.start(j + 2, kC, j + 2 < end, j + 1, vB, j + 1 < end);
+  clean(vA, j);
+  s = zero16();
+#pragma unroll
+  for (int ks = 0; ks < KS; ++ks) s = mma32(row_frag<TK, D, BN>(kA, 0, ks, lane), q[ks].get(), s);
+#pragma unroll
+  for (int m = 0; m < AHEAD; ++m) rf[m] = row_frag<TK, D, BN>(kB, 0, m, lane);
+  for (; j < end; j += 3) {
+    step(vA, kB, vB, kC, vC, kA, j);
+    if (j + 1 < end) step(vB, kC, vC, kA, vA, kB, j + 1);
+    if (j + 2 < end) step(vC, kA, vA, kB, vB, kC, j + 2);
+  }
   }
   __syncthreads();
   a.l += other_half(a.l);

@@ -1,6 +1,6 @@
 // The 8-bit key/value cache and attention over it (include/gdn.h): kernels and
 // C ABI.
-#include "gdn_mma.h"
+#include "gdn_attn_walk.h"
 
 namespace {
 
@@ -242,6 +242,7 @@ struct DecIO {
 };
 constexpr int kSplit = 512;    // tokens a split
 constexpr int kRowsSplit = 64;  // rows for which they are that many
+constexpr int kWideRows = 64;   // a sequence of so many rows goes to the wide kernel
 
 // Tokens a split of a sequence with `rows` rows a head: more where there are rows
 // enough to go round.  A function of the sequence alone, so that its bits do not
@@ -381,8 +382,26 @@ struct KvRegs {
   }
 };
 
-template <typename T, int D, int MT>
+// The sequence and the tile of `rows` rows within it that slot x takes: sequence n's
+// slots begin at cu[n] G / rows + n.
+__device__ __forceinline__ int row_tile(const DecIO& io, int rows, int x, int* tile) {
+  if (!io.cu) {
+    const int per = (io.G + rows - 1) / rows;
+    *tile = x % per;
+    return x / per;
+  }
+  int lo = 0, hi = io.N - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (static_cast<int64_t>(io.cu[mid]) * io.G / rows + mid <= x) lo = mid; else hi = mid - 1;
+  }
+  *tile = static_cast<int>(x - (static_cast<int64_t>(io.cu[lo]) * io.G / rows + lo));
+  return lo;
+}
+
+template <typename T, int D>
 __global__ __launch_bounds__(256) void k_attn_decode(DecIO io) {
+#ifdef GDN_DEVICE_PASS
   constexpr int NP = sizeof(T) == 2 ? 1 : 3, KC = D / 32, ND = D / 16, W = D / 64;
   constexpr int PAD = D + 4;
   __shared__ __align__(16) float sh_o[4][16][PAD];
@@ -393,70 +412,52 @@ __global__ __launch_bounds__(256) void k_attn_decode(DecIO io) {
   __shared__ int odd[D + 1];
   const int hk = blockIdx.x % io.H_kv;
   const int x = blockIdx.x / io.H_kv;
-  int tile, n;
-  if (io.cu) {
-    int lo = 0, hi = io.N - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (static_cast<int64_t>(io.cu[mid]) * io.G / (16 * MT) + mid <= x) lo = mid; else hi = mid - 1;
-    }
-    n = lo;
-    tile = static_cast<int>(x - (static_cast<int64_t>(io.cu[n]) * io.G / (16 * MT) + n));
-  } else {
-    const int per = (io.G + 16 * MT - 1) / (16 * MT);
-    n = x / per;
-    tile = x - n * per;
-  }
+  int tile;
+  const int n = row_tile(io, 16, x, &tile);
   const DecSeq sq = dec_seq(io, n);
-  const int64_t r0 = static_cast<int64_t>(tile) * 16 * MT;
+  const int64_t r0 = static_cast<int64_t>(tile) * 16;
   const int split = blockIdx.y;
-  if (tile < 0 || r0 >= sq.rows || split >= sq.splits) return;
+  if (tile < 0 || r0 >= sq.rows || split >= sq.splits || sq.rows >= kWideRows) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4;
 
   // queries: steps 2 c and 2 c + 1 hold elements 64 c + 16 g + j and + 8 + j
-  u32x4 q[MT][KC][NP];
-  int lim[MT];  // the last token that the row sees
+  u32x4 q[KC][NP];
+  int lim;  // the last token that the row sees
   int lim_lo = INT32_MAX;
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    const int64_t r = r0 + 16 * mt + (lane & 15);
+  {
+    const int64_t r = r0 + (lane & 15);
     const bool in = r < sq.rows;
     const int64_t tok = in ? r / io.G : 0;
     const int head = hk * io.G + static_cast<int>(in ? r - tok * io.G : 0);
-    lim[mt] = in ? sq.sees(tok) : -1;
-    if (in && lim[mt] < lim_lo) lim_lo = lim[mt];
+    lim = in ? sq.sees(tok) : -1;
+    if (in && lim < lim_lo) lim_lo = lim;
     const T* src = static_cast<const T*>(io.q) + (sq.q0 + tok) * io.ldq + static_cast<int64_t>(head) * D + 16 * g;
 #pragma unroll
     for (int k = 0; k < KC; ++k) {
       if constexpr (NP == 1) {
-        q[mt][k][0] = in ? *reinterpret_cast<const u32x4*>(src + 64 * (k / 2) + 8 * (k % 2)) : u32x4{0, 0, 0, 0};
+        q[k][0] = in ? *reinterpret_cast<const u32x4*>(src + 64 * (k / 2) + 8 * (k % 2)) : u32x4{0, 0, 0, 0};
       } else {
         float y[8];
         load_row<8>(reinterpret_cast<const float*>(src) + 64 * (k / 2) + 8 * (k % 2), y);
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] = in ? y[e] : 0.0f;
-        parts8<NP>(y, q[mt][k]);
+        parts8<NP>(y, q[k]);
       }
     }
   }
 #pragma unroll
   for (int m = 1; m < 16; m <<= 1) lim_lo = min(lim_lo, __shfl_xor(lim_lo, m, 64));
   lim_lo = __builtin_amdgcn_readfirstlane(lim_lo);
-  const int64_t lastrow = (r0 + 16 * MT < sq.rows ? r0 + 16 * MT : sq.rows) - 1;
+  const int64_t lastrow = (r0 + 16 < sq.rows ? r0 + 16 : sq.rows) - 1;
   const int lim_hi = sq.sees(lastrow / io.G);
 
   const int64_t t0 = sq.split * split, t1 = t0 + sq.split < lim_hi + 1 ? t0 + sq.split : lim_hi + 1;
   const int b1 = static_cast<int>((t1 + kBlk - 1) / kBlk);
-  v4acc acc[MT][ND];
-  float m[MT], l[MT];
+  v4acc acc[ND];
+  float m = -INFINITY, l = 0.0f;
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    m[mt] = -INFINITY;
-    l[mt] = 0.0f;
-#pragma unroll
-    for (int d = 0; d < ND; ++d) acc[mt][d] = v4acc{0, 0, 0, 0};
-  }
+  for (int d = 0; d < ND; ++d) acc[d] = v4acc{0, 0, 0, 0};
   for (int e = threadIdx.x; e < D + 1; e += 256) odd[e] = INT32_MAX;
   __syncthreads();
   KvRegs<D> cur, nxt;
@@ -467,46 +468,42 @@ __global__ __launch_bounds__(256) void k_attn_decode(DecIO io) {
     if (cur.there) {
       const int j0 = b * kBlk;
       const bool edge = j0 + kBlk - 1 > lim_lo;
-      v4acc s[MT][2];
+      v4acc s[2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) s[mt][t] = v4acc{0, 0, 0, 0};
+        s[t] = v4acc{0, 0, 0, 0};
 #pragma unroll
         for (int k = 0; k < KC; ++k) {
           const u32x4 a = codes8(cur.k[t][k / 2][2 * (k % 2)], cur.k[t][k / 2][2 * (k % 2) + 1], cur.ks);
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int i = NP - 1; i >= 0; --i) s[mt][t] = mma16(a, q[mt][k][i], s[mt][t]);
+          for (int i = NP - 1; i >= 0; --i) s[t] = mma16(a, q[k][i], s[t]);
         }
       }
-      u32x4 p[MT][NP];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
+      u32x4 p[NP];
+      {
         float y[8];
-        float top = m[mt];
+        float top = m;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          y[e] = s[mt][e / 4][e % 4] * io.c;
-          if (edge && j0 + 16 * (e / 4) + 4 * g + e % 4 > lim[mt]) y[e] = -INFINITY;
+          y[e] = s[e / 4][e % 4] * io.c;
+          if (edge && j0 + 16 * (e / 4) + 4 * g + e % 4 > lim) y[e] = -INFINITY;
           top = fmaxf(top, y[e]);
         }
         top = max_rows(top);
-        if (__any(top > m[mt])) {
-          const float f = top > m[mt] ? __builtin_amdgcn_exp2f(m[mt] - top) : 1.0f;
-          m[mt] = top;
-          l[mt] *= f;
+        if (__any(top > m)) {
+          const float f = top > m ? __builtin_amdgcn_exp2f(m - top) : 1.0f;
+          m = top;
+          l *= f;
 #pragma unroll
-          for (int d = 0; d < ND; ++d) acc[mt][d] *= f;
+          for (int d = 0; d < ND; ++d) acc[d] *= f;
         }
-        const float mm = m[mt] == -INFINITY ? 0.0f : m[mt];
+        const float mm = m == -INFINITY ? 0.0f : m;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           y[e] = __builtin_amdgcn_exp2f(y[e] - mm);
-          l[mt] += y[e];
+          l += y[e];
         }
-        parts8<NP>(y, p[mt]);
+        parts8<NP>(y, p);
       }
       if (edge) {
 #pragma unroll
@@ -536,22 +533,18 @@ __global__ __launch_bounds__(256) void k_attn_decode(DecIO io) {
       for (int d = 0; d < ND; ++d) {  // row l % 16 of tile d is element (D / 16) (l % 16) + d
         const u32x4 a = codes8(cur.v[0][d % 4][d / 4], cur.v[1][d % 4][d / 4], cur.vs);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int i = NP - 1; i >= 0; --i) acc[mt][d] = mma16(a, p[mt][i], acc[mt][d]);
+        for (int i = NP - 1; i >= 0; --i) acc[d] = mma16(a, p[i], acc[d]);
       }
     }
     cur = nxt;
   }
 
   // the waves' results, joined in their order
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
+  {
     const int row = lane & 15;
-    const float lw = sum_rows(l[mt]);
-    if (mt > 0) __syncthreads();
+    const float lw = sum_rows(l);
     if (lane < 16) {
-      sh_m[wave][row] = m[mt];
+      sh_m[wave][row] = m;
       sh_l[wave][row] = lw;
     }
     // lane (row, g) holds elements (D / 16) (4 g + i) + d
@@ -559,13 +552,13 @@ __global__ __launch_bounds__(256) void k_attn_decode(DecIO io) {
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int d = 0; d < ND; d += 4) {
-        const v4f y{acc[mt][d][i], acc[mt][d + 1][i], acc[mt][d + 2][i], acc[mt][d + 3][i]};
+        const v4f y{acc[d][i], acc[d + 1][i], acc[d + 2][i], acc[d + 3][i]};
         *reinterpret_cast<v4f*>(&sh_o[wave][row][(D / 16) * (4 * g + i) + d]) = y;
       }
     __syncthreads();
     // 16 threads a row, D / 16 elements each
     const int rr = threadIdx.x >> 4, e0 = (threadIdx.x & 15) * 4;
-    const int64_t r = r0 + 16 * mt + rr;
+    const int64_t r = r0 + rr;
     if (r < sq.rows) {
       float top = -INFINITY;
 #pragma unroll
@@ -613,6 +606,127 @@ __global__ __launch_bounds__(256) void k_attn_decode(DecIO io) {
       }
     }
   }
+#endif
+}
+
+// ---- many rows a sequence
+//
+// Sequences of kWideRows rows and more: 128 rows a workgroup and the walk that
+// attention over prompts takes, with codes that become bf16 on their way into LDS,
+// once for all of the rows.
+
+// Tiles of the cache, one block of it each: 16 codes a thread and step.
+template <int D>
+struct CacheStage {
+  static constexpr bool DIRECT = false, GAPS = true;
+  using P = Plane<bf16_t, D, kBlk>;
+  static_assert(kAttnStep == kBlk);
+  static constexpr int CPR = D / 16, PIECES = kBlk * CPR, STEPS = (PIECES + 255) / 256;
+  const DecIO& io;
+  const DecSeq& sq;
+  int hk;
+  u32x4 k[STEPS], v[STEPS];
+  float ks, vs;
+  int v_first;  // token of the values' tile that is held
+  bool there[3] = {};  // whether the keys' tile has a page: of the step, and of the two after it
+  __device__ __forceinline__ CacheStage(const DecIO& io, const DecSeq& sq, int hk) : io(io), sq(sq), hk(hk) {}
+  __device__ __forceinline__ bool gap() const { return !there[0]; }
+  __device__ __forceinline__ int64_t block(int b) const {
+    const int page = page_of(io.table, io.max_pages, io.pages, io.bpp, sq.n, b);
+    return page < 0 ? -1 : (static_cast<int64_t>(page) * io.H_kv + hk) * io.bpp + b % io.bpp;
+  }
+  static __device__ __forceinline__ void load(const uint8_t* codes, int64_t blk, u32x4* x) {
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      const int at = (s * 256 + threadIdx.x) * 16;
+      x[s] = u32x4{0, 0, 0, 0};
+      if (blk >= 0 && (PIECES >= 256 || threadIdx.x < PIECES)) x[s] = *reinterpret_cast<const u32x4*>(codes + blk * (kBlk * D) + at);
+    }
+  }
+  __device__ __forceinline__ void start(int jk, char*, bool has_k, int jv, char*, bool has_v) {
+    there[0] = there[1];
+    there[1] = there[2];
+    if (has_k) {
+      const int64_t blk = block(jk);
+      load(io.kc, blk, k);
+      ks = blk >= 0 ? io.ks[blk] : 1.0f;
+      there[2] = blk >= 0;
+    }
+    if (has_v) {
+      const int64_t blk = block(jv);
+      load(io.vc, blk, v);
+      vs = blk >= 0 ? io.vs[blk] : 1.0f;
+      v_first = jv * kBlk;
+    }
+  }
+  __device__ __forceinline__ void finish(char* kb, char* vb, bool has_k, bool has_v) {
+    if (has_k) store(kb, k, ks, INT32_MAX);
+    if (has_v) store(vb, v, vs, sq.Lk - v_first);  // nothing stands behind the last token
+  }
+  static __device__ __forceinline__ void store(char* lds, const u32x4* x, float scale, int rows) {
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      if (PIECES < 256 && threadIdx.x >= PIECES) break;
+      const int c = s * 256 + threadIdx.x, r = c / CPR, piece = c % CPR * 2;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t lo = r < rows ? x[s][2 * e] : 0u, hi = r < rows ? x[s][2 * e + 1] : 0u;
+        *reinterpret_cast<u32x4*>(lds + r * P::RB + (((piece + e) ^ swizzle<P::RB>(r)) << 4)) = codes8(lo, hi, scale);
+      }
+    }
+  }
+};
+
+template <typename T, int D>
+__global__ __launch_bounds__(256, (kAttnOcc<T, D>)) void k_attn_decode_wide(DecIO io) {
+#ifdef GDN_DEVICE_PASS
+  constexpr int BM = kAttnRows, BN = kAttnStep;
+  __shared__ int odd[D + 1];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int hk = blockIdx.x % io.H_kv, x = blockIdx.x / io.H_kv, split = blockIdx.y;
+  int tile;
+  const int n = row_tile(io, BM, x, &tile);
+  const DecSeq sq = dec_seq(io, n);
+  const int64_t b0 = static_cast<int64_t>(tile) * BM, r0 = b0 + 32 * wave, r = r0 + (lane & 31);
+  if (tile < 0 || b0 >= sq.rows || split >= sq.splits || sq.rows < kWideRows) return;
+  const int64_t b1 = (b0 + BM < sq.rows ? b0 + BM : sq.rows) - 1, r1 = (r0 + 32 < sq.rows ? r0 + 32 : sq.rows) - 1;
+  const bool in = r < sq.rows;
+  const int64_t tok = in ? r / io.G : 0;
+  const int head = hk * io.G + static_cast<int>(in ? r - tok * io.G : 0);
+  AttnRows at;
+  at.lim = in ? sq.sees(tok) : -1;
+  at.lo = sq.sees(r0 / io.G);
+  at.hi = r0 < sq.rows ? sq.sees(r1 / io.G) : -1;
+  at.block_lo = sq.sees(b0 / io.G);
+  Held<T, D> q[D / 16];
+  {
+    const int64_t t0 = r0 < sq.rows ? r0 / io.G : 0;
+    const char* base = static_cast<const char*>(io.q) + (sq.q0 + t0) * io.ldq * sizeof(T);
+    const int bytes = r0 < sq.rows ? static_cast<int>(((r1 / io.G - t0) * io.ldq + static_cast<int64_t>(io.H_q) * D) * sizeof(T)) : 0;
+    const brsrc_t rq = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), static_cast<short>(0), bytes, 0x00020000);
+    const uint32_t from = in ? static_cast<uint32_t>(((tok - t0) * io.ldq + head * D + 8 * (lane >> 5)) * sizeof(T)) : 0x7fff0000u;
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) q[ks].load(rq, from + 16 * ks * sizeof(T));
+  }
+  const int64_t t0 = sq.split * split;
+  int64_t t1 = sq.sees(b1 / io.G) + 1;
+  t1 = t0 + sq.split < t1 ? t0 + sq.split : t1;
+  CacheStage<D> st(io, sq, hk);
+  AttnState<D> a;
+  attn_walk<T, bf16_t, D, kAttnWaves>(st, q, static_cast<int>(t0 / BN), static_cast<int>((t1 + BN - 1) / BN), at, io.c, lane, odd, a);
+  if (!in) return;
+  if (sq.splits == 1) {
+    store_row<D>(static_cast<T*>(io.o) + (sq.q0 + tok) * io.ldo + static_cast<int64_t>(head) * D, a.acc, inverse_sum(a.l), lane);
+    if (io.lse && lane < 32) io.lse[(sq.q0 + tok) * io.H_q + head] = lse_of(a.m * io.c, a.l);
+  } else {
+    const int64_t pr = (sq.q0 * io.G + n * io.extra + r * sq.splits + split) * io.H_kv + hk;
+    store_row<D>(io.part + pr * D, a.acc, 1.0f, lane);
+    if (lane < 32) {
+      io.stat[2 * pr] = a.m * io.c;
+      io.stat[2 * pr + 1] = a.l;
+    }
+  }
+#endif
 }
 
 // Joins the splits of a row: sixteen sums, of the splits i, i + 16, ..., each in
@@ -822,22 +936,21 @@ int gdn_attn_decode(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t
   io.c = shape->scale * kLog2e;
   hipStream_t st = static_cast<hipStream_t>(stream);
   return kv_dispatch(shape, [&]<typename T, int D>() {
-    constexpr int MT = sizeof(T) == 4 ? 1 : D <= 128 ? 4 : 2;
-    // many rows a sequence: tiles of MT times 16, so that a block of the cache is
-    // read and converted once for more of them (each row's bits are the same)
-    const bool wide = MT > 1 && cu_seqlens && n_tokens * G >= 32 * static_cast<int64_t>(n_seqs);
-    const int rows = wide ? 16 * MT : 16;
-    const int64_t tiles = cu_seqlens ? n_tokens * G / rows + n_seqs : n_seqs * int64_t{(G + 15) / 16};
-    if (tiles * io.H_kv * 256 >= gdn::kLaunchThreads / (splits > 0 ? splits : 1) ||
-        n_tokens * io.H_q >= gdn::kLaunchThreads / 1024)
+    // what a sequence's rows are decides who takes it; a kernel that none of them
+    // can need is not launched
+    const int64_t all = n_tokens * G;
+    const bool wide = cu_seqlens ? all >= kWideRows : G >= kWideRows, narrow = cu_seqlens ? n_seqs > 1 || !wide : !wide;
+    auto tiles = [&](int rows) { return cu_seqlens ? all / rows + n_seqs : n_seqs * int64_t{(G + rows - 1) / rows}; };
+    const int64_t y = splits > 0 ? splits : 1;
+    if (tiles(16) * io.H_kv * 256 >= gdn::kLaunchThreads / y || n_tokens * io.H_q >= gdn::kLaunchThreads / 1024)
       return static_cast<int>(GDN_ERR_UNSUPPORTED);
-    const dim3 grid(static_cast<unsigned>(tiles * io.H_kv), static_cast<unsigned>(splits > 0 ? splits : 1));
-    {
+    if (narrow) {
       Timed t_("k_attn_decode", st);
-      if (wide)
-        hipLaunchKernelGGL((k_attn_decode<T, D, MT>), grid, dim3(256), 0, st, io);
-      else
-        hipLaunchKernelGGL((k_attn_decode<T, D, 1>), grid, dim3(256), 0, st, io);
+      hipLaunchKernelGGL((k_attn_decode<T, D>), dim3(static_cast<unsigned>(tiles(16) * io.H_kv), static_cast<unsigned>(y)), dim3(256), 0, st, io);
+    }
+    if (wide) {
+      Timed t_("k_attn_decode_wide", st);
+      hipLaunchKernelGGL((k_attn_decode_wide<T, D>), dim3(static_cast<unsigned>(tiles(kAttnRows) * io.H_kv), static_cast<unsigned>(y)), dim3(256), 0, st, io);
     }
     if (splits > 1) {
       Timed t_("k_attn_join", st);

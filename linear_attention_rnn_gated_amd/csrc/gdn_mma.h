@@ -159,6 +159,13 @@ __device__ __forceinline__ v16f mma32(const Frag<float>& a, const Frag<float>& b
   return mma32(a.p[0], b.p[0], c);
 }
 
+// A left operand that is exact in one part.
+__device__ __forceinline__ v16f mma32(const Frag<bf16_t>& a, const Frag<float>& b, v16f c) {
+  c = mma32(a.x, b.p[2], c);
+  c = mma32(a.x, b.p[1], c);
+  return mma32(a.x, b.p[0], c);
+}
+
 // A tile of ROWS rows in LDS: one plane of bf16, or three of an fp32 tile's parts.
 template <typename T, int D, int ROWS>
 struct Plane {
