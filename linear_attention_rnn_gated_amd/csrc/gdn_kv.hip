@@ -7,27 +7,48 @@ namespace {
 constexpr int kBlk = GDN_KV_BLOCK;  // tokens that share a scale
 static_assert(kBlk == 32);
 
+
+// Pages of one pool and the table that names those of each sequence.
+struct Pages {
+  const int32_t* table;  // [N, width]
+  int width, pages;
+  uint32_t bpp, magic;   // blocks a page; 2^32 / bpp
+  // The page that holds block b and the block's place there.
+  __device__ __forceinline__ uint32_t page(uint32_t b, uint32_t* place) const {
+    uint32_t i = __umulhi(b, magic);  // or one less
+    if (b - i * bpp >= bpp) ++i;
+    *place = b - i * bpp;
+    return i;
+  }
+  __device__ __forceinline__ int id(int n, uint32_t i) const {
+    if (i >= static_cast<uint32_t>(width)) return -1;
+    const int p = table[static_cast<int64_t>(n) * width + i];
+    return p >= 0 && p < pages ? p : -1;
+  }
+  // The index of sequence n's block b among [pages, H_kv, P / 32], -1 for none.
+  __device__ __forceinline__ int64_t block(int n, int H_kv, int h, uint32_t b) const {
+    uint32_t place;
+    const int p = id(n, page(b, &place));
+    return at(p, place, H_kv, h);
+  }
+  __device__ __forceinline__ int64_t at(int p, uint32_t place, int H_kv, int h) const {
+    return p < 0 ? -1 : (static_cast<int64_t>(p) * H_kv + h) * bpp + place;
+  }
+};
+
 struct KvIO {
   uint8_t* kc;  // [pages, H_kv, P, D]
   uint8_t* vc;
   float* ks;    // [pages, H_kv, P / 32]
   float* vs;
-  const int32_t* table;  // [N, max_pages]
+  Pages pages;
   const int32_t* cu;     // [N + 1], nullptr: a token a sequence
   const int32_t* start;  // [N], nullable
   void* k;               // rows to write, or to read into
   void* v;
   int64_t T, ldk, ldv;
-  int N, H_kv, pages, max_pages, bpp;  // blocks per page
+  int N, H_kv;
 };
-
-// The page that holds block b of sequence n, or -1.
-__device__ __forceinline__ int page_of(const int32_t* __restrict__ table, int max_pages, int pages, int bpp, int n, int b) {
-  const int i = b / bpp;
-  if (i >= max_pages) return -1;
-  const int p = table[static_cast<int64_t>(n) * max_pages + i];
-  return p >= 0 && p < pages ? p : -1;
-}
 
 // The cache block that a workgroup takes, and the packed rows that it holds.
 struct KvItem {
@@ -63,9 +84,8 @@ __device__ __forceinline__ bool kv_item(const KvIO& io, int h, KvItem* it) {
   const int64_t first = io.start ? (io.start[n] > 0 ? io.start[n] : 0) : 0, end = first + (c1 - c0);
   const int64_t b = first / kBlk + local;
   if (local < 0 || b * kBlk >= end || b >= (int64_t{1} << 30)) return false;
-  const int page = page_of(io.table, io.max_pages, io.pages, io.bpp, n, static_cast<int>(b));
-  if (page < 0) return false;
-  it->blk = (static_cast<int64_t>(page) * io.H_kv + h) * io.bpp + b % io.bpp;
+  it->blk = io.pages.block(n, io.H_kv, h, static_cast<uint32_t>(b));
+  if (it->blk < 0) return false;
   it->lo = static_cast<int>(first > b * kBlk ? first - b * kBlk : 0);
   it->hi = static_cast<int>(end - b * kBlk < kBlk ? end - b * kBlk : kBlk);
   it->older = it->lo > 0;
@@ -228,7 +248,7 @@ struct DecIO {
   const uint8_t* vc;
   const float* ks;
   const float* vs;
-  const int32_t* table;
+  Pages pages;
   const int32_t* cu;
   const int32_t* len;
   const void* q;
@@ -236,13 +256,16 @@ struct DecIO {
   float* lse;
   float* part;  // [rows of partial results][D]
   float* stat;  // [..][2]: maximum (of s log2 e) and sum
-  int64_t T, ldq, ldo, extra, rows;
-  int N, H_q, H_kv, G, pages, max_pages, bpp, max_len;
+  int64_t T, ldq, ldo, rows;
+  int64_t mul, extra;  // sequence n's partial results begin at mul cu[n] G + extra n
+  int N, H_q, H_kv, G, max_len;
   float c;
 };
 constexpr int kSplit = 512;    // tokens a split
-constexpr int kRowsSplit = 64;  // rows for which they are that many
-constexpr int kWideRows = 64;   // a sequence of so many rows goes to the wide kernel
+constexpr int kRowsSplit = 256;  // rows for which they are that many
+constexpr int kWideRows = 64;    // a sequence of so many rows goes to the wide kernel
+// Tiles of 16 rows that the narrow one has for a sequence.
+__host__ __device__ inline int narrow_tiles(bool packed, int G) { return (packed ? kWideRows : G + 15) / 16; }
 
 // Tokens a split of a sequence with `rows` rows a head: more where there are rows
 // enough to go round.  A function of the sequence alone, so that its bits do not
@@ -335,11 +358,9 @@ struct KvRegs {
   uint32_t v[2][4][W];
   float ks, vs;
   bool there;
-  __device__ __forceinline__ void load(const DecIO& io, int n, int hk, int b, int lane) {
-    const int page = page_of(io.table, io.max_pages, io.pages, io.bpp, n, b);
-    there = page >= 0;
+  __device__ __forceinline__ void load(const DecIO& io, int64_t blk, int lane) {
+    there = blk >= 0;
     if (!there) return;
-    const int64_t blk = (static_cast<int64_t>(page) * io.H_kv + hk) * io.bpp + b % io.bpp;
     ks = io.ks[blk];
     vs = io.vs[blk];
     const uint8_t* kp = io.kc + blk * (kBlk * D) + (lane & 15) * D + (lane >> 4) * 16;
@@ -412,12 +433,11 @@ __global__ __launch_bounds__(256) void k_attn_decode(DecIO io) {
   __shared__ int odd[D + 1];
   const int hk = blockIdx.x % io.H_kv;
   const int x = blockIdx.x / io.H_kv;
-  int tile;
-  const int n = row_tile(io, 16, x, &tile);
+  const int per = narrow_tiles(io.cu != nullptr, io.G), n = x / per, tile = x - n * per;
   const DecSeq sq = dec_seq(io, n);
   const int64_t r0 = static_cast<int64_t>(tile) * 16;
   const int split = blockIdx.y;
-  if (tile < 0 || r0 >= sq.rows || split >= sq.splits || sq.rows >= kWideRows) return;
+  if (r0 >= sq.rows || split >= sq.splits || sq.rows >= kWideRows) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4;
 
@@ -462,9 +482,12 @@ __global__ __launch_bounds__(256) void k_attn_decode(DecIO io) {
   __syncthreads();
   KvRegs<D> cur, nxt;
   int b = static_cast<int>(t0 / kBlk) + wave;
-  if (b < b1) cur.load(io, n, hk, b, lane);
+  if (b < b1) cur.load(io, io.pages.block(n, io.H_kv, hk, b), lane);
+  // the page is looked up a step before its block is loaded
+  int64_t blk = b + 4 < b1 ? io.pages.block(n, io.H_kv, hk, b + 4) : -1;
   for (; b < b1; b += 4) {
-    if (b + 4 < b1) nxt.load(io, n, hk, b + 4, lane);
+    if (b + 4 < b1) nxt.load(io, blk, lane);
+    if (b + 8 < b1) blk = io.pages.block(n, io.H_kv, hk, b + 8);
     if (cur.there) {
       const int j0 = b * kBlk;
       const bool edge = j0 + kBlk - 1 > lim_lo;
@@ -573,7 +596,7 @@ __global__ __launch_bounds__(256) void k_attn_decode(DecIO io) {
       const int head = hk * io.G + static_cast<int>(r - tok * io.G);
       const bool whole = sq.splits == 1;
       const float inv = !whole ? 1.0f : sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-      const int64_t pr = (sq.q0 * io.G + n * io.extra + r * sq.splits + split) * io.H_kv + hk;
+      const int64_t pr = (sq.q0 * io.G * io.mul + n * io.extra + r * sq.splits + split) * io.H_kv + hk;
 #pragma unroll
       for (int e = e0; e < D; e += 64) {
         float y[4] = {0, 0, 0, 0};
@@ -629,12 +652,16 @@ struct CacheStage {
   float ks, vs;
   int v_first;  // token of the values' tile that is held
   bool there[3] = {};  // whether the keys' tile has a page: of the step, and of the two after it
-  __device__ __forceinline__ CacheStage(const DecIO& io, const DecSeq& sq, int hk) : io(io), sq(sq), hk(hk) {}
-  __device__ __forceinline__ bool gap() const { return !there[0]; }
-  __device__ __forceinline__ int64_t block(int b) const {
-    const int page = page_of(io.table, io.max_pages, io.pages, io.bpp, sq.n, b);
-    return page < 0 ? -1 : (static_cast<int64_t>(page) * io.H_kv + hk) * io.bpp + b % io.bpp;
+  // the tiles follow one another: the keys' next tile, its page (looked up a step
+  // ahead) and place; the values take the tile that the keys had before
+  uint32_t next, place;
+  int page;
+  int64_t blk_v;
+  __device__ __forceinline__ CacheStage(const DecIO& io, const DecSeq& sq, int hk, int first) : io(io), sq(sq), hk(hk) {
+    next = io.pages.page(first, &place);
+    page = io.pages.id(sq.n, next);
   }
+  __device__ __forceinline__ bool gap() const { return !there[0]; }
   static __device__ __forceinline__ void load(const uint8_t* codes, int64_t blk, u32x4* x) {
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
@@ -646,17 +673,23 @@ struct CacheStage {
   __device__ __forceinline__ void start(int jk, char*, bool has_k, int jv, char*, bool has_v) {
     there[0] = there[1];
     there[1] = there[2];
+    if (has_v) {
+      if (jv == jk) blk_v = io.pages.at(page, place, io.H_kv, hk);
+      load(io.vc, blk_v, v);
+      vs = blk_v >= 0 ? io.vs[blk_v] : 1.0f;
+      v_first = jv * kBlk;
+    }
     if (has_k) {
-      const int64_t blk = block(jk);
+      const int64_t blk = io.pages.at(page, place, io.H_kv, hk);
       load(io.kc, blk, k);
       ks = blk >= 0 ? io.ks[blk] : 1.0f;
       there[2] = blk >= 0;
-    }
-    if (has_v) {
-      const int64_t blk = block(jv);
-      load(io.vc, blk, v);
-      vs = blk >= 0 ? io.vs[blk] : 1.0f;
-      v_first = jv * kBlk;
+      blk_v = blk;
+      if (++place == io.pages.bpp) {
+        place = 0;
+        ++next;
+        page = io.pages.id(sq.n, next);
+      }
     }
   }
   __device__ __forceinline__ void finish(char* kb, char* vb, bool has_k, bool has_v) {
@@ -711,7 +744,7 @@ __global__ __launch_bounds__(256, (kAttnOcc<T, D>)) void k_attn_decode_wide(DecI
   const int64_t t0 = sq.split * split;
   int64_t t1 = sq.sees(b1 / io.G) + 1;
   t1 = t0 + sq.split < t1 ? t0 + sq.split : t1;
-  CacheStage<D> st(io, sq, hk);
+  CacheStage<D> st(io, sq, hk, static_cast<int>(t0 / BN));
   AttnState<D> a;
   attn_walk<T, bf16_t, D, kAttnWaves>(st, q, static_cast<int>(t0 / BN), static_cast<int>((t1 + BN - 1) / BN), at, io.c, lane, odd, a);
   if (!in) return;
@@ -719,7 +752,7 @@ __global__ __launch_bounds__(256, (kAttnOcc<T, D>)) void k_attn_decode_wide(DecI
     store_row<D>(static_cast<T*>(io.o) + (sq.q0 + tok) * io.ldo + static_cast<int64_t>(head) * D, a.acc, inverse_sum(a.l), lane);
     if (io.lse && lane < 32) io.lse[(sq.q0 + tok) * io.H_q + head] = lse_of(a.m * io.c, a.l);
   } else {
-    const int64_t pr = (sq.q0 * io.G + n * io.extra + r * sq.splits + split) * io.H_kv + hk;
+    const int64_t pr = (sq.q0 * io.G * io.mul + n * io.extra + r * sq.splits + split) * io.H_kv + hk;
     store_row<D>(io.part + pr * D, a.acc, 1.0f, lane);
     if (lane < 32) {
       io.stat[2 * pr] = a.m * io.c;
@@ -753,7 +786,7 @@ __global__ __launch_bounds__(GROUPS == 1 ? 256 : D / 4 * kJoin) void k_attn_join
   if (sq.splits <= 1 || tk < sq.q0 || tk >= sq.q0 + sq.Lq) return;
   const int hk = head / io.G;
   const int64_t r = (tk - sq.q0) * io.G + head - hk * io.G;
-  const int64_t p0 = sq.q0 * io.G + n * io.extra + r * sq.splits;
+  const int64_t p0 = sq.q0 * io.G * io.mul + n * io.extra + r * sq.splits;
   const float* part = io.part + (p0 * io.H_kv + hk) * D + e;
   const float* stat = io.stat + 2 * (p0 * io.H_kv + hk);
   const int64_t dp = static_cast<int64_t>(io.H_kv) * D, ds = 2 * io.H_kv;
@@ -817,7 +850,12 @@ int kv_dispatch(const gdn_attn_shape_t* s, F&& f) {
   return f.template operator()<float, 256>();
 }
 
-// Checks what kv_write and kv_read share and fills io; *run = false: nothing to do.
+Pages make_pages(const gdn_kv_cache_t* c, const int32_t* table, int32_t width) {
+  const uint32_t bpp = c->page_tokens / kBlk;
+  return Pages{table, width, c->pages, bpp, bpp == 1 ? UINT32_MAX : static_cast<uint32_t>((uint64_t{1} << 32) / bpp)};
+}
+
+// Checks what kv_write and kv_read share and fills io.
 int kv_common(const gdn_attn_shape_t* s, int32_t N, const int32_t* cu, const int32_t* start, int64_t T, const void* k,
               int64_t ldk, const void* v, int64_t ldv, const gdn_kv_cache_t* cache, const int32_t* table,
               int32_t max_pages, KvIO* io) {
@@ -835,19 +873,25 @@ int kv_common(const gdn_attn_shape_t* s, int32_t N, const int32_t* cu, const int
   if (rc != GDN_OK) return rc;
   io->kc = static_cast<uint8_t*>(cache->k); io->vc = static_cast<uint8_t*>(cache->v);
   io->ks = cache->k_scale; io->vs = cache->v_scale;
-  io->table = table; io->cu = cu; io->start = start;
+  io->pages = make_pages(cache, table, max_pages);
+  io->cu = cu; io->start = start;
   io->k = const_cast<void*>(k); io->v = const_cast<void*>(v);
-  io->T = T; io->N = N; io->H_kv = s->H_kv; io->pages = cache->pages; io->max_pages = max_pages;
-  io->bpp = cache->page_tokens / kBlk;
+  io->T = T; io->N = N; io->H_kv = s->H_kv;
   return GDN_OK;
 }
 
 int64_t kv_slots(const KvIO& io) { return io.cu ? io.T / kBlk + 2 * static_cast<int64_t>(io.N) : io.N; }
 
-// Rows of partial results of each head beyond one a query: see split_tokens.
-int64_t decode_extra(int32_t G, bool one, int64_t max_len) {
-  const int64_t most = (max_len + kSplit - 1) / kSplit;
-  return (most > 1 ? most - 1 : 0) * (one && G <= kRowsSplit ? G : kRowsSplit);
+// Where partial results stand: for every query row as many as the longest cache has
+// splits, or one, and for every sequence as many as make up for it: a sequence of r
+// rows has at most 1 + (most - 1) / ceil(r / kRowsSplit) splits, and so at most r +
+// kRowsSplit (most - 1) partial rows.  The smaller of the two.
+void decode_layout(int64_t N, int64_t T, int32_t G, int64_t max_len, int64_t* mul, int64_t* extra) {
+  int64_t most = (max_len + kSplit - 1) / kSplit;
+  most = most > 1 ? most : 1;
+  const bool rows = T * G <= N * kRowsSplit;
+  *mul = rows ? most : 1;
+  *extra = rows ? 0 : kRowsSplit * (most - 1);
 }
 
 }  // namespace
@@ -890,10 +934,10 @@ size_t gdn_attn_decode_workspace_bytes(const gdn_attn_shape_t* shape, int32_t n_
   if (gdn::check_attn_shape(shape) != GDN_OK || n_seqs < 0 || n_tokens < 0 || max_len < 0) return 0;
   if (n_tokens > INT32_MAX || max_len > INT32_MAX) return 0;
   const int32_t G = shape->H_q / shape->H_kv;
-  const int64_t one = decode_extra(G, true, max_len), many = decode_extra(G, false, max_len);
-  const int64_t extra = n_tokens == n_seqs ? (one > many ? one : many) : many;
   if (max_len <= kSplit) return gdn::kAlign;
-  const int64_t rows = (n_tokens * G + n_seqs * extra) * shape->H_kv;
+  int64_t mul, extra;
+  decode_layout(n_seqs, n_tokens, G, max_len, &mul, &extra);
+  const int64_t rows = (n_tokens * G * mul + n_seqs * extra) * shape->H_kv;
   const size_t bytes = static_cast<size_t>(rows) * (shape->d + 2) * sizeof(float);
   return (bytes + gdn::kAlign) / gdn::kAlign * gdn::kAlign;
 }
@@ -920,18 +964,18 @@ int gdn_attn_decode(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t
   const int32_t G = shape->H_q / shape->H_kv;
   const int64_t splits = (max_len + kSplit - 1) / kSplit;
   if (splits > 65535) return GDN_ERR_UNSUPPORTED;
-  io.extra = decode_extra(G, cu_seqlens == nullptr, max_len);
-  io.rows = (n_tokens * G + n_seqs * io.extra) * shape->H_kv;
+  decode_layout(n_seqs, n_tokens, G, max_len, &io.mul, &io.extra);
+  io.rows = (n_tokens * G * io.mul + n_seqs * io.extra) * shape->H_kv;
   if (splits > 1 && (!ws || ws_bytes < static_cast<size_t>(io.rows) * (shape->d + 2) * sizeof(float)))
     return GDN_ERR_WORKSPACE;
   if (n_tokens == 0) return GDN_OK;
   io.kc = static_cast<const uint8_t*>(cache->k); io.vc = static_cast<const uint8_t*>(cache->v);
   io.ks = cache->k_scale; io.vs = cache->v_scale;
-  io.table = block_table; io.cu = cu_seqlens; io.len = kv_len; io.q = q; io.o = o; io.lse = lse;
+  io.pages = make_pages(cache, block_table, max_pages);
+  io.cu = cu_seqlens; io.len = kv_len; io.q = q; io.o = o; io.lse = lse;
   io.part = static_cast<float*>(ws);
   io.stat = splits > 1 ? io.part + io.rows * shape->d : nullptr;
   io.T = n_tokens; io.N = n_seqs; io.H_q = shape->H_q; io.H_kv = shape->H_kv; io.G = G;
-  io.pages = cache->pages; io.max_pages = max_pages; io.bpp = cache->page_tokens / kBlk;
   io.max_len = static_cast<int>(max_len);
   io.c = shape->scale * kLog2e;
   hipStream_t st = static_cast<hipStream_t>(stream);
@@ -940,17 +984,19 @@ int gdn_attn_decode(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t
     // can need is not launched
     const int64_t all = n_tokens * G;
     const bool wide = cu_seqlens ? all >= kWideRows : G >= kWideRows, narrow = cu_seqlens ? n_seqs > 1 || !wide : !wide;
-    auto tiles = [&](int rows) { return cu_seqlens ? all / rows + n_seqs : n_seqs * int64_t{(G + rows - 1) / rows}; };
+    const int64_t tn = int64_t{n_seqs} * narrow_tiles(cu_seqlens != nullptr, G);
+    const int64_t tw = cu_seqlens ? all / kAttnRows + n_seqs : int64_t{n_seqs} * ((G + kAttnRows - 1) / kAttnRows);
     const int64_t y = splits > 0 ? splits : 1;
-    if (tiles(16) * io.H_kv * 256 >= gdn::kLaunchThreads / y || n_tokens * io.H_q >= gdn::kLaunchThreads / 1024)
+    if ((narrow && tn * io.H_kv * 256 >= gdn::kLaunchThreads / y) || (wide && tw * io.H_kv * 256 >= gdn::kLaunchThreads / y) ||
+        n_tokens * io.H_q >= gdn::kLaunchThreads / 1024)
       return static_cast<int>(GDN_ERR_UNSUPPORTED);
     if (narrow) {
       Timed t_("k_attn_decode", st);
-      hipLaunchKernelGGL((k_attn_decode<T, D>), dim3(static_cast<unsigned>(tiles(16) * io.H_kv), static_cast<unsigned>(y)), dim3(256), 0, st, io);
+      hipLaunchKernelGGL((k_attn_decode<T, D>), dim3(static_cast<unsigned>(tn * io.H_kv), static_cast<unsigned>(y)), dim3(256), 0, st, io);
     }
     if (wide) {
       Timed t_("k_attn_decode_wide", st);
-      hipLaunchKernelGGL((k_attn_decode_wide<T, D>), dim3(static_cast<unsigned>(tiles(kAttnRows) * io.H_kv), static_cast<unsigned>(y)), dim3(256), 0, st, io);
+      hipLaunchKernelGGL((k_attn_decode_wide<T, D>), dim3(static_cast<unsigned>(tw * io.H_kv), static_cast<unsigned>(y)), dim3(256), 0, st, io);
     }
     if (splits > 1) {
       Timed t_("k_attn_join", st);
