@@ -27,12 +27,15 @@ FLAGS = [
     "-fPIC",
     "-ffp-contract=off",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-    # MFMA accumulators in ordinary VGPRs: the 4-wave chunk scan otherwise
-    # splits its accumulators into AGPRs and copies them back every chunk
-    "-mllvm", "-amdgpu-mfma-vgpr-form=1",
     "-Wall",
     "-Wno-unused-function",
 ]
+SOURCE_FLAGS = {
+    # MFMA accumulators in ordinary VGPRs: the 4-wave chunk scan otherwise
+    # splits its accumulators into AGPRs and copies them back every chunk.  Not
+    # for attention, whose accumulators stay in the AGPRs.
+    "gdn_library.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+}
 
 def source_digest(extra_flags=()):
     """SHA-256 (first 16 hex digits) over the header, every source and the
@@ -43,7 +46,7 @@ def source_digest(extra_flags=()):
                  *[os.path.join(CSRC, s) for s in [*INCLUDED, *SOURCES]]]:
         with open(path, "rb") as f:
             h.update(f.read())
-    h.update(" ".join([*FLAGS, *extra_flags]).encode())
+    h.update(" ".join([*FLAGS, str(SOURCE_FLAGS), *extra_flags]).encode())
     return h.hexdigest()[:16]
 
 
@@ -52,7 +55,7 @@ def build(verbose=False, extra_flags=()):
     digest = f'-DGDN_SOURCE_DIGEST="{source_digest(extra_flags)}"'
     with tempfile.TemporaryDirectory() as tmp:
         objects = [os.path.join(tmp, s + ".o") for s in SOURCES]
-        cmds = [[HIPCC, *FLAGS, *extra_flags, digest, "-I", os.path.join(ROOT, "include"), "-I", CSRC,
+        cmds = [[HIPCC, *FLAGS, *SOURCE_FLAGS.get(s, []), *extra_flags, digest, "-I", os.path.join(ROOT, "include"), "-I", CSRC,
                  "-c", os.path.join(CSRC, s), "-o", o] for s, o in zip(SOURCES, objects)]
         _run_all(cmds, verbose)
         _run_all([[HIPCC, *FLAGS, *extra_flags, "-shared", *objects, "-o", LIB + ".tmp"]], verbose)

@@ -220,6 +220,12 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && D <= 128 ? 2 : 1) void k_att
       st.finish(kn, vn, j + 1 < end, j + 1 < end);
     }
   };
+  auto keep = [&] {
+    if constexpr (sizeof(T) == 4 || D == 256) {
+#pragma unroll
+      for (int d = 0; d < ND; ++d) in_agprs(acc[d]);
+    }
+  };
   if (end > 0) {
     st.start(0, kA, true, 0, vA, true);
     if constexpr (!st.DIRECT) st.finish(kA, vA, true, true);
@@ -228,9 +234,13 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && D <= 128 ? 2 : 1) void k_att
     for (int j = 0; j < end; j += 2) {
       step(kA, vA, kB, vB, j);
       if (j + 1 < end) step(kB, vB, kA, vA, j + 1);
+      keep();
     }
   } else {
-    for (int j = 0; j < end; ++j) step(kA, vA, kA, vA, j);
+    for (int j = 0; j < end; ++j) {
+      step(kA, vA, kA, vA, j);
+      keep();
+    }
   }
   if (x.row < x.sp.Lq)
     store_row<D>(static_cast<T*>(g.dq) + (x.sp.q0 + x.row) * g.lddq + static_cast<int64_t>(x.hq) * D, acc, g.scale, lane);
@@ -358,6 +368,13 @@ __global__ __launch_bounds__(256, 1) void k_attn_dkv(GradIO g) {
       if constexpr (DK) ds[u].pack(dp, 8 * u);
     }
   };
+  auto keep = [&] {
+#pragma unroll
+    for (int d = 0; d < ND; ++d) {
+      if constexpr (DK) in_agprs(ak[d]);
+      if constexpr (DV) in_agprs(av[d]);
+    }
+  };
   v16f s, dp;
   if constexpr (BUFS == 4) {
     // Step i: first half, the products of tile i + 1 beside p and dS of tile i; then
@@ -452,6 +469,7 @@ __global__ __launch_bounds__(256, 1) void k_attn_dkv(GradIO g) {
       if (i + 1 < steps) step(qB, oB, sB, qC, oC, qD, oD, qA, oA, sA, i + 1);
       if (i + 2 < steps) step(qC, oC, sC, qD, oD, qA, oA, qB, oB, sB, i + 2);
       if (i + 3 < steps) step(qD, oD, sD, qA, oA, qB, oB, qC, oC, sC, i + 3);
+      keep();
     }
   } else {
     if (steps > 0) {
@@ -486,11 +504,13 @@ __global__ __launch_bounds__(256, 1) void k_attn_dkv(GradIO g) {
       for (int i = 0; i < steps; i += 2) {
         step(qA, oA, sA, qB, oB, sB, i);
         if (i + 1 < steps) step(qB, oB, sB, qA, oA, sA, i + 1);
+        keep();
       }
     } else {
       for (int i = 0; i < steps; i += 2) {
         step(qA, oA, sA, qA, oA, sB, i);
         if (i + 1 < steps) step(qA, oA, sB, qA, oA, sA, i + 1);
+        keep();
       }
     }
   }

@@ -77,6 +77,28 @@ constexpr int kAttnOcc = sizeof(T) == 2 ? (D <= 128 ? 2 : 1) : 1;
 // The running maximum moves only where a row's grows by more than 2^kLazy: until
 // then exp(s - m) is at most that, which costs no bits.
 constexpr float kLazy = 8.0f;
+
+// x *= f for sums that stay in the accumulation registers.  Written out, because
+// the compiler otherwise takes them to the others and back on every step (100
+// moves), whether they change or not.  The waits cover a product's result before
+// it is read (18 cycles at most) and a register before a product takes it.
+__device__ __forceinline__ void scale_in_agprs(v16f& x, float f) {
+#pragma unroll
+  for (int i = 0; i < 16; i += 4) {
+    float a = x[i], b = x[i + 1], c = x[i + 2], d = x[i + 3], t, u, v, w;
+    asm volatile(
+        "s_nop 15\n\ts_nop 7\n\t"
+        "v_accvgpr_read_b32 %4, %0\n\tv_accvgpr_read_b32 %5, %1\n\tv_accvgpr_read_b32 %6, %2\n\tv_accvgpr_read_b32 %7, %3\n\t"
+        "s_nop 1\n\t"
+        "v_mul_f32 %4, %4, %8\n\tv_mul_f32 %5, %5, %8\n\tv_mul_f32 %6, %6, %8\n\tv_mul_f32 %7, %7, %8\n\t"
+        "v_accvgpr_write_b32 %0, %4\n\tv_accvgpr_write_b32 %1, %5\n\tv_accvgpr_write_b32 %2, %6\n\tv_accvgpr_write_b32 %3, %7\n\t"
+        "s_nop 7"
+        : "+a"(a), "+a"(b), "+a"(c), "+a"(d), "=&v"(t), "=&v"(u), "=&v"(v), "=&v"(w)
+        : "v"(f));
+    x[i] = a; x[i + 1] = b; x[i + 2] = c; x[i + 3] = d;
+  }
+  asm volatile("" : "+a"(x));
+}
 template <typename T, typename TK, int D, int NW, class Stage>
 __device__ __forceinline__ void attn_walk(Stage& st, const Held<T, D> (&q)[D / 16], int j, int end, const AttnRows& rows,
                                           float c, int lane, int* odd, AttnState<D>& a) {
@@ -120,7 +142,12 @@ __device__ __forceinline__ void attn_walk(Stage& st, const Held<T, D> (&q)[D / 1
       a.m = move ? top : a.m;
       a.l *= f;
 #pragma unroll
-      for (int d = 0; d < ND; ++d) a.acc[d] *= f;
+      for (int d = 0; d < ND; ++d) {
+        if constexpr (kAttnOcc<T, D> == 1)
+          scale_in_agprs(a.acc[d], f);
+        else
+          a.acc[d] *= f;
+      }
     }
     return a.m == -INFINITY ? 0.0f : a.m * c;
   };
@@ -180,12 +207,14 @@ __device__ __forceinline__ void attn_walk(Stage& st, const Held<T, D> (&q)[D / 1
       product(m);
 #pragma unroll
       for (int i = 16 * (m - TOP) / (KS - TOP); i < 16 * (m - TOP + 1) / (KS - TOP); ++i) {
-        s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -mc));
-        a.l += s[i];
+        float e = __builtin_amdgcn_exp2f(fmaf(s[i], c, -mc));
+        asm volatile("" : "+v"(e));  // here, and not where it is used
+        s[i] = e;
+        a.l += e;
       }
+      if (m == KS - 1) p[0].pack(s, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
-    p[0].pack(s, 0);
     if constexpr (!Stage::DIRECT) st.finish(k2, v1, j + 2 < end, j + 1 < end);
     wait_loads();
     __syncthreads();
@@ -219,6 +248,10 @@ __device__ __forceinline__ void attn_walk(Stage& st, const Held<T, D> (&q)[D / 1
     step(vA, kB, vB, kC, vC, kA, j);
     if (j + 1 < end) step(vB, kC, vC, kA, vA, kB, j + 1);
     if (j + 2 < end) step(vC, kA, vA, kB, vB, kC, j + 2);
+    if constexpr (kAttnOcc<T, D> == 1) {
+#pragma unroll
+      for (int d = 0; d < ND; ++d) in_agprs(a.acc[d]);
+    }
   }
   }
   __syncthreads();

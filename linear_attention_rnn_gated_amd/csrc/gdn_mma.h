@@ -46,6 +46,9 @@ __device__ __forceinline__ float other_half(float x) {
   return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
 }
 
+// Says that x stands in the accumulation registers here.
+__device__ __forceinline__ void in_agprs(v16f& x) { asm volatile("" : "+a"(x)); }
+
 // All loads of this wave, those into LDS among them, have arrived.
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
