@@ -538,9 +538,9 @@ int gdn_rope_freqs(int32_t r, double base, const gdn_rope_scaling_t* scaling, fl
  *
  * Rows as for gdn_qk_rotary: token t's heads are d elements each, one after
  * another, at q + t ldq (ld in elements; 0 = dense; a multiple of 8, at most 2^22).
- * All cu_* are on the device and read there; they must start at 0 and be
- * non-decreasing (values outside the T rows are clamped: wrong values, no access
- * outside).  Rows past cu[n_seqs] are neither read nor written, and one
+ * All cu_* are on the device and read there; they, and lse and the int32 arrays
+ * below, start at multiples of 4 bytes, everything else at multiples of 16.  cu_* must start at 0 and be non-decreasing (values outside the T rows are clamped:
+ * wrong values, no access outside).  Rows past cu[n_seqs] are neither read nor written, and one
  * sequence's infinities and NaN reach no other's rows; within the sequence they
  * reach the rows that see them, forward, and any, in the gradient.
  *

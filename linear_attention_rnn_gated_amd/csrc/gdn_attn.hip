@@ -558,12 +558,13 @@ void launch_dkv(const GradIO& g, unsigned blocks, hipStream_t st) {
 }
 
 // Parts that a group's heads are cut into for dk and dv: more where the blocks of
-// 128 keys would not fill the chip.
+// 128 keys, one a CU and the first of a sequence twice as long as the average,
+// would not fill the chip evenly.
 int dkv_parts(const gdn_attn_shape_t* s, int64_t T_k) {
   const int G = s->H_q / s->H_kv;
   const int64_t blocks = (T_k + 127) / 128 * s->H_kv;
   int parts = 1;
-  while (parts < G && blocks * parts < 256) ++parts;
+  while (parts < G && blocks * parts < 1024) ++parts;
   const int heads = (G + parts - 1) / parts;
   return (G + heads - 1) / heads;  // none without a head
 }
@@ -595,7 +596,7 @@ int attn_common(const gdn_attn_shape_t* s, int32_t N, const int32_t* cu_q, const
     if (T_k != T_q) return GDN_ERR_INVALID_ARG;
     cu_k = cu_q;
   }
-  if (!gdn::aligned16({cu_q, cu_k, q, k, v})) return GDN_ERR_INVALID_ARG;
+  if (!gdn::aligned16({q, k, v}) || !gdn::aligned4({cu_q, cu_k})) return GDN_ERR_INVALID_ARG;
   if ((T_q > 0 && !q) || (T_k > 0 && (!k || !v))) return GDN_ERR_INVALID_ARG;
   if (T_q > INT32_MAX || T_k > INT32_MAX) return GDN_ERR_UNSUPPORTED;
   const int64_t wq = static_cast<int64_t>(s->H_q) * s->d, wk = static_cast<int64_t>(s->H_kv) * s->d;
@@ -617,7 +618,7 @@ int gdn_attn_prefill(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_
   AttnIO io{};
   int rc = attn_common(shape, n_seqs, cu_q, cu_k, T_q, T_k, q, ldq, k, ldk, v, ldv, &io);
   if (rc != GDN_OK) return rc;
-  if (!gdn::aligned16({o, lse}) || (T_q > 0 && !o)) return GDN_ERR_INVALID_ARG;
+  if (!gdn::aligned16({o}) || !gdn::aligned4({lse}) || (T_q > 0 && !o)) return GDN_ERR_INVALID_ARG;
   rc = gdn::attn_rows({{ldo, static_cast<int64_t>(shape->H_q) * shape->d, &io.ldo}});
   if (rc != GDN_OK) return rc;
   if (T_q == 0) return GDN_OK;
@@ -646,7 +647,7 @@ int gdn_attn_bwd(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t* c
   GradIO g{};
   int rc = attn_common(shape, n_seqs, cu_q, cu_k, T_q, T_k, q, ldq, k, ldk, v, ldv, &g.a);
   if (rc != GDN_OK) return rc;
-  if (!gdn::aligned16({o, lse, dO, dq, dk, dv, ws})) return GDN_ERR_INVALID_ARG;
+  if (!gdn::aligned16({o, dO, dq, dk, dv, ws}) || !gdn::aligned4({lse})) return GDN_ERR_INVALID_ARG;
   if ((T_q > 0 && (!o || !lse || !dO || !dq)) || (T_k > 0 && (!dk || !dv))) return GDN_ERR_INVALID_ARG;
   const int64_t wq = static_cast<int64_t>(shape->H_q) * shape->d, wk = static_cast<int64_t>(shape->H_kv) * shape->d;
   rc = gdn::attn_rows({{ldo, wq, &g.a.ldo}, {lddo, wq, &g.lddo}, {lddq, wq, &g.lddq}, {lddk, wk, &g.lddk}, {lddv, wk, &g.lddv}});

@@ -1,40 +1,10 @@
 // The 8-bit key/value cache and attention over it (include/gdn.h): kernels and
 // C ABI.
-#include "gdn_attn_walk.h"
+#include "gdn_kv.h"
 
 namespace {
 
-constexpr int kBlk = GDN_KV_BLOCK;  // tokens that share a scale
-static_assert(kBlk == 32);
-
-
-// Pages of one pool and the table that names those of each sequence.
-struct Pages {
-  const int32_t* table;  // [N, width]
-  int width, pages;
-  uint32_t bpp, magic;   // blocks a page; 2^32 / bpp
-  // The page that holds block b and the block's place there.
-  __device__ __forceinline__ uint32_t page(uint32_t b, uint32_t* place) const {
-    uint32_t i = __umulhi(b, magic);  // or one less
-    if (b - i * bpp >= bpp) ++i;
-    *place = b - i * bpp;
-    return i;
-  }
-  __device__ __forceinline__ int id(int n, uint32_t i) const {
-    if (i >= static_cast<uint32_t>(width)) return -1;
-    const int p = table[static_cast<int64_t>(n) * width + i];
-    return p >= 0 && p < pages ? p : -1;
-  }
-  // The index of sequence n's block b among [pages, H_kv, P / 32], -1 for none.
-  __device__ __forceinline__ int64_t block(int n, int H_kv, int h, uint32_t b) const {
-    uint32_t place;
-    const int p = id(n, page(b, &place));
-    return at(p, place, H_kv, h);
-  }
-  __device__ __forceinline__ int64_t at(int p, uint32_t place, int H_kv, int h) const {
-    return p < 0 ? -1 : (static_cast<int64_t>(p) * H_kv + h) * bpp + place;
-  }
-};
+using namespace gdn;
 
 struct KvIO {
   uint8_t* kc;  // [pages, H_kv, P, D]
@@ -243,82 +213,9 @@ __global__ __launch_bounds__(256) void k_kv_read(KvIO io) {
 // become bf16 there, exactly (the scale is a power of two): S^T = K Q^T on 16 x 16
 // x 32 products leaves a row in the lanes l % 16, and O^T = V^T P^T takes exp(S^T)
 // as it stands; the bytes of 4 tokens x 4 elements are transposed in registers.
-struct DecIO {
-  const uint8_t* kc;
-  const uint8_t* vc;
-  const float* ks;
-  const float* vs;
-  Pages pages;
-  const int32_t* cu;
-  const int32_t* len;
-  const void* q;
-  void* o;
-  float* lse;
-  float* part;  // [rows of partial results][D]
-  float* stat;  // [..][2]: maximum (of s log2 e) and sum
-  int64_t T, ldq, ldo, rows;
-  int64_t mul, extra;  // sequence n's partial results begin at mul cu[n] G + extra n
-  int N, H_q, H_kv, G, max_len;
-  float c;
-};
-constexpr int kSplit = 512;    // tokens a split
-constexpr int kRowsSplit = 256;  // rows for which they are that many
-constexpr int kWideRows = 64;    // a sequence of so many rows goes to the wide kernel
-// Tiles of 16 rows that the narrow one has for a sequence.
-__host__ __device__ inline int narrow_tiles(bool packed, int G) { return (packed ? kWideRows : G + 15) / 16; }
-
-// Tokens a split of a sequence with `rows` rows a head: more where there are rows
-// enough to go round.  A function of the sequence alone, so that its bits do not
-// depend on the batch.
-__host__ __device__ inline int64_t split_tokens(int64_t rows) { return kSplit * ((rows + kRowsSplit - 1) / kRowsSplit); }
-
-struct DecSeq {
-  int64_t q0;
-  int n, Lq, Lk;  // Lk: cached tokens that are read
-  int64_t pos;    // of the first query
-  int64_t rows, split;
-  int splits;
-  // the last cached token that query token t sees, -1 for none
-  __device__ __forceinline__ int sees(int64_t t) const {
-    const int64_t p = pos + t < Lk - 1 ? pos + t : Lk - 1;
-    return static_cast<int>(p < -1 ? -1 : p);
-  }
-};
-__device__ __forceinline__ DecSeq dec_seq(const DecIO& io, int n) {
-  DecSeq s;
-  s.n = n;
-  s.q0 = n;
-  s.Lq = 1;
-  if (io.cu) {
-    int64_t c0 = io.cu[n], c1 = io.cu[n + 1];
-    c0 = c0 < 0 ? 0 : c0 > io.T ? io.T : c0;
-    c1 = c1 < c0 ? c0 : c1 > io.T ? io.T : c1;
-    s.q0 = c0;
-    s.Lq = static_cast<int>(c1 - c0);
-  }
-  int64_t len = io.len[n];
-  s.pos = len - s.Lq;
-  len = len < 0 ? 0 : len > io.max_len ? io.max_len : len;
-  s.Lk = static_cast<int>(len);
-  s.rows = static_cast<int64_t>(s.Lq) * io.G;
-  s.split = split_tokens(s.rows > 0 ? s.rows : 1);
-  s.splits = static_cast<int>((s.Lk + s.split - 1) / s.split);
-  if (s.splits < 1) s.splits = 1;
-  return s;
-}
-
 typedef float v4acc __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ v4acc mma16(u32x4 a, u32x4 b, v4acc c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-}
-// Eight codes as bf16, times the power of two s.
-__device__ __forceinline__ u32x4 codes8(uint32_t lo, uint32_t hi, float s) {
-  u32x4 y;
-  y[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, false));
-  y[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, s, true));
-  y[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, false));
-  y[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, s, true));
-  return y;
 }
 // Eight fp32 values in NP bf16 parts that sum to them (exactly, with three).
 template <int NP>
@@ -402,23 +299,6 @@ struct KvRegs {
       }
   }
 };
-
-// The sequence and the tile of `rows` rows within it that slot x takes: sequence n's
-// slots begin at cu[n] G / rows + n.
-__device__ __forceinline__ int row_tile(const DecIO& io, int rows, int x, int* tile) {
-  if (!io.cu) {
-    const int per = (io.G + rows - 1) / rows;
-    *tile = x % per;
-    return x / per;
-  }
-  int lo = 0, hi = io.N - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (static_cast<int64_t>(io.cu[mid]) * io.G / rows + mid <= x) lo = mid; else hi = mid - 1;
-  }
-  *tile = static_cast<int>(x - (static_cast<int64_t>(io.cu[lo]) * io.G / rows + lo));
-  return lo;
-}
 
 template <typename T, int D>
 __global__ __launch_bounds__(256) void k_attn_decode(DecIO io) {
@@ -632,136 +512,6 @@ __global__ __launch_bounds__(256) void k_attn_decode(DecIO io) {
 #endif
 }
 
-// ---- many rows a sequence
-//
-// Sequences of kWideRows rows and more: 128 rows a workgroup and the walk that
-// attention over prompts takes, with codes that become bf16 on their way into LDS,
-// once for all of the rows.
-
-// Tiles of the cache, one block of it each: 16 codes a thread and step.
-template <int D>
-struct CacheStage {
-  static constexpr bool DIRECT = false, GAPS = true;
-  using P = Plane<bf16_t, D, kBlk>;
-  static_assert(kAttnStep == kBlk);
-  static constexpr int CPR = D / 16, PIECES = kBlk * CPR, STEPS = (PIECES + 255) / 256;
-  const DecIO& io;
-  const DecSeq& sq;
-  int hk;
-  u32x4 k[STEPS], v[STEPS];
-  float ks, vs;
-  int v_first;  // token of the values' tile that is held
-  bool there[3] = {};  // whether the keys' tile has a page: of the step, and of the two after it
-  // the tiles follow one another: the keys' next tile, its page (looked up a step
-  // ahead) and place; the values take the tile that the keys had before
-  uint32_t next, place;
-  int page;
-  int64_t blk_v;
-  __device__ __forceinline__ CacheStage(const DecIO& io, const DecSeq& sq, int hk, int first) : io(io), sq(sq), hk(hk) {
-    next = io.pages.page(first, &place);
-    page = io.pages.id(sq.n, next);
-  }
-  __device__ __forceinline__ bool gap() const { return !there[0]; }
-  static __device__ __forceinline__ void load(const uint8_t* codes, int64_t blk, u32x4* x) {
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-      const int at = (s * 256 + threadIdx.x) * 16;
-      x[s] = u32x4{0, 0, 0, 0};
-      if (blk >= 0 && (PIECES >= 256 || threadIdx.x < PIECES)) x[s] = *reinterpret_cast<const u32x4*>(codes + blk * (kBlk * D) + at);
-    }
-  }
-  __device__ __forceinline__ void start(int jk, char*, bool has_k, int jv, char*, bool has_v) {
-    there[0] = there[1];
-    there[1] = there[2];
-    if (has_v) {
-      if (jv == jk) blk_v = io.pages.at(page, place, io.H_kv, hk);
-      load(io.vc, blk_v, v);
-      vs = blk_v >= 0 ? io.vs[blk_v] : 1.0f;
-      v_first = jv * kBlk;
-    }
-    if (has_k) {
-      const int64_t blk = io.pages.at(page, place, io.H_kv, hk);
-      load(io.kc, blk, k);
-      ks = blk >= 0 ? io.ks[blk] : 1.0f;
-      there[2] = blk >= 0;
-      blk_v = blk;
-      if (++place == io.pages.bpp) {
-        place = 0;
-        ++next;
-        page = io.pages.id(sq.n, next);
-      }
-    }
-  }
-  __device__ __forceinline__ void finish(char* kb, char* vb, bool has_k, bool has_v) {
-    if (has_k) store(kb, k, ks, INT32_MAX);
-    if (has_v) store(vb, v, vs, sq.Lk - v_first);  // nothing stands behind the last token
-  }
-  static __device__ __forceinline__ void store(char* lds, const u32x4* x, float scale, int rows) {
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-      if (PIECES < 256 && threadIdx.x >= PIECES) break;
-      const int c = s * 256 + threadIdx.x, r = c / CPR, piece = c % CPR * 2;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint32_t lo = r < rows ? x[s][2 * e] : 0u, hi = r < rows ? x[s][2 * e + 1] : 0u;
-        *reinterpret_cast<u32x4*>(lds + r * P::RB + (((piece + e) ^ swizzle<P::RB>(r)) << 4)) = codes8(lo, hi, scale);
-      }
-    }
-  }
-};
-
-template <typename T, int D>
-__global__ __launch_bounds__(256, (kAttnOcc<T, D>)) void k_attn_decode_wide(DecIO io) {
-#ifdef GDN_DEVICE_PASS
-  constexpr int BM = kAttnRows, BN = kAttnStep;
-  __shared__ int odd[D + 1];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int hk = blockIdx.x % io.H_kv, x = blockIdx.x / io.H_kv, split = blockIdx.y;
-  int tile;
-  const int n = row_tile(io, BM, x, &tile);
-  const DecSeq sq = dec_seq(io, n);
-  const int64_t b0 = static_cast<int64_t>(tile) * BM, r0 = b0 + 32 * wave, r = r0 + (lane & 31);
-  if (tile < 0 || b0 >= sq.rows || split >= sq.splits || sq.rows < kWideRows) return;
-  const int64_t b1 = (b0 + BM < sq.rows ? b0 + BM : sq.rows) - 1, r1 = (r0 + 32 < sq.rows ? r0 + 32 : sq.rows) - 1;
-  const bool in = r < sq.rows;
-  const int64_t tok = in ? r / io.G : 0;
-  const int head = hk * io.G + static_cast<int>(in ? r - tok * io.G : 0);
-  AttnRows at;
-  at.lim = in ? sq.sees(tok) : -1;
-  at.lo = sq.sees(r0 / io.G);
-  at.hi = r0 < sq.rows ? sq.sees(r1 / io.G) : -1;
-  at.block_lo = sq.sees(b0 / io.G);
-  Held<T, D> q[D / 16];
-  {
-    const int64_t t0 = r0 < sq.rows ? r0 / io.G : 0;
-    const char* base = static_cast<const char*>(io.q) + (sq.q0 + t0) * io.ldq * sizeof(T);
-    const int bytes = r0 < sq.rows ? static_cast<int>(((r1 / io.G - t0) * io.ldq + static_cast<int64_t>(io.H_q) * D) * sizeof(T)) : 0;
-    const brsrc_t rq = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), static_cast<short>(0), bytes, 0x00020000);
-    const uint32_t from = in ? static_cast<uint32_t>(((tok - t0) * io.ldq + head * D + 8 * (lane >> 5)) * sizeof(T)) : 0x7fff0000u;
-#pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) q[ks].load(rq, from + 16 * ks * sizeof(T));
-  }
-  const int64_t t0 = sq.split * split;
-  int64_t t1 = sq.sees(b1 / io.G) + 1;
-  t1 = t0 + sq.split < t1 ? t0 + sq.split : t1;
-  CacheStage<D> st(io, sq, hk, static_cast<int>(t0 / BN));
-  AttnState<D> a;
-  attn_walk<T, bf16_t, D, kAttnWaves>(st, q, static_cast<int>(t0 / BN), static_cast<int>((t1 + BN - 1) / BN), at, io.c, lane, odd, a);
-  if (!in) return;
-  if (sq.splits == 1) {
-    store_row<D>(static_cast<T*>(io.o) + (sq.q0 + tok) * io.ldo + static_cast<int64_t>(head) * D, a.acc, inverse_sum(a.l), lane);
-    if (io.lse && lane < 32) io.lse[(sq.q0 + tok) * io.H_q + head] = lse_of(a.m * io.c, a.l);
-  } else {
-    const int64_t pr = (sq.q0 * io.G * io.mul + n * io.extra + r * sq.splits + split) * io.H_kv + hk;
-    store_row<D>(io.part + pr * D, a.acc, 1.0f, lane);
-    if (lane < 32) {
-      io.stat[2 * pr] = a.m * io.c;
-      io.stat[2 * pr + 1] = a.l;
-    }
-  }
-#endif
-}
-
 // Joins the splits of a row: sixteen sums, of the splits i, i + 16, ..., each in
 // order, then those in order.  GROUPS 16: a block a row, D / 4 lanes for each of
 // the sums; GROUPS 1, for up to sixteen splits: D / 4 lanes a row, which gives the
@@ -838,18 +588,6 @@ __global__ __launch_bounds__(GROUPS == 1 ? 256 : D / 4 * kJoin) void k_attn_join
 
 // ---- host side ----------------------------------------------------------------
 
-template <typename F>
-int kv_dispatch(const gdn_attn_shape_t* s, F&& f) {
-  if (s->in_dtype == GDN_BF16) {
-    if (s->d == 64) return f.template operator()<bf16_t, 64>();
-    if (s->d == 128) return f.template operator()<bf16_t, 128>();
-    return f.template operator()<bf16_t, 256>();
-  }
-  if (s->d == 64) return f.template operator()<float, 64>();
-  if (s->d == 128) return f.template operator()<float, 128>();
-  return f.template operator()<float, 256>();
-}
-
 Pages make_pages(const gdn_kv_cache_t* c, const int32_t* table, int32_t width) {
   const uint32_t bpp = c->page_tokens / kBlk;
   return Pages{table, width, c->pages, bpp, bpp == 1 ? UINT32_MAX : static_cast<uint32_t>((uint64_t{1} << 32) / bpp)};
@@ -864,7 +602,7 @@ int kv_common(const gdn_attn_shape_t* s, int32_t N, const int32_t* cu, const int
   rc = gdn::check_kv_cache(cache);
   if (rc != GDN_OK) return rc;
   if (N < 0 || T < 0 || max_pages < 0) return GDN_ERR_INVALID_ARG;
-  if (!gdn::aligned16({cu, start, k, v, table})) return GDN_ERR_INVALID_ARG;
+  if (!gdn::aligned16({k, v}) || !gdn::aligned4({cu, start, table})) return GDN_ERR_INVALID_ARG;
   if (cu ? N == 0 && T > 0 : T != N) return GDN_ERR_INVALID_ARG;
   if (T > 0 && (!k || !v || (max_pages > 0 && !table))) return GDN_ERR_INVALID_ARG;
   if (T > INT32_MAX || s->H_kv > 65535) return GDN_ERR_UNSUPPORTED;
@@ -951,7 +689,7 @@ int gdn_attn_decode(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t
   rc = gdn::check_kv_cache(cache);
   if (rc != GDN_OK) return rc;
   if (n_seqs < 0 || n_tokens < 0 || max_pages < 0 || max_len < 0) return GDN_ERR_INVALID_ARG;
-  if (!gdn::aligned16({cu_seqlens, q, block_table, kv_len, o, lse, ws})) return GDN_ERR_INVALID_ARG;
+  if (!gdn::aligned16({q, o, ws}) || !gdn::aligned4({cu_seqlens, block_table, kv_len, lse})) return GDN_ERR_INVALID_ARG;
   if (cu_seqlens ? n_seqs == 0 && n_tokens > 0 : n_tokens != n_seqs) return GDN_ERR_INVALID_ARG;
   if (n_tokens > 0 && (!q || !o || !kv_len || (max_pages > 0 && !block_table))) return GDN_ERR_INVALID_ARG;
   if (n_tokens > INT32_MAX || max_len > INT32_MAX) return GDN_ERR_UNSUPPORTED;
@@ -995,8 +733,8 @@ int gdn_attn_decode(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t
       hipLaunchKernelGGL((k_attn_decode<T, D>), dim3(static_cast<unsigned>(tn * io.H_kv), static_cast<unsigned>(y)), dim3(256), 0, st, io);
     }
     if (wide) {
-      Timed t_("k_attn_decode_wide", st);
-      hipLaunchKernelGGL((k_attn_decode_wide<T, D>), dim3(static_cast<unsigned>(tw * io.H_kv), static_cast<unsigned>(y)), dim3(256), 0, st, io);
+      const int rc = launch_decode_wide(shape, io, tw, y, st);
+      if (rc != GDN_OK) return rc;
     }
     if (splits > 1) {
       Timed t_("k_attn_join", st);

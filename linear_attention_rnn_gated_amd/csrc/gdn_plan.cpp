@@ -122,6 +122,12 @@ bool aligned16(std::initializer_list<const void*> ptrs) {
   return true;
 }
 
+bool aligned4(std::initializer_list<const void*> ptrs) {
+  for (const void* p : ptrs)
+    if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0) return false;  // NULL passes
+  return true;
+}
+
 int check_lru_shape(const gdn_lru_shape_t* s) {
   if (!s || s->D <= 0) return GDN_ERR_INVALID_ARG;
   if (s->gate != GDN_LRU_GATE_NONE && s->gate != GDN_LRU_GATE_COMPLEMENT && s->gate != GDN_LRU_GATE_NORM)

@@ -74,8 +74,9 @@ Layout layout(const gdn_shape_t* s, int32_t n_seqs, int64_t total_tokens, int op
 
 // Checks the pointer fields of a decode cache (all must be non-NULL).
 int check_cache(const gdn_cache_t* c);
-// True if every pointer is 16-byte aligned (NULL counts as aligned).
+// True if every pointer is 16-byte (4-byte) aligned (NULL counts as aligned).
 bool aligned16(std::initializer_list<const void*> ptrs);
+bool aligned4(std::initializer_list<const void*> ptrs);
 
 // Gated linear recurrence.  Channels per decode-cache position counter.
 constexpr int32_t kLruGroup = 256;
