@@ -83,21 +83,28 @@ __device__ __forceinline__ bool query_tile(const AttnIO& io, int wave, int lane,
 // Keys and values of one head as rows in memory.
 template <typename T, int D, int BN, int NW>
 struct RowStage {
+  using Move = Stager<T, D, BN, NW>;
   static constexpr bool DIRECT = sizeof(T) == 2, GAPS = false;
-  const AttnIO& io;
-  const Span& sp;
-  int hk;
-  Stager<T, D, BN, NW> sk, sv;
+  static constexpr int LOADS = Move::STEPS;
+  RowTiles<T, D, BN> tk, tv;
+  Move sk, sv;
+  // from the sequence's first key on
   __device__ __forceinline__ RowStage(const AttnIO& io, const Span& sp, int hk, int wave, int lane)
-      : io(io), sp(sp), hk(hk), sk(io.ldk, wave, lane), sv(io.ldv, wave, lane) {}
-  // keys of tile jk into kb and values of tile jv into vb, those that there are
-  __device__ __forceinline__ void start(int jk, char* kb, bool k, int jv, char* vb, bool v) {
-    if (k) sk.start(rows_rsrc<T, D>(io.k, sp.k0 + jk * BN, io.ldk, hk, sp.Lk - jk * BN < BN ? sp.Lk - jk * BN : BN), kb);
-    if (v) sv.start(rows_rsrc<T, D>(io.v, sp.k0 + jv * BN, io.ldv, hk, sp.Lk - jv * BN < BN ? sp.Lk - jv * BN : BN), vb);
-  }
-  __device__ __forceinline__ void finish(char* kb, char* vb, bool k, bool v) const {
-    if (k) sk.finish(kb);
-    if (v) sv.finish(vb);
+      : tk(io.k, sp.k0, io.ldk, hk, sp.Lk), tv(io.v, sp.k0, io.ldv, hk, sp.Lk), sk(io.ldk, wave, lane), sv(io.ldv, wave, lane) {}
+  __device__ __forceinline__ void next_k() { tk.next(); }
+  __device__ __forceinline__ void next_v() { tv.next(); }
+  __device__ __forceinline__ void load_k(int i, char* kb) { sk.load(i, tk.rsrc, kb); }
+  __device__ __forceinline__ void load_v(int i, char* vb) { sv.load(i, tv.rsrc, vb); }
+  __device__ __forceinline__ void finish_k(char* kb) const { sk.finish(kb); }
+  __device__ __forceinline__ void finish_v(char* vb) const { sv.finish(vb); }
+  __device__ __forceinline__ void load(char* kb, char* vb) {  // the next tile of both
+    next_k();
+    next_v();
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      load_k(i, kb);
+      load_v(i, vb);
+    }
   }
 };
 
@@ -191,7 +198,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && D <= 128 ? 2 : 1) void k_att
   auto step = [&](char* kb, char* vb, char* kn, char* vn, int j) {
     if constexpr (st.DIRECT) wait_loads();
     __syncthreads();
-    st.start(j + 1, kn, j + 1 < end, j + 1, vn, j + 1 < end);
+    st.load(kn, vn);
     const int j0 = j * BN;
     if (j0 <= x.at.hi) {
       v16f s = zero16(), dp = zero16();
@@ -217,7 +224,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && D <= 128 ? 2 : 1) void k_att
     }
     if constexpr (!st.DIRECT) {
       if constexpr (!TWO) __syncthreads();
-      st.finish(kn, vn, j + 1 < end, j + 1 < end);
+      st.finish_k(kn);
+      st.finish_v(vn);
     }
   };
   auto keep = [&] {
@@ -227,8 +235,11 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && D <= 128 ? 2 : 1) void k_att
     }
   };
   if (end > 0) {
-    st.start(0, kA, true, 0, vA, true);
-    if constexpr (!st.DIRECT) st.finish(kA, vA, true, true);
+    st.load(kA, vA);
+    if constexpr (!st.DIRECT) {
+      st.finish_k(kA);
+      st.finish_v(vA);
+    }
   }
   if constexpr (TWO) {
     for (int j = 0; j < end; j += 2) {
@@ -242,6 +253,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && D <= 128 ? 2 : 1) void k_att
       keep();
     }
   }
+  wait_loads();
   if (x.row < x.sp.Lq)
     store_row<D>(static_cast<T*>(g.dq) + (x.sp.q0 + x.row) * g.lddq + static_cast<int64_t>(x.hq) * D, acc, g.scale, lane);
 #endif

@@ -1,6 +1,12 @@
 // The walk over keys and values that attention over prompts and over the cache
 // share.
 //
+// Stage: where the tiles come from.  next_k and next_v turn to the next tile of the
+// keys or the values (from the first on; behind the last they load zeros or
+// nothing), load_k and load_v start load i of LOADS of a tile, straight into LDS
+// (DIRECT) or into registers, from where finish_k and finish_v take it there.  gap:
+// no token of the step's tile is there; asked for once a step, in order (GAPS).
+//
 // A wave takes 32 query rows, a block NW waves of them, and the block goes over
 // the keys and values 32 tokens at a time.  The transposed product S^T = K Q^T
 // leaves one query row per lane (its other half in lane + 32), so the softmax's
@@ -67,12 +73,13 @@ constexpr int kAttnOcc = sizeof(T) == 2 ? (D <= 128 ? 2 : 1) : 1;
 
 // Goes over tiles [j, end) of 32 tokens.  T: the rows' type, TK: the tiles'.
 //
-// Step j: first half, the products S of tile j + 1 beside the softmax of tile j;
-// then tile j + 2 of the keys and j + 1 of the values have arrived and the ones
-// behind them set out; second half, the products with the values of tile j.  The
-// halves are laid out in slots of one product each, with the LDS reads AHEAD slots
-// before the products that take them (a product is 32 cycles, a read some 100), so
-// that one wave a SIMD keeps the matrix cores busy.
+// Step j: first half, the products S of tile j + 1 beside the first part of the
+// softmax of tile j; then tile j + 2 of the keys and j + 1 of the values have
+// arrived; second half, the products with the values of tile j beside the rest of
+// the softmax and the loads of the tiles behind.  The halves are laid out in slots
+// of one product each, with the LDS reads AHEAD slots before the products that
+// take them (a product is 32 cycles, a read some 100), so that one wave a SIMD
+// keeps the matrix cores busy.
 //
 // The running maximum moves only where a row's grows by more than 2^kLazy: until
 // then exp(s - m) is at most that, which costs no bits.
@@ -151,12 +158,29 @@ __device__ __forceinline__ void attn_walk(Stage& st, const Held<T, D> (&q)[D / 1
     }
     return a.m == -INFINITY ? 0.0f : a.m * c;
   };
+  auto weight = [&](int i, float mc) {
+    float e = __builtin_amdgcn_exp2f(fmaf(s[i], c, -mc));
+    asm volatile("" : "+v"(e));  // here, and not where it is used
+    s[i] = e;
+    a.l += e;
+  };
+  auto load = [&](bool keys, char* buf) {  // a whole tile
+#pragma unroll
+    for (int i = 0; i < Stage::LOADS; ++i) keys ? st.load_k(i, buf) : st.load_v(i, buf);
+  };
+  st.next_k();
+  load(true, kA);
+  st.next_v();
+  load(false, vA);
   if constexpr (ONE) {
-    st.start(j, kA, true, j, vA, true);
     for (; j < end; ++j) {
-      st.finish(kA, vA, true, true);
+      st.finish_k(kA);
+      st.finish_v(vA);
       __syncthreads();
-      st.start(j + 1, kA, j + 1 < end, j + 1, vA, j + 1 < end);
+      st.next_k();
+      load(true, kA);
+      st.next_v();
+      load(false, vA);
       clean(vA, j);
       s = zero16();
 #pragma unroll
@@ -167,10 +191,7 @@ __device__ __forceinline__ void attn_walk(Stage& st, const Held<T, D> (&q)[D / 1
       for (int i = 0; i < 16; ++i) top = fmaxf(top, s[i]);
       const float mc = raise(top);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], c, -mc));
-        a.l += s[i];
-      }
+      for (int i = 0; i < 16; ++i) weight(i, mc);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         Frag<T> p;
@@ -181,79 +202,94 @@ __device__ __forceinline__ void attn_walk(Stage& st, const Held<T, D> (&q)[D / 1
       __syncthreads();
     }
   } else {
-  Frag<TK> rf[KS], cf[2 * ND];
-  auto step = [&](char* v0, char* k1, char* v1, char* k2, char* v2, char* k3, int j) {
-    hide(j * BN);
-    sn = zero16();
-    auto product = [&](int m) {
-      if (m + AHEAD < KS) rf[m + AHEAD] = row_frag<TK, D, BN>(k1, 0, m + AHEAD, lane);
-      if (m >= KS - AHEAD) cf[m - KS + AHEAD] = col_frag<TK, D, BN>(v0, 16 * ((m - KS + AHEAD) / ND), (m - KS + AHEAD) % ND, lane);
-      sn = mma32(rf[m], q[m].get(), sn);
-    };
-    float top = -INFINITY;
+    Frag<TK> rf[KS], cf[2 * ND];
+    // v0: values of tile j, k1 and v1: tile j + 1, k2: keys of tile j + 2; into k3 and
+    // v2 go the next ones
+    auto step = [&](char* v0, char* k1, char* v1, char* k2, char* v2, char* k3, int j) {
+      hide(j * BN);
+      sn = zero16();
+      auto product = [&](int m) {
+        if (m + AHEAD < KS) rf[m + AHEAD] = row_frag<TK, D, BN>(k1, 0, m + AHEAD, lane);
+        if (m >= KS - AHEAD) cf[m - KS + AHEAD] = col_frag<TK, D, BN>(v0, 16 * ((m - KS + AHEAD) / ND), (m - KS + AHEAD) % ND, lane);
+        sn = mma32(rf[m], q[m].get(), sn);
+      };
+      float top = -INFINITY;
 #pragma unroll
-    for (int m = 0; m < TOP; ++m) {
-      __builtin_amdgcn_sched_barrier(0);
-      product(m);
+      for (int m = 0; m < TOP; ++m) {
+        __builtin_amdgcn_sched_barrier(0);
+        product(m);
 #pragma unroll
-      for (int i = 16 * m / TOP; i < 16 * (m + 1) / TOP; ++i) top = fmaxf(top, s[i]);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    const float mc = raise(top);
-    Frag<T> p[2];
-#pragma unroll
-    for (int m = TOP; m < KS; ++m) {
-      __builtin_amdgcn_sched_barrier(0);
-      product(m);
-#pragma unroll
-      for (int i = 16 * (m - TOP) / (KS - TOP); i < 16 * (m - TOP + 1) / (KS - TOP); ++i) {
-        float e = __builtin_amdgcn_exp2f(fmaf(s[i], c, -mc));
-        asm volatile("" : "+v"(e));  // here, and not where it is used
-        s[i] = e;
-        a.l += e;
+        for (int i = 16 * m / TOP; i < 16 * (m + 1) / TOP; ++i) top = fmaxf(top, s[i]);
       }
-      if (m == KS - 1) p[0].pack(s, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      const float mc = raise(top);
+      Frag<T> p[2];
+#pragma unroll
+      for (int m = TOP; m < KS; ++m) {
+        __builtin_amdgcn_sched_barrier(0);
+        product(m);
+#pragma unroll
+        for (int i = 8 * (m - TOP) / (KS - TOP); i < 8 * (m - TOP + 1) / (KS - TOP); ++i) weight(i, mc);
+        if (m == KS - 1) p[0].pack(s, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (!Stage::DIRECT) {
+        st.finish_k(k2);
+        st.finish_v(v1);
+      }
+      wait_loads();
+      __syncthreads();
+      if (j + 1 < end) clean(v1, j + 1);
+      st.next_k();
+      st.next_v();
+#pragma unroll
+      for (int f = 0; f < 2 * ND; ++f) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (f + AHEAD < 2 * ND) cf[f + AHEAD] = col_frag<TK, D, BN>(v0, 16 * ((f + AHEAD) / ND), (f + AHEAD) % ND, lane);
+        if (f >= 2 * ND - AHEAD) rf[f - 2 * ND + AHEAD] = row_frag<TK, D, BN>(k2, 0, f - 2 * ND + AHEAD, lane);
+        a.acc[f % ND] = mma32(cf[f], p[f / ND], a.acc[f % ND]);
+        constexpr int N = 2 * Stage::LOADS;
+#pragma unroll
+        for (int i = f * N / (2 * ND); i < (f + 1) * N / (2 * ND); ++i) i < N / 2 ? st.load_k(i, k3) : st.load_v(i - N / 2, v2);
+        if (f < ND) {
+#pragma unroll
+          for (int i = 8 + 8 * f / ND; i < 8 + 8 * (f + 1) / ND; ++i) weight(i, mc);
+        }
+        if (f == ND - 1) p[1].pack(s, 8);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      s = sn;
+    };
+    if constexpr (!Stage::DIRECT) {
+      st.finish_k(kA);
+      st.finish_v(vA);
     }
-    __builtin_amdgcn_sched_barrier(0);
-    if constexpr (!Stage::DIRECT) st.finish(k2, v1, j + 2 < end, j + 1 < end);
+    st.next_k();
+    load(true, kB);
+    if constexpr (!Stage::DIRECT) st.finish_k(kB);
     wait_loads();
     __syncthreads();
-    st.start(j + 3, k3, j + 3 < end, j + 2, v2, j + 2 < end);
-    if (j + 1 < end) clean(v1, j + 1);
+    st.next_k();
+    load(true, kC);
+    st.next_v();
+    load(false, vB);
+    clean(vA, j);
+    s = zero16();
 #pragma unroll
-    for (int f = 0; f < 2 * ND; ++f) {
-      __builtin_amdgcn_sched_barrier(0);
-      if (f + AHEAD < 2 * ND) cf[f + AHEAD] = col_frag<TK, D, BN>(v0, 16 * ((f + AHEAD) / ND), (f + AHEAD) % ND, lane);
-      if (f >= 2 * ND - AHEAD) rf[f - 2 * ND + AHEAD] = row_frag<TK, D, BN>(k2, 0, f - 2 * ND + AHEAD, lane);
-      if (f == ND / 2) p[1].pack(s, 8);
-      a.acc[f % ND] = mma32(cf[f], p[f / ND], a.acc[f % ND]);
+    for (int ks = 0; ks < KS; ++ks) s = mma32(row_frag<TK, D, BN>(kA, 0, ks, lane), q[ks].get(), s);
+#pragma unroll
+    for (int m = 0; m < AHEAD; ++m) rf[m] = row_frag<TK, D, BN>(kB, 0, m, lane);
+    for (; j < end; j += 3) {
+      step(vA, kB, vB, kC, vC, kA, j);
+      if (j + 1 < end) step(vB, kC, vC, kA, vA, kB, j + 1);
+      if (j + 2 < end) step(vC, kA, vA, kB, vB, kC, j + 2);
+      if constexpr (kAttnOcc<T, D> == 1) {
+#pragma unroll
+        for (int d = 0; d < ND; ++d) in_agprs(a.acc[d]);
+      }
     }
-    __builtin_amdgcn_sched_barrier(0);
-    s = sn;
-  };
-  st.start(j, kA, true, j, vA, true);
-  if constexpr (!Stage::DIRECT) st.finish(kA, vA, true, true);
-  st.start(j + 1, kB, j + 1 < end, j, vA, false);
-  if constexpr (!Stage::DIRECT) st.finish(kB, vA, j + 1 < end, false);
+  }
   wait_loads();
-  __syncthreads();
-  st.start(j + 2, kC, j + 2 < end, j + 1, vB, j + 1 < end);
-  clean(vA, j);
-  s = zero16();
-#pragma unroll
-  for (int ks = 0; ks < KS; ++ks) s = mma32(row_frag<TK, D, BN>(kA, 0, ks, lane), q[ks].get(), s);
-#pragma unroll
-  for (int m = 0; m < AHEAD; ++m) rf[m] = row_frag<TK, D, BN>(kB, 0, m, lane);
-  for (; j < end; j += 3) {
-    step(vA, kB, vB, kC, vC, kA, j);
-    if (j + 1 < end) step(vB, kC, vC, kA, vA, kB, j + 1);
-    if (j + 2 < end) step(vC, kA, vA, kB, vB, kC, j + 2);
-    if constexpr (kAttnOcc<T, D> == 1) {
-#pragma unroll
-      for (int d = 0; d < ND; ++d) in_agprs(a.acc[d]);
-    }
-  }
-  }
   __syncthreads();
   a.l += other_half(a.l);
   if (odd[D] != INT32_MAX) {

@@ -33,58 +33,55 @@ struct CacheStage {
   static constexpr bool DIRECT = false, GAPS = true;
   using P = Plane<bf16_t, D, kBlk>;
   static_assert(kAttnStep == kBlk);
-  static constexpr int CPR = D / 16, PIECES = kBlk * CPR, STEPS = (PIECES + 255) / 256;
+  static constexpr int CPR = D / 16, PIECES = kBlk * CPR, STEPS = (PIECES + 255) / 256, LOADS = STEPS;
   const DecIO& io;
   const DecSeq& sq;
   int hk;
   u32x4 k[STEPS], v[STEPS];
   float ks, vs;
-  int v_first;  // token of the values' tile that is held
-  bool there[3] = {};  // whether the keys' tile has a page: of the step, and of the two after it
-  // the tiles follow one another: the keys' next tile, its page (looked up a step
-  // ahead) and place; the values take the tile that the keys had before
-  uint32_t next, place;
-  int page;
-  int64_t blk_v;
-  __device__ __forceinline__ CacheStage(const DecIO& io, const DecSeq& sq, int hk, int first) : io(io), sq(sq), hk(hk) {
+  // Blocks of the keys' tile that is held (b0) and of the one before it, without a
+  // page -1; the values' tile is the one or the other.  gap: those of the keys' last
+  // three tiles, the step's first.
+  int64_t b0 = -1, b1 = -1, bv = -1;
+  bool there[3] = {};
+  bool begun = false;
+  int left, rows = 0;    // tokens from the values' next tile on, of the one held
+  uint32_t next, place;  // page and place of the keys' next tile
+  int page;              // looked up a step ahead
+  __device__ __forceinline__ CacheStage(const DecIO& io, const DecSeq& sq, int hk, int first)
+      : io(io), sq(sq), hk(hk), left(sq.Lk - first * kBlk) {
     next = io.pages.page(first, &place);
     page = io.pages.id(sq.n, next);
   }
   __device__ __forceinline__ bool gap() const { return !there[0]; }
-  static __device__ __forceinline__ void load(const uint8_t* codes, int64_t blk, u32x4* x) {
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-      const int at = (s * 256 + threadIdx.x) * 16;
-      x[s] = u32x4{0, 0, 0, 0};
-      if (blk >= 0 && (PIECES >= 256 || threadIdx.x < PIECES)) x[s] = *reinterpret_cast<const u32x4*>(codes + blk * (kBlk * D) + at);
-    }
-  }
-  __device__ __forceinline__ void start(int jk, char*, bool has_k, int jv, char*, bool has_v) {
+  // Without a page: block 0 is read, and not used.
+  __device__ __forceinline__ void next_k() {
+    b1 = b0;
+    b0 = io.pages.at(page, place, io.H_kv, hk);
     there[0] = there[1];
     there[1] = there[2];
-    if (has_v) {
-      if (jv == jk) blk_v = io.pages.at(page, place, io.H_kv, hk);
-      load(io.vc, blk_v, v);
-      vs = blk_v >= 0 ? io.vs[blk_v] : 1.0f;
-      v_first = jv * kBlk;
-    }
-    if (has_k) {
-      const int64_t blk = io.pages.at(page, place, io.H_kv, hk);
-      load(io.kc, blk, k);
-      ks = blk >= 0 ? io.ks[blk] : 1.0f;
-      there[2] = blk >= 0;
-      blk_v = blk;
-      if (++place == io.pages.bpp) {
-        place = 0;
-        ++next;
-        page = io.pages.id(sq.n, next);
-      }
-    }
+    there[2] = b0 >= 0;
+    ks = io.ks[b0 < 0 ? 0 : b0];
+    const bool wrap = ++place == io.pages.bpp;
+    place = wrap ? 0 : place;
+    next += wrap ? 1 : 0;
+    page = io.pages.id(sq.n, next);
   }
-  __device__ __forceinline__ void finish(char* kb, char* vb, bool has_k, bool has_v) {
-    if (has_k) store(kb, k, ks, INT32_MAX);
-    if (has_v) store(vb, v, vs, sq.Lk - v_first);  // nothing stands behind the last token
+  __device__ __forceinline__ void next_v() {  // the keys are two tiles ahead, but at first
+    bv = begun ? b1 : b0;
+    begun = true;
+    vs = io.vs[bv < 0 ? 0 : bv];
+    rows = bv < 0 ? 0 : left;  // nothing stands behind the last token
+    left -= kBlk;
   }
+  __device__ __forceinline__ void load_k(int i, char*) { load(io.kc, b0, i, k); }
+  __device__ __forceinline__ void load_v(int i, char*) { load(io.vc, bv, i, v); }
+  static __device__ __forceinline__ void load(const uint8_t* codes, int64_t blk, int i, u32x4* x) {
+    if (PIECES >= 256 || threadIdx.x < PIECES)
+      x[i] = *reinterpret_cast<const u32x4*>(codes + (blk < 0 ? 0 : blk) * (kBlk * D) + (i * 256 + threadIdx.x) * 16);
+  }
+  __device__ __forceinline__ void finish_k(char* kb) const { store(kb, k, ks, INT32_MAX); }
+  __device__ __forceinline__ void finish_v(char* vb) const { store(vb, v, vs, rows); }
   static __device__ __forceinline__ void store(char* lds, const u32x4* x, float scale, int rows) {
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {

@@ -239,6 +239,25 @@ __device__ __forceinline__ brsrc_t rows_rsrc(const void* x, int64_t at, int64_t 
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), static_cast<short>(0), bytes, 0x00020000);
 }
 
+// Rows of one head, ROWS at a time: a buffer over the tile's rows that there are.
+template <typename T, int D, int ROWS>
+struct RowTiles {
+  const char* at;
+  int64_t step;     // bytes to the next tile
+  int ld, left;     // bytes of a row, rows from the tile on
+  brsrc_t rsrc;
+  __device__ __forceinline__ RowTiles(const void* x, int64_t row, int64_t ld, int h, int rows)
+      : at(static_cast<const char*>(x) + (row * ld + static_cast<int64_t>(h) * D) * sizeof(T)),
+        step(ROWS * ld * sizeof(T)), ld(static_cast<int>(ld * sizeof(T))), left(rows) {}
+  __device__ __forceinline__ void next() {
+    const int rows = left < ROWS ? left : ROWS;
+    const int bytes = rows > 0 ? (rows - 1) * ld + static_cast<int>(D * sizeof(T)) : 0;
+    rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(at), static_cast<short>(0), bytes, 0x00020000);
+    at += step;
+    left -= ROWS;
+  }
+};
+
 // Moves a tile of ROWS rows into LDS.  bf16 rows go there straight from memory
 // (start), 64 pieces of 16 bytes a wave and step; fp32 rows through registers
 // (start), and their parts from there (finish).
@@ -260,13 +279,14 @@ struct Stager {
   }
   __device__ __forceinline__ void start(brsrc_t rsrc, char* lds) {
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-      if constexpr (DIRECT) {
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (GDN_LDS void*)(lds + (s * NW + wave) * 1024), 16, at[s], 0, 0, 0);
-      } else {
-        held[2 * s] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at[s], 0, 0));
-        held[2 * s + 1] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at[s] + 16, 0, 0));
-      }
+    for (int s = 0; s < STEPS; ++s) load(s, rsrc, lds);
+  }
+  __device__ __forceinline__ void load(int s, brsrc_t rsrc, char* lds) {
+    if constexpr (DIRECT) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (GDN_LDS void*)(lds + (s * NW + wave) * 1024), 16, at[s], 0, 0, 0);
+    } else {
+      held[2 * s] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at[s], 0, 0));
+      held[2 * s + 1] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at[s] + 16, 0, 0));
     }
   }
   __device__ __forceinline__ void finish(char* lds) const {
