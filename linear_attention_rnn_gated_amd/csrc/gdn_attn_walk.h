@@ -230,13 +230,13 @@ __device__ __forceinline__ void attn_walk(Stage& st, const Held<T, D> (&q)[D / 1
         product(m);
 #pragma unroll
         for (int i = 8 * (m - TOP) / (KS - TOP); i < 8 * (m - TOP + 1) / (KS - TOP); ++i) weight(i, mc);
+        if constexpr (!Stage::DIRECT) {
+          if (m == KS - 2) st.finish_k(k2);
+          if (m == KS - 1) st.finish_v(v1);
+        }
         if (m == KS - 1) p[0].pack(s, 0);
       }
       __builtin_amdgcn_sched_barrier(0);
-      if constexpr (!Stage::DIRECT) {
-        st.finish_k(k2);
-        st.finish_v(v1);
-      }
       wait_loads();
       __syncthreads();
       if (j + 1 < end) clean(v1, j + 1);
@@ -267,12 +267,12 @@ __device__ __forceinline__ void attn_walk(Stage& st, const Held<T, D> (&q)[D / 1
     st.next_k();
     load(true, kB);
     if constexpr (!Stage::DIRECT) st.finish_k(kB);
-    wait_loads();
-    __syncthreads();
     st.next_k();
     load(true, kC);
     st.next_v();
     load(false, vB);
+    if constexpr (Stage::DIRECT) wait_loads<2 * Stage::LOADS>();
+    __syncthreads();
     clean(vA, j);
     s = zero16();
 #pragma unroll

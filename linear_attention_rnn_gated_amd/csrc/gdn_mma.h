@@ -49,8 +49,9 @@ __device__ __forceinline__ float other_half(float x) {
 // Says that x stands in the accumulation registers here.
 __device__ __forceinline__ void in_agprs(v16f& x) { asm volatile("" : "+a"(x)); }
 
-// All loads of this wave, those into LDS among them, have arrived.
-__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// All loads of this wave but the last N, those into LDS among them, have arrived.
+template <int N = 0>
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
 
 template <typename T>
 struct Frag;
