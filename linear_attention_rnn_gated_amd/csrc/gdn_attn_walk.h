@@ -146,15 +146,17 @@ __device__ __forceinline__ void attn_walk(Stage& st, const Held<T, D> (&q)[D / 1
     if (__any(top * c > a.m * c + kLazy)) {
       const bool move = top * c > a.m * c + kLazy;
       const float f = move ? __builtin_amdgcn_exp2f((a.m - top) * c) : 1.0f;  // 0 from m = -inf
-      a.m = move ? top : a.m;
-      a.l *= f;
+      if (__any(a.m > -INFINITY)) {  // else the sums are 0
+        a.l *= f;
 #pragma unroll
-      for (int d = 0; d < ND; ++d) {
-        if constexpr (kAttnOcc<T, D> == 1)
-          scale_in_agprs(a.acc[d], f);
-        else
-          a.acc[d] *= f;
+        for (int d = 0; d < ND; ++d) {
+          if constexpr (kAttnOcc<T, D> == 1)
+            scale_in_agprs(a.acc[d], f);
+          else
+            a.acc[d] *= f;
+        }
       }
+      a.m = move ? top : a.m;
     }
     return a.m == -INFINITY ? 0.0f : a.m * c;
   };
