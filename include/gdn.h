@@ -539,12 +539,18 @@ int gdn_rope_freqs(int32_t r, double base, const gdn_rope_scaling_t* scaling, fl
  * Rows as for gdn_qk_rotary: token t's heads are d elements each, one after
  * another, at q + t ldq (ld in elements; 0 = dense; a multiple of 8, at most 2^22).
  * All cu_* are on the device and read there; they, and lse and the int32 arrays
- * below, start at multiples of 4 bytes, everything else at multiples of 16.  cu_* must start at 0 and be non-decreasing (values outside the T rows are clamped:
- * wrong values, no access outside).  Rows past cu[n_seqs] are neither read nor written, and one
- * sequence's infinities and NaN reach no other's rows; within the sequence they
- * reach the rows that see them, forward, and any, in the gradient.
+ * below, start at multiples of 4 bytes, everything else at multiples of 16.  cu_* must
+ * start at 0 and be non-decreasing (values outside the T rows are clamped: wrong
+ * values, no access outside).  Rows past cu[n_seqs] are neither read nor written.
+ * No output may overlap an input.
  *
- * Supported: d 64, 128 or 256; H_q a multiple of H_kv, at most 4096; scale > 0.
+ * One sequence's infinities and NaN reach no other's rows; within the sequence they
+ * reach the rows that see them, forward (an infinite v as infinities or NaN), and
+ * any, in the gradient.  fp32 inputs over 3.39e38 (the largest bf16) count as
+ * infinite.
+ *
+ * Supported: d 64, 128 or 256; H_q a multiple of H_kv, at most 4096; 0 < scale <=
+ * 2^126.
  */
 typedef struct {
   int32_t H_q, H_kv;
@@ -568,8 +574,7 @@ size_t gdn_attn_workspace_bytes(const gdn_attn_shape_t* shape, int64_t T_q, int6
  *     dS_ij = p_ij (dO_i . v_j - dO_i . o_i),   dv_j = sum p_ij dO_i,
  *     dq_i = scale sum_j dS_ij k_j,   dk_j = scale sum dS_ij q_i,
  * the sums of dk and dv over the queries of all heads of the group.  Keys that no
- * query sees get 0.  No atomics: bitwise reproducible.  All rows are dense but for
- * their distances; no output may overlap an input. */
+ * query sees get 0.  No atomics: bitwise reproducible. */
 int gdn_attn_bwd(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t* cu_q,
                  const int32_t* cu_k, int64_t T_q, int64_t T_k, const void* q, int64_t ldq,
                  const void* k, int64_t ldk, const void* v, int64_t ldv, const void* o,
@@ -607,7 +612,7 @@ typedef struct {
  * the new one (exact, but for codes that become subnormal, which are rounded
  * again); places behind the written ones are left as they are and hold nothing.
  * Writing the same tokens again changes nothing.  No two sequences may write to
- * one page. */
+ * one page, and none may name a page twice where it writes. */
 int gdn_kv_write(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t* cu_seqlens,
                  const int32_t* start, int64_t T, const void* k, int64_t ldk, const void* v,
                  int64_t ldv, const gdn_kv_cache_t* cache, const int32_t* block_table,

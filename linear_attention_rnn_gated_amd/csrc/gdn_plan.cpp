@@ -404,6 +404,7 @@ int check_attn_shape(const gdn_attn_shape_t* s) {
   if (s->in_dtype != GDN_F32 && s->in_dtype != GDN_BF16) return GDN_ERR_UNSUPPORTED;
   if (s->d != 64 && s->d != 128 && s->d != 256) return GDN_ERR_UNSUPPORTED;
   if (s->H_q % s->H_kv != 0 || s->H_q > 4096) return GDN_ERR_UNSUPPORTED;
+  if (s->scale > 0x1p126f) return GDN_ERR_UNSUPPORTED;  // times log2(e) it has to be finite
   return GDN_OK;
 }
 

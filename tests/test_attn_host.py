@@ -59,7 +59,7 @@ def decode(s, c, N=1, cu=P, T=5, q=P, ldq=0, table=P, width=300, kv_len=P, max_l
 @pytest.mark.parametrize("kw,want", [
     (dict(H_q=0), BAD), (dict(H_kv=0), BAD), (dict(d=0), BAD), (dict(scale=0.0), BAD), (dict(scale=-1.0), BAD),
     (dict(scale=float("nan")), BAD), (dict(scale=float("inf")), BAD), (dict(H_q=3), UNS), (dict(H_q=8192), UNS),
-    (dict(d=96), UNS), (dict(d=512), UNS), (dict(in_dtype=2), UNS),
+    (dict(d=96), UNS), (dict(d=512), UNS), (dict(in_dtype=2), UNS), (dict(scale=2.0 ** 127), UNS),
 ])
 def test_shape_claims(kw, want):
     s, c, L = shape(**kw), cache(), B.lib()
