@@ -540,23 +540,28 @@ __global__ __launch_bounds__(GROUPS == 1 ? 256 : D / 4 * kJoin) void k_attn_join
   const float* part = io.part + (p0 * io.H_kv + hk) * D + e;
   const float* stat = io.stat + 2 * (p0 * io.H_kv + hk);
   const int64_t dp = static_cast<int64_t>(io.H_kv) * D, ds = 2 * io.H_kv;
+  // loads of U splits in flight; the first ones set out before the maximum is known
+  constexpr int STEP = GROUPS == 1 ? 1 : kJoin, U = 4;
+  v4f z[U];
+  float m[U], l[U];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * STEP < sq.splits ? i0 + u * STEP : sq.splits - 1;
+      z[u] = *reinterpret_cast<const v4f*>(part + i * dp);
+      m[u] = stat[i * ds];
+      l[u] = stat[i * ds + 1];
+    }
+  };
+  load(group);
   float top = -INFINITY;
   for (int i = threadIdx.x % LANES; i < sq.splits; i += LANES) top = fmaxf(top, stat[i * ds]);
 #pragma unroll
   for (int d = (LANES < 64 ? LANES : 64) / 2; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
   float sum = 0.0f;
   v4f y{0, 0, 0, 0};
-  constexpr int STEP = GROUPS == 1 ? 1 : kJoin, U = 4;  // loads of U splits in flight
   for (int i0 = group; i0 < sq.splits; i0 += U * STEP) {
-    v4f z[U];
-    float m[U], l[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * STEP < sq.splits ? i0 + u * STEP : i0;
-      z[u] = *reinterpret_cast<const v4f*>(part + i * dp);
-      m[u] = stat[i * ds];
-      l[u] = stat[i * ds + 1];
-    }
+    if (i0 != group) load(i0);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (i0 + u * STEP >= sq.splits) break;
