@@ -80,17 +80,18 @@ __device__ __forceinline__ bool query_tile(const AttnIO& io, int wave, int lane,
   return true;
 }
 
-// Keys and values of one head as rows in memory.
-template <typename T, int D, int BN, int NW>
+// Keys and values of one head as rows in memory: group grp's tiles.
+template <typename T, int D, int BN, int NW, int NG>
 struct RowStage {
   using Move = Stager<T, D, BN, NW>;
   static constexpr bool DIRECT = sizeof(T) == 2, GAPS = false;
   static constexpr int LOADS = Move::STEPS;
-  RowTiles<T, D, BN> tk, tv;
+  RowTiles<T, D, BN, NG> tk, tv;
   Move sk, sv;
   // from the sequence's first key on
-  __device__ __forceinline__ RowStage(const AttnIO& io, const Span& sp, int hk, int wave, int lane)
-      : tk(io.k, sp.k0, io.ldk, hk, sp.Lk), tv(io.v, sp.k0, io.ldv, hk, sp.Lk), sk(io.ldk, wave, lane), sv(io.ldv, wave, lane) {}
+  __device__ __forceinline__ RowStage(const AttnIO& io, const Span& sp, int hk, int grp, int wave, int lane)
+      : tk(io.k, sp.k0 + grp * BN, io.ldk, hk, sp.Lk - grp * BN), tv(io.v, sp.k0 + grp * BN, io.ldv, hk, sp.Lk - grp * BN),
+        sk(io.ldk, wave, lane), sv(io.ldv, wave, lane) {}
   __device__ __forceinline__ void next_k() { tk.next(); }
   __device__ __forceinline__ void next_v() { tv.next(); }
   __device__ __forceinline__ void load_k(int i, char* kb) { sk.load(i, tk.rsrc, kb); }
@@ -118,19 +119,21 @@ __device__ __forceinline__ void load_rows(const void* x, int64_t at, int64_t ld,
 }
 
 template <typename T, int D>
-__global__ __launch_bounds__(256, (kAttnOcc<T, D>)) void k_attn_fwd(AttnIO io) {
+__global__ __launch_bounds__((256 * kAttnGroups<T, D>), (kAttnOcc<T, D>)) void k_attn_fwd(AttnIO io) {
 #ifdef GDN_DEVICE_PASS
+  constexpr int NG = kAttnGroups<T, D>;
   __shared__ int odd[D + 1];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, grp = NG == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6 & 3);
   QueryTile x;
   if (!query_tile<kAttnRows>(io, wave, lane, &x)) return;
   Held<T, D> q[D / 16];
   load_rows<T, D>(io.q, x.sp.q0 + (x.rows > 0 ? x.r0 : 0), io.ldq, x.hq, x.rows, lane, q);
-  RowStage<T, D, kAttnStep, kAttnWaves> st(io, x.sp, x.hk, wave, lane);
+  RowStage<T, D, kAttnStep, kAttnWaves, NG> st(io, x.sp, x.hk, grp, wave, lane);
   AttnState<D> a;
   const int steps = x.last >= 0 ? x.last / kAttnStep + 1 : 0;
-  attn_walk<T, T, D, kAttnWaves>(st, q, 0, steps, x.at, io.c, lane, odd, a);
-  if (x.row < x.sp.Lq) {
+  attn_walk<T, T, D, kAttnWaves, NG>(st, grp, q, 0, steps, x.at, io.c, lane, odd, a);
+  if (grp == 0 && x.row < x.sp.Lq) {
     store_row<D>(static_cast<T*>(io.o) + (x.sp.q0 + x.row) * io.ldo + static_cast<int64_t>(x.hq) * D, a.acc, inverse_sum(a.l), lane);
     if (io.lse && lane < 32) io.lse[(x.sp.q0 + x.row) * io.H_q + x.hq] = lse_of(a.m * io.c, a.l);
   }
@@ -159,14 +162,17 @@ struct GradIO {
 };
 
 template <typename T, int D>
-__global__ __launch_bounds__(256, sizeof(T) == 2 && D <= 128 ? 2 : 1) void k_attn_dq(GradIO g) {
+__global__ __launch_bounds__((256 * kAttnGroups<T, D>), (kAttnOcc<T, D>)) void k_attn_dq(GradIO g) {
 #ifdef GDN_DEVICE_PASS
-  constexpr int BN = 32, NW = 4, KS = D / 16, ND = D / 32;
+  constexpr int BN = 32, NW = 4, NG = kAttnGroups<T, D>, KS = D / 16, ND = D / 32;
   using P = Plane<T, D, BN>;
   constexpr bool TWO = 4 * P::TILE <= 144 * 1024;
-  __shared__ __align__(1024) char kA[P::TILE], vA[P::TILE], kB[TWO ? P::TILE : 16], vB[TWO ? P::TILE : 16];
+  constexpr int SB = TWO ? P::TILE : 16;
+  __shared__ __align__(1024) char kA_[NG * P::TILE], vA_[NG * P::TILE], kB_[NG * SB], vB_[NG * SB];
   const AttnIO& io = g.a;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, grp = NG == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6 & 3);
+  char *kA = kA_ + grp * P::TILE, *vA = vA_ + grp * P::TILE, *kB = kB_ + grp * SB, *vB = vB_ + grp * SB;
   QueryTile x;
   if (!query_tile<32 * NW>(io, wave, lane, &x)) return;
   const int64_t at = x.sp.q0 + (x.rows > 0 ? x.r0 : 0);
@@ -184,22 +190,22 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && D <= 128 ? 2 : 1) void k_att
                     static_cast<uint32_t>(r * io.ldo * sizeof(T)) + col + 16 * ks * sizeof(T), dot);
     dot += other_half(dot);
     lse2 = x.row < x.sp.Lq ? io.lse[(x.sp.q0 + x.row) * io.H_q + x.hq] * kLog2e : 0.0f;
-    if (x.row < x.sp.Lq && lane < 32) {
+    if (grp == 0 && x.row < x.sp.Lq && lane < 32) {
       float* s = g.stat + 2 * (static_cast<int64_t>(x.hq) * io.T_q + x.sp.q0 + x.row);
       s[0] = lse2;
       s[1] = dot;
     }
   }
-  RowStage<T, D, BN, NW> st(io, x.sp, x.hk, wave, lane);
+  RowStage<T, D, BN, NW, NG> st(io, x.sp, x.hk, grp, wave, lane);
   v16f acc[ND];
 #pragma unroll
   for (int d = 0; d < ND; ++d) acc[d] = zero16();
-  const int end = x.last >= 0 ? x.last / BN + 1 : 0;
+  const int end = x.last >= 0 ? x.last / (NG * BN) + 1 : 0;
   auto step = [&](char* kb, char* vb, char* kn, char* vn, int j) {
     if constexpr (st.DIRECT) wait_loads();
     __syncthreads();
     st.load(kn, vn);
-    const int j0 = j * BN;
+    const int j0 = (j * NG + grp) * BN;
     if (j0 <= x.at.hi) {
       v16f s = zero16(), dp = zero16();
 #pragma unroll
@@ -254,6 +260,21 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && D <= 128 ? 2 : 1) void k_att
     }
   }
   wait_loads();
+  if constexpr (NG == 2) {  // both groups' sums, half in kA_ and half in vA_
+    static_assert(NG * P::TILE >= D * NW * 64);
+    constexpr int H = D / 4;
+    const int at = threadIdx.x & 255;
+    float *s0 = reinterpret_cast<float*>(kA_) + at, *s1 = reinterpret_cast<float*>(vA_) + at;
+    __syncthreads();
+    if (grp == 1) {
+#pragma unroll
+      for (int i = 0; i < 2 * H; ++i) (i < H ? s0 + i * 256 : s1 + (i - H) * 256)[0] = acc[i / 16][i % 16];
+    }
+    __syncthreads();
+    if (grp == 1) return;
+#pragma unroll
+    for (int i = 0; i < 2 * H; ++i) acc[i / 16][i % 16] += (i < H ? s0 + i * 256 : s1 + (i - H) * 256)[0];
+  }
   if (x.row < x.sp.Lq)
     store_row<D>(static_cast<T*>(g.dq) + (x.sp.q0 + x.row) * g.lddq + static_cast<int64_t>(x.hq) * D, acc, g.scale, lane);
 #endif
@@ -638,9 +659,10 @@ int gdn_attn_prefill(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_
   hipStream_t st = static_cast<hipStream_t>(stream);
   return attn_dispatch(shape, [&]<typename T, int D>() {
     const int64_t blocks = tile_slots(T_q, n_seqs, kAttnRows) * io.H_q;
-    if (blocks * 256 >= gdn::kLaunchThreads) return static_cast<int>(GDN_ERR_UNSUPPORTED);
+    constexpr int threads = 256 * kAttnGroups<T, D>;
+    if (blocks * threads >= gdn::kLaunchThreads) return static_cast<int>(GDN_ERR_UNSUPPORTED);
     Timed t_("k_attn_fwd", st);
-    hipLaunchKernelGGL((k_attn_fwd<T, D>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, io);
+    hipLaunchKernelGGL((k_attn_fwd<T, D>), dim3(static_cast<unsigned>(blocks)), dim3(threads), 0, st, io);
     return static_cast<int>(hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_HIP);
   });
 }
@@ -675,10 +697,11 @@ int gdn_attn_bwd(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t* c
   hipStream_t st = static_cast<hipStream_t>(stream);
   return attn_dispatch(shape, [&]<typename T, int D>() {
     const int64_t nq = tile_slots(T_q, n_seqs, 128) * g.a.H_q, nk = tile_slots(T_k, n_seqs, 128) * g.a.H_kv;
-    if (nq * 256 >= gdn::kLaunchThreads || nk * 256 >= gdn::kLaunchThreads / g.parts) return static_cast<int>(GDN_ERR_UNSUPPORTED);
+    constexpr int threads = 256 * kAttnGroups<T, D>;
+    if (nq * threads >= gdn::kLaunchThreads || nk * 256 >= gdn::kLaunchThreads / g.parts) return static_cast<int>(GDN_ERR_UNSUPPORTED);
     if (T_q > 0) {
       Timed t_("k_attn_dq", st);
-      hipLaunchKernelGGL((k_attn_dq<T, D>), dim3(static_cast<unsigned>(nq)), dim3(256), 0, st, g);
+      hipLaunchKernelGGL((k_attn_dq<T, D>), dim3(static_cast<unsigned>(nq)), dim3(threads), 0, st, g);
     }
     if (T_k > 0) {
       Timed t_("k_attn_dkv", st);

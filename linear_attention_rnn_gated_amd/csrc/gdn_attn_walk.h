@@ -25,11 +25,11 @@ namespace {
 // is one (odd[D] the first of all).  A row that sees that token sees all before
 // it, so its element e is NaN in the end.
 template <typename TK, int D, int ROWS, int THREADS>
-__device__ __forceinline__ void set_aside(char* tile, int j0, int* odd) {
+__device__ __forceinline__ void set_aside(char* tile, int j0, int* odd, int tid) {
   using P = Plane<TK, D, ROWS>;
   constexpr int CPR = P::RB / 16;
 #pragma unroll 1
-  for (int c = threadIdx.x; c < ROWS * CPR; c += THREADS) {
+  for (int c = tid; c < ROWS * CPR; c += THREADS) {
     const u32x4 x = *reinterpret_cast<const u32x4*>(tile + 16 * c);
     bool bad = false;
 #pragma unroll
@@ -69,9 +69,16 @@ constexpr int kAttnStep = 32;             // tokens a step
 constexpr int kAttnWaves = 4, kAttnRows = 32 * kAttnWaves;  // of a block
 // Waves a SIMD that the walk's registers leave room for.
 template <typename T, int D>
-constexpr int kAttnOcc = sizeof(T) == 2 ? (D <= 128 ? 2 : 1) : 1;
+constexpr int kAttnOcc = sizeof(T) == 2 ? (D <= 128 ? 2 : 1) : (D <= 64 ? 2 : 1);
 
-// Goes over tiles [j, end) of 32 tokens.  T: the rows' type, TK: the tiles'.
+// Groups of waves that share a block's rows, each of which takes every second tile.
+template <typename T, int D>
+constexpr int kAttnGroups = sizeof(T) == 4 && D <= 64 ? 2 : 1;
+
+// Goes over tiles [j, end) of 32 tokens.  T: the rows' type, TK: the tiles'.  NG
+// groups of NW waves, of which group grp takes the tiles j + grp, j + grp + NG, ..
+// (the same number of each; what lies behind the end is masked); group 0 has the
+// sums of all in the end.
 //
 // Step j: first half, the products S of tile j + 1 beside the first part of the
 // softmax of tile j; then tile j + 2 of the keys and j + 1 of the values have
@@ -106,8 +113,8 @@ __device__ __forceinline__ void scale_in_agprs(v16f& x, float f) {
   }
   asm volatile("" : "+a"(x));
 }
-template <typename T, typename TK, int D, int NW, class Stage>
-__device__ __forceinline__ void attn_walk(Stage& st, const Held<T, D> (&q)[D / 16], int j, int end, const AttnRows& rows,
+template <typename T, typename TK, int D, int NW, int NG, class Stage>
+__device__ __forceinline__ void attn_walk(Stage& st, int grp, const Held<T, D> (&q)[D / 16], int j, int end, const AttnRows& rows,
                                           float c, int lane, int* odd, AttnState<D>& a) {
   constexpr int BN = kAttnStep, KS = D / 16, ND = D / 32, AHEAD = sizeof(T) == 2 ? 4 : 2, TOP = KS / 4;
   using P = Plane<TK, D, BN>;
@@ -115,15 +122,20 @@ __device__ __forceinline__ void attn_walk(Stage& st, const Held<T, D> (&q)[D / 1
   // after another
   constexpr bool ONE = 6 * P::TILE > 152 * 1024;
   constexpr int REST = ONE ? 16 : P::TILE;
-  __shared__ __align__(1024) char kA[P::TILE], kB[REST], kC[REST], vA[P::TILE], vB[REST], vC[REST];
-  for (int e = threadIdx.x; e < D + 1; e += NW * 64) odd[e] = INT32_MAX;
+  __shared__ __align__(1024) char kA_[NG * P::TILE], kB_[NG * REST], kC_[NG * REST], vA_[NG * P::TILE], vB_[NG * REST], vC_[NG * REST];
+  char *kA = kA_ + grp * P::TILE, *vA = vA_ + grp * P::TILE;
+  char *kB = kB_ + grp * REST, *kC = kC_ + grp * REST, *vB = vB_ + grp * REST, *vC = vC_ + grp * REST;
+  for (int e = threadIdx.x; e < D + 1; e += NG * NW * 64) odd[e] = INT32_MAX;
   if (j >= end) {
     __syncthreads();
     return;
   }
+  const int j_0 = j, own = grp * BN;
+  end = j + (end - j + NG - 1) / NG;                               // steps, from here on
+  auto place = [&](int j) { return (j_0 + (j - j_0) * NG) * BN; };  // of group 0's tile
   auto clean = [&](char* vb, int j) {
-    if (j * BN + BN - 1 > rows.block_lo) {  // some place is masked for some row of the block
-      set_aside<TK, D, BN, NW * 64>(vb, j * BN, odd);
+    if (place(j) + NG * BN - 1 > rows.block_lo) {  // some place is masked for some row of the block
+      set_aside<TK, D, BN, NW * 64>(vb, place(j) + own, odd, threadIdx.x - grp * NW * 64);
       __syncthreads();
     }
   };
@@ -187,7 +199,7 @@ __device__ __forceinline__ void attn_walk(Stage& st, const Held<T, D> (&q)[D / 1
       s = zero16();
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) s = mma32(row_frag<TK, D, BN>(kA, 0, ks, lane), q[ks].get(), s);
-      hide(j * BN);
+      hide(place(j) + own);
       float top = -INFINITY;
 #pragma unroll
       for (int i = 0; i < 16; ++i) top = fmaxf(top, s[i]);
@@ -208,7 +220,7 @@ __device__ __forceinline__ void attn_walk(Stage& st, const Held<T, D> (&q)[D / 1
     // v0: values of tile j, k1 and v1: tile j + 1, k2: keys of tile j + 2; into k3 and
     // v2 go the next ones
     auto step = [&](char* v0, char* k1, char* v1, char* k2, char* v2, char* k3, int j) {
-      hide(j * BN);
+      hide(place(j) + own);
       sn = zero16();
       auto product = [&](int m) {
         if (m + AHEAD < KS) rf[m + AHEAD] = row_frag<TK, D, BN>(k1, 0, m + AHEAD, lane);
@@ -293,6 +305,27 @@ __device__ __forceinline__ void attn_walk(Stage& st, const Held<T, D> (&q)[D / 1
   }
   wait_loads();
   __syncthreads();
+  if constexpr (NG == 2) {  // through LDS: half of the sums in kA_, half in kB_
+    static_assert(NG * P::TILE >= D * NW * 64 && !ONE);
+    const int at = threadIdx.x & (NW * 64 - 1);
+    float *s0 = reinterpret_cast<float*>(kA_) + at, *s1 = reinterpret_cast<float*>(kB_) + at, *ml = reinterpret_cast<float*>(kC_) + at;
+    constexpr int H = D / 4;
+    if (grp == 1) {
+#pragma unroll
+      for (int i = 0; i < 2 * H; ++i) (i < H ? s0 + i * NW * 64 : s1 + (i - H) * NW * 64)[0] = a.acc[i / 16][i % 16];
+      ml[0] = a.m;
+      ml[NW * 64] = a.l;
+    }
+    __syncthreads();
+    if (grp == 1) return;
+    const float top = fmaxf(a.m, ml[0]);
+    const float f0 = top == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((a.m - top) * c);
+    const float f1 = top == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((ml[0] - top) * c);
+#pragma unroll
+    for (int i = 0; i < 2 * H; ++i) a.acc[i / 16][i % 16] = a.acc[i / 16][i % 16] * f0 + (i < H ? s0 + i * NW * 64 : s1 + (i - H) * NW * 64)[0] * f1;
+    a.m = top;
+    a.l = a.l * f0 + ml[NW * 64] * f1;
+  }
   a.l += other_half(a.l);
   if (odd[D] != INT32_MAX) {
 #pragma unroll

@@ -132,7 +132,7 @@ __global__ __launch_bounds__(256, (kAttnOcc<T, D>)) void k_attn_decode_wide(DecI
   t1 = t0 + sq.split < t1 ? t0 + sq.split : t1;
   CacheStage<D> st(io, sq, hk, static_cast<int>(t0 / BN));
   AttnState<D> a;
-  attn_walk<T, bf16_t, D, kAttnWaves>(st, q, static_cast<int>(t0 / BN), static_cast<int>((t1 + BN - 1) / BN), at, io.c, lane, odd, a);
+  attn_walk<T, bf16_t, D, kAttnWaves, 1>(st, 0, q, static_cast<int>(t0 / BN), static_cast<int>((t1 + BN - 1) / BN), at, io.c, lane, odd, a);
   if (!in) return;
   if (sq.splits == 1) {
     store_row<D>(static_cast<T*>(io.o) + (sq.q0 + tok) * io.ldo + static_cast<int64_t>(head) * D, a.acc, inverse_sum(a.l), lane);

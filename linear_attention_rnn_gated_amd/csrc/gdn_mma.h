@@ -240,8 +240,9 @@ __device__ __forceinline__ brsrc_t rows_rsrc(const void* x, int64_t at, int64_t 
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), static_cast<short>(0), bytes, 0x00020000);
 }
 
-// Rows of one head, ROWS at a time: a buffer over the tile's rows that there are.
-template <typename T, int D, int ROWS>
+// Rows of one head, ROWS at a time, of every NG-th such tile: a buffer over the
+// tile's rows that there are.
+template <typename T, int D, int ROWS, int NG = 1>
 struct RowTiles {
   const char* at;
   int64_t step;     // bytes to the next tile
@@ -249,13 +250,13 @@ struct RowTiles {
   brsrc_t rsrc;
   __device__ __forceinline__ RowTiles(const void* x, int64_t row, int64_t ld, int h, int rows)
       : at(static_cast<const char*>(x) + (row * ld + static_cast<int64_t>(h) * D) * sizeof(T)),
-        step(ROWS * ld * sizeof(T)), ld(static_cast<int>(ld * sizeof(T))), left(rows) {}
+        step(NG * ROWS * ld * sizeof(T)), ld(static_cast<int>(ld * sizeof(T))), left(rows) {}
   __device__ __forceinline__ void next() {
     const int rows = left < ROWS ? left : ROWS;
     const int bytes = rows > 0 ? (rows - 1) * ld + static_cast<int>(D * sizeof(T)) : 0;
     rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(at), static_cast<short>(0), bytes, 0x00020000);
     at += step;
-    left -= ROWS;
+    left -= NG * ROWS;
   }
 };
 
