@@ -156,7 +156,8 @@ struct GradIO {
   void* dv;
   float* stat;  // [H_q][T_q][2]: lse log2(e) and dO . o
   float* part;  // [parts][2][T_k][H_kv][D] fp32 sums for dk and dv, where parts > 1
-  int parts;    // that a group's heads are cut into
+  int cuts;     // that the queries of a head are cut into
+  int parts;    // that a group's heads and their queries are cut into
   int64_t lddo, lddq, lddk, lddv;
   float scale;
 };
@@ -315,14 +316,19 @@ __global__ __launch_bounds__(256, 1) void k_attn_dkv(GradIO g) {
   const int n = tile_seq(io.cu_k, io.N, BK, blockIdx.x / io.H_kv, &tile);
   x.sp = span_of(io.cu_q, io.cu_k, io.T_q, io.T_k, n);
   if (tile < 0 || tile * BK >= x.sp.Lk) return;
-  const int heads = (io.G + g.parts - 1) / g.parts;
-  x.h0 = blockIdx.y * heads;
+  const int heads = (io.G * g.cuts + g.parts - 1) / g.parts, cut = blockIdx.y % g.cuts;
+  x.h0 = blockIdx.y / g.cuts * heads;
   x.h1 = x.h0 + heads < io.G ? x.h0 + heads : io.G;
   x.j0 = tile * BK + wave * 32;
   x.key = x.j0 + (lane & 31);
   x.off = x.sp.Lk - x.sp.Lq;
   x.first = tile * BK - x.off > 0 ? (tile * BK - x.off) / BQ : 0;
   x.per = (x.sp.Lq + BQ - 1) / BQ - x.first;
+  if (g.cuts > 1) {
+    const int each = x.per > 0 ? (x.per + g.cuts - 1) / g.cuts : 0;
+    x.first += cut * each;
+    x.per = x.per - cut * each < each ? x.per - cut * each : each;
+  }
   const int steps = x.per > 0 && x.h1 > x.h0 ? x.per * (x.h1 - x.h0) : 0;
 
   Held<T, D> k[KS], v[DK ? KS : 1];
@@ -593,13 +599,19 @@ void launch_dkv(const GradIO& g, unsigned blocks, hipStream_t st) {
 // Parts that a group's heads are cut into for dk and dv: more where the blocks of
 // 128 keys, one a CU and the first of a sequence twice as long as the average,
 // would not fill the chip evenly.
-int dkv_parts(const gdn_attn_shape_t* s, int64_t T_k) {
+struct DkvParts {
+  int heads, cuts;
+  int all() const { return heads * cuts; }
+};
+DkvParts dkv_parts(const gdn_attn_shape_t* s, int64_t T_k) {
   const int G = s->H_q / s->H_kv;
   const int64_t blocks = (T_k + 127) / 128 * s->H_kv;
-  int parts = 1;
+  int parts = 1, cuts = 1;
   while (parts < G && blocks * parts < 1024) ++parts;
   const int heads = (G + parts - 1) / parts;
-  return (G + heads - 1) / heads;  // none without a head
+  parts = (G + heads - 1) / heads;  // none without a head
+  while (cuts < T_k / 512 && blocks * parts * cuts < 512) ++cuts;
+  return DkvParts{parts, cuts};
 }
 size_t stat_bytes(const gdn_attn_shape_t* s, int64_t T_q) {
   const size_t bytes = static_cast<size_t>(T_q) * s->H_q * 2 * sizeof(float);
@@ -669,7 +681,7 @@ int gdn_attn_prefill(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_
 
 size_t gdn_attn_workspace_bytes(const gdn_attn_shape_t* shape, int64_t T_q, int64_t T_k) {
   if (gdn::check_attn_shape(shape) != GDN_OK || T_q < 0 || T_k < 0 || T_q > INT32_MAX || T_k > INT32_MAX) return 0;
-  const int parts = dkv_parts(shape, T_k);
+  const int parts = dkv_parts(shape, T_k).all();
   const size_t sums = parts > 1 ? static_cast<size_t>(parts) * 2 * T_k * shape->H_kv * shape->d * sizeof(float) : 0;
   return stat_bytes(shape, T_q) + (sums + gdn::kAlign - 1) / gdn::kAlign * gdn::kAlign;
 }
@@ -691,7 +703,9 @@ int gdn_attn_bwd(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t* c
   g.a.o = const_cast<void*>(o); g.a.lse = const_cast<float*>(lse);
   g.dO = dO; g.dq = dq; g.dk = dk; g.dv = dv;
   g.stat = static_cast<float*>(ws);
-  g.parts = dkv_parts(shape, T_k);
+  const DkvParts cut = dkv_parts(shape, T_k);
+  g.cuts = cut.cuts;
+  g.parts = cut.all();
   g.part = g.parts > 1 ? g.stat + stat_bytes(shape, T_q) / sizeof(float) : nullptr;
   g.scale = shape->scale;
   hipStream_t st = static_cast<hipStream_t>(stream);
