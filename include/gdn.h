@@ -533,8 +533,8 @@ int gdn_rope_freqs(int32_t r, double base, const gdn_rope_scaling_t* scaling, fl
  *
  * A query that sees nothing (L_k < L_q) has o = 0 and lse = -inf.  Products and
  * sums are fp32; bf16 inputs go into the products as they are, and exp(s - max)
- * is rounded to bf16 there (not in its own sum), with fp32 inputs nothing is.  A
- * sequence's bits do not depend on the batch.
+ * is rounded to bf16 there (not in its own sum), with fp32 inputs nothing is.
+ * Forward, a sequence's bits do not depend on the batch.
  *
  * Rows as for gdn_qk_rotary: token t's heads are d elements each, one after
  * another, at q + t ldq (ld in elements; 0 = dense; a multiple of 8, at most 2^22).
@@ -574,7 +574,9 @@ size_t gdn_attn_workspace_bytes(const gdn_attn_shape_t* shape, int64_t T_q, int6
  *     dS_ij = p_ij (dO_i . v_j - dO_i . o_i),   dv_j = sum p_ij dO_i,
  *     dq_i = scale sum_j dS_ij k_j,   dk_j = scale sum dS_ij q_i,
  * the sums of dk and dv over the queries of all heads of the group.  Keys that no
- * query sees get 0.  No atomics: bitwise reproducible. */
+ * query sees get 0.  No atomics: bitwise reproducible, and T_q and T_k decide the
+ * parts that the sums are cut into.  p and dS go into the products in bf16 (bf16
+ * inputs) or as they are (fp32). */
 int gdn_attn_bwd(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t* cu_q,
                  const int32_t* cu_k, int64_t T_q, int64_t T_k, const void* q, int64_t ldq,
                  const void* k, int64_t ldk, const void* v, int64_t ldv, const void* o,

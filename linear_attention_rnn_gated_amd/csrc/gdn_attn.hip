@@ -80,7 +80,7 @@ __device__ __forceinline__ bool query_tile(const AttnIO& io, int wave, int lane,
   return true;
 }
 
-// Keys and values of one head as rows in memory: group grp's tiles.
+// Keys and values of one head as rows in memory, from tile `first` on every NG-th.
 template <typename T, int D, int BN, int NW, int NG>
 struct RowStage {
   using Move = Stager<T, D, BN, NW>;
@@ -88,9 +88,8 @@ struct RowStage {
   static constexpr int LOADS = Move::STEPS;
   RowTiles<T, D, BN, NG> tk, tv;
   Move sk, sv;
-  // from the sequence's first key on
-  __device__ __forceinline__ RowStage(const AttnIO& io, const Span& sp, int hk, int grp, int wave, int lane)
-      : tk(io.k, sp.k0 + grp * BN, io.ldk, hk, sp.Lk - grp * BN), tv(io.v, sp.k0 + grp * BN, io.ldv, hk, sp.Lk - grp * BN),
+  __device__ __forceinline__ RowStage(const AttnIO& io, const Span& sp, int hk, int first, int wave, int lane)
+      : tk(io.k, sp.k0 + first * BN, io.ldk, hk, sp.Lk - first * BN), tv(io.v, sp.k0 + first * BN, io.ldv, hk, sp.Lk - first * BN),
         sk(io.ldk, wave, lane), sv(io.ldv, wave, lane) {}
   __device__ __forceinline__ void next_k() { tk.next(); }
   __device__ __forceinline__ void next_v() { tv.next(); }
@@ -156,6 +155,8 @@ struct GradIO {
   void* dv;
   float* stat;  // [H_q][T_q][2]: lse log2(e) and dO . o
   float* part;  // [parts][2][T_k][H_kv][D] fp32 sums for dk and dv, where parts > 1
+  float* qpart;  // [qcuts][T_q][H_q][D] fp32 sums for dq, where qcuts > 1
+  int qcuts;    // parts that the keys of a query tile are cut into
   int cuts;     // that the queries of a head are cut into
   int parts;    // that a group's heads and their queries are cut into
   int64_t lddo, lddq, lddk, lddv;
@@ -191,17 +192,18 @@ __global__ __launch_bounds__((256 * kAttnGroups<T, D>), (kAttnOcc<T, D>)) void k
                     static_cast<uint32_t>(r * io.ldo * sizeof(T)) + col + 16 * ks * sizeof(T), dot);
     dot += other_half(dot);
     lse2 = x.row < x.sp.Lq ? io.lse[(x.sp.q0 + x.row) * io.H_q + x.hq] * kLog2e : 0.0f;
-    if (grp == 0 && x.row < x.sp.Lq && lane < 32) {
+    if (grp == 0 && blockIdx.y == 0 && x.row < x.sp.Lq && lane < 32) {
       float* s = g.stat + 2 * (static_cast<int64_t>(x.hq) * io.T_q + x.sp.q0 + x.row);
       s[0] = lse2;
       s[1] = dot;
     }
   }
-  RowStage<T, D, BN, NW, NG> st(io, x.sp, x.hk, grp, wave, lane);
+  const int all = x.last >= 0 ? x.last / (NG * BN) + 1 : 0, each = (all + g.qcuts - 1) / g.qcuts;
+  const int begin = blockIdx.y * each, end = begin + each < all ? begin + each : all;
+  RowStage<T, D, BN, NW, NG> st(io, x.sp, x.hk, begin * NG + grp, wave, lane);
   v16f acc[ND];
 #pragma unroll
   for (int d = 0; d < ND; ++d) acc[d] = zero16();
-  const int end = x.last >= 0 ? x.last / (NG * BN) + 1 : 0;
   auto step = [&](char* kb, char* vb, char* kn, char* vn, int j) {
     if constexpr (st.DIRECT) wait_loads();
     __syncthreads();
@@ -241,7 +243,7 @@ __global__ __launch_bounds__((256 * kAttnGroups<T, D>), (kAttnOcc<T, D>)) void k
       for (int d = 0; d < ND; ++d) in_agprs(acc[d]);
     }
   };
-  if (end > 0) {
+  if (begin < end) {
     st.load(kA, vA);
     if constexpr (!st.DIRECT) {
       st.finish_k(kA);
@@ -249,13 +251,13 @@ __global__ __launch_bounds__((256 * kAttnGroups<T, D>), (kAttnOcc<T, D>)) void k
     }
   }
   if constexpr (TWO) {
-    for (int j = 0; j < end; j += 2) {
+    for (int j = begin; j < end; j += 2) {
       step(kA, vA, kB, vB, j);
       if (j + 1 < end) step(kB, vB, kA, vA, j + 1);
       keep();
     }
   } else {
-    for (int j = 0; j < end; ++j) {
+    for (int j = begin; j < end; ++j) {
       step(kA, vA, kA, vA, j);
       keep();
     }
@@ -276,8 +278,13 @@ __global__ __launch_bounds__((256 * kAttnGroups<T, D>), (kAttnOcc<T, D>)) void k
 #pragma unroll
     for (int i = 0; i < 2 * H; ++i) acc[i / 16][i % 16] += (i < H ? s0 + i * 256 : s1 + (i - H) * 256)[0];
   }
-  if (x.row < x.sp.Lq)
-    store_row<D>(static_cast<T*>(g.dq) + (x.sp.q0 + x.row) * g.lddq + static_cast<int64_t>(x.hq) * D, acc, g.scale, lane);
+  if (x.row < x.sp.Lq) {
+    const int64_t row = x.sp.q0 + x.row;
+    if (g.qcuts == 1)
+      store_row<D>(static_cast<T*>(g.dq) + row * g.lddq + static_cast<int64_t>(x.hq) * D, acc, g.scale, lane);
+    else
+      store_row<D>(g.qpart + ((blockIdx.y * io.T_q + row) * io.H_q + x.hq) * D, acc, g.scale, lane);
+  }
 #endif
 }
 
@@ -568,22 +575,27 @@ __global__ __launch_bounds__(256, 1) void k_attn_dkv(GradIO g) {
 #endif
 }
 
-// dk and dv from the sums of each part of the group's heads, added in order.
+// Gradients from the fp32 sums of their parts, added in order.
+struct SumIO {
+  const float* part;  // [parts][T][width], `between` elements from one to the next
+  int64_t between, T, width, ld;
+  const int32_t* cu;  // [N + 1]
+  int parts, N;
+  void* out;
+};
+struct SumsIO { SumIO of[3]; };
 template <typename T>
-__global__ __launch_bounds__(256) void k_attn_dkv_sum(GradIO g, int D) {
-  const AttnIO& io = g.a;
-  const int64_t size = io.T_k * io.H_kv * D, e = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
-  int64_t end = io.cu_k[io.N];
-  end = end < 0 ? 0 : end > io.T_k ? io.T_k : end;
-  if (e >= end * io.H_kv * D) return;
-  const int64_t row = e / (io.H_kv * D), col = e - row * io.H_kv * D;
-#pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    v4f y = *reinterpret_cast<const v4f*>(g.part + w * size + e);
-    for (int i = 1; i < g.parts; ++i) y += *reinterpret_cast<const v4f*>(g.part + (2 * i + w) * size + e);
-    const float z[4] = {y[0], y[1], y[2], y[3]};
-    store4(static_cast<T*>(w ? g.dv : g.dk) + row * (w ? g.lddv : g.lddk) + col, z);
-  }
+__global__ __launch_bounds__(256) void k_attn_sum(SumsIO sums) {
+  const SumIO& io = sums.of[blockIdx.y];
+  const int64_t e = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  int64_t end = io.cu[io.N];
+  end = end < 0 ? 0 : end > io.T ? io.T : end;
+  if (e >= end * io.width) return;
+  const int64_t row = e / io.width, col = e - row * io.width;
+  v4f y = *reinterpret_cast<const v4f*>(io.part + e);
+  for (int i = 1; i < io.parts; ++i) y += *reinterpret_cast<const v4f*>(io.part + i * io.between + e);
+  const float z[4] = {y[0], y[1], y[2], y[3]};
+  store4(static_cast<T*>(io.out) + row * io.ld + col, z);
 }
 
 // ---- host side ----------------------------------------------------------------
@@ -612,6 +624,12 @@ DkvParts dkv_parts(const gdn_attn_shape_t* s, int64_t T_k) {
   parts = (G + heads - 1) / heads;  // none without a head
   while (cuts < T_k / 512 && blocks * parts * cuts < 512) ++cuts;
   return DkvParts{parts, cuts};
+}
+int dq_cuts(const gdn_attn_shape_t* s, int64_t T_q) {
+  const int64_t blocks = (T_q + 127) / 128 * s->H_q;
+  int cuts = 1;
+  while (cuts < T_q / 512 && blocks * cuts < 512) ++cuts;
+  return cuts;
 }
 size_t stat_bytes(const gdn_attn_shape_t* s, int64_t T_q) {
   const size_t bytes = static_cast<size_t>(T_q) * s->H_q * 2 * sizeof(float);
@@ -681,9 +699,10 @@ int gdn_attn_prefill(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_
 
 size_t gdn_attn_workspace_bytes(const gdn_attn_shape_t* shape, int64_t T_q, int64_t T_k) {
   if (gdn::check_attn_shape(shape) != GDN_OK || T_q < 0 || T_k < 0 || T_q > INT32_MAX || T_k > INT32_MAX) return 0;
-  const int parts = dkv_parts(shape, T_k).all();
-  const size_t sums = parts > 1 ? static_cast<size_t>(parts) * 2 * T_k * shape->H_kv * shape->d * sizeof(float) : 0;
-  return stat_bytes(shape, T_q) + (sums + gdn::kAlign - 1) / gdn::kAlign * gdn::kAlign;
+  const int parts = dkv_parts(shape, T_k).all(), cuts = dq_cuts(shape, T_q);
+  const size_t dkv = parts > 1 ? static_cast<size_t>(parts) * 2 * T_k * shape->H_kv : 0;
+  const size_t dq = cuts > 1 ? static_cast<size_t>(cuts) * T_q * shape->H_q : 0;
+  return stat_bytes(shape, T_q) + ((dkv + dq) * shape->d * sizeof(float) + gdn::kAlign - 1) / gdn::kAlign * gdn::kAlign;
 }
 
 int gdn_attn_bwd(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t* cu_q, const int32_t* cu_k, int64_t T_q,
@@ -706,25 +725,35 @@ int gdn_attn_bwd(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t* c
   const DkvParts cut = dkv_parts(shape, T_k);
   g.cuts = cut.cuts;
   g.parts = cut.all();
-  g.part = g.parts > 1 ? g.stat + stat_bytes(shape, T_q) / sizeof(float) : nullptr;
+  g.part = g.stat + stat_bytes(shape, T_q) / sizeof(float);
+  g.qcuts = dq_cuts(shape, T_q);
+  g.qpart = g.part + (g.parts > 1 ? g.parts * 2 * T_k * wk : 0);
   g.scale = shape->scale;
   hipStream_t st = static_cast<hipStream_t>(stream);
   return attn_dispatch(shape, [&]<typename T, int D>() {
     const int64_t nq = tile_slots(T_q, n_seqs, 128) * g.a.H_q, nk = tile_slots(T_k, n_seqs, 128) * g.a.H_kv;
     constexpr int threads = 256 * kAttnGroups<T, D>;
-    if (nq * threads >= gdn::kLaunchThreads || nk * 256 >= gdn::kLaunchThreads / g.parts) return static_cast<int>(GDN_ERR_UNSUPPORTED);
+    if (nq * threads >= gdn::kLaunchThreads / g.qcuts || nk * 256 >= gdn::kLaunchThreads / g.parts) return static_cast<int>(GDN_ERR_UNSUPPORTED);
     if (T_q > 0) {
       Timed t_("k_attn_dq", st);
-      hipLaunchKernelGGL((k_attn_dq<T, D>), dim3(static_cast<unsigned>(nq)), dim3(threads), 0, st, g);
+      hipLaunchKernelGGL((k_attn_dq<T, D>), dim3(static_cast<unsigned>(nq), g.qcuts), dim3(threads), 0, st, g);
     }
     if (T_k > 0) {
       Timed t_("k_attn_dkv", st);
       launch_dkv<T, D>(g, static_cast<unsigned>(nk), st);
     }
+    SumsIO sums{};
+    int n = 0;
     if (T_k > 0 && g.parts > 1) {
-      Timed t_("k_attn_dkv_sum", st);
-      const int64_t blocks = (T_k * g.a.H_kv * D / 4 + 255) / 256;
-      hipLaunchKernelGGL(k_attn_dkv_sum<T>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, g, D);
+      const int64_t size = T_k * wk;
+      sums.of[n++] = SumIO{g.part, 2 * size, T_k, wk, g.lddk, g.a.cu_k, g.parts, n_seqs, dk};
+      sums.of[n++] = SumIO{g.part + size, 2 * size, T_k, wk, g.lddv, g.a.cu_k, g.parts, n_seqs, dv};
+    }
+    if (g.qcuts > 1) sums.of[n++] = SumIO{g.qpart, T_q * wq, T_q, wq, g.lddq, g.a.cu_q, g.qcuts, n_seqs, dq};
+    if (n > 0) {
+      Timed t_("k_attn_sum", st);
+      const int64_t size = g.qcuts > 1 && T_q * wq > T_k * wk ? T_q * wq : T_k * wk;
+      hipLaunchKernelGGL(k_attn_sum<T>, dim3(static_cast<unsigned>((size / 4 + 255) / 256), n), dim3(256), 0, st, sums);
     }
     return static_cast<int>(hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_HIP);
   });

@@ -148,6 +148,26 @@ def test_keys_and_queries_of_different_lengths(t, d):
     assert not g["dk"][275:284].any() and not g["dv"][275:284].any()  # keys that no query sees
 
 
+@pytest.mark.parametrize("t,d,Hq,Hkv", [("bf16", 64, 2, 1), ("bf16", 128, 2, 2), ("bf16", 256, 3, 1), ("f32", 64, 4, 2),
+                                        ("f32", 128, 1, 1), ("f32", 256, 2, 1)])
+def test_gradient_in_parts(t, d, Hq, Hkv):
+    """Few heads of many tokens: the tiles of a head are cut into parts, some of them
+    empty, and rows behind the last sequence stay as they were."""
+    p = make([1030, 0, 3, 391], Hq, Hkv, d, t, seed=23, sliced=True, lens_k=[700, 5, 33, 800])
+    T, Tk = 1424, 1538
+    assert B.attn_workspace_bytes(p["shape"], T, Tk) >= 4 * d * (2 * T * Hq + 2 * 2 * Tk * Hkv)
+    o, lse = forward(p)
+    g = backward(p, o, lse)
+    check_all(p, o, lse, g)
+    again = backward(p, o, lse)
+    assert all(torch.equal(g[k], again[k]) for k in g)
+    less = dict(p, cu=cu_of(p["lens"][:3]).cuda(), cu_k=cu_of(p["lens_k"][:3]).cuda())
+    out = {k: torch.full_like(g[k], 5.0) for k in g}
+    backward(less, o, lse, out=out)
+    for key, end in (("dq", 1033), ("dk", 738), ("dv", 738)):
+        assert torch.equal(out[key][:end], g[key][:end]) and (out[key][end:] == 5).all(), key
+
+
 @pytest.mark.parametrize("size", [1e-3, 30.0])
 def test_flat_and_peaked_rows(size):
     for t in ("bf16", "f32"):
