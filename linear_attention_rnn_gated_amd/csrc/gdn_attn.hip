@@ -299,8 +299,9 @@ struct KeyTile {
   int first, per;   // first query tile, tiles a head
 };
 
-// WHAT: 3 both gradients, 1 dk, 2 dv (rows of 512 bytes and more, whose two sums
-// and operands together pass the registers of a wave).
+// WHAT: 3 both gradients, 1 dk, 2 dv (heads of 256, whose two sums and operands
+// together pass the registers of a wave: 4x4096 tokens, 16 and 2 heads, bf16: 2.84 ms
+// in two, 14.8 in one; 4x1024, heads of 128, fp32: 388 us in two, 282 in one).
 //
 // One wave a SIMD (two gradients' sums and two operands take 192 of its registers
 // at d = 128), so a wave has to hide its own latencies: the products S and dP of
@@ -602,7 +603,7 @@ __global__ __launch_bounds__(256) void k_attn_sum(SumsIO sums) {
 
 template <typename T, int D>
 void launch_dkv(const GradIO& g, unsigned blocks, hipStream_t st) {
-  constexpr bool split = D * sizeof(T) >= 512;
+  constexpr bool split = D >= 256;
   const dim3 grid(blocks, g.parts);
   hipLaunchKernelGGL((k_attn_dkv<T, D, split ? 1 : 3>), grid, dim3(256), 0, st, g);
   if constexpr (split) hipLaunchKernelGGL((k_attn_dkv<T, D, 2>), grid, dim3(256), 0, st, g);

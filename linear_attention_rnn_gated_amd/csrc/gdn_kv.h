@@ -55,16 +55,26 @@ struct DecIO {
   int N, H_q, H_kv, G, max_len;
   float c;
 };
-constexpr int kSplit = 512;    // tokens a split
-constexpr int kRowsSplit = 256;  // rows for which they are that many
-constexpr int kWideRows = 64;    // a sequence of so many rows goes to the wide kernel
+constexpr int kSplit = 512;        // tokens a split
+constexpr int kLongLen = 4096;     // cached tokens over which the narrow kernel takes twice as many
+constexpr int kRowsSplit = 256;    // rows for which the wide one's are that many
+// A sequence of so many rows goes to the wide kernel: 32 sequences of 4000 cached
+// tokens, 8 heads of 128: 32 rows each 144 us there and 156 in the narrow one, 64 rows
+// 173 (172), 124 rows 239 (300); 2 heads of 256: 32 rows 95 (144).  The other way:
+// one token of 32 heads that share one key head, 24 (18).
+constexpr int kWideRows = 32;
 // Tiles of 16 rows that the narrow one has for a sequence.
 __host__ __device__ inline int narrow_tiles(bool packed, int G) { return (packed ? kWideRows : G + 15) / 16; }
 
 // Tokens a split of a sequence with `rows` rows a head: more where there are rows
 // enough to go round.  A function of the sequence alone, so that its bits do not
-// depend on the batch.
-__host__ __device__ inline int64_t split_tokens(int64_t rows) { return kSplit * ((rows + kRowsSplit - 1) / kRowsSplit); }
+// depend on the batch.  One new token, 64 sequences of 128 to 8192: 116 us (all with
+// 1024 tokens 112, with 512 123, with 256 134), four of 4000: 16 us with 512, 24 with
+// 1024.  Eight sequences' 64 to 500 new tokens: 360 us with 512 for 256 rows, 391 for
+// 512 rows, 380 with 1024 for 256, 609 with 256.
+__host__ __device__ inline int64_t split_tokens(int64_t rows, int64_t len) {
+  return rows < kWideRows ? (len > kLongLen ? 2 * kSplit : kSplit) : kSplit * ((rows + kRowsSplit - 1) / kRowsSplit);
+}
 
 struct DecSeq {
   int64_t q0;
@@ -95,7 +105,7 @@ __device__ __forceinline__ DecSeq dec_seq(const DecIO& io, int n) {
   len = len < 0 ? 0 : len > io.max_len ? io.max_len : len;
   s.Lk = static_cast<int>(len);
   s.rows = static_cast<int64_t>(s.Lq) * io.G;
-  s.split = split_tokens(s.rows > 0 ? s.rows : 1);
+  s.split = split_tokens(s.rows > 0 ? s.rows : 1, len);
   s.splits = static_cast<int>((s.Lk + s.split - 1) / s.split);
   if (s.splits < 1) s.splits = 1;
   return s;

@@ -627,8 +627,9 @@ int64_t kv_slots(const KvIO& io) { return io.cu ? io.T / kBlk + 2 * static_cast<
 
 // Where partial results stand: for every query row as many as the longest cache has
 // splits, or one, and for every sequence as many as make up for it: a sequence of r
-// rows has at most 1 + (most - 1) / ceil(r / kRowsSplit) splits, and so at most r +
-// kRowsSplit (most - 1) partial rows.  The smaller of the two.
+// rows has at most 1 + (most - 1) / ceil(r / kRowsSplit) splits (of at least kSplit
+// tokens), and so at most r + kRowsSplit (most - 1) partial rows.  The smaller of the
+// two.
 void decode_layout(int64_t N, int64_t T, int32_t G, int64_t max_len, int64_t* mul, int64_t* extra) {
   int64_t most = (max_len + kSplit - 1) / kSplit;
   most = most > 1 ? most : 1;
@@ -729,22 +730,24 @@ int gdn_attn_decode(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t
     const bool wide = cu_seqlens ? all >= kWideRows : G >= kWideRows, narrow = cu_seqlens ? n_seqs > 1 || !wide : !wide;
     const int64_t tn = int64_t{n_seqs} * narrow_tiles(cu_seqlens != nullptr, G);
     const int64_t tw = cu_seqlens ? all / kAttnRows + n_seqs : int64_t{n_seqs} * ((G + kAttnRows - 1) / kAttnRows);
-    const int64_t y = splits > 0 ? splits : 1;
-    if ((narrow && tn * io.H_kv * 256 >= gdn::kLaunchThreads / y) || (wide && tw * io.H_kv * 256 >= gdn::kLaunchThreads / y) ||
+    const int64_t y = splits > 0 ? splits : 1, few = kLongLen / kSplit;
+    const int64_t yn = y <= few ? y : (y + 1) / 2 > few ? (y + 1) / 2 : few;
+    if ((narrow && tn * io.H_kv * 256 >= gdn::kLaunchThreads / yn) || (wide && tw * io.H_kv * 256 >= gdn::kLaunchThreads / y) ||
         n_tokens * io.H_q >= gdn::kLaunchThreads / 1024)
       return static_cast<int>(GDN_ERR_UNSUPPORTED);
     if (narrow) {
       Timed t_("k_attn_decode", st);
-      hipLaunchKernelGGL((k_attn_decode<T, D>), dim3(static_cast<unsigned>(tn * io.H_kv), static_cast<unsigned>(y)), dim3(256), 0, st, io);
+      hipLaunchKernelGGL((k_attn_decode<T, D>), dim3(static_cast<unsigned>(tn * io.H_kv), static_cast<unsigned>(yn)), dim3(256), 0, st, io);
     }
     if (wide) {
       const int rc = launch_decode_wide(shape, io, tw, y, st);
       if (rc != GDN_OK) return rc;
     }
-    if (splits > 1) {
+    const int64_t most = wide ? y : yn;  // splits of a sequence
+    if (most > 1) {
       Timed t_("k_attn_join", st);
       const int64_t items = n_tokens * io.H_q, per = 1024 / D;
-      if (splits <= kJoin)
+      if (most <= kJoin)
         hipLaunchKernelGGL((k_attn_join<T, D, 1>), dim3(static_cast<unsigned>((items + per - 1) / per)), dim3(256), 0, st, io);
       else
         hipLaunchKernelGGL((k_attn_join<T, D, kJoin>), dim3(static_cast<unsigned>(items)), dim3(D / 4 * kJoin), 0, st, io);
