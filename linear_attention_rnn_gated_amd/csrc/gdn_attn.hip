@@ -117,6 +117,9 @@ __device__ __forceinline__ void load_rows(const void* x, int64_t at, int64_t ld,
   for (int ks = 0; ks < D / 16; ++ks) y[ks].load(r, col + 16 * ks * sizeof(T));
 }
 
+// 128 rows a block: a tile of keys and values is read from L2 once for them (8x4096,
+// 32 and 8 heads: 454 MB from memory where q, k and v have 403).  One prompt of 128
+// tokens, 16 heads of 256, is 16 blocks: 16 us, the launch and four steps' latencies.
 template <typename T, int D>
 __global__ __launch_bounds__((256 * kAttnGroups<T, D>), (kAttnOcc<T, D>)) void k_attn_fwd(AttnIO io) {
 #ifdef GDN_DEVICE_PASS
@@ -146,7 +149,16 @@ __global__ __launch_bounds__((256 * kAttnGroups<T, D>), (kAttnOcc<T, D>)) void k
 // dO . o are then one number each) and keeps those two numbers for the second.
 // k_attn_dkv goes over the queries of all heads of the group for 32 keys a wave,
 // with S and dP in the other orientation (a key per lane), so that P and dS are
-// right operands of dV^T = dO^T P and dK^T = Q^T dS as they stand.
+// right operands of dV^T = dO^T P and dK^T = Q^T dS as they stand.  S and dP are thus
+// formed twice (seven products where five would do), which is cheaper than adding dq
+// up in memory and keeps its order.
+//
+// 8x4096 tokens, 32 and 8 heads of 128, bf16: dq 1.65 ms (three products, 1000
+// TFLOP/s), dkv 2.58 ms (four, 850 TFLOP/s), bound by the matrix cores (54% and 46% of
+// the cycles, at 1.9 GHz).  P and dS of bf16 rows are rounded to bf16 for their
+// products, 2^-8 of each: with the outputs' own rounding and that of o within dO . o,
+// dq is 2.5e-3 off (norms), where rounding the output alone is 1.7e-3.  In two parts
+// they would take a third more products.  fp32 rows' are taken in three parts.
 struct GradIO {
   AttnIO a;  // o: the forward's output, read
   const void* dO;
@@ -611,7 +623,11 @@ void launch_dkv(const GradIO& g, unsigned blocks, hipStream_t st) {
 
 // Parts that a group's heads are cut into for dk and dv: more where the blocks of
 // 128 keys, one a CU and the first of a sequence twice as long as the average,
-// would not fill the chip evenly.
+// would not fill the chip evenly (4x4096, 16 and 2 heads of 256: 2.84 ms in four, 3.15
+// in two); where that does not fill it either, the queries of a head as well (2048
+// tokens, 4 heads of 128: 35 us + 7 for their sums in four, 68 in one; 4096 tokens, 4
+// heads and 1: 90 + 14 in twelve, 120 + 28 in twenty-four, 132 + 6 in four).  For dq the
+// keys of a query tile (4096 tokens, 4 heads: 115 us in one, 54 in four).
 struct DkvParts {
   int heads, cuts;
   int all() const { return heads * cuts; }

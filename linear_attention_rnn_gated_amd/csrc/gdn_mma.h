@@ -5,7 +5,8 @@
 // 32][8 (l / 32) + j] and B[8 (l / 32) + j][l % 32], j = 0..7, and C's rows 8 (i /
 // 4) + 4 (l / 32) + i % 4, i = 0..15, of column l % 32: v_mfma_f32_32x32x16_bf16,
 // which sums in fp32.  fp32 operands are three bf16 parts each and take six of them,
-// 192 cycles where v_mfma_f32_32x32x2_f32 would take 512.
+// 192 cycles where v_mfma_f32_32x32x2_f32 would take 512 (forward and gradient of 3830
+// tokens, 6 heads of 64: 1238 us with those, 431 in parts, both as first built).
 //
 // A tile in LDS is rows of RB bytes in 16-byte pieces; piece c of row r stands at
 // c ^ swizzle(r), so that neither the reads along rows (32 rows, one piece each)
