@@ -605,6 +605,41 @@ def test_a_long_cache():
     assert torch.equal(*mid)  # joined one way and the other
 
 
+@pytest.mark.parametrize("Hq,Hkv,d,t", [(2, 1, 64, "bf16"), (4, 1, 128, "f32"), (33, 1, 64, "bf16"), (32, 1, 64, "f32")])
+def test_lengths_around_a_split(Hq, Hkv, d, t):
+    """One token over lengths at and beside the ends of splits, and where splits grow."""
+    lens = [511, 512, 513, 4095, 4096, 4097, 5121, 1]
+    pool = Pool(Hq, Hkv, d, t, 128, lens, seed=5)
+    pool.write(pool.rows(sum(lens)), pool.rows(sum(lens)), lens, [0] * len(lens))
+    q = pool.queries(len(lens))
+    o, lse = B.gdn_attn_decode(pool.shape, q, pool.cache, pool.dev_table, i32(lens), max(lens), want_lse=True)
+    decode_check(pool, q, [1] * len(lens), lens, o, lse)
+    for n in range(len(lens)):
+        one = B.gdn_attn_decode(pool.shape, q[n:n + 1], pool.cache, pool.dev_table[n:n + 1], i32(lens[n:n + 1]), lens[n])
+        assert torch.equal(one[0], o[n]), n
+    o2 = B.gdn_attn_decode(pool.shape, q, pool.cache, pool.dev_table, i32(lens), 2 * max(lens),
+                           cu_seqlens=cu_of([1] * len(lens)).cuda())
+    assert torch.equal(o, o2)
+
+
+@pytest.mark.parametrize("G,d,t", [(1, 64, "bf16"), (4, 128, "bf16"), (8, 256, "f32")])
+def test_rows_around_a_kernels_limit(G, d, t):
+    """31, 32, 33, 128, 256 and 264 rows a sequence over caches of several splits."""
+    new = [max(1, r // G) for r in (31, 32, 33, 128, 256, 264)]
+    lens = [1300 + 7 * n for n in new]
+    pool = Pool(G, 1, d, t, 64, lens, seed=6)
+    pool.write(pool.rows(sum(lens)), pool.rows(sum(lens)), lens, [0] * len(lens))
+    q, cu = pool.queries(sum(new)), cu_of(new).cuda()
+    o, lse = B.gdn_attn_decode(pool.shape, q, pool.cache, pool.dev_table, i32(lens), max(lens), cu_seqlens=cu, want_lse=True)
+    decode_check(pool, q, new, lens, o, lse)
+    at = 0
+    for n, r in enumerate(new):
+        one = B.gdn_attn_decode(pool.shape, q[at:at + r], pool.cache, pool.dev_table[n:n + 1], i32(lens[n:n + 1]), lens[n] + 600,
+                                cu_seqlens=cu_of([r]).cuda())
+        assert torch.equal(one, o[at:at + r]), n
+        at += r
+
+
 def test_decode_captured_in_a_graph():
     """Write and attend in one graph; the lengths grow between replays."""
     lens = [600, 33, 1, 1000]
