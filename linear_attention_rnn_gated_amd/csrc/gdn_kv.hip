@@ -736,9 +736,10 @@ int gdn_attn_decode(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t
   hipStream_t st = static_cast<hipStream_t>(stream);
   return kv_dispatch(shape, [&]<typename T, int D>() {
     // what a sequence's rows are decides who takes it; a kernel that none of them
-    // can need is not launched
+    // can need is not launched.  Packed, a sequence may have anything from no rows to
+    // all of them, one sequence too: only the device's cu_seqlens says how many.
     const int64_t all = n_tokens * G;
-    const bool wide = cu_seqlens ? all >= kWideRows : G >= kWideRows, narrow = cu_seqlens ? n_seqs > 1 || !wide : !wide;
+    const bool wide = (cu_seqlens ? all : G) >= kWideRows, narrow = G < kWideRows;
     const int64_t tn = int64_t{n_seqs} * narrow_tiles(cu_seqlens != nullptr, G);
     const int64_t tw = cu_seqlens ? all / kAttnRows + n_seqs : int64_t{n_seqs} * ((G + kAttnRows - 1) / kAttnRows);
     const int64_t y = splits > 0 ? splits : 1, few = kLongLen / kSplit;
