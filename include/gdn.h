@@ -614,7 +614,8 @@ typedef struct {
  * the new one (exact, but for codes that become subnormal, which are rounded
  * again); places behind the written ones are left as they are and hold nothing.
  * Writing the same tokens again changes nothing.  No two sequences may write to
- * one page, and none may name a page twice where it writes. */
+ * one page, and none may name a page twice where it writes; one without new tokens
+ * touches no page, whatever its start. */
 int gdn_kv_write(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t* cu_seqlens,
                  const int32_t* start, int64_t T, const void* k, int64_t ldk, const void* v,
                  int64_t ldv, const gdn_kv_cache_t* cache, const int32_t* block_table,

@@ -53,7 +53,9 @@ __device__ __forceinline__ bool kv_item(const KvIO& io, int h, KvItem* it) {
   }
   const int64_t first = io.start ? (io.start[n] > 0 ? io.start[n] : 0) : 0, end = first + (c1 - c0);
   const int64_t b = first / kBlk + local;
-  if (local < 0 || b * kBlk >= end || b >= (int64_t{1} << 30)) return false;
+  // a sequence without tokens has no block, be its start in the middle of one: another
+  // may be writing there
+  if (local < 0 || end <= first || b * kBlk >= end || b >= (int64_t{1} << 30)) return false;
   it->blk = io.pages.block(n, io.H_kv, h, static_cast<uint32_t>(b));
   if (it->blk < 0) return false;
   it->lo = static_cast<int>(first > b * kBlk ? first - b * kBlk : 0);

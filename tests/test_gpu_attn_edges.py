@@ -66,3 +66,46 @@ def test_a_captured_chunk_that_gets_shorter():
         torch.cuda.synchronize()
         assert (out[real:] == 3).all(), real
         decode_check(pool, q, [real], [L], out[:real], lse[:real], f"{real} tokens")
+
+
+def contents(cache):
+    return [x.view(torch.uint8).clone() for x in cache.tensors()]
+
+
+@pytest.mark.parametrize("t,d", [("bf16", 64), ("bf16", 128), ("bf16", 256), ("f32", 128)])
+@pytest.mark.parametrize("scale", [2.0 ** -120, 0.0, NAN, -1.0])
+def test_a_sequence_without_new_tokens_writes_nothing(t, d, scale):
+    """Whatever stands where its next token would go."""
+    pool = Pool(4, 2, d, t, 64, [100, 100, 100], seed=d)
+    pool.cache.k_scale.fill_(scale)
+    pool.cache.v_scale.fill_(scale)
+    before = contents(pool.cache)
+    none = pool.rows(0)
+    B.gdn_kv_write(pool.shape, none, none, pool.cache, pool.dev_table, cu_seqlens=cu_of([0, 0, 0]).cuda(),
+                   start=i32([40, 31, 1]))
+    rows = pool.rows(7)  # rows behind the last sequence: none of them has one
+    B.gdn_kv_write(pool.shape, rows, rows, pool.cache, pool.dev_table, cu_seqlens=cu_of([0, 0, 0]).cuda(),
+                   start=i32([33, 95, 64]))
+    assert all(torch.equal(a, b) for a, b in zip(before, contents(pool.cache)))
+    out = [torch.full((7, 2, d), 9.0, dtype=DT[t], device="cuda") for _ in range(2)]
+    B.gdn_kv_read(pool.shape, pool.cache, pool.dev_table, cu_of([0, 0, 0]).cuda(), 7, start=i32([40, 31, 1]),
+                  k_out=out[0], v_out=out[1])
+    assert all((x == 9).all() for x in out)
+
+
+def test_an_idle_sequence_may_name_a_page_that_another_writes():
+    """As an idle slot with a stale row of the table does, or a sequence that shares a prefix."""
+    pool = Pool(4, 2, 128, "bf16", 64, [100] * 8, seed=2)
+    pool.write(pool.rows(8 * 40), pool.rows(8 * 40), [40] * 8, [0] * 8)
+    table = pool.dev_table.repeat(9, 1)  # eight idle copies of every sequence
+    for r in range(4):
+        at, n = 40 + 3 * r, 9 * 8
+        lens, start = [0] * n, [at - r] * n
+        for i in range(8):
+            lens[8 * r + i], start[8 * r + i] = 3, at
+        k, v = pool.rows(24, 10.0 ** r), pool.rows(24, 0.1 ** r)  # scales grow on one side
+        B.gdn_kv_write(pool.shape, k, v, pool.cache, table, cu_seqlens=cu_of(lens).cuda(), start=i32(start))
+        for i in range(8):
+            pool.k.write(np64(k[3 * i:3 * i + 3]), pool.table[i], at)
+            pool.v.write(np64(v[3 * i:3 * i + 3]), pool.table[i], at)
+        pool.check()
