@@ -56,7 +56,9 @@ struct CacheStage {
     page = io.pages.id(sq.n, next);
   }
   __device__ __forceinline__ bool gap() const { return !there[0]; }
-  // Without a page: block 0 is read, and not used.
+  // Without a page: block 0 is read, and not used.  Its scores are masked whatever they
+  // are; its values' scale may be NaN, where nothing was written yet, and zeros for
+  // codes times that would be, so finish_v takes 1.
   __device__ __forceinline__ void next_k() {
     b1 = b0;
     b0 = io.pages.at(page, place, io.H_kv, hk);
@@ -83,7 +85,7 @@ struct CacheStage {
       x[i] = *reinterpret_cast<const u32x4*>(codes + (blk < 0 ? 0 : blk) * (kBlk * D) + (i * 256 + threadIdx.x) * 16);
   }
   __device__ __forceinline__ void finish_k(char* kb) const { store(kb, k, ks, INT32_MAX); }
-  __device__ __forceinline__ void finish_v(char* vb) const { store(vb, v, vs, rows); }
+  __device__ __forceinline__ void finish_v(char* vb) const { store(vb, v, rows > 0 ? vs : 1.0f, rows); }
   static __device__ __forceinline__ void store(char* lds, const u32x4* x, float scale, int rows) {
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {

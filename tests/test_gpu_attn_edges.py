@@ -109,3 +109,31 @@ def test_an_idle_sequence_may_name_a_page_that_another_writes():
             pool.k.write(np64(k[3 * i:3 * i + 3]), pool.table[i], at)
             pool.v.write(np64(v[3 * i:3 * i + 3]), pool.table[i], at)
         pool.check()
+
+
+def without_page_0(pool):
+    """Moves what stands in page 0 to a page that no sequence has."""
+    used = set(pool.table.ravel().tolist())
+    free = next(p for p in range(1, pool.cache.pages) if p not in used)
+    pool.table[pool.table == 0] = free
+    pool.dev_table.copy_(torch.from_numpy(pool.table))
+
+
+@pytest.mark.parametrize("scale", [NAN, INF, 0.0])
+@pytest.mark.parametrize("d,t,new", [(64, "bf16", 100), (128, "bf16", 40), (256, "bf16", 64), (64, "f32", 50),
+                                     (128, "f32", 40), (256, "f32", 40), (128, "bf16", 3), (64, "f32", 1)])
+def test_holes_beside_an_unwritten_page(d, t, new, scale):
+    """Blocks without a page, that all rows see and that some see, while page 0 of the pool holds nothing yet."""
+    kv = [200, 333]
+    pool = Pool(4, 2, d, t, 32, kv, seed=d)
+    without_page_0(pool)
+    pool.write(pool.rows(sum(kv)), pool.rows(sum(kv)), kv, [0, 0])
+    pool.cache.k_scale[0] = scale
+    pool.cache.v_scale[0] = scale
+    pool.table[1, 2] = pool.table[1, 9] = -1
+    pool.table[0, 0] = pool.cache.pages
+    pool.dev_table.copy_(torch.from_numpy(pool.table))
+    q = pool.queries(2 * new)
+    o, lse = B.gdn_attn_decode(pool.shape, q, pool.cache, pool.dev_table, i32(kv), 400, cu_seqlens=cu_of([new] * 2).cuda(),
+                               want_lse=True)
+    decode_check(pool, q, [new] * 2, kv, o, lse)
