@@ -769,7 +769,8 @@ int gdn_attn_bwd(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t* c
     if (g.qcuts > 1) sums.of[n++] = SumIO{g.qpart, T_q * wq, T_q, wq, g.lddq, g.a.cu_q, g.qcuts, n_seqs, dq};
     if (n > 0) {
       Timed t_("k_attn_sum", st);
-      const int64_t size = g.qcuts > 1 && T_q * wq > T_k * wk ? T_q * wq : T_k * wk;
+      int64_t size = 0;  // the largest that there is; what is cut has under 2^17 rows times heads
+      for (int i = 0; i < n; ++i) size = sums.of[i].T * sums.of[i].width > size ? sums.of[i].T * sums.of[i].width : size;
       hipLaunchKernelGGL(k_attn_sum<T>, dim3(static_cast<unsigned>((size / 4 + 255) / 256), n), dim3(256), 0, st, sums);
     }
     return static_cast<int>(hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_HIP);

@@ -51,3 +51,24 @@ def test_packed_rows_may_be_fewer_than_the_buffer(record, Hq, Hkv, n, T, max_len
     assert ("k_attn_decode" in [k for k, *_ in launches]) == (Hq // Hkv < 32)
     assert ("k_attn_decode_wide" in [k for k, *_ in launches]) == (T * (Hq // Hkv) >= 32)
     assert ("k_attn_join" in [k for k, *_ in launches]) == (max_len > 512)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,t,n,Tq,Tk,cut", [
+    (8, 8, 128, BF16, 1, 1024, 20_000_000, "q"),   # a few queries over very many keys: the keys' gradients are not cut
+    (8, 8, 128, BF16, 1, 1024, 30_000, "q"),
+    (4, 1, 64, F32, 3, 1030, 1538, "both"),
+    (64, 2, 256, BF16, 2, 100_000, 700, "k"),
+    (32, 8, 128, BF16, 8, 32768, 32768, "none"),
+])
+def test_the_gradients_sums(record, Hq, Hkv, d, t, n, Tq, Tk, cut):
+    """Only what was cut into parts is summed, over a grid of its own size."""
+    launches, rc = record("bwd", Hq, Hkv, d, t, n, Tq, Tk)
+    assert rc == B.GDN_OK
+    grids = {k: (x, y) for k, x, y, _ in launches}
+    assert (grids["k_attn_dq"][1] > 1) == (cut in ("q", "both"))
+    assert (grids["k_attn_dkv"][1] > 1) == (cut in ("k", "both"))
+    sizes = {"q": [Tq * Hq], "k": [Tk * Hkv] * 2, "both": [Tq * Hq] + [Tk * Hkv] * 2, "none": []}[cut]
+    if sizes:
+        assert grids["k_attn_sum"] == (-(-max(sizes) * d // 1024), len(sizes))
+    assert ("k_attn_sum" in grids) == bool(sizes)
+    assert all(x * y * threads < 1 << 32 for _, x, y, threads in launches)
