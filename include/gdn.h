@@ -550,7 +550,10 @@ int gdn_rope_freqs(int32_t r, double base, const gdn_rope_scaling_t* scaling, fl
  * infinite.
  *
  * Supported: d 64, 128 or 256; H_q a multiple of H_kv, at most 4096; 0 < scale <=
- * 2^126.
+ * 2^126.  A batch whose launches would hold 2^32 threads is refused
+ * (GDN_ERR_UNSUPPORTED); none is where (T / 128 + n_seqs) max(H_q, 64) <= 2^21, T the
+ * larger of T_q and T_k (for the cache (T / 32 + 2 n_seqs) max(H_q, 64) <= 2^23,
+ * whatever max_len is).
  */
 typedef struct {
   int32_t H_q, H_kv;

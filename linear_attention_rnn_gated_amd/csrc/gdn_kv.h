@@ -52,6 +52,8 @@ struct DecIO {
   float* stat;  // [..][2]: maximum (of s log2 e) and sum
   int64_t T, ldq, ldo, rows;
   int64_t mul, extra;  // sequence n's partial results begin at mul cu[n] G + extra n
+  int64_t item0;       // the join's first row of a head
+  int split0;          // the launch's first split
   int N, H_q, H_kv, G, max_len;
   float c;
 };
@@ -130,6 +132,14 @@ int kv_dispatch(const gdn_attn_shape_t* s, F&& f) {
   if (s->d == 64) return f.template operator()<float, 64>();
   if (s->d == 128) return f.template operator()<float, 128>();
   return f.template operator()<float, 256>();
+}
+
+// Launches go(y0, y) over `y` of splits and x blocks of `threads` for each, in as
+// many launches as keep each within what one may hold.
+template <typename F>
+void in_launches(int64_t x, int64_t y, int threads, F&& go) {
+  const int64_t fit = (kLaunchThreads - 1) / (x * threads), most = fit < 65535 ? fit : 65535;
+  for (int64_t y0 = 0; y0 < y; y0 += most) go(static_cast<int>(y0), static_cast<unsigned>(y - y0 < most ? y - y0 : most));
 }
 
 // Launches k_attn_decode_wide over `tiles` tiles of kAttnRows rows and `splits`

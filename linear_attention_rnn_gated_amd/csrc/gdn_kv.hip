@@ -328,7 +328,7 @@ __global__ __launch_bounds__(256) void k_attn_decode(DecIO io) {
   const int per = narrow_tiles(io.cu != nullptr, io.G), n = x / per, tile = x - n * per;
   const DecSeq sq = dec_seq(io, n);
   const int64_t r0 = static_cast<int64_t>(tile) * 16;
-  const int split = blockIdx.y;
+  const int split = io.split0 + blockIdx.y;
   if (r0 >= sq.rows || split >= sq.splits || sq.rows >= kWideRows) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4;
@@ -536,7 +536,7 @@ __global__ __launch_bounds__(GROUPS == 1 ? 256 : D / 4 * kJoin) void k_attn_join
   __shared__ __align__(16) float sh_y[GROUPS == 1 ? 1 : kJoin][D];
   __shared__ float sh_s[kJoin];
   const int e = threadIdx.x % LANES * 4, group = GROUPS == 1 ? 0 : threadIdx.x / LANES;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * PER + (GROUPS == 1 ? threadIdx.x / LANES : 0);
+  const int64_t item = io.item0 + static_cast<int64_t>(blockIdx.x) * PER + (GROUPS == 1 ? threadIdx.x / LANES : 0);
   const int64_t tk = item / io.H_q;
   const int head = static_cast<int>(item - tk * io.H_q);
   if (tk >= io.T) return;
@@ -720,7 +720,6 @@ int gdn_attn_decode(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t
   if (max_len > holds) max_len = holds;
   const int32_t G = shape->H_q / shape->H_kv;
   const int64_t splits = (max_len + kSplit - 1) / kSplit;
-  if (splits > 65535) return GDN_ERR_UNSUPPORTED;
   decode_layout(n_seqs, n_tokens, G, max_len, &io.mul, &io.extra);
   io.rows = (n_tokens * G * io.mul + n_seqs * io.extra) * shape->H_kv;
   if (splits > 1 && (!ws || ws_bytes < static_cast<size_t>(io.rows) * (shape->d + 2) * sizeof(float)))
@@ -746,12 +745,15 @@ int gdn_attn_decode(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t
     const int64_t tw = cu_seqlens ? all / kAttnRows + n_seqs : int64_t{n_seqs} * ((G + kAttnRows - 1) / kAttnRows);
     const int64_t y = splits > 0 ? splits : 1, few = kLongLen / kSplit;
     const int64_t yn = y <= few ? y : (y + 1) / 2 > few ? (y + 1) / 2 : few;
-    if ((narrow && tn * io.H_kv * 256 >= gdn::kLaunchThreads / yn) || (wide && tw * io.H_kv * 256 >= gdn::kLaunchThreads / y) ||
-        n_tokens * io.H_q >= gdn::kLaunchThreads / 1024)
+    if ((narrow && tn * io.H_kv * 256 >= gdn::kLaunchThreads) || (wide && tw * io.H_kv * 256 >= gdn::kLaunchThreads))
       return static_cast<int>(GDN_ERR_UNSUPPORTED);
     if (narrow) {
       Timed t_("k_attn_decode", st);
-      hipLaunchKernelGGL((k_attn_decode<T, D>), dim3(static_cast<unsigned>(tn * io.H_kv), static_cast<unsigned>(yn)), dim3(256), 0, st, io);
+      in_launches(tn * io.H_kv, yn, 256, [&](int y0, unsigned ny) {
+        DecIO at = io;
+        at.split0 = y0;
+        hipLaunchKernelGGL((k_attn_decode<T, D>), dim3(static_cast<unsigned>(tn * io.H_kv), ny), dim3(256), 0, st, at);
+      });
     }
     if (wide) {
       const int rc = launch_decode_wide(shape, io, tw, y, st);
@@ -760,11 +762,17 @@ int gdn_attn_decode(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t
     const int64_t most = wide ? y : yn;  // splits of a sequence
     if (most > 1) {
       Timed t_("k_attn_join", st);
-      const int64_t items = n_tokens * io.H_q, per = 1024 / D;
-      if (most <= kJoin)
-        hipLaunchKernelGGL((k_attn_join<T, D, 1>), dim3(static_cast<unsigned>((items + per - 1) / per)), dim3(256), 0, st, io);
-      else
-        hipLaunchKernelGGL((k_attn_join<T, D, kJoin>), dim3(static_cast<unsigned>(items)), dim3(D / 4 * kJoin), 0, st, io);
+      // rows of a head, and as many of them as a launch of 1024 threads each holds (a multiple of per)
+      const int64_t items = n_tokens * io.H_q, fit = gdn::kLaunchThreads / 1024 - 16;
+      const bool brief = most <= kJoin;
+      for (io.item0 = 0; io.item0 < items; io.item0 += fit) {
+        const int64_t now = items - io.item0 < fit ? items - io.item0 : fit, per = brief ? 1024 / D : 1;
+        const dim3 grid(static_cast<unsigned>((now + per - 1) / per));
+        if (brief)
+          hipLaunchKernelGGL((k_attn_join<T, D, 1>), grid, dim3(256), 0, st, io);
+        else
+          hipLaunchKernelGGL((k_attn_join<T, D, kJoin>), grid, dim3(D / 4 * kJoin), 0, st, io);
+      }
     }
     return static_cast<int>(hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_HIP);
   });

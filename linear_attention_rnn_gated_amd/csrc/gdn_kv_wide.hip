@@ -106,7 +106,7 @@ __global__ __launch_bounds__(256, (kAttnOcc<T, D>)) void k_attn_decode_wide(DecI
   constexpr int BM = kAttnRows, BN = kAttnStep;
   __shared__ int odd[D + 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int hk = blockIdx.x % io.H_kv, x = blockIdx.x / io.H_kv, split = blockIdx.y;
+  const int hk = blockIdx.x % io.H_kv, x = blockIdx.x / io.H_kv, split = io.split0 + blockIdx.y;
   int tile;
   const int n = row_tile(io, BM, x, &tile);
   const DecSeq sq = dec_seq(io, n);
@@ -157,7 +157,11 @@ __global__ __launch_bounds__(256, (kAttnOcc<T, D>)) void k_attn_decode_wide(DecI
 int gdn::launch_decode_wide(const gdn_attn_shape_t* shape, const DecIO& io, int64_t tiles, int64_t splits, hipStream_t st) {
   return kv_dispatch(shape, [&]<typename T, int D>() {
     Timed t_("k_attn_decode_wide", st);
-    hipLaunchKernelGGL((k_attn_decode_wide<T, D>), dim3(static_cast<unsigned>(tiles * io.H_kv), static_cast<unsigned>(splits)), dim3(256), 0, st, io);
+    in_launches(tiles * io.H_kv, splits, 256, [&](int y0, unsigned y) {
+      DecIO at = io;
+      at.split0 = y0;
+      hipLaunchKernelGGL((k_attn_decode_wide<T, D>), dim3(static_cast<unsigned>(tiles * io.H_kv), y), dim3(256), 0, st, at);
+    });
     return static_cast<int>(hipGetLastError() == hipSuccess ? GDN_OK : GDN_ERR_HIP);
   });
 }

@@ -72,3 +72,28 @@ def test_the_gradients_sums(record, Hq, Hkv, d, t, n, Tq, Tk, cut):
         assert grids["k_attn_sum"] == (-(-max(sizes) * d // 1024), len(sizes))
     assert ("k_attn_sum" in grids) == bool(sizes)
     assert all(x * y * threads < 1 << 32 for _, x, y, threads in launches)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,n,T,max_len", [
+    (32, 8, 128, 8, 200_000, 500),        # many rows, nothing to join
+    (32, 8, 128, 1, 131_072, 131_072),
+    (32, 8, 256, 3, 140_000, 20_000),     # more rows than one launch of the join holds
+    (32, 8, 128, 1024, 1024, 1 << 20),    # many sequences that may become long
+    (2, 1, 64, 1, 20, 40_000_000),        # more splits than a grid's second dimension holds
+])
+def test_large_calls_take_several_launches(record, Hq, Hkv, d, n, T, max_len):
+    launches, rc = record("decode", Hq, Hkv, d, BF16, 1, n, T, max_len)
+    assert rc == B.GDN_OK
+    assert all(x * y * threads < 1 << 32 and y < 65536 for _, x, y, threads in launches)
+    splits = -(-max_len // 512)
+    halves = splits if splits <= 8 else max(8, -(-splits // 2))
+    assert sum(y for k, _, y, _ in launches if k == "k_attn_decode") == halves
+    assert sum(y for k, _, y, _ in launches if k == "k_attn_decode_wide") == (splits if T * Hq // Hkv >= 32 else 0)
+    per = 1024 // d if splits <= 16 else 1
+    assert sum(x * per for k, x, _, _ in launches if k == "k_attn_join") == (T * Hq if splits > 1 else 0)
+
+
+def test_what_no_launch_holds_is_refused(record):
+    for args in ((32, 8, 128, BF16, 1, 1 << 20, 1 << 20, 100), (32, 8, 128, BF16, 0, 1 << 21, 1 << 21, 100),
+                 (32, 8, 128, BF16, 1, 1, 1 << 29, 100)):
+        assert record("decode", *args) == ([], B.GDN_ERR_UNSUPPORTED), args

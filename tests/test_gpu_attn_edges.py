@@ -137,3 +137,55 @@ def test_holes_beside_an_unwritten_page(d, t, new, scale):
     o, lse = B.gdn_attn_decode(pool.shape, q, pool.cache, pool.dev_table, i32(kv), 400, cu_seqlens=cu_of([new] * 2).cuda(),
                                want_lse=True)
     decode_check(pool, q, [new] * 2, kv, o, lse)
+
+
+def test_more_rows_than_a_launch_of_the_join_holds():
+    """4.5 million rows of a head: those of the last sequence are joined by a second launch."""
+    lens, kv, Hq, Hkv, d = [139_990, 10], [64, 20_000], 32, 8, 256
+    shape = B.make_attn_shape(Hq, Hkv, d, BF16)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    cache = B.KvCache(shape, 400, 64, "cuda")
+    table = torch.arange(2 * 320, dtype=torch.int32, device="cuda").view(2, 320)
+    table[0, 1:] = -1
+    table[1] = torch.arange(320, device="cuda") + 60
+    k, v = (torch.randn(sum(kv), Hkv, d, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    B.gdn_kv_write(shape, k, v, cache, table, cu_seqlens=cu_of(kv).cuda())
+    q = torch.randn(sum(lens), Hq, d, generator=gen, device="cuda").bfloat16()
+    o, lse = B.gdn_attn_decode(shape, q, cache, table, i32(kv), 20_000, cu_seqlens=cu_of(lens).cuda(), want_lse=True)
+    assert not o[:lens[0] - 64].any() and torch.isneginf(lse[:lens[0] - 64]).all()
+    for n, r, m in ((0, slice(lens[0] - 64, lens[0]), 64), (1, slice(lens[0], None), 10)):
+        one, l1 = B.gdn_attn_decode(shape, q[r], cache, table[n:n + 1], i32(kv[n:n + 1]), kv[n], want_lse=True,
+                                    cu_seqlens=cu_of([m]).cuda())
+        assert torch.equal(one, o[r]) and torch.equal(l1, lse[r]), n
+
+
+@pytest.mark.parametrize("m", [1, 40])
+def test_more_splits_than_a_grids_second_dimension(m):
+    """34 million cached tokens, with one row and with forty."""
+    L, d, P = 34_000_000, 64, 4096
+    shape = B.make_attn_shape(1, 1, d, BF16, scale=1.0)
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    pages = -(-L // P)
+    cache = B.KvCache(shape, pages, P, "cuda")
+    table = torch.randperm(pages, generator=gen, device="cuda").to(torch.int32).view(1, pages)
+    k, v = (torch.randn(L, 1, d, generator=gen, device="cuda", dtype=BF16) for _ in range(2))
+    v[L - 70_000:] += 2  # the end counts
+    cu = cu_of([L]).cuda()
+    B.gdn_kv_write(shape, k, v, cache, table, cu_seqlens=cu)
+    B.gdn_kv_read(shape, cache, table, cu, L, k_out=k, v_out=v)
+    q = 0.4 * torch.randn(m, 1, d, generator=gen, device="cuda").bfloat16()
+    o, lse = B.gdn_attn_decode(shape, q, cache, table, i32([L]), L, cu_seqlens=cu_of([m]).cuda(), want_lse=True)
+    for i in {0, m - 1}:
+        top, sums, acc, end = -1e30, 0.0, 0.0, L - m + 1 + i
+        for a in range(0, end, 1 << 21):
+            b = min(a + (1 << 21), end)
+            s = (k[a:b, 0].float() * q[i, 0].float()).double().sum(1)
+            new = max(top, float(s.max()))
+            p, f = torch.exp(s - new), float(np.exp(top - new))
+            sums, acc, top = sums * f + float(p.sum()), acc * f + (p[:, None] * v[a:b, 0].double()).sum(0), new
+        # exp(s - max) is rounded to bf16 (2^-8 of each weight at most, and sum p |v| is near the mean of |v|), and so
+        # is the output
+        want = acc / sums
+        assert float((o[i, 0].double() - want).abs().max()) < 2.0 ** -8 * (float(want.abs().max()) + 2 * float(v.float().abs().mean()))
+        assert abs(float(lse[i, 0]) - (top + np.log(sums))) < 1e-4
+    del cache, k, v
