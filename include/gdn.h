@@ -547,7 +547,8 @@ int gdn_rope_freqs(int32_t r, double base, const gdn_rope_scaling_t* scaling, fl
  * One sequence's infinities and NaN reach no other's rows; within the sequence they
  * reach the rows that see them, forward (an infinite v as infinities or NaN), and
  * any, in the gradient.  fp32 inputs over 3.39e38 (the largest bf16) count as
- * infinite.
+ * infinite.  Scores s_ij hold up to 2^30 in magnitude; beyond that a row may become
+ * NaN.
  *
  * Supported: d 64, 128 or 256; H_q a multiple of H_kv, at most 4096; 0 < scale <=
  * 2^126.  A batch whose launches would hold 2^32 threads is refused
@@ -577,7 +578,8 @@ size_t gdn_attn_workspace_bytes(const gdn_attn_shape_t* shape, int64_t T_q, int6
  *     dS_ij = p_ij (dO_i . v_j - dO_i . o_i),   dv_j = sum p_ij dO_i,
  *     dq_i = scale sum_j dS_ij k_j,   dk_j = scale sum dS_ij q_i,
  * the sums of dk and dv over the queries of all heads of the group.  Keys that no
- * query sees get 0.  No atomics: bitwise reproducible, and T_q and T_k decide the
+ * query sees get 0.  lse is fp32: its rounding, 2^-24 |lse|, is an error of s in p.
+ * No atomics: bitwise reproducible, and T_q and T_k decide the
  * parts that the sums are cut into.  p and dS go into the products in bf16 (bf16
  * inputs) or as they are (fp32). */
 int gdn_attn_bwd(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t* cu_q,

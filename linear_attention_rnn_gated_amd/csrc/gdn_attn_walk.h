@@ -342,6 +342,10 @@ __device__ __forceinline__ void attn_walk(Stage& st, int grp, const Held<T, D> (
     a.l = a.l * f0 + ml[NW * 64] * f1;
   }
   a.l += other_half(a.l);
+  // The maximum's own weight is exp2 of what m c lost when it was rounded, 2^-64 at
+  // least up to scores of 2^30.  Of far larger ones, or where m c is infinite, all
+  // weights may be 0: NaN, and not a row that sees nothing.
+  if (a.l == 0.0f && a.m > -INFINITY) a.l = NAN;
   if (odd[D] != INT32_MAX) {
 #pragma unroll
     for (int d = 0; d < ND; ++d)

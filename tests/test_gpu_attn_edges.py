@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from linear_attention_rnn_gated_amd import binding as B
-from test_gpu_attn import BF16, DT, INF, NAN, Pool, _need_gpu, cu_of, decode_check, i32, np64  # noqa: F401
+from test_gpu_attn import BF16, DT, INF, NAN, UNIT, Pool, _need_gpu, cu_of, decode_check, i32, np64  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -189,3 +189,58 @@ def test_more_splits_than_a_grids_second_dimension(m):
         assert float((o[i, 0].double() - want).abs().max()) < 2.0 ** -8 * (float(want.abs().max()) + 2 * float(v.float().abs().mean()))
         assert abs(float(lse[i, 0]) - (top + np.log(sums))) < 1e-4
     del cache, k, v
+
+
+@pytest.mark.parametrize("d,t,new", [(64, "bf16", 0), (128, "bf16", 0), (256, "bf16", 0), (64, "f32", 0), (256, "f32", 0),
+                                     (64, "bf16", 40), (128, "f32", 40), (128, "bf16", 12), (64, "f32", 12)])
+def test_a_score_past_fp32(d, t, new):
+    """A score that fp32 does not hold times log2(e) gives NaN, not the answer of a row that sees nothing."""
+    n, big, m = 50, 1.7e19, new or 50
+    pool = Pool(2, 1, d, t, 32, [n], seed=4)
+    s = B.make_attn_shape(2, 1, d, DT[t], 1.0)
+    q, k, v, cu = pool.queries(m), pool.rows(n), pool.rows(n), cu_of([n]).cuda()
+    k[20, 0] = 0
+    k[20, 0, 0] = big
+    B.gdn_kv_write(s, k, v, pool.cache, pool.dev_table, cu_seqlens=cu)
+
+    def call():
+        if new:
+            return B.gdn_attn_decode(s, q, pool.cache, pool.dev_table, i32([n]), n, cu_seqlens=cu_of([m]).cuda(), want_lse=True)
+        return B.gdn_attn_prefill(s, q, k, v, cu)
+    o, lse = call()
+    at = m - 10
+    q[at, 0] = 0
+    q[at, 0, 0] = big  # big^2 is 2.9e38
+    o2, lse2 = call()
+    assert torch.isnan(o2[at, 0]).all() and torch.isnan(lse2[at, 0])
+    o2[at, 0], lse2[at, 0] = o[at, 0], lse[at, 0]
+    for a, b in ((o, o2), (lse, lse2)):  # other rows' scores with that key are some 1e19: NaN both times, or neither
+        torch.testing.assert_close(a, b, rtol=0, atol=0, equal_nan=True)
+
+
+@pytest.mark.parametrize("d,t,new", [(64, "bf16", 0), (128, "bf16", 0), (256, "bf16", 0), (64, "f32", 0), (256, "f32", 0),
+                                     (64, "bf16", 40), (128, "f32", 40), (128, "bf16", 12), (64, "f32", 12)])
+def test_equal_scores_near_the_largest(d, t, new):
+    """Scores of 5.4e8, the same for all keys: running means."""
+    n, m, big = 90, new or 90, 23168.0
+    pool = Pool(2, 1, d, t, 32, [n], seed=5)
+    s = B.make_attn_shape(2, 1, d, DT[t], 1.0)
+    q, k, v, cu = torch.zeros_like(pool.queries(m)), torch.zeros_like(pool.rows(n)), pool.rows(n), cu_of([n]).cuda()
+    q[:, 0, 0], q[:, 1, 0], k[:, 0, 0] = big, -big, big
+    if new:
+        B.gdn_kv_write(s, k, v, pool.cache, pool.dev_table, cu_seqlens=cu)
+        k, v = B.gdn_kv_read(s, pool.cache, pool.dev_table, cu, n)
+        o, lse = B.gdn_attn_decode(s, q, pool.cache, pool.dev_table, i32([n]), n, cu_seqlens=cu_of([m]).cuda(), want_lse=True)
+    else:
+        o, lse = B.gdn_attn_prefill(s, q, k, v, cu)
+    at, vd = np.arange(n - m + 1, n + 1), np64(v)[:, 0]
+    score = np64(k)[0, 0, 0] * big
+    for h, sign in ((0, 1), (1, -1)):
+        want = np.cumsum(vd, 0)[at - 1] / at[:, None]
+        size = np.cumsum(np.abs(vd), 0)[at - 1] / at[:, None]
+        # equal weights, rounded to bf16 (one part) or held in three; fp32 sums of `at` weights and of `at` products,
+        # each addition of which is off by 2^-24 of a sum that is no larger than the last one's size; the output's rounding
+        tol = (UNIT[t] + 2 * at[:, None] * 2.0 ** -24) * size + torch.finfo(DT[t]).eps / 2 * np.abs(want)
+        assert (np.abs(np64(o)[:, h] - want) <= tol).all()
+        # fp32: score log2(e), its logarithm added, and both times ln 2, a rounding each
+        assert (np.abs(np64(lse)[:, h] - (sign * score + np.log(at))) <= 3 * 2.0 ** -24 * 1.01 * score).all()
