@@ -639,9 +639,10 @@ int gdn_kv_read(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t* cu
  * query i sees the tokens up to kv_len - L_q + i.  max_len, at least every
  * kv_len[n] (tokens past it are not seen), sizes the launches and the workspace:
  * a captured call holds for lengths up to it.  lse fp32 [T, H_q], nullable.  The
- * cache's values go into the products exactly, in bf16, with q and exp(s - max) in
- * one bf16 part (bf16 q) or three that sum to them (fp32 q).  No atomics; a
- * sequence's bits depend on neither batch, page size nor max_len. */
+ * cache's values go into the products exactly, in bf16; of bf16 rows q does too, with
+ * exp(s - max) in two bf16 parts for a sequence of fewer than 32 rows a key/value
+ * head and in one for more; of fp32 rows both are three that sum to them.  No
+ * atomics; a sequence's bits depend on neither batch, page size nor max_len. */
 size_t gdn_attn_decode_workspace_bytes(const gdn_attn_shape_t* shape, int32_t n_seqs,
                                        int64_t T, int64_t max_len);
 int gdn_attn_decode(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t* cu_seqlens,

@@ -223,8 +223,12 @@ __global__ __launch_bounds__(256) void k_kv_read(KvIO io) {
 // of 128: 112 us, 536 MB at 4.8 TB/s (products fill 7% of the cycles); one of 131071,
 // 2 heads of 256: 31 us, 135 MB at 4.3 TB/s.  With its sums in the accumulation
 // registers (the compiler's choice where it has one) 134 instead of 117 and 37 instead
-// of 28, with splits of 512 tokens.  q and exp(s - m) of
-// bf16 rows go in as bf16 (2^-8 of each weight), of fp32 rows in three parts.
+// of 28, with splits of 512 tokens.
+//
+// q of bf16 rows goes in as it is and exp(s - m) in two bf16 parts, 2^-16 of each weight:
+// products have room (64 sequences: 112 us in one part, 113.5 in two, 114 in three; one
+// long: 30.5, 31.5, 32.5), and in one part outputs are 2.0e-3 to 2.2e-3 off (norms) where
+// their own rounding is 1.65e-3 to 1.7e-3.  Of fp32 rows both go in in three.
 typedef float v4acc __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ v4acc mma16(u32x4 a, u32x4 b, v4acc c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
@@ -315,7 +319,8 @@ struct KvRegs {
 template <typename T, int D>
 __global__ __launch_bounds__(256) void k_attn_decode(DecIO io) {
 #ifdef GDN_DEVICE_PASS
-  constexpr int NP = sizeof(T) == 2 ? 1 : 3, KC = D / 32, ND = D / 16, W = D / 64;
+  constexpr int NP = sizeof(T) == 2 ? 1 : 3, PP = sizeof(T) == 2 ? 2 : 3;  // parts of q and of the weights
+  constexpr int KC = D / 32, ND = D / 16, W = D / 64;
   constexpr int PAD = D + 4;
   __shared__ __align__(16) float sh_o[4][16][PAD];
   __shared__ float sh_m[4][16], sh_l[4][16];
@@ -394,7 +399,7 @@ __global__ __launch_bounds__(256) void k_attn_decode(DecIO io) {
           for (int i = NP - 1; i >= 0; --i) s[t] = mma16(a, q[k][i], s[t]);
         }
       }
-      u32x4 p[NP];
+      u32x4 p[PP];
       {
         float y[8];
         float top = m;
@@ -418,7 +423,7 @@ __global__ __launch_bounds__(256) void k_attn_decode(DecIO io) {
           y[e] = __builtin_amdgcn_exp2f(y[e] - mm);
           l += y[e];
         }
-        parts8<NP>(y, p);
+        parts8<PP>(y, p);
       }
       if (edge) {
 #pragma unroll
@@ -448,7 +453,7 @@ __global__ __launch_bounds__(256) void k_attn_decode(DecIO io) {
       for (int d = 0; d < ND; ++d) {  // row l % 16 of tile d is element (D / 16) (l % 16) + d
         const u32x4 a = codes8(cur.v[0][d % 4][d / 4], cur.v[1][d % 4][d / 4], cur.vs);
 #pragma unroll
-        for (int i = NP - 1; i >= 0; --i) acc[d] = mma16(a, p[i], acc[d]);
+        for (int i = PP - 1; i >= 0; --i) acc[d] = mma16(a, p[i], acc[d]);
       }
     }
     cur = nxt;

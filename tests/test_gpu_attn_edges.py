@@ -1,12 +1,14 @@
 """Attention over the cache and the cache's writes at the edges of what the entry
-points allow: padded batches, sequences without new tokens, pages that are not there."""
+points allow: padded batches, sequences without new tokens, pages that are not there,
+calls of several launches, very large scores; and what few rows of bf16 lose."""
 
 import numpy as np
 import pytest
 import torch
 
 from linear_attention_rnn_gated_amd import binding as B
-from test_gpu_attn import BF16, DT, INF, NAN, UNIT, Pool, _need_gpu, cu_of, decode_check, i32, np64  # noqa: F401
+from oracle import attn_oracle as A
+from test_gpu_attn import BF16, DT, INF, NAN, UNIT, Pool, _need_gpu, check, cu_of, decode_check, i32, np64  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -244,3 +246,20 @@ def test_equal_scores_near_the_largest(d, t, new):
         assert (np.abs(np64(o)[:, h] - want) <= tol).all()
         # fp32: score log2(e), its logarithm added, and both times ln 2, a rounding each
         assert (np.abs(np64(lse)[:, h] - (sign * score + np.log(at))) <= 3 * 2.0 ** -24 * 1.01 * score).all()
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,lens,new", [(8, 2, 128, [5, 600, 9000], 1), (16, 2, 256, [130, 4100], 3),
+                                               (31, 1, 64, [64, 1500], 1), (1, 1, 64, [1, 2, 40], 1)])
+def test_few_rows_of_bf16_lose_nothing_but_the_outputs_rounding(Hq, Hkv, d, lens, new):
+    """exp(s - max) in two bf16 parts: each rounding leaves 2^-8 of what it is given, 2^-16 of a weight."""
+    pool = Pool(Hq, Hkv, d, "bf16", 64, lens, seed=d)
+    pool.write(pool.rows(sum(lens)), pool.rows(sum(lens)), lens, [0] * len(lens))
+    q = pool.queries(new * len(lens))
+    o = B.gdn_attn_decode(pool.shape, q, pool.cache, pool.dev_table, i32(lens), max(lens),
+                          cu_seqlens=cu_of([new] * len(lens)).cuda())
+    for n, L in enumerate(lens):
+        k, there = pool.k.read(pool.table[n], 0, L)
+        v, _ = pool.v.read(pool.table[n], 0, L)
+        r = slice(n * new, (n + 1) * new)
+        want, _, bound, _ = A.decode_fwd(np64(q[r]), k, v, there, float(pool.shape.scale), 2.0 ** -16, L)
+        check(o[r], want, bound, f"o of {n}")
