@@ -2,13 +2,16 @@
 points allow: padded batches, sequences without new tokens, pages that are not there,
 calls of several launches, very large scores; and what few rows of bf16 lose."""
 
+import copy
+
 import numpy as np
 import pytest
 import torch
 
 from linear_attention_rnn_gated_amd import binding as B
 from oracle import attn_oracle as A
-from test_gpu_attn import BF16, DT, INF, NAN, UNIT, Pool, _need_gpu, check, cu_of, decode_check, i32, np64  # noqa: F401
+from test_gpu_attn import (BF16, DT, INF, NAN, UNIT, Pool, _need_gpu, backward, check, check_all, cu_of,  # noqa: F401
+                           decode_check, forward, i32, make, np64)
 
 pytestmark = pytest.mark.gpu
 
@@ -263,3 +266,93 @@ def test_few_rows_of_bf16_lose_nothing_but_the_outputs_rounding(Hq, Hkv, d, lens
         r = slice(n * new, (n + 1) * new)
         want, _, bound, _ = A.decode_fwd(np64(q[r]), k, v, there, float(pool.shape.scale), 2.0 ** -16, L)
         check(o[r], want, bound, f"o of {n}")
+
+
+@pytest.mark.parametrize("t,d,Hq,Hkv", [("bf16", 128, 4, 2), ("bf16", 256, 2, 1), ("f32", 64, 2, 1)])
+def test_a_captured_step_with_other_lengths(t, d, Hq, Hkv):
+    """Forward and gradient in one graph; between replays the sequences' lengths change, and the rows behind the last."""
+    T = 1100
+    p = make([T], Hq, Hkv, d, t, seed=d)
+    p["cu"] = cu_of([T, 0, 0]).cuda()
+    ws = torch.empty(B.attn_workspace_bytes(p["shape"], T), dtype=torch.uint8, device="cuda")
+    outs = {k: torch.empty_like(p[i]) for k, i in (("o", "q"), ("dq", "q"), ("dk", "k"), ("dv", "v"))}
+    grads = {k: outs[k] for k in ("dq", "dk", "dv")}
+
+    def step():
+        o, lse = forward(p, out=outs["o"])
+        backward(p, o, lse, ws=ws, out=grads)
+        return lse
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lse = step()
+    for lens in ([T, 0, 0], [300, 0, 500], [1, 700, 30], [0, 0, 0], [129, 128, 127]):
+        p["cu"].copy_(cu_of(lens))
+        for x in outs.values():
+            x.fill_(6.0)
+        ws.fill_(255)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        end = sum(lens)
+        assert all((x[end:] == 6).all() for x in outs.values()), lens
+        now = dict(p, lens=lens, lens_k=lens)
+        check_all(now, outs["o"], lse, grads)
+
+
+def test_two_streams_over_one_cache():
+    """Side by side, each with a workspace of its own, while a third writes to other pages."""
+    lens = [3000, 700, 40]
+    pool = Pool(8, 2, 128, "bf16", 64, [n + 64 for n in lens], seed=7, spare=4)
+    pool.write(pool.rows(sum(lens)), pool.rows(sum(lens)), lens, [0] * 3)
+    one, many = pool.queries(3), pool.queries(90)
+    cu = cu_of([50, 30, 10]).cuda()
+    used = set(pool.table.ravel().tolist())
+    free = i32([[p for p in range(pool.cache.pages) if p not in used][:2]])
+    k, v = pool.rows(100), pool.rows(100)
+    kw = [dict(q=one), dict(q=many, cu_seqlens=cu)]
+    ws = [torch.empty(B.attn_decode_workspace_bytes(pool.shape, 3, len(a["q"]), 3100), dtype=torch.uint8, device="cuda")
+          for a in kw]
+
+    def call(a, w):
+        a = dict(a)
+        return B.gdn_attn_decode(pool.shape, a.pop("q"), pool.cache, pool.dev_table, i32_lens, 3100, ws=w, **a)
+    i32_lens = i32(lens)
+    want = [call(a, w) for a, w in zip(kw, ws)]
+    sides = [torch.cuda.Stream() for _ in range(3)]
+    cu_new = cu_of([100]).cuda()
+    for s in sides:
+        s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for r in range(4):
+        for s, a, w in zip(sides, kw, ws):
+            with torch.cuda.stream(s):
+                got.append(call(a, w))
+        with torch.cuda.stream(sides[2]):
+            B.gdn_kv_write(pool.shape, k, v, pool.cache, free, cu_seqlens=cu_new)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want[i % 2]) for i, x in enumerate(got))
+
+
+def test_copies_of_a_cache_have_memory_of_their_own():
+    pool = Pool(4, 2, 64, "f32", 32, [90], seed=9)
+    pool.write(pool.rows(90), pool.rows(90), [90], [0])
+    q = pool.queries(1)
+    args = (pool.dev_table, i32([90]), 90)
+    want = B.gdn_attn_decode(pool.shape, q, pool.cache, *args)
+    copies = [copy.deepcopy(pool.cache), pool.cache.clone(), B.KvCache.of(*pool.cache.tensors())]
+    for c in copies:
+        assert torch.equal(B.gdn_attn_decode(pool.shape, q, c, *args), want)
+    pool.write(pool.rows(20), pool.rows(20), [20], [70])
+    now = B.gdn_attn_decode(pool.shape, q, pool.cache, *args)
+    assert not torch.equal(now, want)
+    for c, same in zip(copies, (want, want, now)):
+        assert torch.equal(B.gdn_attn_decode(pool.shape, q, c, *args), same)
+    with pytest.raises(ValueError, match="k_scale"):
+        B.KvCache.of(pool.cache.k, pool.cache.k_scale[:1], pool.cache.v, pool.cache.v_scale)
+    with pytest.raises(ValueError, match="v: expected|v:"):
+        B.KvCache.of(pool.cache.k, pool.cache.k_scale, pool.cache.v[:, :1], pool.cache.v_scale)
