@@ -61,7 +61,7 @@ struct AttnState {
 // The places of a wave's rows and of its block's.
 struct AttnRows {
   int lim;       // the lane's row sees tokens up to here
-  int lo, hi;    // the least and the largest of the wave's rows
+  int lo, hi;    // the least and (for the gradient) the largest of the wave's rows
   int block_lo;  // the least of the block's
 };
 

@@ -119,7 +119,6 @@ __global__ __launch_bounds__(256, (kAttnOcc<T, D>)) void k_attn_decode_wide(DecI
   AttnRows at;
   at.lim = in ? sq.sees(tok) : -1;
   at.lo = sq.sees(r0 / io.G);
-  at.hi = r0 < sq.rows ? sq.sees(r1 / io.G) : -1;
   at.block_lo = sq.sees(b0 / io.G);
   Held<T, D> q[D / 16];
   {
