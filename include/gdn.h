@@ -579,9 +579,10 @@ size_t gdn_attn_workspace_bytes(const gdn_attn_shape_t* shape, int64_t T_q, int6
  *     dq_i = scale sum_j dS_ij k_j,   dk_j = scale sum dS_ij q_i,
  * the sums of dk and dv over the queries of all heads of the group.  Keys that no
  * query sees get 0.  lse is fp32: its rounding, 2^-24 |lse|, is an error of s in p.
- * No atomics: bitwise reproducible, and T_q and T_k decide the
- * parts that the sums are cut into.  p and dS go into the products in bf16 (bf16
- * inputs) or as they are (fp32). */
+ * Of bf16 inputs p goes into dv and dS into dk rounded to bf16, and dS into dq in two
+ * bf16 parts; o's own rounding is in dq's dO_i . o_i, not in dk's.  Of fp32 inputs all go
+ * in as they are.  No atomics: bitwise reproducible, and T_q and T_k decide the parts
+ * that the sums are cut into. */
 int gdn_attn_bwd(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t* cu_q,
                  const int32_t* cu_k, int64_t T_q, int64_t T_k, const void* q, int64_t ldq,
                  const void* k, int64_t ldk, const void* v, int64_t ldv, const void* o,

@@ -2,6 +2,8 @@
 // kernels and C ABI.
 #include "gdn_attn_walk.h"
 
+#include <type_traits>
+
 namespace {
 
 struct AttnIO {
@@ -153,21 +155,27 @@ __global__ __launch_bounds__((256 * kAttnGroups<T, D>), (kAttnOcc<T, D>)) void k
 // formed twice (seven products where five would do), which is cheaper than adding dq
 // up in memory and keeps its order.
 //
-// 8x4096 tokens, 32 and 8 heads of 128, bf16: dq 1.65 ms (three products, 1000
-// TFLOP/s), dkv 2.58 ms (four, 850 TFLOP/s), bound by the matrix cores (54% and 46% of
-// the cycles, at 1.9 GHz).  P and dS of bf16 rows are rounded to bf16 for their
-// products, 2^-8 of each: with the outputs' own rounding and that of o within dO . o,
-// dq is 2.5e-3 off (norms), where rounding the output alone is 1.7e-3.  In two parts
-// they would take a third more products.  fp32 rows' are taken in three parts.
+// 8x4096 tokens, 32 and 8 heads of 128, bf16: dq 1.97 ms (four products, 1120 TFLOP/s),
+// dkv 2.5 ms (four, 880 TFLOP/s), bound by the matrix cores.
+//
+// What bf16 rows lose.  p goes into dv and dS into dk rounded to bf16, 2^-8 of each; in
+// two parts both, dkv takes 3.3 ms.  dS goes into dq in two parts (in one, dq 1.58 ms).
+// dO . o comes from an o that was rounded: of a row's dS, which sum to 0 but for that, dq
+// takes the sum, and dk's dO . o is corrected by it at no cost; dq would need p K beside
+// dS K, a product more.  Errors (norms; rounding the outputs alone is 1.66e-3), 8x4096
+// tokens: dq 1.84e-3, dk 2.35e-3, dv 2.3e-3 (with dS in one part and o as given 2.52e-3,
+// 2.44e-3); sequences of 16: 2.4e-3, 2.3e-3, 2.2e-3 (2.9e-3, 2.9e-3).  fp32 rows'
+// operands are all taken in three parts.
 struct GradIO {
   AttnIO a;  // o: the forward's output, read
   const void* dO;
   void* dq;
   void* dk;
   void* dv;
-  float* stat;  // [H_q][T_q][2]: lse log2(e) and dO . o
+  float* stat;  // [H_q][T_q][2]: lse log2(e) and dO . o, for dk and dv
   float* part;  // [parts][2][T_k][H_kv][D] fp32 sums for dk and dv, where parts > 1
   float* qpart;  // [qcuts][T_q][H_q][D] fp32 sums for dq, where qcuts > 1
+  float* gaps;   // [qcuts][H_q][T_q] sums of dS, likewise and of bf16 rows
   int qcuts;    // parts that the keys of a query tile are cut into
   int cuts;     // that the queries of a head are cut into
   int parts;    // that a group's heads and their queries are cut into
@@ -180,6 +188,8 @@ __global__ __launch_bounds__((256 * kAttnGroups<T, D>), (kAttnOcc<T, D>)) void k
 #ifdef GDN_DEVICE_PASS
   constexpr int BN = 32, NW = 4, NG = kAttnGroups<T, D>, KS = D / 16, ND = D / 32;
   using P = Plane<T, D, BN>;
+  constexpr bool SHORT = sizeof(T) == 2;  // o has lost bits of dO . o
+  static_assert(!SHORT || NG == 1);
   constexpr bool TWO = 4 * P::TILE <= 144 * 1024;
   constexpr int SB = TWO ? P::TILE : 16;
   __shared__ __align__(1024) char kA_[NG * P::TILE], vA_[NG * P::TILE], kB_[NG * SB], vB_[NG * SB];
@@ -204,12 +214,8 @@ __global__ __launch_bounds__((256 * kAttnGroups<T, D>), (kAttnOcc<T, D>)) void k
                     static_cast<uint32_t>(r * io.ldo * sizeof(T)) + col + 16 * ks * sizeof(T), dot);
     dot += other_half(dot);
     lse2 = x.row < x.sp.Lq ? io.lse[(x.sp.q0 + x.row) * io.H_q + x.hq] * kLog2e : 0.0f;
-    if (grp == 0 && blockIdx.y == 0 && x.row < x.sp.Lq && lane < 32) {
-      float* s = g.stat + 2 * (static_cast<int64_t>(x.hq) * io.T_q + x.sp.q0 + x.row);
-      s[0] = lse2;
-      s[1] = dot;
-    }
   }
+  float gap = 0.0f;  // sum of dS
   const int all = x.last >= 0 ? x.last / (NG * BN) + 1 : 0, each = (all + g.qcuts - 1) / g.qcuts;
   const int begin = blockIdx.y * each, end = begin + each < all ? begin + each : all;
   RowStage<T, D, BN, NW, NG> st(io, x.sp, x.hk, begin * NG + grp, wave, lane);
@@ -234,10 +240,11 @@ __global__ __launch_bounds__((256 * kAttnGroups<T, D>), (kAttnOcc<T, D>)) void k
         const float p = __builtin_amdgcn_exp2f(fmaf(s[i], io.c, -lse2));
         s[i] = p * (dp[i] - dot);
         if (edge && j0 + c_row(i, lane) > x.at.lim) s[i] = 0.0f;
+        if constexpr (SHORT) gap += s[i];
       }
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        Frag<T> ds;
+        std::conditional_t<SHORT, TwoParts, Frag<T>> ds;
         ds.pack(s, 8 * u);
 #pragma unroll
         for (int d = 0; d < ND; ++d) acc[d] = mma32(col_frag<T, D, BN>(kb, 16 * u, d, lane), ds, acc[d]);
@@ -290,14 +297,32 @@ __global__ __launch_bounds__((256 * kAttnGroups<T, D>), (kAttnOcc<T, D>)) void k
 #pragma unroll
     for (int i = 0; i < 2 * H; ++i) acc[i / 16][i % 16] += (i < H ? s0 + i * 256 : s1 + (i - H) * 256)[0];
   }
+  if constexpr (SHORT) gap += other_half(gap);
   if (x.row < x.sp.Lq) {
     const int64_t row = x.sp.q0 + x.row;
+    if (lane < 32) {
+      const int64_t i = static_cast<int64_t>(x.hq) * io.T_q + row;
+      if (SHORT && g.qcuts > 1) g.gaps[blockIdx.y * (io.H_q * io.T_q) + i] = gap;
+      if (blockIdx.y == 0) {
+        g.stat[2 * i] = lse2;
+        g.stat[2 * i + 1] = SHORT && g.qcuts == 1 ? dot + gap : dot;
+      }
+    }
     if (g.qcuts == 1)
       store_row<D>(static_cast<T*>(g.dq) + row * g.lddq + static_cast<int64_t>(x.hq) * D, acc, g.scale, lane);
     else
       store_row<D>(g.qpart + ((blockIdx.y * io.T_q + row) * io.H_q + x.hq) * D, acc, g.scale, lane);
   }
 #endif
+}
+
+// dO . o of bf16 rows from what dS of the parts of k_attn_dq sums to, in order.
+__global__ __launch_bounds__(256) void k_attn_stat(float* stat, const float* gaps, int64_t rows, int parts) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= rows) return;
+  float gap = 0.0f;
+  for (int c = 0; c < parts; ++c) gap += gaps[c * rows + i];
+  stat[2 * i + 1] += gap;
 }
 
 // The keys of a block of k_attn_dkv, 32 for each wave, and the query tiles of BQ
@@ -719,7 +744,7 @@ size_t gdn_attn_workspace_bytes(const gdn_attn_shape_t* shape, int64_t T_q, int6
   const int parts = dkv_parts(shape, T_k).all(), cuts = dq_cuts(shape, T_q);
   const size_t dkv = parts > 1 ? static_cast<size_t>(parts) * 2 * T_k * shape->H_kv : 0;
   const size_t dq = cuts > 1 ? static_cast<size_t>(cuts) * T_q * shape->H_q : 0;
-  return stat_bytes(shape, T_q) + ((dkv + dq) * shape->d * sizeof(float) + gdn::kAlign - 1) / gdn::kAlign * gdn::kAlign;
+  return stat_bytes(shape, T_q) + (((dkv + dq) * shape->d + dq) * sizeof(float) + gdn::kAlign - 1) / gdn::kAlign * gdn::kAlign;
 }
 
 int gdn_attn_bwd(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t* cu_q, const int32_t* cu_k, int64_t T_q,
@@ -745,6 +770,7 @@ int gdn_attn_bwd(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t* c
   g.part = g.stat + stat_bytes(shape, T_q) / sizeof(float);
   g.qcuts = dq_cuts(shape, T_q);
   g.qpart = g.part + (g.parts > 1 ? g.parts * 2 * T_k * wk : 0);
+  g.gaps = g.qpart + (g.qcuts > 1 ? g.qcuts * T_q * wq : 0);
   g.scale = shape->scale;
   hipStream_t st = static_cast<hipStream_t>(stream);
   return attn_dispatch(shape, [&]<typename T, int D>() {
@@ -754,6 +780,11 @@ int gdn_attn_bwd(const gdn_attn_shape_t* shape, int32_t n_seqs, const int32_t* c
     if (T_q > 0) {
       Timed t_("k_attn_dq", st);
       hipLaunchKernelGGL((k_attn_dq<T, D>), dim3(static_cast<unsigned>(nq), g.qcuts), dim3(threads), 0, st, g);
+    }
+    if (sizeof(T) == 2 && g.qcuts > 1 && T_k > 0) {
+      Timed t_("k_attn_stat", st);
+      const int64_t rows = T_q * g.a.H_q;
+      hipLaunchKernelGGL(k_attn_stat, dim3(static_cast<unsigned>((rows + 255) / 256)), dim3(256), 0, st, g.stat, g.gaps, rows, g.qcuts);
     }
     if (T_k > 0) {
       Timed t_("k_attn_dkv", st);

@@ -92,6 +92,20 @@ struct Frag<float> {
   }
 };
 
+// Right operands in two bf16 parts, which hold 16 bits of them.
+struct TwoParts {
+  u32x4 p[2];
+  __device__ __forceinline__ void pack(const v16f& c, int i0) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float a = c[i0 + 2 * e], b = c[i0 + 2 * e + 1];
+      const uint32_t w = pack_bf16(a, b);
+      p[0][e] = w;
+      p[1][e] = pack_bf16(a - __uint_as_float(w << 16), b - __uint_as_float(w & 0xffff0000u));
+    }
+  }
+};
+
 // An operand that a wave holds throughout: as loaded where its parts would take
 // too many registers (fp32 at d = 256), else ready for the products.
 template <typename T, int D>
@@ -167,6 +181,11 @@ __device__ __forceinline__ v16f mma32(const Frag<float>& a, const Frag<float>& b
 // A left operand that is exact in one part.
 __device__ __forceinline__ v16f mma32(const Frag<bf16_t>& a, const Frag<float>& b, v16f c) {
   c = mma32(a.x, b.p[2], c);
+  c = mma32(a.x, b.p[1], c);
+  return mma32(a.x, b.p[0], c);
+}
+
+__device__ __forceinline__ v16f mma32(const Frag<bf16_t>& a, const TwoParts& b, v16f c) {
   c = mma32(a.x, b.p[1], c);
   return mma32(a.x, b.p[0], c);
 }

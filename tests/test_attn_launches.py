@@ -32,14 +32,14 @@ def record(tmp_path_factory):
         for row in rows:
             name, x, y, z, threads = row.split()
             assert z == "1"
-            known = [k for k in KERNELS if k + "I" in name]
+            known = [k for k in KERNELS if k + "I" in name or k + "E" in name]
             assert len(known) == 1, name
             out.append((known[0], int(x), int(y), int(threads)))
         return out, int(last.split()[1])
     return run
 
 
-KERNELS = ("k_attn_decode", "k_attn_decode_wide", "k_attn_join", "k_attn_dq", "k_attn_dkv", "k_attn_sum")
+KERNELS = ("k_attn_decode", "k_attn_decode_wide", "k_attn_join", "k_attn_dq", "k_attn_dkv", "k_attn_sum", "k_attn_stat")
 
 
 @pytest.mark.parametrize("Hq,Hkv,n,T", [(4, 2, 1, 64), (8, 1, 1, 4), (31, 1, 1, 2), (4, 2, 2, 64), (16, 2, 5, 5)])
@@ -71,6 +71,7 @@ def test_the_gradients_sums(record, Hq, Hkv, d, t, n, Tq, Tk, cut):
     if sizes:
         assert grids["k_attn_sum"] == (-(-max(sizes) * d // 1024), len(sizes))
     assert ("k_attn_sum" in grids) == bool(sizes)
+    assert ("k_attn_stat" in grids) == (t == BF16 and cut in ("q", "both"))
     assert all(x * y * threads < 1 << 32 for _, x, y, threads in launches)
 
 

@@ -1,6 +1,6 @@
 """Attention over the cache and the cache's writes at the edges of what the entry
 points allow: padded batches, sequences without new tokens, pages that are not there,
-calls of several launches, very large scores; and what few rows of bf16 lose."""
+calls of several launches, very large scores; and what bf16 rows lose."""
 
 import copy
 
@@ -11,7 +11,7 @@ import torch
 from linear_attention_rnn_gated_amd import binding as B
 from oracle import attn_oracle as A
 from test_gpu_attn import (BF16, DT, INF, NAN, UNIT, Pool, _need_gpu, backward, check, check_all, cu_of,  # noqa: F401
-                           decode_check, forward, i32, make, np64)
+                           decode_check, forward, i32, make, np64, spans)
 
 pytestmark = pytest.mark.gpu
 
@@ -356,3 +356,48 @@ def test_copies_of_a_cache_have_memory_of_their_own():
         B.KvCache.of(pool.cache.k, pool.cache.k_scale[:1], pool.cache.v, pool.cache.v_scale)
     with pytest.raises(ValueError, match="v: expected|v:"):
         B.KvCache.of(pool.cache.k, pool.cache.k_scale, pool.cache.v[:, :1], pool.cache.v_scale)
+
+
+def small_units(p, o):
+    """For each sequence its rows, and the gradients from exact weights and the o that the call was given, with bounds that
+    leave dS 2^-16 of each weight and o nothing."""
+    for rq, rk in spans(p):
+        q, k, v, do, og = (np64(x) for x in (p["q"][rq], p["k"][rk], p["v"][rk], p["do"][rq], o[rq]))
+        (lq, hq, d), (lk, hkv, _) = q.shape, k.shape
+        g = A.attn_bwd(q, k, v, do, p["scale"], 2.0 ** -16, 0.0)
+        kk, vv = np.repeat(k, hq // hkv, axis=1), np.repeat(v, hq // hkv, axis=1)
+        s = p["scale"] * np.einsum("ihd,jhd->hij", q, kk)
+        s = np.where(np.arange(lk) <= np.arange(lq)[:, None] + lk - lq, s, -np.inf)
+        w = np.exp(s - s.max(2, keepdims=True))
+        w /= w.sum(2, keepdims=True)
+        ds = w * (np.einsum("ihd,jhd->hij", do, vv) - np.einsum("ihd,ihd->hi", do, og)[..., None])
+        yield rq, rk, g, p["scale"] * np.einsum("hij,jhd->ihd", ds, kk)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,lens", [(4, 2, 128, [1, 2, 40, 300]), (2, 1, 64, [1100, 7]), (8, 2, 256, [65, 130]),
+                                           (1, 1, 128, [1030])])
+def test_dq_of_bf16_rows_loses_nothing_but_its_own_rounding(Hq, Hkv, d, lens):
+    """dS goes into dq in two bf16 parts."""
+    p = make(lens, Hq, Hkv, d, "bf16", seed=d)
+    o, lse = forward(p)
+    g = backward(p, o, lse)
+    for rq, _, bounds, want in small_units(p, o):
+        check(g["dq"][rq], want, bounds["dq"][1], "dq")
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,n", [(4, 2, 128, 9), (2, 1, 64, 1100), (8, 4, 256, 5), (1, 1, 128, 1030)])
+def test_dk_of_bf16_rows_takes_no_error_from_o(Hq, Hkv, d, n):
+    """Pairs of tokens with the same key: weights of 1/2 exactly, and o the mean of two values, which bf16 rounds."""
+    p = make([2] * n, Hq, Hkv, d, "bf16", seed=n)
+    p["k"][1::2] = p["k"][::2]
+    o, lse = forward(p)
+    g = backward(p, o, lse)
+    for _, rk, bounds, _ in small_units(p, o):
+        want, bound = bounds["dk"]
+        # dS goes in in one bf16 part: 2^-8 of each |dS q|
+        q, do, v = (np64(x) for x in (p["q"][rk], p["do"][rk], p["v"][rk]))
+        vv = np.repeat(v, Hq // Hkv, axis=1)
+        dp = np.einsum("ihd,jhd->hij", do, vv)
+        ds = 0.25 * np.abs(dp[:, 1, 0] - dp[:, 1, 1])  # of the second row, for either key
+        more = p["scale"] * (ds[:, None] * np.abs(q[1])).reshape(Hkv, Hq // Hkv, d).sum(1)
+        check(g["dk"][rk], want, bound + 2.0 ** -8 * more[None], "dk")
