@@ -2,8 +2,10 @@
 
 Flags that are part of the arithmetic contract: -ffp-contract=off (the only
 fused multiply-adds are the explicit fmaf calls), no fast-math, and packed
-FP32 instructions disabled; every source is built with the same flags, the
-kernels whose bits have to agree in one translation unit (gdn_library.hip).
+FP32 instructions disabled.  These are the same for every source; SOURCE_FLAGS
+says beside them where a source's matrix sums stand, which changes no bits.  The
+recurrences' kernels, whose bits have to agree, are one translation unit
+(gdn_library.hip).
 """
 
 import hashlib

@@ -63,7 +63,9 @@ constexpr int kRowsSplit = 256;    // rows for which the wide one's are that man
 // A sequence of so many rows goes to the wide kernel: 32 sequences of 4000 cached
 // tokens, 8 heads of 128: 32 rows each 144 us there and 156 in the narrow one, 64 rows
 // 173 (172), 124 rows 239 (300); 2 heads of 256: 32 rows 95 (96), 64 rows 102
-// (144).  The other way: one token of 32 heads that share one key head, 24 (18).
+// (144).  The rule counts rows and does not look at what they are of: one token of 32
+// heads that share one key head loses by it (24 us where the narrow one takes 18), as
+// three of the wide one's four waves then have no rows.
 constexpr int kWideRows = 32;
 // Tiles of 16 rows that the narrow one has for a sequence.
 __host__ __device__ inline int narrow_tiles(bool packed, int G) { return (packed ? kWideRows : G + 15) / 16; }

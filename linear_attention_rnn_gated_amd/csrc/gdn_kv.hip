@@ -220,7 +220,7 @@ __global__ __launch_bounds__(256) void k_kv_read(KvIO io) {
 // as it stands; the bytes of 4 tokens x 4 elements are transposed in registers.
 //
 // Bound by memory and the loads in flight: 64 sequences of 128 to 8192 tokens, 8 heads
-// of 128: 112 us, 536 MB at 4.8 TB/s (products fill 7% of the cycles); one of 131071,
+// of 128: 113 us, 536 MB at 4.7 TB/s (products fill 11% of the cycles); one of 131071,
 // 2 heads of 256: 31 us, 135 MB at 4.3 TB/s.  With its sums in the accumulation
 // registers (the compiler's choice where it has one) 134 instead of 117 and 37 instead
 // of 28, with splits of 512 tokens.

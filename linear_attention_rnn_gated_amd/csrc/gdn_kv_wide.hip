@@ -26,8 +26,9 @@ __device__ __forceinline__ int row_tile(const DecIO& io, int rows, int x, int* t
 // Sequences of kWideRows rows and more: 128 rows a workgroup and the walk that
 // attention over prompts takes, with codes that become bf16 on their way into LDS,
 // once for all of the rows.  Eight sequences with 64 to 500 new tokens and 500 to 8192
-// cached ones, 32 and 8 heads of 128: 304 us, 650 TFLOP/s (and 27 to join); bound by
-// the walk's steps and by 830 blocks of uneven length on 512 places.
+// cached ones, 32 and 8 heads of 128: 307 us, 640 TFLOP/s (and 27 to join); bound by
+// the walk's steps, in which vector instructions take 51% of the cycles (codes to bf16
+// once for 128 rows) and products 30%, and by 830 blocks of uneven length on 512 places.
 
 // Tiles of the cache, one block of it each: 16 codes a thread and step.
 template <int D>
