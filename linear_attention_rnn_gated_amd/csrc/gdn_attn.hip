@@ -652,7 +652,8 @@ void launch_dkv(const GradIO& g, unsigned blocks, hipStream_t st) {
 // in two); where that does not fill it either, the queries of a head as well (2048
 // tokens, 4 heads of 128: 35 us + 7 for their sums in four, 68 in one; 4096 tokens, 4
 // heads and 1: 90 + 14 in twelve, 120 + 28 in twenty-four, 132 + 6 in four).  For dq the
-// keys of a query tile (4096 tokens, 4 heads: 115 us in one, 54 in four).
+// keys of a query tile (4096 tokens, 4 heads, bf16: 131 us in one, 63 and 10 more for
+// their sums in four).
 struct DkvParts {
   int heads, cuts;
   int all() const { return heads * cuts; }
